@@ -115,6 +115,43 @@ pa_status pa_reshape_and_cache_quant(const void* k, const void* v, pa_dtype in_d
                                      const int64_t* slot_mapping, int num_tokens,
                                      const pa_cache_desc* cache, void* stream);
 
+/* ---------------------------------------------------------------- rotary embedding + cache write
+ * Rotates q and k by the angles of their tokens' positions and appends the
+ * rotated k and v to the pool, in one pass over the projections.  With
+ * a_i = position * base^(-2i / rot_dim), i < rot_dim / 2, pair i of every q and k
+ * head turns as (x, y) -> (x cos a_i - y sin a_i, y cos a_i + x sin a_i); the pair is
+ * elements (i, i + rot_dim/2) of the head, or (2i, 2i + 1) if interleaved != 0.
+ * Elements at and past rot_dim, and v, pass unchanged.  The arithmetic is fp32 and
+ * every result is rounded once, to the dtype it is stored in.
+ *   q, k, v       : in_dtype (PA_F32, PA_F16 or PA_BF16); token t's heads
+ *                   ([n_q_heads][head_dim] for q, [n_kv_heads][head_dim] for k and v) are
+ *                   contiguous at q + t * q_stride (k_stride, v_stride), strides in elements:
+ *                   the three may be slices of one fused projection.
+ *   q_out         : rotated q in in_dtype, tokens q_out_stride elements apart.  May be q
+ *                   itself with the same stride; otherwise it must not overlap q, k or v.
+ *   positions     : int32 [num_tokens], each in [0, max_position).
+ *   cos_sin       : fp32 [max_position][rot_dim] on the device: the cosines of a row's
+ *                   rot_dim / 2 angles, then their sines (pa_rope_table fills one).
+ *   rot_dim       : a multiple of 16 in [16, head_dim].
+ *   k_cache, v_cache, slot_mapping: as for pa_reshape_and_cache; the pool has dtype in_dtype, or
+ *                   is an FP8 pool (codes as pa_reshape_and_cache_quant makes them, of the rotated
+ *                   k before any rounding; head_dim 64 or 128).
+ * Of a token with slot < 0 (padding) nothing is written, its q_out row included; neither of
+ * one whose slot or position is out of range, which sets PA_ERR_OUT_OF_RANGE on the device.
+ * Pointers 16-byte aligned (positions 4, slot_mapping 8); strides multiples of 16 bytes and at
+ * least heads * head_dim.  num_tokens == 0 is a no-op; num_tokens * (n_q_heads + 2 n_kv_heads) *
+ * head_dim must be below 2^35 (2^34 for fp32), else PA_ERR_UNSUPPORTED. */
+pa_status pa_rope_and_cache(void* q_out, const void* q, const void* k, const void* v,
+                            pa_dtype in_dtype, int64_t q_out_stride, int64_t q_stride,
+                            int64_t k_stride, int64_t v_stride, const int32_t* positions,
+                            const float* cos_sin, int max_position, int rot_dim, int interleaved,
+                            void* k_cache, void* v_cache, const int64_t* slot_mapping,
+                            int num_tokens, int n_q_heads, const pa_cache_desc* cache,
+                            void* stream);
+/* Host: fills table (host memory, fp32 [max_position][rot_dim]) with the cosines and sines
+ * above, computed in fp64.  Returns 0, or -1 on bad arguments (rot_dim odd, base <= 0, ...). */
+int pa_rope_table(float* table, int max_position, int rot_dim, double base);
+
 /* ---------------------------------------------------------------- decode
  * One query row per sequence ("Life of a prompt", "The decode stage"):
  *   out[s][h] = softmax(scale * q[s][h] . K_s^T) V_s

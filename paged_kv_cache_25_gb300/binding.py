@@ -17,7 +17,8 @@ import torch
 from . import build as _build
 
 __all__ = [
-    "PAError", "lib", "pa_reshape_and_cache", "pa_reshape_and_cache_quant", "pa_decode",
+    "PAError", "lib", "pa_reshape_and_cache", "pa_reshape_and_cache_quant",
+    "pa_rope_and_cache", "pa_rope_table", "pa_decode",
     "pa_decode_workspace_size", "pa_decode_verify", "pa_decode_verify_workspace_size",
     "pa_decode_no_alloc", "PA_DECODE_NO_ALLOC_SCRATCH_BYTES",
     "pa_prefill_chunk", "pa_prefill_workspace_size", "pa_get_device_error", "pa_status_string",
@@ -46,6 +47,9 @@ _SIGS = {
     "pa_decode_verify": (I, [P, I, P, P, P, C.POINTER(_Desc), P, I, P, I, I, I, F, I, P, SZ, P]),
     "pa_decode_verify_workspace_size": (SZ, [I, I, I, I, I, I, I]),
     "pa_reshape_and_cache_quant": (I, [P, P, I, P, P, P, I, C.POINTER(_Desc), P]),
+    "pa_rope_and_cache": (I, [P, P, P, P, I, L, L, L, L, P, P, I, I, I, P, P, P, I, I,
+                              C.POINTER(_Desc), P]),
+    "pa_rope_table": (I, [P, I, I, C.c_double]),
     "pa_prefill_chunk": (I, [P, I, P, P, P, C.POINTER(_Desc), P, I, P, P, I, I, I, F, I, P, SZ, P]),
     "pa_prefill_workspace_size": (SZ, [I, I, I, I]),
     "pa_copy_blocks": (I, [P, P, C.POINTER(_Desc), P, I, P]),
@@ -201,6 +205,53 @@ def pa_reshape_and_cache_quant(k, v, k_cache, v_cache, slot_mapping, k_scale=Non
                                             _ptr(v_cache), _ptr(slot_mapping), int(k.shape[0]),
                                             C.byref(d), _stream(stream)),
            "pa_reshape_and_cache_quant")
+
+
+def _token_stride(t, name: str) -> int:
+    """Elements from token to token of [T][heads][d]; a token's heads are contiguous."""
+    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"{name}: [tokens][heads][head_dim] with contiguous heads expected")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def pa_rope_and_cache(q_out, q, k, v, positions, cos_sin, k_cache, v_cache, slot_mapping,
+                      interleaved: bool = False, stream=None, k_scale=None, v_scale=None):
+    """q_out [T][n_q][d] = q rotated by its tokens' positions (int32 [T]); k, rotated, and v
+    [T][n_kv][d] go to slot_mapping (int64 [T]) of the pools.  q, k and v may be slices of one
+    projection (any token stride).  cos_sin: fp32 [max_position][rot_dim], see pa_rope_table.
+    FP8 pools take their scales."""
+    T, n_q, hd = q.shape
+    if tuple(q_out.shape) != (T, n_q, hd) or k.shape != v.shape or \
+            tuple(k.shape) != (T, k_cache.shape[1], hd) or hd != k_cache.shape[3]:
+        raise ValueError("q_out, q [T][n_q][d] and k, v [T][n_kv][d] expected")
+    if q_out.dtype != q.dtype or k.dtype != q.dtype or v.dtype != q.dtype:
+        raise TypeError("q_out, q, k and v must have one dtype")
+    if positions.dtype != torch.int32 or slot_mapping.dtype != torch.int64 or \
+            cos_sin.dtype != torch.float32:
+        raise TypeError("positions int32, slot_mapping int64 and cos_sin float32 expected")
+    if positions.numel() != T or slot_mapping.numel() != T or cos_sin.dim() != 2 or \
+            not (positions.is_contiguous() and slot_mapping.is_contiguous() and
+                 cos_sin.is_contiguous()):
+        raise ValueError("positions [T], slot_mapping [T] and cos_sin [max_position][rot_dim], "
+                         "contiguous, expected")
+    d = _desc(k_cache, k_scale, v_scale, q.dtype)
+    _check(lib().pa_rope_and_cache(_ptr(q_out), _ptr(q), _ptr(k), _ptr(v), dtype_code(q.dtype),
+                                   _token_stride(q_out, "q_out"), _token_stride(q, "q"),
+                                   _token_stride(k, "k"), _token_stride(v, "v"), _ptr(positions),
+                                   _ptr(cos_sin), cos_sin.shape[0], cos_sin.shape[1],
+                                   int(interleaved), _ptr(k_cache), _ptr(v_cache),
+                                   _ptr(slot_mapping), T, n_q, C.byref(d), _stream(stream)),
+           "pa_rope_and_cache")
+
+
+def pa_rope_table(max_position: int, rot_dim: int, base: float = 10000.0) -> torch.Tensor:
+    """fp32 [max_position][rot_dim] (host): cosines, then sines, of position * base^(-2i/rot_dim)."""
+    if max_position < 1 or rot_dim < 1:
+        raise PAError(PA_ERR_INVALID_ARG, "pa_rope_table: bad size")
+    table = torch.empty(max_position, rot_dim, dtype=torch.float32)
+    if lib().pa_rope_table(_ptr(table), max_position, rot_dim, float(base)) != 0:
+        raise PAError(PA_ERR_INVALID_ARG, "pa_rope_table: bad rot_dim or base")
+    return table
 
 
 def pa_decode(out, q, k_cache, v_cache, block_tables, context_lens, scale: float,

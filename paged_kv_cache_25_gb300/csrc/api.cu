@@ -309,6 +309,61 @@ pa_status pa_reshape_and_cache(const void* k, const void* v, void* k_cache, void
     return ok();
 }
 
+pa_status pa_rope_and_cache(void* q_out, const void* q, const void* k, const void* v,
+                            pa_dtype in_dtype, int64_t q_out_stride, int64_t q_stride,
+                            int64_t k_stride, int64_t v_stride, const int32_t* positions,
+                            const float* cos_sin, int max_position, int rot_dim, int interleaved,
+                            void* k_cache, void* v_cache, const int64_t* slot_mapping,
+                            int num_tokens, int n_q_heads, const pa_cache_desc* cache, void* stream)
+{
+    pa_status st = check_cache(cache, false);
+    if (st != PA_OK) return st;
+    if (in_dtype != PA_F32 && in_dtype != PA_F16 && in_dtype != PA_BF16)
+        return fail(PA_ERR_INVALID_ARG, "unknown in_dtype %d", (int)in_dtype);
+    if (cache->dtype != in_dtype && cache->dtype != PA_FP8_E4M3)
+        return fail(PA_ERR_UNSUPPORTED, "cache write from dtype %d into dtype %d", (int)in_dtype,
+                    (int)cache->dtype);
+    if (cache->dtype == PA_FP8_E4M3 && cache->head_dim != 64 && cache->head_dim != 128)
+        return fail(PA_ERR_UNSUPPORTED, "FP8 pools take head_dim 64 or 128");
+    if (n_q_heads <= 0) return fail(PA_ERR_INVALID_ARG, "n_q_heads must be positive");
+    if (rot_dim < 16 || rot_dim > cache->head_dim || rot_dim % 16 != 0)
+        return fail(PA_ERR_INVALID_ARG, "rot_dim %d is not a multiple of 16 in [16, head_dim]", rot_dim);
+    if (max_position <= 0) return fail(PA_ERR_INVALID_ARG, "max_position must be positive");
+    if (num_tokens < 0) return fail(PA_ERR_INVALID_ARG, "num_tokens < 0");
+    if (num_tokens == 0) return ok();
+    if (!q_out || !q || !k || !v || !positions || !cos_sin || !k_cache || !v_cache || !slot_mapping)
+        return fail(PA_ERR_INVALID_ARG, "NULL pointer argument");
+    if (!aligned16(q_out) || !aligned16(q) || !aligned16(k) || !aligned16(v) ||
+        !aligned16(cos_sin) || !aligned16(k_cache) || !aligned16(v_cache))
+        return fail(PA_ERR_INVALID_ARG, "q, k, v, the table and the pools must be 16-byte aligned");
+    if ((reinterpret_cast<uintptr_t>(slot_mapping) & 7u) != 0 ||
+        (reinterpret_cast<uintptr_t>(positions) & 3u) != 0)
+        return fail(PA_ERR_INVALID_ARG, "slot_mapping must be 8-byte and positions 4-byte aligned");
+    const int64_t align = 16 / elem_bytes(in_dtype);
+    const int64_t q_row = static_cast<int64_t>(n_q_heads) * cache->head_dim;
+    const int64_t kv_row = static_cast<int64_t>(cache->n_kv_heads) * cache->head_dim;
+    if (q_out_stride < q_row || q_stride < q_row || k_stride < kv_row || v_stride < kv_row)
+        return fail(PA_ERR_INVALID_ARG, "a token stride is smaller than the token's heads");
+    if (q_out_stride % align || q_stride % align || k_stride % align || v_stride % align)
+        return fail(PA_ERR_INVALID_ARG, "token strides must be multiples of 16 bytes");
+    if (q_out == q && q_out_stride != q_stride)
+        return fail(PA_ERR_INVALID_ARG, "q rotated in place needs one stride");
+    if (num_tokens * ((q_row + 2 * kv_row) / (2 * align)) >= (1ll << 31))
+        return fail(PA_ERR_UNSUPPORTED, "too many elements for one call");
+    unsigned* err = device_error_word();
+    if (!err) return fail(PA_ERR_CUDA, "cannot locate the device error word");
+    RopeArgs a{};
+    a.q_out = q_out; a.q = q; a.k = k; a.v = v; a.in_dtype = in_dtype;
+    a.q_out_stride = q_out_stride; a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;
+    a.positions = positions; a.cos_sin = cos_sin; a.max_position = max_position;
+    a.rot_dim = rot_dim; a.interleaved = interleaved != 0;
+    a.k_cache = k_cache; a.v_cache = v_cache; a.slots = slot_mapping;
+    a.num_tokens = num_tokens; a.n_q = n_q_heads; a.cache = *cache; a.err = err;
+    const cudaError_t e = launch_rope(a, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "rotary cache write launch");
+    return ok();
+}
+
 pa_status pa_swap_blocks(const void* src_k, const void* src_v, int src_num_blocks, void* dst_k,
                          void* dst_v, int dst_num_blocks, const pa_cache_desc* layout,
                          const int32_t* block_mapping, int num_pairs, void* stream)

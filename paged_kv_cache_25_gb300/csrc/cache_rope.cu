@@ -1,0 +1,314 @@
+// Rotary position embedding fused with the cache write: q and k are rotated by
+// the angle of their token's position, q goes to its output and k (rotated) and
+// v into their slots of the paged pool, in one pass over the projections.
+//
+// Mathematics: with angle a = position * base^(-2i/rot), i < rot/2, pair i of a
+// head turns as  (x, y) -> (x cos a - y sin a, y cos a + x sin a).  The pair is
+// elements (i, i + rot/2) of the head, or (2i, 2i + 1) in the interleaved form;
+// elements at and past `rot` pass unchanged.  cos and sin come from the caller's
+// fp32 table, the products are fp32 and each result is rounded once, to the
+// dtype it is stored in (an E4M3 code of the value over the scale for FP8 pools).
+//
+// Bound: HBM for long chunks (every element is read once and written once,
+// 3 flops each), launch latency for a decode step.
+#include <cuda_fp8.h>
+
+#include "pa_device.cuh"
+#include "pa_internal.h"
+
+namespace pa {
+
+// Elements of one 16-byte piece as floats and back.
+template <typename T>
+struct Piece {
+    static constexpr int kN = 16 / static_cast<int>(sizeof(T));
+    __device__ __forceinline__ static void load(const T* p, float (&x)[kN])
+    {
+        const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p));   // read once: streaming
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                x[i] = __uint_as_float(w[i]);
+            } else {
+                const float2 f = Cvt<T>::unpack(w[i]);
+                x[2 * i] = f.x;
+                x[2 * i + 1] = f.y;
+            }
+        }
+    }
+    __device__ __forceinline__ static void store(T* p, const float (&x)[kN])
+    {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(x[i]);
+            else w[i] = Cvt<T>::pack(x[2 * i], x[2 * i + 1]);
+        }
+        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+
+// Four values as E4M3 codes of x / scale (IEEE division, rounded to nearest
+// even, saturated), first value in the low byte.
+__device__ __forceinline__ uint32_t codes4(const float* x, float scale)
+{
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(
+        make_float2(__fdiv_rn(x[0], scale), __fdiv_rn(x[1], scale)), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(
+        make_float2(__fdiv_rn(x[2], scale), __fdiv_rn(x[3], scale)), __NV_SATFINITE, __NV_E4M3);
+    return (lo & 0xFFFFu) | (hi << 16);
+}
+
+struct RopeParams {
+    const void *q, *k, *v;
+    void *q_out, *k_cache, *v_cache;
+    int64_t q_out_stride, q_stride, k_stride, v_stride;   // elements from token to token
+    const int32_t* positions;
+    const float* cos_sin;
+    const int64_t* slots;
+    int64_t num_slots;
+    int num_tokens, max_position, rot, interleaved;
+    int n_q, n_kv, head_dim, block_size;
+    float k_scale, v_scale;
+    unsigned* err;
+};
+
+// The token's slot, or -1 for a token of which nothing is written: padding, or
+// (flagged) a slot or a position out of range.
+__device__ __forceinline__ int64_t rope_slot(const RopeParams& p, int t, int& pos)
+{
+    const int64_t slot = __ldg(p.slots + t);
+    pos = __ldg(p.positions + t);
+    if (slot < 0) return -1;
+    if (slot >= p.num_slots || pos < 0 || pos >= p.max_position) {
+        set_error(p.err, PA_ERR_OUT_OF_RANGE);
+        return -1;
+    }
+    return slot;
+}
+
+constexpr int kRopeThreads = 256;
+constexpr int kVTok = 16;             // FP8: tokens of one transposed V tile
+
+// A thread moves two 16-byte pieces of one head of one token: in the rotated
+// part the two that its pairs lie in (pieces c and c + rot/2, or 2c and 2c + 1
+// interleaved: either way pairs c * kN .. + kN - 1), else two neighbours.
+// Consecutive threads take consecutive pieces, then heads, then tokens.
+template <typename T, bool F8>
+__device__ __forceinline__ void rope_item(const RopeParams& p, int64_t index, int heads, int per_head)
+{
+    using Pc = Piece<T>;
+    constexpr int N = Pc::kN;
+    const unsigned per_token = static_cast<unsigned>(heads * per_head);
+    const unsigned i = static_cast<unsigned>(index);
+    const int t = static_cast<int>(i / per_token);
+    if (t >= p.num_tokens) return;
+    const unsigned rem = i - static_cast<unsigned>(t) * per_token;
+    const int head = static_cast<int>(rem / per_head);
+    const int c = static_cast<int>(rem) - head * per_head;
+
+    const bool is_q = head < p.n_q, is_v = head >= p.n_q + p.n_kv;
+    const int rot_items = is_v ? 0 : p.rot / (2 * N);
+    const bool turn = c < rot_items;
+    const int e0 = turn && !p.interleaved ? c * N : 2 * c * N;            // first piece's element
+    const int e1 = turn && !p.interleaved ? p.rot / 2 + c * N : e0 + N;   // second piece's
+    const int h = is_q ? head : (is_v ? head - p.n_q - p.n_kv : head - p.n_q);
+    const T* src = static_cast<const T*>(is_q ? p.q : (is_v ? p.v : p.k)) +
+                   t * (is_q ? p.q_stride : (is_v ? p.v_stride : p.k_stride)) +
+                   static_cast<int64_t>(h) * p.head_dim;
+    float a[N], b[N];
+    Pc::load(src + e0, a);
+    Pc::load(src + e1, b);
+    int pos;
+    const int64_t slot = rope_slot(p, t, pos);
+    if (slot < 0) return;
+    if (turn) {
+        const float4* cs = reinterpret_cast<const float4*>(p.cos_sin + static_cast<int64_t>(pos) * p.rot + c * N);
+        const float4* sn = cs + p.rot / 8;
+        float co[N], si[N];
+#pragma unroll
+        for (int x = 0; x < N / 4; ++x) {
+            const float4 f = __ldg(cs + x), g = __ldg(sn + x);
+            co[4 * x] = f.x; co[4 * x + 1] = f.y; co[4 * x + 2] = f.z; co[4 * x + 3] = f.w;
+            si[4 * x] = g.x; si[4 * x + 1] = g.y; si[4 * x + 2] = g.z; si[4 * x + 3] = g.w;
+        }
+        if (p.interleaved) {
+#pragma unroll
+            for (int x = 0; x < N / 2; ++x) {
+                const float u = a[2 * x], w = a[2 * x + 1];
+                a[2 * x] = u * co[x] - w * si[x];
+                a[2 * x + 1] = w * co[x] + u * si[x];
+                const float u1 = b[2 * x], w1 = b[2 * x + 1];
+                b[2 * x] = u1 * co[N / 2 + x] - w1 * si[N / 2 + x];
+                b[2 * x + 1] = w1 * co[N / 2 + x] + u1 * si[N / 2 + x];
+            }
+        } else {
+#pragma unroll
+            for (int x = 0; x < N; ++x) {
+                const float u = a[x], w = b[x];
+                a[x] = u * co[x] - w * si[x];
+                b[x] = w * co[x] + u * si[x];
+            }
+        }
+    }
+    if (is_q) {
+        T* dst = static_cast<T*>(p.q_out) + t * p.q_out_stride + static_cast<int64_t>(h) * p.head_dim;
+        Pc::store(dst + e0, a);
+        Pc::store(dst + e1, b);
+        return;
+    }
+    const int64_t blk = slot / p.block_size, o = slot - blk * p.block_size;
+    const int64_t row = ((blk * p.n_kv + h) * p.block_size + o) * p.head_dim;
+    if constexpr (F8) {   // K codes (V has its own tiles)
+        uint8_t* dst = static_cast<uint8_t*>(p.k_cache) + row;
+#pragma unroll
+        for (int x = 0; x < N; x += 4) {
+            *reinterpret_cast<uint32_t*>(dst + e0 + x) = codes4(a + x, p.k_scale);
+            *reinterpret_cast<uint32_t*>(dst + e1 + x) = codes4(b + x, p.k_scale);
+        }
+    } else {
+        T* dst = static_cast<T*>(is_v ? p.v_cache : p.k_cache) + row;
+        Pc::store(dst + e0, a);
+        Pc::store(dst + e1, b);
+    }
+}
+
+// 16-bit and fp32 pools: q, k and v heads alike.
+template <typename T>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p)
+{
+    allow_dependent_launch();   // a decode launched next waits for this grid before it reads
+    const int per_head = p.head_dim / (2 * Piece<T>::kN);
+    rope_item<T, false>(p, static_cast<int64_t>(blockIdx.x) * kRopeThreads + threadIdx.x,
+                        p.n_q + 2 * p.n_kv, per_head);
+}
+
+// FP8 pools: the first qk_blocks blocks take the q and k heads; each of the
+// others a V tile of 16 tokens and 256 / D heads, whose codes are transposed
+// through shared memory and written in the pool's V layout ([d][16 tokens] per
+// piece): 16-byte rows when the 16 tokens fill one piece (a prompt's chunk),
+// 4-byte words for aligned runs of 4, single bytes else (a decode step's
+// tokens lie in 16 blocks).
+template <typename T, int D>
+__global__ void __launch_bounds__(kRopeThreads) rope_f8_kernel(const RopeParams p, unsigned qk_blocks)
+{
+    allow_dependent_launch();
+    if (blockIdx.x < qk_blocks) {
+        rope_item<T, true>(p, static_cast<int64_t>(blockIdx.x) * kRopeThreads + threadIdx.x,
+                           p.n_q + p.n_kv, D / (2 * Piece<T>::kN));
+        return;
+    }
+    constexpr int kHeads = kRopeThreads / D;      // V heads of a tile
+    constexpr int kPieces = D / 16;               // 16-element pieces of a row
+    constexpr int kItems = kVTok * kPieces * kHeads;   // = threads
+    static_assert(kItems == kRopeThreads, "one 16-element piece a thread");
+    __shared__ __align__(16) uint8_t vt[kHeads][D][kVTok];
+    __shared__ int64_t s_slot[kVTok];
+    const int tid = threadIdx.x;
+    const int head_tiles = (p.n_kv + kHeads - 1) / kHeads;
+    const unsigned tile = blockIdx.x - qk_blocks;
+    const int t0 = static_cast<int>(tile / head_tiles) * kVTok;
+    const int h0 = static_cast<int>(tile % head_tiles) * kHeads;
+    if (tid < kVTok) {
+        int pos;
+        s_slot[tid] = t0 + tid < p.num_tokens ? rope_slot(p, t0 + tid, pos) : -1;
+    }
+    {
+        const int hh = tid / (kVTok * kPieces), tt = (tid / kPieces) % kVTok, c = tid % kPieces;
+        const int t = t0 + tt, h = h0 + hh;
+        if (t < p.num_tokens && h < p.n_kv) {
+            const T* src = static_cast<const T*>(p.v) + t * p.v_stride + static_cast<int64_t>(h) * D + c * 16;
+            constexpr int N = Piece<T>::kN;
+#pragma unroll
+            for (int x = 0; x < 16; x += N) {
+                float f[N];
+                Piece<T>::load(src + x, f);
+#pragma unroll
+                for (int y = 0; y < N; y += 4) {
+                    const uint32_t w = codes4(f + y, p.v_scale);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        vt[hh][c * 16 + x + y + e][tt] = static_cast<uint8_t>(w >> (8 * e));
+                }
+            }
+        }
+    }
+    __syncthreads();
+    const int hh = tid / D, d = tid % D, h = h0 + hh;
+    if (h >= p.n_kv) return;
+    const uint8_t* row = vt[hh][d];
+    auto dst = [&](int64_t sl) {   // byte address of slot sl's code in row d
+        const int64_t b = sl / p.block_size, o = sl - b * p.block_size;
+        return static_cast<uint8_t*>(p.v_cache) +
+               (((b * p.n_kv + h) * (p.block_size / 16) + o / 16) * D + d) * 16 + (o & 15);
+    };
+    const int64_t s0 = s_slot[0];
+    bool whole = s0 >= 0 && s0 % kVTok == 0;
+#pragma unroll
+    for (int i = 1; i < kVTok; ++i) whole = whole && s_slot[i] == s0 + i;
+    if (whole) {
+        *reinterpret_cast<uint4*>(dst(s0)) = *reinterpret_cast<const uint4*>(row);
+        return;
+    }
+#pragma unroll
+    for (int q4 = 0; q4 < kVTok; q4 += 4) {
+        const int64_t a = s_slot[q4];
+        if (a >= 0 && a % 4 == 0 && s_slot[q4 + 1] == a + 1 && s_slot[q4 + 2] == a + 2 &&
+            s_slot[q4 + 3] == a + 3) {
+            *reinterpret_cast<uint32_t*>(dst(a)) = *reinterpret_cast<const uint32_t*>(row + q4);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (s_slot[q4 + i] >= 0) *dst(s_slot[q4 + i]) = row[q4 + i];
+        }
+    }
+}
+
+template <typename T>
+static cudaError_t run_rope(const RopeParams& p, bool f8, cudaStream_t s)
+{
+    const int per_head = p.head_dim / (2 * Piece<T>::kN);
+    const int heads = p.n_q + (f8 ? 1 : 2) * p.n_kv;
+    const int64_t items = static_cast<int64_t>(p.num_tokens) * heads * per_head;
+    const unsigned blocks = static_cast<unsigned>((items + kRopeThreads - 1) / kRopeThreads);
+    if (!f8) {
+        rope_kernel<T><<<blocks, kRopeThreads, 0, s>>>(p);
+        return cudaGetLastError();
+    }
+    const int tile_heads = kRopeThreads / p.head_dim;
+    const unsigned v_blocks = static_cast<unsigned>((p.num_tokens + kVTok - 1) / kVTok) *
+                              static_cast<unsigned>((p.n_kv + tile_heads - 1) / tile_heads);
+    if (p.head_dim == 128)
+        rope_f8_kernel<T, 128><<<blocks + v_blocks, kRopeThreads, 0, s>>>(p, blocks);
+    else if (p.head_dim == 64)
+        rope_f8_kernel<T, 64><<<blocks + v_blocks, kRopeThreads, 0, s>>>(p, blocks);
+    else
+        return cudaErrorInvalidValue;
+    return cudaGetLastError();
+}
+
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s)
+{
+    RopeParams p;
+    p.q = a.q; p.k = a.k; p.v = a.v; p.q_out = a.q_out;
+    p.k_cache = a.k_cache; p.v_cache = a.v_cache;
+    p.q_out_stride = a.q_out_stride; p.q_stride = a.q_stride;
+    p.k_stride = a.k_stride; p.v_stride = a.v_stride;
+    p.positions = a.positions; p.cos_sin = a.cos_sin; p.slots = a.slots;
+    p.num_slots = static_cast<int64_t>(a.cache.num_blocks) * a.cache.block_size;
+    p.num_tokens = a.num_tokens; p.max_position = a.max_position;
+    p.rot = a.rot_dim; p.interleaved = a.interleaved;
+    p.n_q = a.n_q; p.n_kv = a.cache.n_kv_heads; p.head_dim = a.cache.head_dim;
+    p.block_size = a.cache.block_size;
+    p.k_scale = a.cache.k_scale; p.v_scale = a.cache.v_scale; p.err = a.err;
+    const bool f8 = a.cache.dtype == PA_FP8_E4M3;
+    switch (a.in_dtype) {
+        case PA_BF16: return run_rope<__nv_bfloat16>(p, f8, s);
+        case PA_F16: return run_rope<__half>(p, f8, s);
+        case PA_F32: return run_rope<float>(p, f8, s);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace pa

@@ -39,6 +39,15 @@ cudaError_t launch_cache_write_fp8(const void* k, const void* v, pa_dtype in_dty
                                    void* vc, const int64_t* slots, int T, const pa_cache_desc& c,
                                    unsigned* err, cudaStream_t s);
 
+struct RopeArgs {
+    void* q_out; const void *q, *k, *v; pa_dtype in_dtype;
+    int64_t q_out_stride, q_stride, k_stride, v_stride;   // elements between tokens
+    const int32_t* positions; const float* cos_sin; int max_position; int rot_dim; int interleaved;
+    void* k_cache; void* v_cache; const int64_t* slots; int num_tokens; int n_q;
+    pa_cache_desc cache; unsigned* err;
+};
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s);
+
 cudaError_t launch_copy_blocks(const void* src_k, const void* src_v, int src_blocks, void* dst_k,
                                void* dst_v, int dst_blocks, const pa_cache_desc& layout,
                                const int32_t* mapping, int pairs, unsigned* err, cudaStream_t s);
