@@ -248,6 +248,44 @@ pa_status pa_decode_no_alloc(void* out, pa_dtype out_dtype, const void* q,
                              const int32_t* context_lens, int num_seqs, int n_q_heads,
                              float scale, int block_size, void* stream);
 
+/* ---------------------------------------------------------------- scored attention
+ * Attention whose scores or visible keys differ from plain causal softmax.  Query
+ * row i (the row at absolute position i) and key j of one sequence score
+ *   z(i, j) = cap(scale * q_i . k_j) - alibi_slopes[h] * |i - j|,
+ *   cap(s) = softcap * tanh(s / softcap), or s without a cap,
+ * and row i sees the keys  max(i - window + 1, first_key of the row, 0) <= j <=
+ * max(i, prefix_len - 1)  of the sequence's context_lens tokens; out = softmax(z) V over
+ * them.  A row that sees no key (its first_key lies past its last) is 0.
+ * Keys that no row of the sequence's call sees may hold anything, and table entries of
+ * blocks in which no row sees a key are never read (blocks behind a window may have been
+ * freed); a key that some row sees must be finite for the others. */
+typedef struct {
+    float softcap;              /* > 0: cap; 0: none (negative or not finite: refused)       */
+    const float* alibi_slopes;  /* device fp32 [n_q_heads] (linear distance bias), or NULL    */
+    int window;                 /* > 0: row i sees no key before i - window + 1; 0: no window */
+    const int32_t* first_key;   /* device int32, one per query row in the order of q's rows   */
+                                /* (document mask: the first token of the row's document), or NULL */
+    const int32_t* prefix_lens; /* device int32 [num_reqs], prefill only: keys below it are   */
+                                /* visible to every row (prefix mask; at most the context     */
+                                /* length counts), or NULL                                    */
+} pa_score_mod;
+
+/* pa_decode (q_per_seq 1) or pa_decode_verify (q_per_seq up to 16) with scores and
+ * visible keys as above; mod->prefix_lens must be NULL (a decode row lies past its
+ * prefix), first_key is [num_seqs][q_per_seq].  Pools and head dims as pa_decode for one
+ * row, as pa_decode_verify for more; other rules theirs too.  Only the blocks from the first
+ * visible key on are read.  workspace: pa_decode_scored_workspace_size bytes for the same
+ * shapes and window (0 for none): a window bounds the partitions, so it needs less. */
+pa_status pa_decode_scored(void* out, pa_dtype out_dtype, const void* q,
+                           const void* k_cache, const void* v_cache, const pa_cache_desc* cache,
+                           const int32_t* block_tables, int max_blocks_per_seq,
+                           const int32_t* context_lens, int num_seqs, int q_per_seq,
+                           int n_q_heads, float scale, int block_size, const pa_score_mod* mod,
+                           void* workspace, size_t workspace_bytes, void* stream);
+size_t pa_decode_scored_workspace_size(int num_seqs, int q_per_seq, int n_q_heads,
+                                       int n_kv_heads, int head_dim, int block_size,
+                                       int max_context_len, int window);
+
 /* ---------------------------------------------------------------- chunked prefill
  * A chunk of C_r new query rows of request r attends causally over the paged
  * context ("The hands-on guide ...", chunked prefill): query row i sits at

@@ -8,6 +8,7 @@ machine where libpa.so has not been built raises at first use.
 from __future__ import annotations
 
 import ctypes as C
+import dataclasses
 import os
 import threading
 
@@ -18,7 +19,8 @@ from . import build as _build
 
 __all__ = [
     "PAError", "lib", "pa_reshape_and_cache", "pa_reshape_and_cache_quant",
-    "pa_rope_and_cache", "pa_rope_table", "pa_decode",
+    "pa_rope_and_cache", "pa_rope_table", "ScoreMod", "pa_decode_scored",
+    "pa_decode_scored_workspace_size", "pa_decode",
     "pa_decode_workspace_size", "pa_decode_verify", "pa_decode_verify_workspace_size",
     "pa_decode_no_alloc", "PA_DECODE_NO_ALLOC_SCRATCH_BYTES",
     "pa_prefill_chunk", "pa_prefill_workspace_size", "pa_get_device_error", "pa_status_string",
@@ -38,6 +40,11 @@ class _Desc(C.Structure):
                 ("v_scale", C.c_float), ("act_dtype", C.c_int)]
 
 
+class _ScoreMod(C.Structure):
+    _fields_ = [("softcap", C.c_float), ("alibi_slopes", C.c_void_p), ("window", C.c_int),
+                ("first_key", C.c_void_p), ("prefix_lens", C.c_void_p)]
+
+
 P, I, L, F, SZ, U8P = C.c_void_p, C.c_int, C.c_int64, C.c_float, C.c_size_t, C.c_void_p
 _SIGS = {
     "pa_reshape_and_cache": (I, [P, P, P, P, P, I, C.POINTER(_Desc), P]),
@@ -49,6 +56,9 @@ _SIGS = {
     "pa_reshape_and_cache_quant": (I, [P, P, I, P, P, P, I, C.POINTER(_Desc), P]),
     "pa_rope_and_cache": (I, [P, P, P, P, I, L, L, L, L, P, P, I, I, I, P, P, P, I, I,
                               C.POINTER(_Desc), P]),
+    "pa_decode_scored": (I, [P, I, P, P, P, C.POINTER(_Desc), P, I, P, I, I, I, F, I,
+                             C.POINTER(_ScoreMod), P, SZ, P]),
+    "pa_decode_scored_workspace_size": (SZ, [I, I, I, I, I, I, I, I]),
     "pa_rope_table": (I, [P, I, I, C.c_double]),
     "pa_prefill_chunk": (I, [P, I, P, P, P, C.POINTER(_Desc), P, I, P, P, I, I, I, F, I, P, SZ, P]),
     "pa_prefill_workspace_size": (SZ, [I, I, I, I]),
@@ -283,6 +293,52 @@ def pa_decode_no_alloc(out, q, k_cache, v_cache, block_tables, context_lens, sca
 
 
 PA_DECODE_NO_ALLOC_SCRATCH_BYTES = 16 << 20
+
+
+@dataclasses.dataclass(frozen=True)
+class ScoreMod:
+    """What a scored call does to scores and visible keys (pa_score_mod)."""
+    softcap: float = 0.0                          # > 0: s -> softcap * tanh(s / softcap)
+    alibi_slopes: torch.Tensor | None = None      # float32 [n_q]: - slope * |i - j|
+    window: int = 0                               # > 0: keys from i - window + 1 on
+    first_key: torch.Tensor | None = None         # int32, one per query row: its first visible key
+    prefix_lens: torch.Tensor | None = None       # int32 [requests], prefill: keys every row sees
+
+    def _c(self, n_q: int, rows: int, reqs: int) -> _ScoreMod:
+        for name, t, dt, n in (("alibi_slopes", self.alibi_slopes, torch.float32, n_q),
+                               ("first_key", self.first_key, torch.int32, rows),
+                               ("prefix_lens", self.prefix_lens, torch.int32, reqs)):
+            if t is None:
+                continue
+            if t.dtype != dt:
+                raise TypeError(f"{name}: {dt} expected")
+            if t.numel() != n or not t.is_contiguous():
+                raise ValueError(f"{name}: {n} contiguous values expected")
+        return _ScoreMod(float(self.softcap), _ptr(self.alibi_slopes), int(self.window),
+                         _ptr(self.first_key), _ptr(self.prefix_lens))
+
+
+def pa_decode_scored_workspace_size(num_seqs, q_per_seq, n_q_heads, n_kv_heads, head_dim,
+                                    block_size, max_context_len, window: int = 0) -> int:
+    return int(lib().pa_decode_scored_workspace_size(num_seqs, q_per_seq, n_q_heads, n_kv_heads,
+                                                     head_dim, block_size, max_context_len, window))
+
+
+def pa_decode_scored(out, q, k_cache, v_cache, block_tables, context_lens, mod: ScoreMod,
+                     scale: float, block_size: int, workspace=None, stream=None, k_scale=None,
+                     v_scale=None):
+    """out, q [B][n_q][d] or [B][q_per_seq][n_q][d]: pa_decode / pa_decode_verify with capped or
+    biased scores and masks (mod)."""
+    B, n_q = q.shape[0], q.shape[-2]
+    nq = q.shape[1] if q.dim() == 4 else 1
+    d = _desc(k_cache, k_scale, v_scale, q.dtype)
+    m = mod._c(n_q, B * nq, B)
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check(lib().pa_decode_scored(_ptr(out), dtype_code(out.dtype), _ptr(q), _ptr(k_cache),
+                                  _ptr(v_cache), C.byref(d), _ptr(block_tables),
+                                  int(block_tables.shape[1]), _ptr(context_lens), B, nq, n_q,
+                                  float(scale), int(block_size), C.byref(m), _ptr(workspace),
+                                  ws_bytes, _stream(stream)), "pa_decode_scored")
 
 
 def pa_prefill_workspace_size(num_reqs, n_q_heads, head_dim, total_q) -> int:

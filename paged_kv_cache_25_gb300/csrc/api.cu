@@ -158,8 +158,10 @@ static size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255);
 // partial outputs [B][n_q][J][D], all fp32.
 static constexpr size_t kControlBytes = 256;
 
+// `extra` more partial slots a row (the prefix pass of a shared decode) come
+// before the partitions' slots, and `head` bytes (256-aligned) after the control area.
 static size_t decode_ws_bytes(int B, int nq, int n_q, int n_kv, int D, int BS, int max_ctx,
-                              int* part, int* parts)
+                              int* part, int* parts, int extra = 0, size_t head = 0)
 {
     // work units per partition index: (sequence, KV head, 8-row sub-group)
     const int64_t groups = static_cast<int64_t>(B) * n_kv * ((n_q / n_kv * nq + 7) / 8);
@@ -171,9 +173,43 @@ static size_t decode_ws_bytes(int B, int nq, int n_q, int n_kv, int D, int BS, i
     const int J = (max_ctx + p - 1) / p;
     if (part) *part = p;
     if (parts) *parts = J < 1 ? 1 : J;
-    if (J <= 1) return kControlBytes;
-    const size_t units = static_cast<size_t>(B) * nq * n_q * J;
-    return kControlBytes + align256(units * 2 * sizeof(float)) + units * D * sizeof(float);
+    if (J <= 1 && extra == 0) return kControlBytes;
+    const size_t units = static_cast<size_t>(B) * nq * n_q * ((J < 1 ? 1 : J) + extra);
+    return kControlBytes + head + align256(units * 2 * sizeof(float)) + units * D * sizeof(float);
+}
+
+// Tokens that the partitions of a sequence can span: with a window, its rows' keys
+// from the block of the first row's first key on.
+static int scored_span(int max_ctx, int window, int nq, int BS)
+{
+    if (window <= 0) return max_ctx;
+    const int64_t span = static_cast<int64_t>(window) + nq + BS - 2;
+    return span < max_ctx ? static_cast<int>(span) : max_ctx;
+}
+
+// Checks a score modification and turns it into kernel parameters.
+static pa_status check_mod(const pa_score_mod* mod, ScoreParams* sc)
+{
+    if (!mod) return fail(PA_ERR_INVALID_ARG, "score modification is NULL");
+    if (!std::isfinite(mod->softcap) || mod->softcap < 0.f)
+        return fail(PA_ERR_INVALID_ARG, "softcap must be finite and not negative");
+    if (mod->softcap > 0.f && (mod->softcap < 1e-6f || mod->softcap > 1e6f))
+        return fail(PA_ERR_UNSUPPORTED, "softcap outside [1e-6, 1e6]");
+    if (mod->window < 0) return fail(PA_ERR_INVALID_ARG, "window must not be negative");
+    if ((reinterpret_cast<uintptr_t>(mod->alibi_slopes) & 3u) ||
+        (reinterpret_cast<uintptr_t>(mod->first_key) & 3u) ||
+        (reinterpret_cast<uintptr_t>(mod->prefix_lens) & 3u))
+        return fail(PA_ERR_INVALID_ARG, "score modification arrays must be 4-byte aligned");
+    *sc = ScoreParams{};
+    if (mod->softcap > 0.f) {
+        sc->cap2 = mod->softcap * 1.4426950408889634f;
+        sc->cap_rate = 2.f / mod->softcap;
+    }
+    sc->slopes = mod->alibi_slopes;
+    sc->window = mod->window < (1 << 30) ? mod->window : (1 << 30);   // (contexts end there)
+    sc->first_key = mod->first_key;
+    sc->prefix_lens = mod->prefix_lens;
+    return PA_OK;
 }
 
 // One thread waits on an mbarrier that nothing ever completes: the bounded
@@ -425,7 +461,7 @@ static pa_status decode_common(void* out, pa_dtype out_dtype, const void* q, con
                                const int32_t* block_tables, int max_blocks_per_seq,
                                const int32_t* context_lens, int num_seqs, int q_per_seq,
                                int n_q_heads, float scale, int block_size, void* workspace,
-                               size_t workspace_bytes, void* stream)
+                               size_t workspace_bytes, void* stream, ScoreParams* score = nullptr)
 {
     pa_status st = check_cache(cache);
     if (st != PA_OK) return st;
@@ -452,7 +488,8 @@ static pa_status decode_common(void* out, pa_dtype out_dtype, const void* q, con
     if (cache->dtype == PA_FP8_E4M3 && cache->head_dim != 64 && cache->head_dim != 128)
         return fail(PA_ERR_UNSUPPORTED, "FP8 pools decode with head_dim 64 or 128");
 
-    const int max_ctx = max_blocks_per_seq * block_size;
+    const int max_ctx = scored_span(max_blocks_per_seq * block_size, score ? score->window : 0,
+                                    q_per_seq, block_size);
     int part = 0, parts = 0;
     const size_t need = decode_ws_bytes(num_seqs, q_per_seq, n_q_heads, cache->n_kv_heads,
                                         cache->head_dim, block_size, max_ctx, &part, &parts);
@@ -478,6 +515,11 @@ static pa_status decode_common(void* out, pa_dtype out_dtype, const void* q, con
         char* base = static_cast<char*>(workspace) + kControlBytes;
         a.ws_ml = reinterpret_cast<float*>(base);
         a.ws_acc = reinterpret_cast<float*>(base + align256(units * 2 * sizeof(float)));
+    }
+    if (score) {
+        score->slots = parts;
+        score->slot0 = 0;
+        a.score = score;
     }
     cudaError_t e = launch_decode(a, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "decode launch");
@@ -512,6 +554,39 @@ pa_status pa_decode_verify(void* out, pa_dtype out_dtype, const void* q, const v
     return decode_common(out, out_dtype, q, k_cache, v_cache, cache, block_tables,
                          max_blocks_per_seq, context_lens, num_seqs, q_per_seq, n_q_heads, scale,
                          block_size, workspace, workspace_bytes, stream);
+}
+
+size_t pa_decode_scored_workspace_size(int num_seqs, int q_per_seq, int n_q_heads, int n_kv_heads,
+                                       int head_dim, int block_size, int max_context_len, int window)
+{
+    if (window < 0) return 0;
+    return pa_decode_verify_workspace_size(
+        num_seqs, q_per_seq, n_q_heads, n_kv_heads, head_dim, block_size,
+        max_context_len > 0 ? scored_span(max_context_len, window, q_per_seq, block_size) : 0);
+}
+
+pa_status pa_decode_scored(void* out, pa_dtype out_dtype, const void* q, const void* k_cache,
+                           const void* v_cache, const pa_cache_desc* cache,
+                           const int32_t* block_tables, int max_blocks_per_seq,
+                           const int32_t* context_lens, int num_seqs, int q_per_seq, int n_q_heads,
+                           float scale, int block_size, const pa_score_mod* mod, void* workspace,
+                           size_t workspace_bytes, void* stream)
+{
+    pa_status st = check_cache(cache);
+    if (st != PA_OK) return st;
+    if (q_per_seq < 1 || q_per_seq > 16)
+        return fail(PA_ERR_INVALID_ARG, "q_per_seq %d outside [1, 16]", q_per_seq);
+    if (q_per_seq > 1 && (cache->dtype == PA_F32 || (cache->head_dim != 64 && cache->head_dim != 128)))
+        return fail(PA_ERR_UNSUPPORTED,
+                    "multi-query decode runs on bf16/fp16/FP8 pools with head_dim 64 or 128");
+    ScoreParams sc{};
+    st = check_mod(mod, &sc);
+    if (st != PA_OK) return st;
+    if (mod->prefix_lens)
+        return fail(PA_ERR_INVALID_ARG, "a prefix mask is for prefill: decode rows lie past the prefix");
+    return decode_common(out, out_dtype, q, k_cache, v_cache, cache, block_tables,
+                         max_blocks_per_seq, context_lens, num_seqs, q_per_seq, n_q_heads, scale,
+                         block_size, workspace, workspace_bytes, stream, &sc);
 }
 
 size_t pa_prefill_workspace_size(int num_reqs, int n_q_heads, int head_dim, int total_q)

@@ -37,10 +37,15 @@
 // widened to fp16 in registers.  With at most 4 query heads a KV head the
 // FP8 decode runs transposed (4-row units, RU 4): the stage's 16 tokens are
 // the MMA rows, see kTr below.
+// Scored instantiations (SC) serve the scored decode and the sequences' own part of
+// the shared-prefix decode: a sequence's keys start at its first visible block
+// instead of 0, scores may be capped or biased (score_mod.cuh), keys before a row's
+// first are masked as keys past its last are, and a row that sees no key is 0.
 #include <cuda_fp8.h>
 
 #include "pa_device.cuh"
 #include "pa_internal.h"
+#include "score_mod.cuh"
 
 #include <math.h>
 
@@ -143,7 +148,7 @@ __device__ __forceinline__ uint32_t q_pair(const QT* p)
     return __ldg(reinterpret_cast<const unsigned int*>(p));   // q already in the MMA type
 }
 
-template <typename T, typename QT, int D, int BS, int NS, bool FP8, bool MQ, int RU = 8>
+template <typename T, typename QT, int D, int BS, int NS, bool FP8, bool MQ, int RU = 8, bool SC = false>
 __global__ void __launch_bounds__(kDecWarps * 32, decode_ctas_per_sm(FP8, D, RU))
 decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                   const uint8_t* __restrict__ v_codes, void* __restrict__ out, pa_dtype out_dtype,
@@ -152,7 +157,8 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                   const int32_t* __restrict__ context_lens, int num_seqs, int n_q, int nq_arg,
                   int n_kv, int group, int num_blocks, float scale_log2, float v_scale,
                   float* __restrict__ ws_ml, float* __restrict__ ws_acc, int part_tokens,
-                  int max_parts, unsigned* __restrict__ ticket, unsigned* err)
+                  int max_parts, unsigned* __restrict__ ticket, unsigned* err,
+                  const __grid_constant__ std::conditional_t<SC, ScoreParams, NoScore> sc)
 {
     using Cfg = DecodeCfg<T, D, NS, FP8, RU>;
     static_assert(!FP8 || std::is_same<T, __half>::value, "FP8 pools compute in fp16");
@@ -192,6 +198,13 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     const int n_sub = (group * nq + RU - 1) / RU;
     const int n_groups = n_kv * n_sub;
     const bool use_prefix = num_seqs <= kPrefixCap;
+    // SC: first visible key of sequence i and the block-aligned token its
+    // partitions count from (0 otherwise)
+    auto seq_lo = [&](int i, int Li) -> int {
+        if constexpr (SC) return first_visible(sc, i, Li, nq, BS, max_blocks, err);
+        return 0;
+    };
+    auto seq_base = [&](int i, int Li) -> int { return SC ? seq_lo(i, Li) / BS * BS : 0; };
 
     // ---- units: first every full partition, then every sequence's last one.
     // The last partitions are the ragged, cheaper units, so handing them out
@@ -202,7 +215,7 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         const int b0 = tid * per, b1 = min(num_seqs, b0 + per);
         int local = 0;
         for (int i = b0; i < b1; ++i) {
-            const int L = __ldg(context_lens + i);
+            const int Lt = __ldg(context_lens + i), L = Lt - seq_base(i, Lt);
             const int p = L > 0 ? min((L + part_tokens - 1) / part_tokens, max_parts) - 1 : 0;
             s_prefix[i] = p;
             local += p;
@@ -252,7 +265,9 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     // before that combine.
     struct Unit {
         int s, part, L, tok0, kvh, h0, r0, nh, nblk, nchunk, blk0, nparts;
+        int lo;        // SC: first key that some row may see
         bool live;
+        bool to_ws;    // partials to the workspace (a merge follows)
     };
     auto describe = [&](int64_t uu) {
         Unit x{};
@@ -262,7 +277,7 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         const int grp = static_cast<int>(uu - static_cast<int64_t>(gp) * n_groups);
         if (gp >= n_full) {                           // a sequence's last partition
             x.s = gp - n_full;
-            const int Ls = __ldg(context_lens + x.s);
+            const int Lt = __ldg(context_lens + x.s), Ls = Lt - seq_base(x.s, Lt);
             x.part = Ls > 0 ? min((Ls + part_tokens - 1) / part_tokens, max_parts) - 1 : 0;
         } else if (use_prefix) {
             int lo = 0, hi = num_seqs - 1;            // first s with prefix[s] > gp
@@ -277,7 +292,9 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             x.part = gp - x.s * (max_parts - 1);
         }
         x.L = __ldg(context_lens + x.s);
-        x.tok0 = x.part * part_tokens;
+        x.lo = seq_lo(x.s, x.L);
+        const int base = SC ? x.lo / BS * BS : 0;
+        x.tok0 = base + x.part * part_tokens;
         x.live = x.tok0 < x.L && x.L >= nq;           // same decision in every thread
         if (x.L > 0 && x.L < nq) set_error(err, PA_ERR_OUT_OF_RANGE);   // fewer keys than queries
         x.kvh = grp / n_sub;
@@ -289,7 +306,10 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         x.nblk = (tok1 - x.tok0 + BS - 1) / BS;
         x.nchunk = (tok1 - x.tok0 + kRows - 1) / kRows;
         x.blk0 = x.tok0 / BS;
-        x.nparts = min((x.L + part_tokens - 1) / part_tokens, max_parts);
+        x.nparts = min((x.L - base + part_tokens - 1) / part_tokens, max_parts);
+        x.to_ws = x.nparts > 1;
+        // (a member of a prefix group merges with the prefix pass)
+        if constexpr (SC) x.to_ws = x.to_ws || (sc.group_of_seq != nullptr && x.lo > 0);
         // without the prefix sums (very large batches) the full-partition
         // numbering covers every partition index below max_parts - 1: a
         // sequence's own last partition there belongs to the second numbering
@@ -447,6 +467,30 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         __syncwarp();
     };
 
+    // SC: the first n tokens of a stage lie before every row's first key and may
+    // hold anything: their V becomes zero (whole warp)
+    auto zero_v_head = [&](uint32_t vbase, int n) {
+        uint8_t* vt = smem + (vbase - smem_u32(smem));
+        if constexpr (FP8) {
+            for (int row = lane; row < D; row += 32) {
+                uint4 w = *reinterpret_cast<uint4*>(vt + row * 16);
+                uint32_t* ww = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int drop = min(4, max(0, n - 4 * e));         // bytes dropped
+                    ww[e] &= drop >= 4 ? 0u : ~((1u << (8 * drop)) - 1u);
+                }
+                *reinterpret_cast<uint4*>(vt + row * 16) = w;
+            }
+        } else {
+            for (int hx = 0; hx < kHalves; ++hx)
+                for (int off = lane * 16; off < n * 128; off += 32 * 16)
+                    *reinterpret_cast<uint4*>(vt + hx * kHalfTile + off) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+    };
+
     // ---- the first unit: ids checked before any load is issued
     int64_t u = blockIdx.x;
     if (u >= units) return;                           // uniform over the CTA
@@ -523,10 +567,36 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         if (nx.live && tid < nx.nblk) nb_id = load_id(nx, tid, nb_bad);
 
         const int s = cu.s, part = cu.part, L = cu.L, tok0 = cu.tok0, kvh = cu.kvh;
-        const int h0 = cu.h0, r0 = cu.r0, nh = cu.nh, nchunk = cu.nchunk, nparts = cu.nparts;
+        const int h0 = cu.h0, r0 = cu.r0, nh = cu.nh, nchunk = cu.nchunk;
         // keys this thread's row may see: query qi of nq sits at L - nq + qi
         const int lim = g < nh ? L - nq + (r0 + g) % nq + 1 : L;
         const int lim1 = (R16 && g + 8 < nh) ? L - nq + (r0 + g + 8) % nq + 1 : L;
+        // SC: the rows' first keys, and slopes (kTr: of columns 2*t4 and 2*t4 + 1, mod 4)
+        int first0 = cu.lo, first1 = cu.lo;
+        float slope0 = 0.f, slope1 = 0.f;
+        if constexpr (SC) {
+            if (!sc.group_of_seq) {
+                const int i0 = kTr ? 0 : (r0 + min(g, nh - 1)) % nq;
+                first0 = row_first(sc, s, nq, i0, L - nq + i0);
+                if constexpr (R16) {
+                    const int i1 = (r0 + min(g + 8, nh - 1)) % nq;
+                    first1 = row_first(sc, s, nq, i1, L - nq + i1);
+                }
+                if (sc.slopes) {
+                    const int a = kTr ? (2 * t4) & 3 : g, b = kTr ? a + 1 : g + 8;
+                    slope0 = a < nh ? __ldg(sc.slopes + h0 + (r0 + a) / nq) * kLog2e : 0.f;
+                    slope1 = (kTr || R16) && b < nh ? __ldg(sc.slopes + h0 + (r0 + b) / nq) * kLog2e : 0.f;
+                }
+            }
+        }
+        // a visible score (log2 domain) with the cap and the bias; `ahead` = key - query position
+        auto modify = [&](float z, float slope, int ahead) -> float {
+            if constexpr (SC) {
+                if (sc.cap2 > 0.f) z = soft_cap(z, sc.cap2, sc.cap_rate);
+                return fmaf(slope, static_cast<float>(ahead), z);
+            }
+            return z;
+        };
         int timed_out = 0;
         if (cu.live) {
             // ---- per-warp TMA ring over the partition's 16-row stages --------
@@ -562,6 +632,8 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                 const int valid = min(kRows, L - pos0);
                 const uint32_t kbase = ring + st * Cfg::kStageBytes;
                 const uint32_t vbase = kbase + Cfg::kSlabBytes;
+                if constexpr (SC)
+                    if (pos0 < cu.lo) zero_v_head(vbase, min(kRows, cu.lo - pos0));
                 if constexpr (kTr) {
                     if (valid < kRows) zero_v_tail(vbase, valid);
                     // S^T = K q^T.  Row r of the tile is token 4*((r&7)>>1) + 2*(r>>3)
@@ -590,20 +662,25 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                     // tokens tA and tA + 2 of columns 2*t4 and 2*t4 + 1; the column
                     // max meets over the eight lanes of each t4
                     const int tA = pos0 + 4 * (g >> 1) + (g & 1);
-                    const float z0 = tA < L ? (st[0] + st2[0]) * cl2_0 : -INFINITY;
-                    const float z1 = tA < L ? (st[1] + st2[1]) * cl2_1 : -INFINITY;
-                    const float z2 = tA + 2 < L ? (st[2] + st2[2]) * cl2_0 : -INFINITY;
-                    const float z3 = tA + 2 < L ? (st[3] + st2[3]) * cl2_1 : -INFINITY;
+                    const bool inA = tA < L && (!SC || tA >= first0);
+                    const bool inB = tA + 2 < L && (!SC || tA + 2 >= first0);
+                    const float z0 = inA ? modify((st[0] + st2[0]) * cl2_0, slope0, tA + 1 - L) : -INFINITY;
+                    const float z1 = inA ? modify((st[1] + st2[1]) * cl2_1, slope1, tA + 1 - L) : -INFINITY;
+                    const float z2 = inB ? modify((st[2] + st2[2]) * cl2_0, slope0, tA + 3 - L) : -INFINITY;
+                    const float z3 = inB ? modify((st[3] + st2[3]) * cl2_1, slope1, tA + 3 - L) : -INFINITY;
                     float mx0 = fmaxf(z0, z2), mx1 = fmaxf(z1, z3);
 #pragma unroll
                     for (int w = 4; w < 32; w <<= 1) {
                         mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, w));
                         mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, w));
                     }
-                    // (every stage holds a visible token, so the maxima are finite)
+                    // (without a first key every stage holds a visible token, so the
+                    // maxima are finite; else exponents are taken against 0, giving 0)
                     const float mn0 = fmaxf(m_run, mx0), mn1 = fmaxf(m_run1, mx1);
+                    const float mu0 = SC && mn0 == -INFINITY ? 0.f : mn0;
+                    const float mu1 = SC && mn1 == -INFINITY ? 0.f : mn1;
                     if (__any_sync(0xffffffffu, mn0 != m_run || mn1 != m_run1)) {
-                        const float a0 = fast_exp2(m_run - mn0), a1 = fast_exp2(m_run1 - mn1);
+                        const float a0 = fast_exp2(m_run - mu0), a1 = fast_exp2(m_run1 - mu1);
                         l_run *= a0;
                         l_run1 *= a1;
 #pragma unroll
@@ -613,8 +690,8 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                     }
                     m_run = mn0;
                     m_run1 = mn1;
-                    const float p0 = fast_exp2(z0 - mn0), p1 = fast_exp2(z1 - mn1);
-                    const float p2 = fast_exp2(z2 - mn0), p3 = fast_exp2(z3 - mn1);
+                    const float p0 = fast_exp2(z0 - mu0), p1 = fast_exp2(z1 - mu1);
+                    const float p2 = fast_exp2(z2 - mu0), p3 = fast_exp2(z3 - mu1);
                     l_run += p0 + p2;
                     l_run1 += p1 + p3;
                     // P^T as the B operand: columns 0-3 take P's hi part, columns 4-7
@@ -640,8 +717,8 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                         MmaOp<T>::run(o[2 * q2 + 1], a, pb0, pb1);
                     }
                 } else {
-                    float sc[2][4];
-                    float sc2[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+                    float sv[2][4];
+                    float sv2[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 
                     if constexpr (FP8) {
                         if (valid < kRows) zero_v_tail(vbase, valid);
@@ -649,7 +726,7 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                         // which leaves P in the token order the V fragments use below.
 #pragma unroll
                         for (int nt = 0; nt < 2; ++nt) {
-                            sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+                            sv[nt][0] = sv[nt][1] = sv[nt][2] = sv[nt][3] = 0.f;
                             const int i = lane & 7;
                             const int r = 4 * (i >> 1) + 2 * nt + (i & 1);
 #pragma unroll
@@ -666,11 +743,11 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                                     e4m3x4_to_h2x2(w[jj], b0, b1);
                                     // two accumulator chains (even / odd 16 columns) halve the
                                     // dependent MMA sequence per n-tile
-                                    MmaOp<T>::run((jj & 1) ? sc2[nt] : sc[nt], a, b0, b1);
+                                    MmaOp<T>::run((jj & 1) ? sv2[nt] : sv[nt], a, b0, b1);
                                 }
                             }
-                            sc[nt][0] += sc2[nt][0]; sc[nt][1] += sc2[nt][1];
-                            sc[nt][2] += sc2[nt][2]; sc[nt][3] += sc2[nt][3];
+                            sv[nt][0] += sv2[nt][0]; sv[nt][1] += sv2[nt][1];
+                            sv[nt][2] += sv2[nt][2]; sv[nt][3] += sv2[nt][3];
                         }
                     } else {
                         if (valid < kRows) {
@@ -688,7 +765,7 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                         // S = Q K^T for the 16 rows
 #pragma unroll
                         for (int nt = 0; nt < 2; ++nt) {
-                            sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+                            sv[nt][0] = sv[nt][1] = sv[nt][2] = sv[nt][3] = 0.f;
 #pragma unroll
                             for (int kc = 0; kc < D / 16; kc += 2) {
                                 const int r = nt * 8 + (lane & 7);
@@ -701,8 +778,8 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                                                         R16 ? qb[R16 ? kc : 0][1] : 0u};
                                 const uint32_t a1[4] = {qa[kc + 1][0], R16 ? qb[R16 ? kc + 1 : 0][0] : 0u,
                                                         qa[kc + 1][1], R16 ? qb[R16 ? kc + 1 : 0][1] : 0u};
-                                MmaOp<T>::run(sc[nt], a0, b0, b1);
-                                MmaOp<T>::run(sc[nt], a1, b2, b3);
+                                MmaOp<T>::run(sv[nt], a0, b0, b1);
+                                MmaOp<T>::run(sv[nt], a1, b2, b3);
                             }
                         }
                     }
@@ -714,8 +791,9 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const int p = pos0 + (FP8 ? 4 * t4 + 2 * nt + e : nt * 8 + 2 * t4 + e);
-                            const float z = p < lim ? sc[nt][e] * row_l2 : -INFINITY;
-                            sc[nt][e] = z;
+                            const bool in = p < lim && (!SC || p >= first0);
+                            const float z = in ? modify(sv[nt][e] * row_l2, slope0, p + 1 - lim) : -INFINITY;
+                            sv[nt][e] = z;
                             mx = fmaxf(mx, z);
                         }
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
@@ -723,7 +801,7 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                     const float m_new = fmaxf(m_run, mx);
                     // a row with no visible key so far (several queries per sequence)
                     // keeps m = -inf: exponents are then taken against 0, giving 0
-                    const float m_use = (MQ && m_new == -INFINITY) ? 0.f : m_new;
+                    const float m_use = ((MQ || SC) && m_new == -INFINITY) ? 0.f : m_new;
                     float m_new1 = -INFINITY, m_use1 = 0.f;
                     if constexpr (R16) {   // the second row of this thread, same steps
                         float mx1 = -INFINITY;
@@ -732,8 +810,9 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 #pragma unroll
                             for (int e = 2; e < 4; ++e) {
                                 const int p = pos0 + nt * 8 + 2 * t4 + e - 2;
-                                const float z = p < lim1 ? sc[nt][e] * scale_log2 : -INFINITY;
-                                sc[nt][e] = z;
+                                const bool in = p < lim1 && (!SC || p >= first1);
+                                const float z = in ? modify(sv[nt][e] * scale_log2, slope1, p + 1 - lim1) : -INFINITY;
+                                sv[nt][e] = z;
                                 mx1 = fmaxf(mx1, z);
                             }
                         mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
@@ -761,8 +840,8 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                     for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
                         for (int e = 0; e < (R16 ? 4 : 2); ++e) {
-                            const float p = fast_exp2(sc[nt][e] - (e < 2 ? m_use : m_use1));
-                            sc[nt][e] = p;
+                            const float p = fast_exp2(sv[nt][e] - (e < 2 ? m_use : m_use1));
+                            sv[nt][e] = p;
                             if (e < 2) psum += p; else psum1 += p;
                         }
                     l_run += psum;
@@ -772,13 +851,13 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                     // g + 8 both real, hi in pa and lo in pb, two MMAs
                     uint32_t pa[4], pb[4];
                     if constexpr (R16) {
-                        split_pair<T>(sc[0][0], sc[0][1], pa[0], pb[0]);
-                        split_pair<T>(sc[0][2], sc[0][3], pa[1], pb[1]);
-                        split_pair<T>(sc[1][0], sc[1][1], pa[2], pb[2]);
-                        split_pair<T>(sc[1][2], sc[1][3], pa[3], pb[3]);
+                        split_pair<T>(sv[0][0], sv[0][1], pa[0], pb[0]);
+                        split_pair<T>(sv[0][2], sv[0][3], pa[1], pb[1]);
+                        split_pair<T>(sv[1][0], sv[1][1], pa[2], pb[2]);
+                        split_pair<T>(sv[1][2], sv[1][3], pa[3], pb[3]);
                     } else {
-                        split_pair<T>(sc[0][0], sc[0][1], pa[0], pa[1]);
-                        split_pair<T>(sc[1][0], sc[1][1], pa[2], pa[3]);
+                        split_pair<T>(sv[0][0], sv[0][1], pa[0], pa[1]);
+                        split_pair<T>(sv[1][0], sv[1][1], pa[2], pa[3]);
                     }
                     if constexpr (FP8) {
                         // transposed V tile: row d holds tokens 0..15; a fragment word is
@@ -886,7 +965,7 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                 for (int w = 0; w < kDecWarps; ++w) M = fmaxf(M, red_m[w * RU + hh]);
                 // M = -inf: no key of this partition is visible to the row (a
                 // later query's keys only); it contributes l = 0, acc = 0
-                const float M_use = (MQ && M == -INFINITY) ? 0.f : M;
+                const float M_use = ((MQ || SC) && M == -INFINITY) ? 0.f : M;
                 float lsum = 0.f, acc = 0.f;
 #pragma unroll
                 for (int w = 0; w < kDecWarps; ++w) {
@@ -896,10 +975,12 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                 }
                 acc *= v_scale;                                    // 1 unless the pool is FP8
                 const int64_t sh = MQ ? s_rowoff[hh] : static_cast<int64_t>(s) * n_q + h0 + r0 + hh;
-                if (nparts == 1) {
-                    store_any(out, sh * D + dd, acc / lsum, out_dtype);
+                if (!cu.to_ws) {
+                    // (SC: a row that sees no key is 0)
+                    store_any(out, sh * D + dd, SC && lsum == 0.f ? 0.f : acc / lsum, out_dtype);
                 } else {
-                    const int64_t w_idx = sh * max_parts + part;
+                    int64_t w_idx = sh * max_parts + part;
+                    if constexpr (SC) w_idx = sh * sc.slots + sc.slot0 + part;
                     ws_acc[w_idx * D + dd] = acc;
                     if (dd == 0) {
                         ws_ml[2 * w_idx] = M;
@@ -919,6 +1000,13 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     }
 }
 
+template <bool SC>
+std::conditional_t<SC, ScoreParams, NoScore> score_params(const DecodeArgs& a)
+{
+    if constexpr (SC) return *a.score;
+    else return NoScore{};
+}
+
 inline int decode_sm_count()
 {
     static std::mutex mu;
@@ -935,14 +1023,14 @@ inline int decode_sm_count()
     return cache[dev];
 }
 
-template <typename T, typename QT, int D, int BS, bool FP8, bool MQ, int RU = 8>
+template <typename T, typename QT, int D, int BS, bool FP8, bool MQ, int RU = 8, bool SC = false>
 cudaError_t run_mma(const DecodeArgs& a, cudaStream_t s, float scale_log2)
 {
     // FP8 runs 3 CTAs per SM (registers capped at 168 by the launch bounds):
     // Llama-3-8B batch 0.273 -> 0.231 ms against 2 CTAs with 24 KB rings.
     constexpr int NS = decode_stages<T, D, FP8, RU>();
     using Cfg = DecodeCfg<T, D, NS, FP8, RU>;
-    auto kern = decode_mma_kernel<T, QT, D, BS, NS, FP8, MQ, RU>;
+    auto kern = decode_mma_kernel<T, QT, D, BS, NS, FP8, MQ, RU, SC>;
     static std::once_flag once;
     static cudaError_t attr_err = cudaSuccess;
     static int per_sm = 1;
@@ -999,11 +1087,11 @@ cudaError_t run_mma(const DecodeArgs& a, cudaStream_t s, float scale_log2)
         static_cast<const QT*>(a.q), a.block_tables, a.max_blocks, a.context_lens, a.num_seqs,
         a.n_q, a.q_per_seq, a.cache.n_kv_heads, group, a.cache.num_blocks,
         FP8 ? scale_log2 * a.cache.k_scale : scale_log2, FP8 ? a.cache.v_scale : 1.f, a.ws_ml,
-        a.ws_acc, a.part_tokens, a.max_parts, ticket, a.err);
+        a.ws_acc, a.part_tokens, a.max_parts, ticket, a.err, score_params<SC>(a));
 }
 
 // Tensor-core kernels by shape; cudaErrorNotSupported for other shapes.
-template <typename T, bool MQ>
+template <typename T, bool MQ, bool SC>
 cudaError_t run_mma_tc(const DecodeArgs& a, cudaStream_t s, float sl2)
 {
     const int D = a.cache.head_dim, BS = a.cache.block_size;
@@ -1011,52 +1099,52 @@ cudaError_t run_mma_tc(const DecodeArgs& a, cudaStream_t s, float sl2)
         // more than 8 (head, query) rows per KV head: 16-row units, so each K/V
         // stage is read and widened once for all of them
         if (a.q_per_seq * (a.n_q / a.cache.n_kv_heads) > 8) {
-            if (D == 64 && BS == 16) return run_mma<T, T, 64, 16, false, MQ, 16>(a, s, sl2);
-            if (D == 64 && BS == 32) return run_mma<T, T, 64, 32, false, MQ, 16>(a, s, sl2);
-            if (D == 128 && BS == 16) return run_mma<T, T, 128, 16, false, MQ, 16>(a, s, sl2);
-            if (D == 128 && BS == 32) return run_mma<T, T, 128, 32, false, MQ, 16>(a, s, sl2);
+            if (D == 64 && BS == 16) return run_mma<T, T, 64, 16, false, MQ, 16, SC>(a, s, sl2);
+            if (D == 64 && BS == 32) return run_mma<T, T, 64, 32, false, MQ, 16, SC>(a, s, sl2);
+            if (D == 128 && BS == 16) return run_mma<T, T, 128, 16, false, MQ, 16, SC>(a, s, sl2);
+            if (D == 128 && BS == 32) return run_mma<T, T, 128, 32, false, MQ, 16, SC>(a, s, sl2);
             return cudaErrorNotSupported;
         }
     }
-    if (D == 64 && BS == 16) return run_mma<T, T, 64, 16, false, MQ>(a, s, sl2);
-    if (D == 64 && BS == 32) return run_mma<T, T, 64, 32, false, MQ>(a, s, sl2);
-    if (D == 128 && BS == 16) return run_mma<T, T, 128, 16, false, MQ>(a, s, sl2);
-    if (D == 128 && BS == 32) return run_mma<T, T, 128, 32, false, MQ>(a, s, sl2);
+    if (D == 64 && BS == 16) return run_mma<T, T, 64, 16, false, MQ, 8, SC>(a, s, sl2);
+    if (D == 64 && BS == 32) return run_mma<T, T, 64, 32, false, MQ, 8, SC>(a, s, sl2);
+    if (D == 128 && BS == 16) return run_mma<T, T, 128, 16, false, MQ, 8, SC>(a, s, sl2);
+    if (D == 128 && BS == 32) return run_mma<T, T, 128, 32, false, MQ, 8, SC>(a, s, sl2);
     return cudaErrorNotSupported;
 }
 
-template <typename QT, bool MQ>
+template <typename QT, bool MQ, bool SC>
 cudaError_t run_fp8_qt(const DecodeArgs& a, cudaStream_t s, float sl2)
 {
     const int D = a.cache.head_dim, BS = a.cache.block_size;
     if constexpr (!MQ) {
         // up to 4 query heads a KV head: the transposed kernel (4-row units)
         if (a.n_q / a.cache.n_kv_heads <= 4) {
-            if (D == 64 && BS == 16) return run_mma<__half, QT, 64, 16, true, false, 4>(a, s, sl2);
-            if (D == 64 && BS == 32) return run_mma<__half, QT, 64, 32, true, false, 4>(a, s, sl2);
-            if (D == 128 && BS == 16) return run_mma<__half, QT, 128, 16, true, false, 4>(a, s, sl2);
-            if (D == 128 && BS == 32) return run_mma<__half, QT, 128, 32, true, false, 4>(a, s, sl2);
+            if (D == 64 && BS == 16) return run_mma<__half, QT, 64, 16, true, false, 4, SC>(a, s, sl2);
+            if (D == 64 && BS == 32) return run_mma<__half, QT, 64, 32, true, false, 4, SC>(a, s, sl2);
+            if (D == 128 && BS == 16) return run_mma<__half, QT, 128, 16, true, false, 4, SC>(a, s, sl2);
+            if (D == 128 && BS == 32) return run_mma<__half, QT, 128, 32, true, false, 4, SC>(a, s, sl2);
             return cudaErrorNotSupported;
         }
     }
-    if (D == 64 && BS == 16) return run_mma<__half, QT, 64, 16, true, MQ>(a, s, sl2);
-    if (D == 64 && BS == 32) return run_mma<__half, QT, 64, 32, true, MQ>(a, s, sl2);
-    if (D == 128 && BS == 16) return run_mma<__half, QT, 128, 16, true, MQ>(a, s, sl2);
-    if (D == 128 && BS == 32) return run_mma<__half, QT, 128, 32, true, MQ>(a, s, sl2);
+    if (D == 64 && BS == 16) return run_mma<__half, QT, 64, 16, true, MQ, 8, SC>(a, s, sl2);
+    if (D == 64 && BS == 32) return run_mma<__half, QT, 64, 32, true, MQ, 8, SC>(a, s, sl2);
+    if (D == 128 && BS == 16) return run_mma<__half, QT, 128, 16, true, MQ, 8, SC>(a, s, sl2);
+    if (D == 128 && BS == 32) return run_mma<__half, QT, 128, 32, true, MQ, 8, SC>(a, s, sl2);
     return cudaErrorNotSupported;
 }
 
 // The attention kernel of a decode call for every cache dtype the tensor
 // cores cover (FP32 pools: cudaErrorNotSupported).
-template <bool MQ>
+template <bool MQ, bool SC = false>
 cudaError_t run_mma_any(const DecodeArgs& a, cudaStream_t s, float sl2)
 {
     switch (a.cache.dtype) {
-        case PA_BF16: return run_mma_tc<__nv_bfloat16, MQ>(a, s, sl2);
-        case PA_F16: return run_mma_tc<__half, MQ>(a, s, sl2);
+        case PA_BF16: return run_mma_tc<__nv_bfloat16, MQ, SC>(a, s, sl2);
+        case PA_F16: return run_mma_tc<__half, MQ, SC>(a, s, sl2);
         case PA_FP8_E4M3:
-            return a.cache.act_dtype == PA_BF16 ? run_fp8_qt<__nv_bfloat16, MQ>(a, s, sl2)
-                                                : run_fp8_qt<__half, MQ>(a, s, sl2);
+            return a.cache.act_dtype == PA_BF16 ? run_fp8_qt<__nv_bfloat16, MQ, SC>(a, s, sl2)
+                                                : run_fp8_qt<__half, MQ, SC>(a, s, sl2);
         default: return cudaErrorNotSupported;
     }
 }

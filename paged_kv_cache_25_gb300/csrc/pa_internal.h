@@ -52,6 +52,24 @@ cudaError_t launch_copy_blocks(const void* src_k, const void* src_v, int src_blo
                                void* dst_v, int dst_blocks, const pa_cache_desc& layout,
                                const int32_t* mapping, int pairs, unsigned* err, cudaStream_t s);
 
+// What the scored and shared-prefix kernels take besides a decode's or prefill's
+// arguments (device functions: score_mod.cuh).
+struct ScoreParams {
+    float cap2;                  // C = softcap * log2(e); 0: no cap
+    float cap_rate;              // 2 / softcap
+    const float* slopes;         // [n_q] distance slopes, or null
+    int window;                  // 0: none
+    const int32_t* first_key;    // first visible key of every query row, or null
+    const int32_t* prefix_lens;  // prefill: keys below it are visible to every row, or null
+    // shared-prefix decode: a member sequence's own pass starts after its group's prefix
+    const int32_t* group_of_seq; // null: not a shared decode
+    const int32_t* group_prefix;
+    const int32_t* group_splits; // partials of each group's prefix pass (written by that pass)
+    int num_groups;
+    // partial slots of an output row: [0, slot0) the prefix pass's, then the partitions'
+    int slots, slot0;
+};
+
 struct DecodeArgs {
     void* out; pa_dtype out_dtype; const void* q;
     const void* k_cache; const void* v_cache; pa_cache_desc cache;
@@ -65,8 +83,11 @@ struct DecodeArgs {
     unsigned* ticket;  // work counter in the workspace's control area; null: units are
                        // dealt round robin (unit blockIdx.x + k * gridDim.x), no counter
     unsigned* err;
+    const ScoreParams* score;   // scored or shared-prefix decode (host memory); else null
 };
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t s);
+// attention kernel of a scored or shared-prefix call (decode_scored.cu)
+cudaError_t launch_decode_scored(const DecodeArgs& a, cudaStream_t s, float scale_log2);
 // attention kernel of a call with q_per_seq > 1 (decode_verify.cu)
 cudaError_t launch_decode_mq(const DecodeArgs& a, cudaStream_t s, float scale_log2);
 

@@ -1,0 +1,63 @@
+"""CPU checks of the scored calls: workspace rules and refusals before any launch."""
+import ctypes as C
+
+import pytest
+
+from paged_kv_cache_25_gb300 import binding as pa
+from paged_kv_cache_25_gb300 import build
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    build.build()
+    return pa.lib()
+
+
+def _decode(mod=None, dt=2, d=128, nq=1, B=4, mb=16, ws=0x10000, ws_bytes=1 << 24, null_mod=False, **kw):
+    desc = pa._Desc(64, 16, 8, d, dt, 1.0, 1.0, 2)
+    m = pa._ScoreMod(*(mod or (0.0, None, 0, None, None)))
+    a = dict(out=0x1000, q=0x2000, kc=0x3000, vc=0x4000, bt=0x5000, cl=0x6000, n_q=32, scale=0.1, bs=16)
+    a.update(kw)
+    return pa.lib().pa_decode_scored(a["out"], 0, a["q"], a["kc"], a["vc"], C.byref(desc), a["bt"], mb,
+                                     a["cl"], B, nq, a["n_q"], a["scale"], a["bs"],
+                                     None if null_mod else C.byref(m), ws, ws_bytes, None)
+
+
+BAD_MODS = [(-1.0, None, 0, None, None), (float("nan"), None, 0, None, None),
+            (float("inf"), None, 0, None, None), (0.0, None, -1, None, None),
+            (0.0, 0x1002, 0, None, None), (0.0, None, 0, 0x1001, None),
+            (0.0, None, 0, None, 0x1003)]
+
+
+@pytest.mark.parametrize("mod", BAD_MODS + [(0.0, None, 0, None, 0x1000)])
+def test_decode_refuses_bad_modifications(mod):
+    assert _decode(mod) == pa.PA_ERR_INVALID_ARG
+    assert pa.lib().pa_last_error_message()
+
+
+def test_decode_refusals():
+    assert _decode(null_mod=True) == pa.PA_ERR_INVALID_ARG
+    assert _decode(nq=0) == pa.PA_ERR_INVALID_ARG
+    assert _decode(nq=17) == pa.PA_ERR_INVALID_ARG
+    assert _decode(nq=2, dt=0) == pa.PA_ERR_UNSUPPORTED
+    assert _decode(nq=2, d=96) == pa.PA_ERR_UNSUPPORTED
+    assert _decode((1e9, None, 0, None, None)) == pa.PA_ERR_UNSUPPORTED
+    assert _decode(q=0x2008) == pa.PA_ERR_INVALID_ARG
+    assert _decode(n_q=30) == pa.PA_ERR_INVALID_ARG
+    assert _decode(scale=float("nan")) == pa.PA_ERR_INVALID_ARG
+    assert _decode(ws=None, ws_bytes=0) == pa.PA_ERR_WORKSPACE
+    assert _decode(B=0) == pa.PA_OK
+
+
+def test_a_window_bounds_the_workspace():
+    size = pa.pa_decode_scored_workspace_size
+    assert size(256, 1, 32, 8, 128, 16, 65536) == pa.pa_decode_workspace_size(256, 32, 8, 128, 16, 65536)
+    # 1024 + 15 tokens of the first block at most: two partitions of 1024
+    w = size(256, 1, 32, 8, 128, 16, 65536, 1024)
+    assert 256 < w < size(256, 1, 32, 8, 128, 16, 65536) // 16
+    assert size(256, 4, 32, 8, 128, 16, 4096) == pa.pa_decode_verify_workspace_size(256, 4, 32, 8, 128, 16, 4096)
+    assert size(256, 1, 32, 8, 128, 16, 4096, -1) == 0
+    assert size(0, 1, 32, 8, 128, 16, 4096, 0) == 0
+    # enough for exactly what the call asks
+    need = size(4, 1, 32, 8, 128, 16, 256, 100)
+    assert _decode((0.0, None, 100, None, None), ws_bytes=need - 1) == pa.PA_ERR_WORKSPACE
