@@ -319,6 +319,19 @@ pa_status pa_prefill_chunk(void* out, pa_dtype out_dtype, const void* q,
 
 size_t pa_prefill_workspace_size(int num_reqs, int n_q_heads, int head_dim, int total_q);
 
+/* pa_prefill_chunk with scores and visible keys modified as for pa_decode_scored
+ * (pa_score_mod): first_key is [total_q], prefix_lens [num_reqs].  A prefix mask makes the
+ * keys below prefix_len visible to every row of the chunk, also those behind a row of the
+ * prefix itself; a window and first_key then still bound a row's keys from below.  Only the
+ * 128-key tiles that some row of a 256-row tile sees are computed.  Other rules as
+ * pa_prefill_chunk (no workspace). */
+pa_status pa_prefill_scored(void* out, pa_dtype out_dtype, const void* q,
+                            const void* k_cache, const void* v_cache, const pa_cache_desc* cache,
+                            const int32_t* block_tables, int max_blocks_per_seq,
+                            const int32_t* query_start_loc, const int32_t* context_lens,
+                            int num_reqs, int max_query_len, int n_q_heads,
+                            float scale, int block_size, const pa_score_mod* mod, void* stream);
+
 /* ---------------------------------------------------------------- block copies
  * Copy-on-write ("vLLM Serving ...", "Sharing and copy-on-write": a sharer
  * that diverges gets a copy of the one shared block it writes to, then its

@@ -20,7 +20,7 @@ from . import build as _build
 __all__ = [
     "PAError", "lib", "pa_reshape_and_cache", "pa_reshape_and_cache_quant",
     "pa_rope_and_cache", "pa_rope_table", "ScoreMod", "pa_decode_scored",
-    "pa_decode_scored_workspace_size", "pa_decode",
+    "pa_decode_scored_workspace_size", "pa_prefill_scored", "pa_decode",
     "pa_decode_workspace_size", "pa_decode_verify", "pa_decode_verify_workspace_size",
     "pa_decode_no_alloc", "PA_DECODE_NO_ALLOC_SCRATCH_BYTES",
     "pa_prefill_chunk", "pa_prefill_workspace_size", "pa_get_device_error", "pa_status_string",
@@ -59,6 +59,8 @@ _SIGS = {
     "pa_decode_scored": (I, [P, I, P, P, P, C.POINTER(_Desc), P, I, P, I, I, I, F, I,
                              C.POINTER(_ScoreMod), P, SZ, P]),
     "pa_decode_scored_workspace_size": (SZ, [I, I, I, I, I, I, I, I]),
+    "pa_prefill_scored": (I, [P, I, P, P, P, C.POINTER(_Desc), P, I, P, P, I, I, I, F, I,
+                              C.POINTER(_ScoreMod), P]),
     "pa_rope_table": (I, [P, I, I, C.c_double]),
     "pa_prefill_chunk": (I, [P, I, P, P, P, C.POINTER(_Desc), P, I, P, P, I, I, I, F, I, P, SZ, P]),
     "pa_prefill_workspace_size": (SZ, [I, I, I, I]),
@@ -360,6 +362,23 @@ def pa_prefill_chunk(out, q, k_cache, v_cache, block_tables, query_start_loc, co
                                   _ptr(context_lens), R, int(max_query_len), n_q, float(scale),
                                   int(block_size), _ptr(workspace), ws_bytes, _stream(stream)),
            "pa_prefill_chunk")
+
+
+def pa_prefill_scored(out, q, k_cache, v_cache, block_tables, query_start_loc, context_lens,
+                      max_query_len: int, mod: ScoreMod, scale: float, block_size: int,
+                      stream=None, k_scale=None, v_scale=None):
+    """pa_prefill_chunk with capped or biased scores and masks (mod); first_key is [total_q],
+    prefix_lens [R]."""
+    R = int(context_lens.shape[0])
+    total, n_q = q.shape[0], q.shape[1]
+    d = _desc(k_cache, k_scale, v_scale, q.dtype)
+    m = mod._c(n_q, total, R)
+    _check(lib().pa_prefill_scored(_ptr(out), dtype_code(out.dtype), _ptr(q), _ptr(k_cache),
+                                   _ptr(v_cache), C.byref(d), _ptr(block_tables),
+                                   int(block_tables.shape[1]), _ptr(query_start_loc),
+                                   _ptr(context_lens), R, int(max_query_len), n_q, float(scale),
+                                   int(block_size), C.byref(m), _stream(stream)),
+           "pa_prefill_scored")
 
 
 def pa_copy_blocks(k_cache, v_cache, block_mapping, stream=None):

@@ -595,14 +595,13 @@ size_t pa_prefill_workspace_size(int num_reqs, int n_q_heads, int head_dim, int 
     return 0;
 }
 
-pa_status pa_prefill_chunk(void* out, pa_dtype out_dtype, const void* q, const void* k_cache,
-                           const void* v_cache, const pa_cache_desc* cache,
-                           const int32_t* block_tables, int max_blocks_per_seq,
-                           const int32_t* query_start_loc, const int32_t* context_lens,
-                           int num_reqs, int max_query_len, int n_q_heads, float scale,
-                           int block_size, void* workspace, size_t workspace_bytes, void* stream)
+static pa_status prefill_common(void* out, pa_dtype out_dtype, const void* q, const void* k_cache,
+                                const void* v_cache, const pa_cache_desc* cache,
+                                const int32_t* block_tables, int max_blocks_per_seq,
+                                const int32_t* query_start_loc, const int32_t* context_lens,
+                                int num_reqs, int max_query_len, int n_q_heads, float scale,
+                                int block_size, void* stream, const ScoreParams* score)
 {
-    (void)workspace; (void)workspace_bytes;
     pa_status st = check_cache(cache);
     if (st != PA_OK) return st;
     if (num_reqs < 0 || max_query_len < 0) return fail(PA_ERR_INVALID_ARG, "negative size");
@@ -635,10 +634,39 @@ pa_status pa_prefill_chunk(void* out, pa_dtype out_dtype, const void* q, const v
     a.block_tables = block_tables; a.max_blocks = max_blocks_per_seq;
     a.q_start = query_start_loc; a.context_lens = context_lens;
     a.num_reqs = num_reqs; a.max_q = max_query_len; a.n_q = n_q_heads; a.scale = scale;
-    a.err = err;
-    cudaError_t e = launch_prefill_tc(a, static_cast<cudaStream_t>(stream));
+    a.err = err; a.score = score;
+    cudaError_t e = score ? launch_prefill_scored(a, static_cast<cudaStream_t>(stream))
+                          : launch_prefill_tc(a, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "prefill launch");
     return ok();
+}
+
+pa_status pa_prefill_chunk(void* out, pa_dtype out_dtype, const void* q, const void* k_cache,
+                           const void* v_cache, const pa_cache_desc* cache,
+                           const int32_t* block_tables, int max_blocks_per_seq,
+                           const int32_t* query_start_loc, const int32_t* context_lens,
+                           int num_reqs, int max_query_len, int n_q_heads, float scale,
+                           int block_size, void* workspace, size_t workspace_bytes, void* stream)
+{
+    (void)workspace; (void)workspace_bytes;
+    return prefill_common(out, out_dtype, q, k_cache, v_cache, cache, block_tables,
+                          max_blocks_per_seq, query_start_loc, context_lens, num_reqs,
+                          max_query_len, n_q_heads, scale, block_size, stream, nullptr);
+}
+
+pa_status pa_prefill_scored(void* out, pa_dtype out_dtype, const void* q, const void* k_cache,
+                            const void* v_cache, const pa_cache_desc* cache,
+                            const int32_t* block_tables, int max_blocks_per_seq,
+                            const int32_t* query_start_loc, const int32_t* context_lens,
+                            int num_reqs, int max_query_len, int n_q_heads, float scale,
+                            int block_size, const pa_score_mod* mod, void* stream)
+{
+    ScoreParams sc{};
+    const pa_status st = check_mod(mod, &sc);
+    if (st != PA_OK) return st;
+    return prefill_common(out, out_dtype, q, k_cache, v_cache, cache, block_tables,
+                          max_blocks_per_seq, query_start_loc, context_lens, num_reqs,
+                          max_query_len, n_q_heads, scale, block_size, stream, &sc);
 }
 
 }  // extern "C"

@@ -98,7 +98,10 @@ struct PrefillArgs {
     const int32_t* q_start; const int32_t* context_lens;
     int num_reqs; int max_q; int n_q; float scale;
     unsigned* err;
+    const ScoreParams* score;   // scored prefill (host memory); else null
 };
 cudaError_t launch_prefill_tc(const PrefillArgs& a, cudaStream_t s);
+cudaError_t launch_prefill_scored(const PrefillArgs& a, cudaStream_t s);
+cudaError_t launch_prefill_bias(const PrefillArgs& a, cudaStream_t s);   // (its forms with a bias)
 
 }  // namespace pa

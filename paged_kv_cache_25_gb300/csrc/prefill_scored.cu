@@ -1,0 +1,14 @@
+// Scored chunked prefill: the kernel of prefill_tc.cuh with masks of every row's
+// own, and with a cap on the scores or without.  (Forms with a distance bias:
+// prefill_scored_bias.cu.)
+#include "prefill_tc.cuh"
+
+namespace pa {
+
+cudaError_t launch_prefill_scored(const PrefillArgs& a, cudaStream_t s)
+{
+    if (a.score->slopes) return launch_prefill_bias(a, s);
+    return a.score->cap2 > 0.f ? run_prefill_any<kPfScored | kPfCap>(a, s) : run_prefill_any<kPfScored>(a, s);
+}
+
+}  // namespace pa

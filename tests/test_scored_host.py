@@ -61,3 +61,30 @@ def test_a_window_bounds_the_workspace():
     # enough for exactly what the call asks
     need = size(4, 1, 32, 8, 128, 16, 256, 100)
     assert _decode((0.0, None, 100, None, None), ws_bytes=need - 1) == pa.PA_ERR_WORKSPACE
+
+
+def _prefill(mod=None, dt=2, d=128, reqs=2, max_q=16, null_mod=False, **kw):
+    desc = pa._Desc(64, 16, 8, d, dt, 1.0, 1.0, 2)
+    m = pa._ScoreMod(*(mod or (0.0, None, 0, None, None)))
+    a = dict(out=0x1000, q=0x2000, kc=0x3000, vc=0x4000, bt=0x5000, qs=0x6000, cl=0x7000, n_q=32,
+             scale=0.1, bs=16, mb=8)
+    a.update(kw)
+    return pa.lib().pa_prefill_scored(a["out"], 0, a["q"], a["kc"], a["vc"], C.byref(desc), a["bt"],
+                                      a["mb"], a["qs"], a["cl"], reqs, max_q, a["n_q"], a["scale"],
+                                      a["bs"], None if null_mod else C.byref(m), None)
+
+
+@pytest.mark.parametrize("mod", BAD_MODS)
+def test_prefill_refuses_bad_modifications(mod):
+    assert _prefill(mod) == pa.PA_ERR_INVALID_ARG
+
+
+def test_prefill_refusals():
+    assert _prefill(null_mod=True) == pa.PA_ERR_INVALID_ARG
+    assert _prefill(dt=0) == pa.PA_ERR_UNSUPPORTED
+    assert _prefill(d=96) == pa.PA_ERR_UNSUPPORTED
+    assert _prefill((1e-9, None, 0, None, None)) == pa.PA_ERR_UNSUPPORTED
+    assert _prefill(q=None) == pa.PA_ERR_INVALID_ARG
+    assert _prefill(n_q=30) == pa.PA_ERR_INVALID_ARG
+    assert _prefill(reqs=0) == pa.PA_OK
+    assert _prefill(max_q=0) == pa.PA_OK
