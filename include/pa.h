@@ -248,6 +248,46 @@ pa_status pa_decode_no_alloc(void* out, pa_dtype out_dtype, const void* q,
                              const int32_t* context_lens, int num_seqs, int n_q_heads,
                              float scale, int block_size, void* stream);
 
+/* ---------------------------------------------------------------- decode with shared prefixes
+ * pa_decode for a batch in which groups of sequences start with the same blocks (one
+ * system prompt, several samples of one prompt; see the prefix cache below): a group's
+ * common blocks are read once for all its members instead of once per member.  The
+ * result is pa_decode's up to rounding.
+ *   group_of_seq  : int32 [num_seqs] on the device, the group of each sequence, or a negative
+ *                   value for one that shares nothing.  A value >= num_groups sets
+ *                   PA_ERR_OUT_OF_RANGE on the device and counts as negative.
+ *   prefix_lens   : int32 [num_groups] on the device: tokens that the group's members have in
+ *                   common, rounded down to whole blocks (and to the table's width).  The
+ *                   members' first prefix_lens / block_size table entries must be the same
+ *                   (those of the lowest-numbered member are read).  A member may be as short
+ *                   as its prefix, or shorter: it sees its own context_lens tokens.
+ *   num_groups    : 0 .. 1024; 0 is pa_decode.  Groups may be empty or have one member.
+ *   workspace     : pa_decode_shared_workspace_size(...) bytes for the same shapes and
+ *                   num_groups; other rules as pa_decode's.
+ * Both arrays are read on the device only: a captured call follows new groups, lengths and
+ * tables.  bf16/fp16/FP8 pools with head_dim 64 or 128 (else PA_ERR_UNSUPPORTED); other
+ * rules as pa_decode.  From fp16 and FP8 pools the prefix's probabilities enter P V as one
+ * fp16 part, as in pa_prefill_chunk. */
+pa_status pa_decode_shared(void* out, pa_dtype out_dtype, const void* q,
+                           const void* k_cache, const void* v_cache, const pa_cache_desc* cache,
+                           const int32_t* block_tables, int max_blocks_per_seq,
+                           const int32_t* context_lens, int num_seqs, int n_q_heads,
+                           float scale, int block_size, const int32_t* group_of_seq,
+                           const int32_t* prefix_lens, int num_groups,
+                           void* workspace, size_t workspace_bytes, void* stream);
+size_t pa_decode_shared_workspace_size(int num_seqs, int n_q_heads, int n_kv_heads,
+                                       int head_dim, int block_size, int max_context_len,
+                                       int num_groups);
+/* Host: groups for pa_decode_shared from a batch's block tables (host memory, unused entries
+ * negative).  Sequences are grouped by common leading full blocks so that the block reads saved
+ * (members - 1 times the prefix's blocks, summed over the groups) are the most that nested
+ * choices allow; prefixes of fewer than min_prefix_tokens (or of no full block) are left out.
+ * Fills group_of_seq [num_seqs] (-1: none) and prefix_lens (room for num_seqs / 2 groups);
+ * returns the number of groups, or -1 on bad arguments. */
+int pa_shared_prefix_groups(const int32_t* tables, int max_blocks, const int32_t* lens,
+                            int num_seqs, int block_size, int min_prefix_tokens,
+                            int32_t* group_of_seq, int32_t* prefix_lens);
+
 /* ---------------------------------------------------------------- scored attention
  * Attention whose scores or visible keys differ from plain causal softmax.  Query
  * row i (the row at absolute position i) and key j of one sequence score

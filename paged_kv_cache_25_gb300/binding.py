@@ -19,7 +19,8 @@ from . import build as _build
 
 __all__ = [
     "PAError", "lib", "pa_reshape_and_cache", "pa_reshape_and_cache_quant",
-    "pa_rope_and_cache", "pa_rope_table", "ScoreMod", "pa_decode_scored",
+    "pa_rope_and_cache", "pa_rope_table", "pa_decode_shared",
+    "pa_decode_shared_workspace_size", "pa_shared_prefix_groups", "ScoreMod", "pa_decode_scored",
     "pa_decode_scored_workspace_size", "pa_prefill_scored", "pa_decode",
     "pa_decode_workspace_size", "pa_decode_verify", "pa_decode_verify_workspace_size",
     "pa_decode_no_alloc", "PA_DECODE_NO_ALLOC_SCRATCH_BYTES",
@@ -56,6 +57,9 @@ _SIGS = {
     "pa_reshape_and_cache_quant": (I, [P, P, I, P, P, P, I, C.POINTER(_Desc), P]),
     "pa_rope_and_cache": (I, [P, P, P, P, I, L, L, L, L, P, P, I, I, I, P, P, P, I, I,
                               C.POINTER(_Desc), P]),
+    "pa_decode_shared": (I, [P, I, P, P, P, C.POINTER(_Desc), P, I, P, I, I, F, I, P, P, I, P, SZ, P]),
+    "pa_decode_shared_workspace_size": (SZ, [I, I, I, I, I, I, I]),
+    "pa_shared_prefix_groups": (I, [P, I, P, I, I, I, P, P]),
     "pa_decode_scored": (I, [P, I, P, P, P, C.POINTER(_Desc), P, I, P, I, I, I, F, I,
                              C.POINTER(_ScoreMod), P, SZ, P]),
     "pa_decode_scored_workspace_size": (SZ, [I, I, I, I, I, I, I, I]),
@@ -295,6 +299,48 @@ def pa_decode_no_alloc(out, q, k_cache, v_cache, block_tables, context_lens, sca
 
 
 PA_DECODE_NO_ALLOC_SCRATCH_BYTES = 16 << 20
+
+
+def pa_decode_shared_workspace_size(num_seqs, n_q_heads, n_kv_heads, head_dim, block_size,
+                                    max_context_len, num_groups) -> int:
+    return int(lib().pa_decode_shared_workspace_size(num_seqs, n_q_heads, n_kv_heads, head_dim,
+                                                     block_size, max_context_len, num_groups))
+
+
+def pa_decode_shared(out, q, k_cache, v_cache, block_tables, context_lens, group_of_seq,
+                     prefix_lens, scale: float, block_size: int, workspace=None, stream=None,
+                     k_scale=None, v_scale=None):
+    """pa_decode with the common prefix of each group of sequences read once: group_of_seq int32
+    [B] (negative: none), prefix_lens int32 [groups], see pa_shared_prefix_groups."""
+    B, n_q, _ = q.shape
+    if group_of_seq.dtype != torch.int32 or prefix_lens.dtype != torch.int32:
+        raise TypeError("group_of_seq and prefix_lens: int32 expected")
+    if group_of_seq.numel() != B or not group_of_seq.is_contiguous() or \
+            not prefix_lens.is_contiguous():
+        raise ValueError("group_of_seq [B] and prefix_lens [groups], contiguous, expected")
+    d = _desc(k_cache, k_scale, v_scale, q.dtype)
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check(lib().pa_decode_shared(_ptr(out), dtype_code(out.dtype), _ptr(q), _ptr(k_cache),
+                                  _ptr(v_cache), C.byref(d), _ptr(block_tables),
+                                  int(block_tables.shape[1]), _ptr(context_lens), B, n_q,
+                                  float(scale), int(block_size), _ptr(group_of_seq),
+                                  _ptr(prefix_lens), prefix_lens.numel(), _ptr(workspace), ws_bytes,
+                                  _stream(stream)), "pa_decode_shared")
+
+
+def pa_shared_prefix_groups(tables, lens, block_size: int, min_prefix_tokens: int = 0):
+    """(group_of_seq int32 [B], prefix_lens int32 [groups]) of a batch's host block tables."""
+    tables = np.ascontiguousarray(tables, np.int32)
+    lens = np.ascontiguousarray(lens, np.int32)
+    if tables.ndim != 2 or lens.shape != tables.shape[:1]:
+        raise ValueError("tables [B][max_blocks] and lens [B] expected")
+    group = np.full(len(lens), -1, np.int32)
+    prefix = np.empty(max(1, len(lens)), np.int32)
+    n = lib().pa_shared_prefix_groups(_ptr(tables), tables.shape[1], _ptr(lens), len(lens),
+                                      block_size, min_prefix_tokens, _ptr(group), _ptr(prefix))
+    if n < 0:
+        raise PAError(PA_ERR_INVALID_ARG, "pa_shared_prefix_groups: bad arguments")
+    return group, prefix[:n].copy()
 
 
 @dataclasses.dataclass(frozen=True)

@@ -456,6 +456,17 @@ size_t pa_decode_verify_workspace_size(int num_seqs, int q_per_seq, int n_q_head
                            max_context_len, nullptr, nullptr);
 }
 
+// Shared decode: ranges a prefix may be cut into (a thread block each for every KV
+// head on 152 SMs, no more than its 128-key tiles, and the 32 that the plan tries).
+static int shared_max_splits(int n_kv, int max_ctx)
+{
+    const int fill = (152 + n_kv - 1) / n_kv, tiles = (max_ctx + 127) / 128;
+    const int s = fill < tiles ? fill : tiles;
+    return s < 1 ? 1 : (s > 32 ? 32 : s);
+}
+
+static constexpr int kMaxGroups = 1024;   // prefix groups of a call
+
 static pa_status decode_common(void* out, pa_dtype out_dtype, const void* q, const void* k_cache,
                                const void* v_cache, const pa_cache_desc* cache,
                                const int32_t* block_tables, int max_blocks_per_seq,
@@ -491,8 +502,11 @@ static pa_status decode_common(void* out, pa_dtype out_dtype, const void* q, con
     const int max_ctx = scored_span(max_blocks_per_seq * block_size, score ? score->window : 0,
                                     q_per_seq, block_size);
     int part = 0, parts = 0;
+    const bool shared = score && score->group_of_seq;
+    const int splits = shared ? shared_max_splits(cache->n_kv_heads, max_ctx) : 0;
+    const size_t head = shared ? align256(score->num_groups * sizeof(int32_t)) : 0;
     const size_t need = decode_ws_bytes(num_seqs, q_per_seq, n_q_heads, cache->n_kv_heads,
-                                        cache->head_dim, block_size, max_ctx, &part, &parts);
+                                        cache->head_dim, block_size, max_ctx, &part, &parts, splits, head);
     if (parts > 65535) return fail(PA_ERR_UNSUPPORTED, "too many partitions per sequence");
     if (!workspace || workspace_bytes < need)
         return fail(PA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need,
@@ -511,15 +525,25 @@ static pa_status decode_common(void* out, pa_dtype out_dtype, const void* q, con
     a.part_tokens = part; a.max_parts = parts; a.err = err;
     a.ticket = static_cast<unsigned*>(workspace);
     if (need > kControlBytes) {
-        const size_t units = static_cast<size_t>(num_seqs) * q_per_seq * n_q_heads * parts;
-        char* base = static_cast<char*>(workspace) + kControlBytes;
+        const size_t units = static_cast<size_t>(num_seqs) * q_per_seq * n_q_heads * (parts + splits);
+        char* base = static_cast<char*>(workspace) + kControlBytes + head;
         a.ws_ml = reinterpret_cast<float*>(base);
         a.ws_acc = reinterpret_cast<float*>(base + align256(units * 2 * sizeof(float)));
     }
     if (score) {
-        score->slots = parts;
-        score->slot0 = 0;
+        score->slots = parts + splits;
+        score->slot0 = splits;
         a.score = score;
+    }
+    if (shared) {
+        PrefixPass pass{};
+        pass.num_seqs = num_seqs;
+        pass.ml = a.ws_ml; pass.acc = a.ws_acc;
+        pass.splits = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + kControlBytes);
+        pass.max_splits = splits;
+        score->group_splits = pass.splits;
+        const cudaError_t e0 = launch_prefix_pass(a, pass, static_cast<cudaStream_t>(stream));
+        if (e0 != cudaSuccess) return cuda_fail(e0, "prefix pass launch");
     }
     cudaError_t e = launch_decode(a, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "decode launch");
@@ -554,6 +578,49 @@ pa_status pa_decode_verify(void* out, pa_dtype out_dtype, const void* q, const v
     return decode_common(out, out_dtype, q, k_cache, v_cache, cache, block_tables,
                          max_blocks_per_seq, context_lens, num_seqs, q_per_seq, n_q_heads, scale,
                          block_size, workspace, workspace_bytes, stream);
+}
+
+size_t pa_decode_shared_workspace_size(int num_seqs, int n_q_heads, int n_kv_heads, int head_dim,
+                                       int block_size, int max_context_len, int num_groups)
+{
+    if (num_seqs <= 0 || n_q_heads <= 0 || n_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 ||
+        max_context_len <= 0 || n_q_heads % n_kv_heads != 0 || num_groups < 0 || num_groups > kMaxGroups)
+        return 0;
+    if (num_groups == 0)
+        return pa_decode_workspace_size(num_seqs, n_q_heads, n_kv_heads, head_dim, block_size,
+                                        max_context_len);
+    return decode_ws_bytes(num_seqs, 1, n_q_heads, n_kv_heads, head_dim, block_size, max_context_len,
+                           nullptr, nullptr, shared_max_splits(n_kv_heads, max_context_len),
+                           align256(num_groups * sizeof(int32_t)));
+}
+
+pa_status pa_decode_shared(void* out, pa_dtype out_dtype, const void* q, const void* k_cache,
+                           const void* v_cache, const pa_cache_desc* cache,
+                           const int32_t* block_tables, int max_blocks_per_seq,
+                           const int32_t* context_lens, int num_seqs, int n_q_heads, float scale,
+                           int block_size, const int32_t* group_of_seq, const int32_t* prefix_lens,
+                           int num_groups, void* workspace, size_t workspace_bytes, void* stream)
+{
+    pa_status st = check_cache(cache);
+    if (st != PA_OK) return st;
+    if (cache->dtype == PA_F32 || (cache->head_dim != 64 && cache->head_dim != 128))
+        return fail(PA_ERR_UNSUPPORTED,
+                    "shared-prefix decode runs on bf16/fp16/FP8 pools with head_dim 64 or 128");
+    if (num_groups < 0) return fail(PA_ERR_INVALID_ARG, "num_groups < 0");
+    if (num_groups > kMaxGroups)
+        return fail(PA_ERR_UNSUPPORTED, "more than %d prefix groups per call", kMaxGroups);
+    if (num_groups > 0 && num_seqs > 0) {
+        if (!group_of_seq || !prefix_lens) return fail(PA_ERR_INVALID_ARG, "NULL pointer argument");
+        if ((reinterpret_cast<uintptr_t>(group_of_seq) & 3u) || (reinterpret_cast<uintptr_t>(prefix_lens) & 3u))
+            return fail(PA_ERR_INVALID_ARG, "group arrays must be 4-byte aligned");
+    }
+    ScoreParams sc{};
+    sc.group_of_seq = group_of_seq;
+    sc.group_prefix = prefix_lens;
+    sc.num_groups = num_groups;
+    return decode_common(out, out_dtype, q, k_cache, v_cache, cache, block_tables,
+                         max_blocks_per_seq, context_lens, num_seqs, 1, n_q_heads, scale, block_size,
+                         workspace, workspace_bytes, stream, num_groups > 0 ? &sc : nullptr);
 }
 
 size_t pa_decode_scored_workspace_size(int num_seqs, int q_per_seq, int n_q_heads, int n_kv_heads,

@@ -70,6 +70,16 @@ struct ScoreParams {
     int slots, slot0;
 };
 
+// The prefix pass of a shared decode: partials of every member row and prefix range.
+struct PrefixPass {
+    int num_seqs;
+    float* ml;          // [B][n_q][slots][2]
+    float* acc;         // [B][n_q][slots][d]
+    int32_t* splits;    // [num_groups], written by the pass
+    int max_splits;     // ranges a prefix may be cut into (at most 32, at most slot0)
+    int target;         // thread blocks that run at once
+};
+
 struct DecodeArgs {
     void* out; pa_dtype out_dtype; const void* q;
     const void* k_cache; const void* v_cache; pa_cache_desc cache;
@@ -88,6 +98,8 @@ struct DecodeArgs {
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t s);
 // attention kernel of a scored or shared-prefix call (decode_scored.cu)
 cudaError_t launch_decode_scored(const DecodeArgs& a, cudaStream_t s, float scale_log2);
+// prefix pass of a shared-prefix call (prefix_pass.cu)
+cudaError_t launch_prefix_pass(const DecodeArgs& a, const PrefixPass& pass, cudaStream_t s);
 // attention kernel of a call with q_per_seq > 1 (decode_verify.cu)
 cudaError_t launch_decode_mq(const DecodeArgs& a, cudaStream_t s, float scale_log2);
 

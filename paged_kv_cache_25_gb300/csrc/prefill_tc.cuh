@@ -1,6 +1,7 @@
 #pragma once
 // Chunked-prefill attention on the fifth-generation tensor cores (tcgen05), shared
-// by the plain chunked prefill and the scored one.
+// by the plain chunked prefill, the scored one and the prefix pass of the shared
+// decode.
 //
 // Semantics ("The hands-on guide to LLM Inference with vLLM", chunked
 // prefill): query row i of request r's chunk of C_r rows sits at absolute
@@ -45,11 +46,15 @@
 // The running maximum is then kept in the log2 domain of the modified scores; the
 // cap is monotone, so with a cap alone the row maximum is found on raw scores and
 // capped once.
+// The prefix pass (kPfShared): the M rows are (member sequence, head) pairs of a prefix
+// group, the keys one range of the group's prefix, with no mask but the members' own
+// lengths; O stays unnormalised and goes to the decode's partials with its (m, l).
 // All waits are bounded; the kernel never traps.
 #include <cuda_fp8.h>
 
 #include "pa_device.cuh"
 #include "pa_internal.h"
+#include "prefix_plan.cuh"
 #include "score_mod.cuh"
 
 #include <limits.h>
@@ -122,6 +127,7 @@ __device__ __forceinline__ void umma4_ts(uint32_t d, uint32_t a0, uint64_t b0, u
 constexpr int kPfScored = 1;      // masks: every row has a first and a last visible key
 constexpr int kPfCap = 2;         // capped scores
 constexpr int kPfBias = 4;        // distance bias
+constexpr int kPfShared = 8;      // prefix pass of the shared decode
 
 constexpr int kTcRows = 128;      // M rows per tile
 constexpr int kTcTiles = 2;       // tiles per CTA (A, B)
@@ -271,8 +277,10 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                   const int32_t* __restrict__ q_start, const int32_t* __restrict__ context_lens,
                   int max_q, int n_q, int n_kv, int group, int num_blocks, float scale_log2,
                   float v_scale, unsigned* err,
-                  const __grid_constant__ std::conditional_t<MODE != 0, ScoreParams, NoScore> sc)
+                  const __grid_constant__ std::conditional_t<MODE != 0, ScoreParams, NoScore> sc,
+                  const __grid_constant__ std::conditional_t<(MODE & kPfShared) != 0, PrefixPass, NoScore> sp)
 {
+    constexpr bool kShared = (MODE & kPfShared) != 0;
     constexpr bool kCap = (MODE & kPfCap) != 0, kBias = (MODE & kPfBias) != 0;
     constexpr bool kZ = kCap || kBias;   // maxima in the log2 domain of modified scores
     constexpr bool kBq = std::is_same<QT, __nv_bfloat16>::value;
@@ -300,7 +308,21 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     // the last position blocks, which see the most keys, come first
     static_assert(kRankedReqs <= Wp::kThreads, "one thread per ranked request");
     int r = blockIdx.z;
-    if (gridDim.z > 1 && gridDim.z <= kRankedReqs) {
+    extern __shared__ uint8_t dyn_smem[];
+    __shared__ std::conditional_t<kShared, PrefixUnit, NoScore> s_unit;
+    __shared__ int s_member[kShared ? kUnitMembers : 1];
+    if constexpr (kShared) {
+        plan_prefix_unit(sc, sp, n_kv, group, BS, max_blocks, reinterpret_cast<int*>(dyn_smem), s_member,
+                         &s_unit, err);
+        if (!s_unit.live) return;
+        __syncthreads();   // the members are listed, and the scratch is free
+    }
+    auto unit = [&]() -> PrefixUnit {
+        if constexpr (kShared) return s_unit;
+        else return PrefixUnit{};
+    };
+    if constexpr (kShared) r = unit().first_seq;
+    if (!kShared && gridDim.z > 1 && gridDim.z <= kRankedReqs) {
         __shared__ int s_req;
         const int R = gridDim.z, i = threadIdx.x;
         if (i < R) {
@@ -316,12 +338,12 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         r = s_req;
     }
     const int blk = gridDim.x - 1 - blockIdx.x;
-    const int kvh = blockIdx.y;
-    const int qs = __ldg(q_start + r);
-    const int C = __ldg(q_start + r + 1) - qs;
-    const int L = __ldg(context_lens + r);
-    const int rows_total = C * group;
-    const int row0 = blk * (kTcTiles * kTcRows);
+    const int kvh = kShared ? unit().kvh : blockIdx.y;
+    const int qs = kShared ? 0 : __ldg(q_start + r);
+    const int C = kShared ? 0 : __ldg(q_start + r + 1) - qs;
+    const int L = kShared ? unit().prefix : __ldg(context_lens + r);
+    const int rows_total = kShared ? unit().rows : C * group;
+    const int row0 = kShared ? unit().row0 : blk * (kTcTiles * kTcRows);
     // the grid covers max_q rows per request: a longer chunk would leave its
     // last rows unwritten, so it is flagged (once, by the request's first CTA)
     if (C > max_q && blk == 0 && threadIdx.x == 0) set_error(err, PA_ERR_OUT_OF_RANGE);
@@ -330,7 +352,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         if (threadIdx.x == 0) set_error(err, PA_ERR_OUT_OF_RANGE);
         return;
     }
-    const int ctx0 = L - C;
+    const int ctx0 = kShared ? 0 : L - C;
     // key tiles each tile's rows need (0: the tile has no rows); when both
     // tiles have rows, n_t[0] <= n_t[1]
     int n_t[kTcTiles];
@@ -338,18 +360,19 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     // (a prefix mask shows the whole prefix to every row), the first key that some
     // row of the CTA sees, and the key tile it lies in
     int prefix_end = 0, lo_cta = 0, tile0 = 0;
-    if constexpr (MODE != 0)
+    if constexpr (kShared) tile0 = unit().tile0;
+    if constexpr (MODE != 0 && !kShared)
         if (sc.prefix_lens) prefix_end = min(__ldg(sc.prefix_lens + r), L);
     auto first_key = [&](int i) -> int {
         int f = 0;
-        if constexpr (MODE != 0) {
+        if constexpr (MODE != 0 && !kShared) {
             if (sc.window > 0) f = max(f, ctx0 + i - sc.window + 1);
             if (sc.first_key) f = max(f, __ldg(sc.first_key + qs + i));
         }
         return f;
     };
     auto last_key = [&](int i) -> int { return MODE != 0 ? max(ctx0 + i, prefix_end - 1) : ctx0 + i; };
-    if constexpr (MODE != 0) {
+    if constexpr (MODE != 0 && !kShared) {
         if (sc.window > 0 || sc.first_key) {
             __shared__ int s_lo;
             if (threadIdx.x == 0) s_lo = INT_MAX;
@@ -371,6 +394,10 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     for (int t = 0; t < kTcTiles; ++t) {
         const int first = row0 + t * kTcRows;
         const int last = min(rows_total, first + kTcRows) - 1;
+        if constexpr (kShared) {
+            n_t[t] = first < rows_total ? unit().tiles : 0;
+            continue;
+        }
         n_t[t] = first < rows_total ? last_key(last / group) / kTcKeys + 1 - tile0 : 0;
         // (a tile whose rows see nothing that the other's do: masked throughout)
         if (MODE != 0 && first < rows_total) n_t[t] = max(n_t[t], 1);
@@ -391,7 +418,6 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     __shared__ uint8_t xstop[2][kTcTiles][2][kTcRows];
     __shared__ float xsum[kTcTiles][2][kTcRows];
     __shared__ uint8_t xstop_end[kTcTiles][2][kTcRows];
-    extern __shared__ uint8_t dyn_smem[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn_smem) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
     const uint32_t sbase = smem_u32(smem);
@@ -802,7 +828,11 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         const bool valid = grow < rows_total;
         const int pos_local = valid ? grow / group : 0;
         const int head = kvh * group + (valid ? grow - (grow / group) * group : 0);
-        const int p_abs = valid ? last_key(pos_local) : L - 1;   // padding rows see every key
+        // kShared: pos_local counts the group's members, the row is this sequence's
+        const int seq = kShared && valid ? s_member[pos_local - row0 / group] : 0;
+        const int q_row = kShared ? seq : qs + pos_local;
+        const int p_abs = !valid ? L - 1   // padding rows see every key
+                          : kShared ? min(L, __ldg(context_lens + seq)) - 1 : last_key(pos_local);
         const int p_lo = MODE != 0 && valid ? first_key(pos_local) : 0;
         auto sees = [&](int k) -> bool { return k <= p_abs && (MODE == 0 || k >= p_lo); };
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
@@ -818,7 +848,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         scale_log2 = fabsf(scale_log2);
         {
             const uint4* qp = reinterpret_cast<const uint4*>(
-                q + (static_cast<int64_t>(qs + pos_local) * n_q + head) * D);
+                q + (static_cast<int64_t>(q_row) * n_q + head) * D);
             const uint32_t qbase = sbase + Ly::kOffQ + t * Ly::kQBytes;
             if constexpr (kDirectK) {
                 // bf16 q -> two E4M3 parts: the row is scaled by 2^-e so that its
@@ -952,7 +982,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             if constexpr (kBias) z = fmaf(-slope2, fabsf(d), z);
             return z;
         };
-        const float unit = kZ ? 1.f : scale_log2;   // log2 units of the running maximum
+        const float unit_log2 = kZ ? 1.f : scale_log2;   // log2 units of the running maximum
         float m_raw = -INFINITY, l = 0.f;
         bool stop = false;   // a wait of this warp ran out
         bool quit = false;   // the pair left the loop together
@@ -1010,14 +1040,14 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             // lazy: move the reference max only when the first tile sets it or
             // the max grew by more than 2^8 (written so that scale 0 stays finite)
             const bool first = m_raw == -INFINITY;
-            const bool resc = first ? (mx > -INFINITY) : ((mx - m_raw) * unit > 8.f);
+            const bool resc = first ? (mx > -INFINITY) : ((mx - m_raw) * unit_log2 > 8.f);
             float fac = 1.f;
             if (resc) {
-                fac = first ? 0.f : fast_exp2((m_raw - mx) * unit);
+                fac = first ? 0.f : fast_exp2((m_raw - mx) * unit_log2);
                 m_raw = mx;
                 l *= fac;
             }
-            const float neg_mc = -m_raw * unit;
+            const float neg_mc = -m_raw * unit_log2;
             if (j >= 1 && __any_sync(0xffffffffu, resc)) {   // TMEM access is warp-wide
 #pragma unroll
                 for (int c0 = 0; c0 < D / 2; c0 += 32) {
@@ -1135,8 +1165,17 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             if (__all_sync(0xffffffffu, ok)) {
                 tc_fence_after();
                 // (MODE: a row that sees no key is 0)
-                const float inv = MODE != 0 && lsum == 0.f ? 0.f : (F8 ? v_scale : 1.f) / lsum;
-                const int64_t obase = (static_cast<int64_t>(qs + pos_local) * n_q + head) * D;
+                const float inv = kShared ? (F8 ? v_scale : 1.f)
+                                          : (MODE != 0 && lsum == 0.f ? 0.f : (F8 ? v_scale : 1.f) / lsum);
+                int64_t obase = (static_cast<int64_t>(q_row) * n_q + head) * D;
+                if constexpr (kShared) {
+                    // unnormalised O and its (max, sum), the max in log2 units
+                    const int64_t slot = (static_cast<int64_t>(q_row) * n_q + head) * sc.slots + unit().split;
+                    obase = slot * D;
+                    if (valid && hf == 0)
+                        *reinterpret_cast<float2*>(sp.ml + 2 * slot) =
+                            make_float2(lsum > 0.f ? m_raw * unit_log2 : -INFINITY, lsum);
+                }
 #pragma unroll
                 for (int c0 = 0; c0 < D / 2; c0 += 32) {
                     uint32_t o[32];
@@ -1145,7 +1184,11 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                     float v[32];
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(o[i]) * inv;
-                    if (valid) store_row<T>(out, obase, hf * (D / 2) + c0, v, 32, out_dtype);
+                    if constexpr (kShared) {
+                        if (valid) store_row<T>(sp.acc, obase, hf * (D / 2) + c0, v, 32, PA_F32);
+                    } else {
+                        if (valid) store_row<T>(out, obase, hf * (D / 2) + c0, v, 32, out_dtype);
+                    }
                 }
             }
         }
@@ -1155,6 +1198,25 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     __syncthreads();
     tc_fence_after();
     if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+}
+
+// The tensor maps of a call's pools (FP8: of the K codes, where the score MMA reads
+// them; the other FP8 copies are plain bulk copies).
+template <typename T, int D, int BS, bool F8, bool BQ>
+cudaError_t prefill_maps(const pa_cache_desc& c, const void* k_cache, const void* v_cache,
+                         CUtensorMap* kmap, CUtensorMap* vmap)
+{
+    const uint64_t rows = static_cast<uint64_t>(c.num_blocks) * c.n_kv_heads * BS;
+    if constexpr (!F8) {
+        if (encode_pool_map(kmap, k_cache, c.dtype, D, rows, 64, 16) != PA_OK ||
+            encode_pool_map(vmap, v_cache, c.dtype, D, rows, 64, 16) != PA_OK)
+            return cudaErrorInvalidValue;
+    } else if constexpr (PfLayout<T, D, F8, BQ>::kDirectK) {
+        // boxes of 16 rows x 128 codes, 128-byte swizzle
+        if (encode_pool_map(kmap, k_cache, c.dtype, D, rows, D, 16, 128) != PA_OK)
+            return cudaErrorInvalidValue;
+    }
+    return cudaSuccess;
 }
 
 template <int MODE>
@@ -1178,17 +1240,8 @@ cudaError_t run_prefill_tc(const PrefillArgs& a, cudaStream_t s, float sl2)
     });
     if (attr_err != cudaSuccess) return attr_err;
     CUtensorMap kmap{}, vmap{};
-    const uint64_t rows = static_cast<uint64_t>(a.cache.num_blocks) * a.cache.n_kv_heads * BS;
-    if constexpr (!F8) {
-        if (encode_pool_map(&kmap, a.k_cache, a.cache.dtype, D, rows, 64, 16) != PA_OK ||
-            encode_pool_map(&vmap, a.v_cache, a.cache.dtype, D, rows, 64, 16) != PA_OK)
-            return cudaErrorInvalidValue;
-    } else if constexpr (Ly::kDirectK) {
-        // K codes read by the score MMA: boxes of 16 rows x 128 codes, 128-byte
-        // swizzle (the other FP8 copies are plain bulk copies; vmap stays unused)
-        if (encode_pool_map(&kmap, a.k_cache, a.cache.dtype, D, rows, D, 16, 128) != PA_OK)
-            return cudaErrorInvalidValue;
-    }
+    const cudaError_t map_err = prefill_maps<T, D, BS, F8, kBq>(a.cache, a.k_cache, a.v_cache, &kmap, &vmap);
+    if (map_err != cudaSuccess) return map_err;
     const int group = a.n_q / a.cache.n_kv_heads;
     const int64_t tiles = (static_cast<int64_t>(a.max_q) * group + kTcTiles * kTcRows - 1) /
                           (kTcTiles * kTcRows);
@@ -1197,7 +1250,7 @@ cudaError_t run_prefill_tc(const PrefillArgs& a, cudaStream_t s, float sl2)
         kmap, vmap, static_cast<const uint8_t*>(a.k_cache), static_cast<const uint8_t*>(a.v_cache),
         a.out, a.out_dtype, static_cast<const QT*>(a.q), a.block_tables, a.max_blocks,
         a.q_start, a.context_lens, a.max_q, a.n_q, a.cache.n_kv_heads, group, a.cache.num_blocks,
-        F8 ? sl2 * a.cache.k_scale : sl2, F8 ? a.cache.v_scale : 1.f, a.err, prefill_score<MODE>(a));
+        F8 ? sl2 * a.cache.k_scale : sl2, F8 ? a.cache.v_scale : 1.f, a.err, prefill_score<MODE>(a), NoScore{});
     return cudaGetLastError();
 }
 
