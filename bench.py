@@ -50,8 +50,8 @@ NCU_TRAFFIC = {
 # chunked prefill of the mixed step (the compact-pool capture runs the same four
 # chunks as the 60 GB pool): bytes per launch
 NCU_PREFILL_TRAFFIC = {
-    ("mixed-llama3-8b-bf16", "da5ac5d7daa2efd3"): (98487552 + 4037120, "compact pool, one-pass capture"),
-    ("mixed-llama3-8b-fp8", "da5ac5d7daa2efd3"): (57575936 + 1072384, "compact pool, one-pass capture"),
+    ("mixed-llama3-8b-bf16", "4262d850e1fa2e78"): (98472960 + 3946496, "compact pool, one-pass capture"),
+    ("mixed-llama3-8b-fp8", "4262d850e1fa2e78"): (57580288 + 948480, "compact pool, one-pass capture"),
 }
 
 
