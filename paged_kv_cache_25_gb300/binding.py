@@ -114,6 +114,8 @@ class PAError(RuntimeError):
 def lib(path: str | None = None):
     """Loads libpa.so (built in-tree by build.build()); raises if it is missing."""
     global _lib
+    if _lib is not None and path is None:
+        return _lib
     with _lock:
         if _lib is None:
             p = path or _build.LIB
@@ -152,8 +154,8 @@ def _ptr(t) -> int | None:
 
 
 def _stream(stream) -> int | None:
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream or None
+    if stream is None:     # the current stream's handle, without building a Stream object
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) or None
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream or None
     return stream
@@ -168,6 +170,30 @@ def _desc(k_cache: torch.Tensor, k_scale=None, v_scale=None, act_dtype=None) -> 
         return _Desc(nb, bs, n_kv, d, dt, float(k_scale or 0.0), float(v_scale or 0.0),
                      dtype_code(act_dtype) if act_dtype is not None else -1)
     return _Desc(nb, bs, n_kv, d, dt, 1.0, 1.0, dt)
+
+
+def _attention_args(out, q, k_cache, v_cache, block_tables, context_lens, seqs: int):
+    """Layout checks of a scored or shared-prefix call: what the library reads through bare
+    pointers has the types, the order and the device that it expects."""
+    if not (out.is_contiguous() and q.is_contiguous() and k_cache.is_contiguous() and
+            v_cache.is_contiguous() and block_tables.is_contiguous() and
+            context_lens.is_contiguous()):
+        raise ValueError("contiguous tensors expected")
+    if out.shape != q.shape or q.shape[-1] != k_cache.shape[3] or v_cache.numel() != k_cache.numel():
+        raise ValueError("out and q [..][n_q][d] and pools of that head_dim expected")
+    if block_tables.shape[0] != seqs or context_lens.numel() != seqs:
+        raise ValueError("one block table and one context length a sequence expected")
+    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+        raise TypeError("block_tables and context_lens: int32 expected")
+    kv = k_cache.dtype
+    if v_cache.dtype != kv or (q.dtype != kv and kv != torch.float8_e4m3fn):
+        raise TypeError("q and the pools must have one dtype (FP8 pools: bf16 or fp16 q)")
+    _check_device(q)
+
+
+def _check_device(t):
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError("the tensors must be on the current CUDA device")
 
 
 def pa_status_string(st: int) -> str:
@@ -223,11 +249,12 @@ def pa_reshape_and_cache_quant(k, v, k_cache, v_cache, slot_mapping, k_scale=Non
            "pa_reshape_and_cache_quant")
 
 
-def _token_stride(t, name: str) -> int:
-    """Elements from token to token of [T][heads][d]; a token's heads are contiguous."""
-    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
-        raise ValueError(f"{name}: [tokens][heads][head_dim] with contiguous heads expected")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+def _token_stride(t, T: int, heads: int, d: int) -> int:
+    """Elements from token to token of t [T][heads][d]; a token's heads are contiguous."""
+    tok, head, elem = t.stride()
+    if elem != 1 or (head != d and heads > 1):
+        raise ValueError("[tokens][heads][head_dim] with contiguous heads expected")
+    return tok if T > 1 else heads * d
 
 
 def pa_rope_and_cache(q_out, q, k, v, positions, cos_sin, k_cache, v_cache, slot_mapping,
@@ -236,28 +263,39 @@ def pa_rope_and_cache(q_out, q, k, v, positions, cos_sin, k_cache, v_cache, slot
     [T][n_kv][d] go to slot_mapping (int64 [T]) of the pools.  q, k and v may be slices of one
     projection (any token stride).  cos_sin: fp32 [max_position][rot_dim], see pa_rope_table.
     FP8 pools take their scales."""
-    T, n_q, hd = q.shape
-    if tuple(q_out.shape) != (T, n_q, hd) or k.shape != v.shape or \
-            tuple(k.shape) != (T, k_cache.shape[1], hd) or hd != k_cache.shape[3]:
+    shape = q.shape
+    T, n_q, hd = shape
+    kv_shape = k.shape
+    n_kv = k_cache.shape[1]
+    if q_out.shape != shape or v.shape != kv_shape or kv_shape != (T, n_kv, hd) or \
+            hd != k_cache.shape[3]:
         raise ValueError("q_out, q [T][n_q][d] and k, v [T][n_kv][d] expected")
-    if q_out.dtype != q.dtype or k.dtype != q.dtype or v.dtype != q.dtype:
+    dt = q.dtype
+    if q_out.dtype != dt or k.dtype != dt or v.dtype != dt:
         raise TypeError("q_out, q, k and v must have one dtype")
     if positions.dtype != torch.int32 or slot_mapping.dtype != torch.int64 or \
             cos_sin.dtype != torch.float32:
         raise TypeError("positions int32, slot_mapping int64 and cos_sin float32 expected")
-    if positions.numel() != T or slot_mapping.numel() != T or cos_sin.dim() != 2 or \
+    max_position, rot_dim = cos_sin.shape
+    if positions.numel() != T or slot_mapping.numel() != T or \
             not (positions.is_contiguous() and slot_mapping.is_contiguous() and
                  cos_sin.is_contiguous()):
         raise ValueError("positions [T], slot_mapping [T] and cos_sin [max_position][rot_dim], "
                          "contiguous, expected")
-    d = _desc(k_cache, k_scale, v_scale, q.dtype)
-    _check(lib().pa_rope_and_cache(_ptr(q_out), _ptr(q), _ptr(k), _ptr(v), dtype_code(q.dtype),
-                                   _token_stride(q_out, "q_out"), _token_stride(q, "q"),
-                                   _token_stride(k, "k"), _token_stride(v, "v"), _ptr(positions),
-                                   _ptr(cos_sin), cos_sin.shape[0], cos_sin.shape[1],
-                                   int(interleaved), _ptr(k_cache), _ptr(v_cache),
-                                   _ptr(slot_mapping), T, n_q, C.byref(d), _stream(stream)),
-           "pa_rope_and_cache")
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous()) or v_cache.dtype != k_cache.dtype \
+            or v_cache.numel() != k_cache.numel():
+        raise ValueError("contiguous pools of one dtype and size expected")
+    strides = (_token_stride(q_out, T, n_q, hd), _token_stride(q, T, n_q, hd),
+               _token_stride(k, T, n_kv, hd), _token_stride(v, T, n_kv, hd))
+    _check_device(q)
+    d = _desc(k_cache, k_scale, v_scale, dt)
+    st = lib().pa_rope_and_cache(
+        q_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), _DT[dt],
+        *strides, positions.data_ptr(), cos_sin.data_ptr(), max_position, rot_dim,
+        interleaved, k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), T, n_q,
+        C.byref(d), _stream(stream))
+    if st != PA_OK:
+        _check(st, "pa_rope_and_cache")
 
 
 def pa_rope_table(max_position: int, rot_dim: int, base: float = 10000.0) -> torch.Tensor:
@@ -313,19 +351,22 @@ def pa_decode_shared(out, q, k_cache, v_cache, block_tables, context_lens, group
     """pa_decode with the common prefix of each group of sequences read once: group_of_seq int32
     [B] (negative: none), prefix_lens int32 [groups], see pa_shared_prefix_groups."""
     B, n_q, _ = q.shape
+    groups = prefix_lens.numel()
     if group_of_seq.dtype != torch.int32 or prefix_lens.dtype != torch.int32:
         raise TypeError("group_of_seq and prefix_lens: int32 expected")
+    _attention_args(out, q, k_cache, v_cache, block_tables, context_lens, B)
     if group_of_seq.numel() != B or not group_of_seq.is_contiguous() or \
             not prefix_lens.is_contiguous():
         raise ValueError("group_of_seq [B] and prefix_lens [groups], contiguous, expected")
     d = _desc(k_cache, k_scale, v_scale, q.dtype)
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _check(lib().pa_decode_shared(_ptr(out), dtype_code(out.dtype), _ptr(q), _ptr(k_cache),
-                                  _ptr(v_cache), C.byref(d), _ptr(block_tables),
-                                  int(block_tables.shape[1]), _ptr(context_lens), B, n_q,
-                                  float(scale), int(block_size), _ptr(group_of_seq),
-                                  _ptr(prefix_lens), prefix_lens.numel(), _ptr(workspace), ws_bytes,
-                                  _stream(stream)), "pa_decode_shared")
+    ws, ws_bytes = (workspace.data_ptr(), workspace.nbytes) if workspace is not None else (None, 0)
+    st = lib().pa_decode_shared(
+        out.data_ptr(), dtype_code(out.dtype), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        C.byref(d), block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), B, n_q,
+        scale, block_size, group_of_seq.data_ptr(), prefix_lens.data_ptr(), groups, ws, ws_bytes,
+        _stream(stream))
+    if st != PA_OK:
+        _check(st, "pa_decode_shared")
 
 
 def pa_shared_prefix_groups(tables, lens, block_size: int, min_prefix_tokens: int = 0):
@@ -353,17 +394,18 @@ class ScoreMod:
     prefix_lens: torch.Tensor | None = None       # int32 [requests], prefill: keys every row sees
 
     def _c(self, n_q: int, rows: int, reqs: int) -> _ScoreMod:
-        for name, t, dt, n in (("alibi_slopes", self.alibi_slopes, torch.float32, n_q),
-                               ("first_key", self.first_key, torch.int32, rows),
-                               ("prefix_lens", self.prefix_lens, torch.int32, reqs)):
+        def array(name, t, dt, n):
             if t is None:
-                continue
+                return None
             if t.dtype != dt:
                 raise TypeError(f"{name}: {dt} expected")
             if t.numel() != n or not t.is_contiguous():
                 raise ValueError(f"{name}: {n} contiguous values expected")
-        return _ScoreMod(float(self.softcap), _ptr(self.alibi_slopes), int(self.window),
-                         _ptr(self.first_key), _ptr(self.prefix_lens))
+            return t.data_ptr()
+
+        return _ScoreMod(self.softcap, array("alibi_slopes", self.alibi_slopes, torch.float32, n_q),
+                         self.window, array("first_key", self.first_key, torch.int32, rows),
+                         array("prefix_lens", self.prefix_lens, torch.int32, reqs))
 
 
 def pa_decode_scored_workspace_size(num_seqs, q_per_seq, n_q_heads, n_kv_heads, head_dim,
@@ -377,16 +419,18 @@ def pa_decode_scored(out, q, k_cache, v_cache, block_tables, context_lens, mod: 
                      v_scale=None):
     """out, q [B][n_q][d] or [B][q_per_seq][n_q][d]: pa_decode / pa_decode_verify with capped or
     biased scores and masks (mod)."""
-    B, n_q = q.shape[0], q.shape[-2]
-    nq = q.shape[1] if q.dim() == 4 else 1
+    B, *nq, n_q, _ = q.shape
+    nq = nq[0] if nq else 1
+    _attention_args(out, q, k_cache, v_cache, block_tables, context_lens, B)
     d = _desc(k_cache, k_scale, v_scale, q.dtype)
     m = mod._c(n_q, B * nq, B)
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _check(lib().pa_decode_scored(_ptr(out), dtype_code(out.dtype), _ptr(q), _ptr(k_cache),
-                                  _ptr(v_cache), C.byref(d), _ptr(block_tables),
-                                  int(block_tables.shape[1]), _ptr(context_lens), B, nq, n_q,
-                                  float(scale), int(block_size), C.byref(m), _ptr(workspace),
-                                  ws_bytes, _stream(stream)), "pa_decode_scored")
+    ws, ws_bytes = (workspace.data_ptr(), workspace.nbytes) if workspace is not None else (None, 0)
+    st = lib().pa_decode_scored(
+        out.data_ptr(), dtype_code(out.dtype), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        C.byref(d), block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), B, nq, n_q,
+        scale, block_size, C.byref(m), ws, ws_bytes, _stream(stream))
+    if st != PA_OK:
+        _check(st, "pa_decode_scored")
 
 
 def pa_prefill_workspace_size(num_reqs, n_q_heads, head_dim, total_q) -> int:
@@ -415,16 +459,20 @@ def pa_prefill_scored(out, q, k_cache, v_cache, block_tables, query_start_loc, c
                       stream=None, k_scale=None, v_scale=None):
     """pa_prefill_chunk with capped or biased scores and masks (mod); first_key is [total_q],
     prefix_lens [R]."""
-    R = int(context_lens.shape[0])
-    total, n_q = q.shape[0], q.shape[1]
+    R = context_lens.numel()
+    total, n_q, _ = q.shape
+    _attention_args(out, q, k_cache, v_cache, block_tables, context_lens, R)
+    if query_start_loc.dtype != torch.int32 or query_start_loc.numel() != R + 1 or \
+            not query_start_loc.is_contiguous():
+        raise ValueError("query_start_loc int32 [R + 1], contiguous, expected")
     d = _desc(k_cache, k_scale, v_scale, q.dtype)
     m = mod._c(n_q, total, R)
-    _check(lib().pa_prefill_scored(_ptr(out), dtype_code(out.dtype), _ptr(q), _ptr(k_cache),
-                                   _ptr(v_cache), C.byref(d), _ptr(block_tables),
-                                   int(block_tables.shape[1]), _ptr(query_start_loc),
-                                   _ptr(context_lens), R, int(max_query_len), n_q, float(scale),
-                                   int(block_size), C.byref(m), _stream(stream)),
-           "pa_prefill_scored")
+    st = lib().pa_prefill_scored(
+        out.data_ptr(), dtype_code(out.dtype), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        C.byref(d), block_tables.data_ptr(), block_tables.shape[1], query_start_loc.data_ptr(),
+        context_lens.data_ptr(), R, max_query_len, n_q, scale, block_size, C.byref(m), _stream(stream))
+    if st != PA_OK:
+        _check(st, "pa_prefill_scored")
 
 
 def pa_copy_blocks(k_cache, v_cache, block_mapping, stream=None):

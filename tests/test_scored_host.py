@@ -2,6 +2,7 @@
 import ctypes as C
 
 import pytest
+import torch
 
 from paged_kv_cache_25_gb300 import binding as pa
 from paged_kv_cache_25_gb300 import build
@@ -88,3 +89,35 @@ def test_prefill_refusals():
     assert _prefill(n_q=30) == pa.PA_ERR_INVALID_ARG
     assert _prefill(reqs=0) == pa.PA_OK
     assert _prefill(max_q=0) == pa.PA_OK
+
+
+def test_bindings_check_layouts_and_types():
+    """The scored and shared-prefix bindings refuse what the library would misread."""
+    q = torch.zeros(2, 4, 64, dtype=torch.bfloat16)
+    kc = torch.zeros(8, 2, 16, 64, dtype=torch.bfloat16)
+    bt, cl = torch.zeros(2, 3, dtype=torch.int32), torch.ones(2, dtype=torch.int32)
+    base = dict(out=q, q=q, k_cache=kc, v_cache=kc, block_tables=bt, context_lens=cl, scale=0.1,
+                block_size=16)
+    qs = torch.zeros(3, dtype=torch.int32)
+    calls = [lambda **k: pa.pa_decode_scored(mod=pa.ScoreMod(), **{**base, **k}),
+             lambda **k: pa.pa_decode_shared(group_of_seq=cl, prefix_lens=cl, **{**base, **k}),
+             lambda **k: pa.pa_prefill_scored(mod=pa.ScoreMod(), query_start_loc=qs, max_query_len=1,
+                                              **{**base, **k})]
+    for call in calls:
+        for change, err in [(dict(q=q.transpose(0, 1).contiguous().transpose(0, 1)), ValueError),
+                            (dict(q=q.half()), TypeError), (dict(out=q[:1]), ValueError),
+                            (dict(block_tables=bt.long()), TypeError),
+                            (dict(context_lens=cl.long()), TypeError),
+                            (dict(block_tables=bt.T.contiguous().T), ValueError),
+                            (dict(block_tables=bt[:1]), ValueError),
+                            (dict(v_cache=kc.half()), TypeError),
+                            (dict(k_cache=kc[:, :, :, :32]), ValueError),
+                            (dict(v_cache=kc[:4]), ValueError)]:
+            with pytest.raises(err):
+                call(**change)
+    with pytest.raises(ValueError):
+        pa.pa_prefill_scored(mod=pa.ScoreMod(), query_start_loc=qs[:2], max_query_len=1, **base)
+    with pytest.raises(TypeError):
+        pa.pa_decode_shared(group_of_seq=cl.long(), prefix_lens=cl, **base)
+    with pytest.raises(ValueError):
+        pa.pa_decode_shared(group_of_seq=cl[:1], prefix_lens=cl, **base)
