@@ -300,7 +300,7 @@ int pa_shared_prefix_groups(const int32_t* tables, int max_blocks, const int32_t
  * blocks in which no row sees a key are never read (blocks behind a window may have been
  * freed); a key that some row sees must be finite for the others. */
 typedef struct {
-    float softcap;              /* > 0: cap; 0: none (negative or not finite: refused)       */
+    float softcap;              /* in [0.125, 1e6]: cap; 0: none (others are refused)          */
     const float* alibi_slopes;  /* device fp32 [n_q_heads] (linear distance bias), or NULL    */
     int window;                 /* > 0: row i sees no key before i - window + 1; 0: no window */
     const int32_t* first_key;   /* device int32, one per query row in the order of q's rows   */

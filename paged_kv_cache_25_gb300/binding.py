@@ -181,8 +181,8 @@ def _attention_args(out, q, k_cache, v_cache, block_tables, context_lens, seqs: 
         raise ValueError("contiguous tensors expected")
     if out.shape != q.shape or q.shape[-1] != k_cache.shape[3] or v_cache.numel() != k_cache.numel():
         raise ValueError("out and q [..][n_q][d] and pools of that head_dim expected")
-    if block_tables.shape[0] != seqs or context_lens.numel() != seqs:
-        raise ValueError("one block table and one context length a sequence expected")
+    if block_tables.shape[0] < seqs or context_lens.numel() < seqs:
+        raise ValueError("a block table and a context length for every sequence expected")
     if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
         raise TypeError("block_tables and context_lens: int32 expected")
     kv = k_cache.dtype
@@ -354,10 +354,10 @@ def pa_decode_shared(out, q, k_cache, v_cache, block_tables, context_lens, group
     groups = prefix_lens.numel()
     if group_of_seq.dtype != torch.int32 or prefix_lens.dtype != torch.int32:
         raise TypeError("group_of_seq and prefix_lens: int32 expected")
-    _attention_args(out, q, k_cache, v_cache, block_tables, context_lens, B)
     if group_of_seq.numel() != B or not group_of_seq.is_contiguous() or \
             not prefix_lens.is_contiguous():
         raise ValueError("group_of_seq [B] and prefix_lens [groups], contiguous, expected")
+    _attention_args(out, q, k_cache, v_cache, block_tables, context_lens, B)
     d = _desc(k_cache, k_scale, v_scale, q.dtype)
     ws, ws_bytes = (workspace.data_ptr(), workspace.nbytes) if workspace is not None else (None, 0)
     st = lib().pa_decode_shared(
@@ -461,10 +461,10 @@ def pa_prefill_scored(out, q, k_cache, v_cache, block_tables, query_start_loc, c
     prefix_lens [R]."""
     R = context_lens.numel()
     total, n_q, _ = q.shape
-    _attention_args(out, q, k_cache, v_cache, block_tables, context_lens, R)
     if query_start_loc.dtype != torch.int32 or query_start_loc.numel() != R + 1 or \
             not query_start_loc.is_contiguous():
         raise ValueError("query_start_loc int32 [R + 1], contiguous, expected")
+    _attention_args(out, q, k_cache, v_cache, block_tables, context_lens, R)
     d = _desc(k_cache, k_scale, v_scale, q.dtype)
     m = mod._c(n_q, total, R)
     st = lib().pa_prefill_scored(

@@ -173,9 +173,11 @@ decode_merge_kernel(void* __restrict__ out, pa_dtype out_dtype,
     if (!member && J <= 1) return;                       // finished by the partial kernel
     const int P = member ? __ldg(sc.group_splits + __ldg(sc.group_of_seq + s)) : 0;
     // partial i of P + J: slot i of the prefix pass's, or partition i - P
-    auto slot = [&](int i) { return sh * sc.slots + (i < P ? i : sc.slot0 + i - P); };
+    const int n = P + J;
+    const float* ml = ws_ml + 2 * sh * sc.slots;
+    auto slot = [&](int i) { return i < P ? i : sc.slot0 + i - P; };
     float M = -INFINITY;
-    for (int i = lane; i < P + J; i += 32) M = fmaxf(M, ws_ml[2 * slot(i)]);
+    for (int i = lane; i < n; i += 32) M = fmaxf(M, ml[2 * slot(i)]);
 #pragma unroll
     for (int w = 16; w > 0; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
     const float M_use = M == -INFINITY ? 0.f : M;
@@ -183,12 +185,24 @@ decode_merge_kernel(void* __restrict__ out, pa_dtype out_dtype,
     float acc[DPL];
 #pragma unroll
     for (int i = 0; i < DPL; ++i) acc[i] = 0.f;
-    for (int j = 0; j < P + J; ++j) {
-        const int64_t u = slot(j);
-        const float w = exp2f(ws_ml[2 * u] - M_use);
-        lsum += w * ws_ml[2 * u + 1];
+    const float* a = ws_acc + sh * sc.slots * D;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        // this lane's partial of the next 32: its weight 2^(m - M) and its sum
+        float w = 0.f, l = 0.f;
+        if (i0 + lane < n) {
+            const float2 p = *reinterpret_cast<const float2*>(ml + 2 * slot(i0 + lane));
+            w = exp2f(p.x - M_use);
+            l = p.y;
+        }
+        const int todo = min(32, n - i0);
+#pragma unroll 4
+        for (int j = 0; j < todo; ++j) {
+            const float wj = __shfl_sync(0xffffffffu, w, j);
+            lsum += wj * __shfl_sync(0xffffffffu, l, j);   // in the order of decode_reduce_kernel
+            const float* r = a + static_cast<int64_t>(slot(i0 + j)) * D + lane;
 #pragma unroll
-        for (int i = 0; i < DPL; ++i) acc[i] = fmaf(w, ws_acc[u * D + lane + 32 * i], acc[i]);
+            for (int i = 0; i < DPL; ++i) acc[i] = fmaf(wj, r[32 * i], acc[i]);
+        }
     }
     const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
 #pragma unroll

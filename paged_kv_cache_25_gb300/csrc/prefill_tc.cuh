@@ -966,21 +966,27 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         const int warp_min_pos = MODE != 0 ? __reduce_min_sync(0xffffffffu, p_abs)
                                            : (wrow < rows_total ? ctx0 + wrow / group : L - 1);
         const int warp_max_lo = MODE != 0 ? __reduce_max_sync(0xffffffffu, p_lo) : 0;
-        // modified scores (log2 domain): the cap's exponent rate on a raw score, the
-        // row's slope, and d = key - position for the bias -slope * |d|
-        float cap_raw = 0.f, cap2 = 0.f, slope2 = 0.f;
-        if constexpr (kCap) {
-            cap2 = sc.cap2;
-            cap_raw = scale_log2 * sc.cap_rate;
-        }
+        // modified scores (log2 domain): the cap, the row's slope, and d = key -
+        // position for the bias -slope * |d|
+        [[maybe_unused]] CapForm cap;
+        float slope2 = 0.f;
+        if constexpr (kCap) cap = cap_form(sc.cap2, sc.cap_rate, scale_log2);
         if constexpr (kBias) slope2 = __ldg(sc.slopes + head) * kLog2e;
         const int q_pos = ctx0 + pos_local;
-        // modified score minus a reference (neg_ref = -reference)
-        auto modified = [&](float s, float d, float neg_ref) -> float {
-            float z = kCap ? fmaf(-2.f * cap2, fast_rcp(1.f + fast_exp2(s * cap_raw)), cap2 + neg_ref)
-                           : fmaf(s, scale_log2, neg_ref);
-            if constexpr (kBias) z = fmaf(-slope2, fabsf(d), z);
-            return z;
+        // modified scores of keys d .. d + 3 past the position, minus a reference
+        // (neg_ref = -reference); clamp: see soft_cap4
+        using Clamp = std::true_type;
+        auto modified4 = [&](auto clamp, const float (&s)[4], float d, float neg_ref, float (&z)[4]) {
+            if constexpr (kCap) {
+                soft_cap4<decltype(clamp)::value>(cap, s, neg_ref, z);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) z[i] = fmaf(s[i], scale_log2, neg_ref);
+            }
+            if constexpr (kBias) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) z[i] = fmaf(-slope2, fabsf(d + i), z[i]);
+            }
         };
         const float unit_log2 = kZ ? 1.f : scale_log2;   // log2 units of the running maximum
         float m_raw = -INFINITY, l = 0.f;
@@ -1006,11 +1012,19 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                 tmem_ld_wait();
                 if constexpr (kBias) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const float za = modified(__uint_as_float(sa[i]), d0 + i, 0.f);
-                        const float zb = modified(__uint_as_float(sb[i]), d0 + (32 + i), 0.f);
-                        if (full_tile || sees(hkey0 + i)) m4[i & 3] = fmaxf(m4[i & 3], za);
-                        if (full_tile || sees(hkey0 + 32 + i)) m4[i & 3] = fmaxf(m4[i & 3], zb);
+                    for (int i = 0; i < 32; i += 4) {
+                        const float s0[4] = {__uint_as_float(sa[i]), __uint_as_float(sa[i + 1]),
+                                             __uint_as_float(sa[i + 2]), __uint_as_float(sa[i + 3])};
+                        const float s1[4] = {__uint_as_float(sb[i]), __uint_as_float(sb[i + 1]),
+                                             __uint_as_float(sb[i + 2]), __uint_as_float(sb[i + 3])};
+                        float za[4], zb[4];
+                        modified4(Clamp{}, s0, d0 + i, 0.f, za);
+                        modified4(Clamp{}, s1, d0 + (32 + i), 0.f, zb);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            if (full_tile || sees(hkey0 + i + e)) m4[e] = fmaxf(m4[e], za[e]);
+                            if (full_tile || sees(hkey0 + 32 + i + e)) m4[e] = fmaxf(m4[e], zb[e]);
+                        }
                     }
                 } else if (full_tile) {
 #pragma unroll
@@ -1030,7 +1044,14 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             named_bar_sync(bar_id, 64);
             mx = fmaxf(mx, xmax[j & 1][t][hf ^ 1][rr]);
             // the cap is monotone: the largest capped score is the capped largest
-            if constexpr (kCap && !kBias) mx = mx == -INFINITY ? mx : modified(mx, 0.f, 0.f);
+            bool open = true;   // kCap: no score of these rows needs the clamp
+            if constexpr (kCap && !kBias) {
+                open = __all_sync(0xffffffffu, mx * cap.rate <= kCapExp);
+                const float s[4] = {mx, mx, mx, mx};
+                float z[4];
+                soft_cap4<true>(cap, s, 0.f, z);
+                mx = mx == -INFINITY ? mx : z[0];
+            }
             stop = stop || !ok || xstop[j & 1][t][hf ^ 1][rr] != 0;
             if (__any_sync(0xffffffffu, stop)) {   // the partner warp sees the same flags
                 quit = true;
@@ -1071,7 +1092,8 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                 tmem_ld32(lane_addr + s_col + h2 * 32, sr);
                 tmem_ld_wait();
                 uint32_t ph[16], pl[16];
-                if (full_tile) {
+                float z[4];   // modified scores of two neighbouring pairs of keys
+                auto full = [&](auto clamp) {
                     // pairs of keys in paired fp32 instructions: the exponent's
                     // argument, the row sum and P's lo residual
                     const float2 c2 = make_float2(scale_log2, scale_log2), n2 = make_float2(neg_mc, neg_mc);
@@ -1079,8 +1101,12 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                     for (int i = 0; i < 16; ++i) {
                         float2 x;
                         if constexpr (kZ) {
-                            x.x = modified(__uint_as_float(sr[2 * i]), d0 + (h2 * 32 + 2 * i), neg_mc);
-                            x.y = modified(__uint_as_float(sr[2 * i + 1]), d0 + (h2 * 32 + 2 * i + 1), neg_mc);
+                            if (i % 2 == 0) {
+                                const float s[4] = {__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1]),
+                                                    __uint_as_float(sr[2 * i + 2]), __uint_as_float(sr[2 * i + 3])};
+                                modified4(clamp, s, d0 + (h2 * 32 + 2 * i), neg_mc, z);
+                            }
+                            x = make_float2(z[2 * (i % 2)], z[2 * (i % 2) + 1]);
                         } else {
                             x = fma2(make_float2(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1])),
                                      c2, n2);
@@ -1099,13 +1125,22 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                             pl[i] = Cvt<T>::pack(r.x, r.y);
                         }
                     }
+                };
+                if (full_tile && open) {
+                    full(std::bool_constant<kBias>{});
+                } else if (full_tile) {
+                    full(std::true_type{});
                 } else {   // masked keys give exactly 0 (even with scale 0, where -inf * 0 is NaN)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const int k = hkey0 + h2 * 32 + 2 * i;
-                        const float d = d0 + (h2 * 32 + 2 * i);
-                        const float p0 = sees(k) ? fast_exp2(modified(__uint_as_float(sr[2 * i]), d, neg_mc)) : 0.f;
-                        const float p1 = sees(k + 1) ? fast_exp2(modified(__uint_as_float(sr[2 * i + 1]), d + 1.f, neg_mc)) : 0.f;
+                        if (i % 2 == 0) {
+                            const float s[4] = {__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1]),
+                                                __uint_as_float(sr[2 * i + 2]), __uint_as_float(sr[2 * i + 3])};
+                            modified4(Clamp{}, s, d0 + (h2 * 32 + 2 * i), neg_mc, z);
+                        }
+                        const float p0 = sees(k) ? fast_exp2(z[2 * (i % 2)]) : 0.f;
+                        const float p1 = sees(k + 1) ? fast_exp2(z[2 * (i % 2) + 1]) : 0.f;
                         s4[i & 3] += p0 + p1;
                         if constexpr (kOneP) ph[i] = Cvt<__half>::pack(p0, p1);
                         else split_trunc<T>(p0, p1, ph[i], pl[i]);

@@ -32,6 +32,60 @@ __device__ __forceinline__ float soft_cap(float z, float cap2, float cap_rate)
     return fmaf(-2.f * cap2, fast_rcp(1.f + fast_exp2(z * cap_rate)), cap2);
 }
 
+// The prefill's form of the cap, for four raw scores of a row at a time: with
+// t_i = 1 + 2^(rate s_i) and h = -1 / (2C), z_i = C + 1 / (h t_i), and the four quotients
+// share one reciprocal, r = 1 / (h t_0 h t_1 h t_2 h t_3).  The prefill's softmax is bound by
+// its instructions and, with three results of the exponent unit a score (16 results a
+// cycle and SM), by that unit; sharing leaves 2.25 results.  Mixed step's four chunks
+// (bf16 / fp16 / FP8 pool): 284 / 256 / 267 us with a reciprocal each, 257 / 221 / 232 with
+// one for two, 251 / 210 / 217 with one for four (193 / 153 / 149 without a cap).  Also
+// measured: tanh as a rational function of degree 7/6 on the FMA pipe (330 / 286 / 301),
+// and a polynomial for |x| < 3/4 behind a vote on the largest |score| (258 / 212 / 226).
+// CLAMP keeps the exponents within +-kCapExp, so that the product cannot overflow (past
+// it tanh is 1 to 2^-kCapExp) and a NaN, which a masked key's score may be, becomes the
+// lower bound; without it the caller has checked the row's largest exponent.  (C is at
+// least 0.18, so h^4 2^(4 kCapExp) stays below 2^126.)
+struct CapForm {
+    float rate;           // log2 of e^(2 x) for a raw score of 1
+    float cap2, h;
+};
+constexpr float kCapExp = 30.f;
+
+// scale_log2: log2-domain scale of the row's raw scores
+__device__ __forceinline__ CapForm cap_form(float cap2, float cap_rate, float scale_log2)
+{
+    CapForm f;
+    f.rate = scale_log2 * cap_rate;
+    f.cap2 = cap2;
+    f.h = -0.5f / cap2;
+    return f;
+}
+
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// z[i] = C tanh(x_i) + add
+template <bool CLAMP>
+__device__ __forceinline__ void soft_cap4(const CapForm& f, const float (&s)[4], float add, float (&z)[4])
+{
+    const float top = f.cap2 + add;
+    float2 t[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        float2 e;
+        if constexpr (CLAMP) {
+            e.x = fminf(fmaxf(s[2 * i] * f.rate, -kCapExp), kCapExp);
+            e.y = fminf(fmaxf(s[2 * i + 1] * f.rate, -kCapExp), kCapExp);
+        } else {
+            e = fma2(make_float2(s[2 * i], s[2 * i + 1]), both(f.rate), both(0.f));
+        }
+        t[i] = fma2(make_float2(fast_exp2(e.x), fast_exp2(e.y)), both(f.h), both(f.h));
+    }
+    const float qa = t[0].x * t[0].y, qb = t[1].x * t[1].y;
+    const float r = fast_rcp(qa * qb), ra = r * qb, rb = r * qa;   // 1 / qa, 1 / qb
+    z[0] = fmaf(ra, t[0].y, top); z[1] = fmaf(ra, t[0].x, top);
+    z[2] = fmaf(rb, t[1].y, top); z[3] = fmaf(rb, t[1].x, top);
+}
+
 // Tokens of group g's prefix, in whole blocks.
 __device__ __forceinline__ int prefix_tokens(const int32_t* group_prefix, int g, int block_size, int max_blocks)
 {

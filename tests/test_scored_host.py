@@ -53,9 +53,11 @@ def test_decode_refusals():
 def test_a_window_bounds_the_workspace():
     size = pa.pa_decode_scored_workspace_size
     assert size(256, 1, 32, 8, 128, 16, 65536) == pa.pa_decode_workspace_size(256, 32, 8, 128, 16, 65536)
-    # 1024 + 15 tokens of the first block at most: two partitions of 1024
-    w = size(256, 1, 32, 8, 128, 16, 65536, 1024)
-    assert 256 < w < size(256, 1, 32, 8, 128, 16, 65536) // 16
+    # 1024 + 15 tokens of the first block at most: one partition, no partials
+    assert size(256, 1, 32, 8, 128, 16, 65536, 1024) == 256
+    # 2999 + 15 tokens: three partitions
+    w = size(256, 1, 32, 8, 128, 16, 65536, 2999)
+    assert 256 + 256 * 32 * 3 * 130 * 4 <= w < size(256, 1, 32, 8, 128, 16, 65536) // 16
     assert size(256, 4, 32, 8, 128, 16, 4096) == pa.pa_decode_verify_workspace_size(256, 4, 32, 8, 128, 16, 4096)
     assert size(256, 1, 32, 8, 128, 16, 4096, -1) == 0
     assert size(0, 1, 32, 8, 128, 16, 4096, 0) == 0
