@@ -190,8 +190,13 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // launched as a programmatic dependent: every input may come from the
-    // kernel before this one in the stream
-    grid_dependency_wait();
+    // kernel before this one in the stream.  The sequences' own part of a shared
+    // decode follows the prefix pass, of which it needs nothing (and what it reads was
+    // written before that pass began): it runs beside it, on SMs that the pass leaves
+    // free, and waits at its end, so that the merge after it finds both done.
+    bool beside = false;
+    if constexpr (SC) beside = sc.group_of_seq != nullptr;
+    if (!beside) grid_dependency_wait();
     // a KV head serves group x nq rows (head-major: row = head * nq + query),
     // taken RU at a time; plain decode (MQ false) has nq = 1 at compile time
     const int nq = MQ ? nq_arg : 1;
@@ -257,7 +262,8 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 
     // Units are handed out dynamically: unit blockIdx.x first, then tickets
     // from a counter that starts at zero for every launch (or, for batches of
-    // at most a few units per CTA, round robin with no counter).  Work for the next
+    // at most a few units per CTA, round robin with no counter; beside a prefix
+    // pass, whose SMs come free late, the first unit is a ticket too).  Work for the next
     // unit overlaps the current one: its ticket is drawn one unit ahead, its
     // block ids are loaded (one per thread) while the current unit streams,
     // its q fragments while the current unit's warps combine, and - when the
@@ -493,7 +499,17 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 
     // ---- the first unit: ids checked before any load is issued
     int64_t u = blockIdx.x;
-    if (u >= units) return;                           // uniform over the CTA
+    if (beside) {
+        if (tid == 0) s_next = atomicAdd(ticket, 1u);
+        __syncthreads();
+        u = s_next;
+        __syncthreads();
+    }
+    const int64_t dealt = beside ? 0 : static_cast<int64_t>(gridDim.x);   // units dealt without a ticket
+    if (u >= units) {                                 // uniform over the CTA
+        if (beside) grid_dependency_wait();
+        return;
+    }
     Unit cu = describe(u);
     {
         int bad = 0;
@@ -501,8 +517,7 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         load_q(cu);
         const int any_bad = __syncthreads_or(bad);
         if (tid == 0)
-            s_next = ticket ? static_cast<long long>(gridDim.x) + atomicAdd(ticket, 1u)
-                            : u + static_cast<long long>(gridDim.x);
+            s_next = ticket ? dealt + atomicAdd(ticket, 1u) : u + static_cast<long long>(gridDim.x);
         cu.live = cu.live && !any_bad;
         __syncthreads();
     }
@@ -932,10 +947,9 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         }
         // every ring is idle and (separate buffer) the partials are written
         const int flags = __syncthreads_or(timed_out | (nb_bad << 1));
-        if (flags & 1) return;
+        if (flags & 1) break;
         if (tid == 0)
-            s_next = ticket ? static_cast<long long>(gridDim.x) + atomicAdd(ticket, 1u)
-                            : un + static_cast<long long>(gridDim.x);
+            s_next = ticket ? dealt + atomicAdd(ticket, 1u) : un + static_cast<long long>(gridDim.x);
         // this CTA's last unit: the kernel after this one may be scheduled now
         if (un >= units) allow_dependent_launch();
         const bool next_live = nx.live && !(flags & 2);
@@ -998,6 +1012,7 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         cu.live = next_live;
         cb ^= 1;
     }
+    if (beside) grid_dependency_wait();
 }
 
 template <bool SC>
@@ -1065,7 +1080,10 @@ cudaError_t run_mma(const DecodeArgs& a, cudaStream_t s, float scale_log2)
     // with every sequence at the longest length) are dealt round robin: no
     // counter to clear, so no memset before the launch
     unsigned* ticket = upper <= kStaticUnitsPerCta * resident ? nullptr : a.ticket;
-    if (ticket) {
+    bool beside = false;   // a prefix pass: it goes before, and the counter was cleared before it
+    if constexpr (SC) beside = a.score->group_of_seq != nullptr;
+    if (beside) ticket = a.ticket;
+    if (ticket && !beside) {
         const cudaError_t e0 = cudaMemsetAsync(ticket, 0, sizeof(unsigned), s);
         if (e0 != cudaSuccess) return e0;
     }
@@ -1081,7 +1099,7 @@ cudaError_t run_mma(const DecodeArgs& a, cudaStream_t s, float scale_log2)
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = ticket ? 0 : 1;
+    cfg.numAttrs = ticket && !beside ? 0 : 1;
     return cudaLaunchKernelEx(
         &cfg, kern, kmap, vmap, static_cast<const uint8_t*>(a.v_cache), a.out, a.out_dtype,
         static_cast<const QT*>(a.q), a.block_tables, a.max_blocks, a.context_lens, a.num_seqs,

@@ -312,6 +312,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     __shared__ std::conditional_t<kShared, PrefixUnit, NoScore> s_unit;
     __shared__ int s_member[kShared ? kUnitMembers : 1];
     if constexpr (kShared) {
+        allow_dependent_launch();   // the sequences' own part may start beside this pass
         plan_prefix_unit(sc, sp, n_kv, group, BS, max_blocks, reinterpret_cast<int*>(dyn_smem), s_member,
                          &s_unit, err);
         if (!s_unit.live) return;

@@ -58,9 +58,13 @@ static cudaError_t run_prefix_dt(const DecodeArgs& a, const PrefixPass& p, cudaS
 cudaError_t launch_prefix_pass(const DecodeArgs& a, const PrefixPass& pass, cudaStream_t s)
 {
     const float sl2 = a.scale * kLog2e;
+    // the work counter of the decode kernel that follows: nothing may come between
+    // the two launches
+    cudaError_t e = cudaMemsetAsync(a.ticket, 0, sizeof(unsigned), s);
+    if (e != cudaSuccess) return e;
     PrefixPass p = pass;
     int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&p.target, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
     if (a.cache.dtype == PA_BF16) return run_prefix_dt<__nv_bfloat16, __nv_bfloat16, false>(a, p, s, sl2);
