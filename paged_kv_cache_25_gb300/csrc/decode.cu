@@ -160,18 +160,24 @@ decode_merge_kernel(void* __restrict__ out, pa_dtype out_dtype,
                     const __grid_constant__ ScoreParams sc)
 {
     constexpr int D = DPL * 32;
+    constexpr int V = DPL % 4 == 0 ? 4 : (DPL % 2 == 0 ? 2 : 1);   // floats of a load
+    using Vec = std::conditional_t<V == 4, float4, std::conditional_t<V == 2, float2, float>>;
     const int lane = threadIdx.x & 31;
-    grid_dependency_wait();   // launched as a programmatic dependent of the partial kernel
     const int64_t sh = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    if (sh >= static_cast<int64_t>(num_seqs) * nq * n_q) return;
-    const int s = static_cast<int>(sh / (static_cast<int64_t>(nq) * n_q));
+    const bool mine = sh < static_cast<int64_t>(num_seqs) * nq * n_q;
+    // the call's inputs, read before the wait: this kernel is a programmatic dependent of
+    // the partial kernel, whose blocks let it start only after their own wait, so
+    // whatever wrote the inputs has completed
+    const int s = mine ? static_cast<int>(sh / (static_cast<int64_t>(nq) * n_q)) : 0;
     const int L = __ldg(context_lens + s);
-    if (L < nq) return;                                  // nothing of such a sequence is written
     const int lo = first_visible(sc, s, L, nq, block_size, max_blocks, err);
     const int J = min((L - lo / block_size * block_size + part_tokens - 1) / part_tokens, max_parts);
     const bool member = sc.group_of_seq != nullptr && lo > 0;
+    const int g = member ? __ldg(sc.group_of_seq + s) : 0;
+    grid_dependency_wait();                              // the partials are written
+    if (!mine || L < nq) return;                         // (nothing of a sequence below nq is written)
     if (!member && J <= 1) return;                       // finished by the partial kernel
-    const int P = member ? __ldg(sc.group_splits + __ldg(sc.group_of_seq + s)) : 0;
+    const int P = member ? sc.group_splits[g] : 0;
     // partial i of P + J: slot i of the prefix pass's, or partition i - P
     const int n = P + J;
     const float* ml = ws_ml + 2 * sh * sc.slots;
@@ -182,10 +188,10 @@ decode_merge_kernel(void* __restrict__ out, pa_dtype out_dtype,
     for (int w = 16; w > 0; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
     const float M_use = M == -INFINITY ? 0.f : M;
     float lsum = 0.f;
-    float acc[DPL];
+    float acc[DPL];                                      // [DPL / V] runs of V elements
 #pragma unroll
     for (int i = 0; i < DPL; ++i) acc[i] = 0.f;
-    const float* a = ws_acc + sh * sc.slots * D;
+    const float* a = ws_acc + sh * sc.slots * D + V * lane;
     for (int i0 = 0; i0 < n; i0 += 32) {
         // this lane's partial of the next 32: its weight 2^(m - M) and its sum
         float w = 0.f, l = 0.f;
@@ -195,18 +201,24 @@ decode_merge_kernel(void* __restrict__ out, pa_dtype out_dtype,
             l = p.y;
         }
         const int todo = min(32, n - i0);
-#pragma unroll 4
+#pragma unroll 8
         for (int j = 0; j < todo; ++j) {
             const float wj = __shfl_sync(0xffffffffu, w, j);
             lsum += wj * __shfl_sync(0xffffffffu, l, j);   // in the order of decode_reduce_kernel
-            const float* r = a + static_cast<int64_t>(slot(i0 + j)) * D + lane;
+            const float* r = a + static_cast<int64_t>(slot(i0 + j)) * D;
 #pragma unroll
-            for (int i = 0; i < DPL; ++i) acc[i] = fmaf(wj, r[32 * i], acc[i]);
+            for (int i = 0; i < DPL / V; ++i) {
+                const Vec x = *reinterpret_cast<const Vec*>(r + 32 * V * i);
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    acc[V * i + e] = fmaf(wj, reinterpret_cast<const float*>(&x)[e], acc[V * i + e]);
+            }
         }
     }
     const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
 #pragma unroll
-    for (int i = 0; i < DPL; ++i) store_any(out, sh * D + lane + 32 * i, acc[i] * inv, out_dtype);
+    for (int i = 0; i < DPL; ++i)
+        store_any(out, sh * D + (i / V * 32 + lane) * V + i % V, acc[i] * inv, out_dtype);
 }
 
 // Second pass, one warp per (sequence, query head):

@@ -178,7 +178,7 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     static_assert(BS % kRows == 0, "block_size must be a multiple of 16");
 
     __shared__ int s_prefix[kPrefixCap];
-    __shared__ int s_scan[kDecWarps * 32];
+    __shared__ int s_scan[kDecWarps];
     __shared__ int s_blk[2][kMaxPartBlocks];   // this unit's and the next unit's block ids
     __shared__ int s_total;
     __shared__ long long s_next;
@@ -225,19 +225,17 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             s_prefix[i] = p;
             local += p;
         }
-        s_scan[tid] = local;
-        __syncthreads();
-        if (tid == 0) {
-            int acc = 0;
-            for (int i = 0; i < kDecWarps * 32; ++i) {
-                const int v = s_scan[i];
-                s_scan[i] = acc;
-                acc += v;
-            }
-            s_total = acc;                  // full partitions
+        int run = local;                    // inclusive over the warp, then exclusive over the block
+#pragma unroll
+        for (int w = 1; w < 32; w <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, run, w);
+            if (lane >= w) run += up;
         }
+        if (lane == 31) s_scan[warp] = run;
         __syncthreads();
-        int run = s_scan[tid];
+        run -= local;
+        for (int i = 0; i < warp; ++i) run += s_scan[i];
+        if (tid == kDecWarps * 32 - 1) s_total = run + local;   // full partitions
         for (int i = b0; i < b1; ++i) {
             run += s_prefix[i];
             s_prefix[i] = run;
@@ -499,8 +497,8 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 
     // ---- the first unit: ids checked before any load is issued
     int64_t u = blockIdx.x;
-    if (beside) {
-        if (tid == 0) s_next = atomicAdd(ticket, 1u);
+    if (beside) {                                     // the first unit and the next one
+        if (tid == 0) s_next = atomicAdd(ticket, 2u);
         __syncthreads();
         u = s_next;
         __syncthreads();
@@ -517,7 +515,7 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         load_q(cu);
         const int any_bad = __syncthreads_or(bad);
         if (tid == 0)
-            s_next = ticket ? dealt + atomicAdd(ticket, 1u) : u + static_cast<long long>(gridDim.x);
+            s_next = beside ? u + 1 : ticket ? dealt + atomicAdd(ticket, 1u) : u + static_cast<long long>(gridDim.x);
         cu.live = cu.live && !any_bad;
         __syncthreads();
     }

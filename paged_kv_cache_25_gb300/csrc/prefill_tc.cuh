@@ -203,6 +203,21 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t
                  : "memory");
 }
 
+// Bulk copy of `bytes` contiguous bytes shared -> global (both 16-byte aligned, bytes a
+// multiple of 16) by this thread, and the wait for all of its copies.
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes)
+{
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+                     reinterpret_cast<uint64_t>(dst)),
+                 "r"(src), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_store_wait()
+{
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
 template <typename T>
 __device__ __forceinline__ void store_row(void* out, int64_t base, int col, const float* v, int n,
                                           pa_dtype dt)
@@ -286,6 +301,10 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     constexpr bool kBq = std::is_same<QT, __nv_bfloat16>::value;
     using Ly = PfLayout<T, D, F8, kBq>;
     using Wp = PfWarps<F8, D, kBq>;
+    // kShared: bytes of an O row staged in shared memory (16 more, so that the rows of
+    // eight threads storing together lie in different banks)
+    constexpr uint32_t kORow = D * 4 + 16;
+    static_assert(!kShared || kTcTiles * kTcRows * kORow <= Ly::kDynBytes - 1024, "O rows fit");
     constexpr bool kDirectK = Ly::kDirectK;
     constexpr int kMmaWarp = Wp::kMma;
     constexpr int kFirstConv = Wp::kFirstConverter;
@@ -302,6 +321,50 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     constexpr uint32_t kIdescPV = idesc_f16(kBf16, false, !F8, kTcRows, D);
     static_assert(BS % 16 == 0 && kTcKeys % BS == 0, "block size must divide the key tile");
 
+    // Every barrier below is waited on in completion order and its waiter is
+    // never two phases behind: S_t(j + 1) is issued after P_t(j) V, which
+    // waits for P_t(j), which needs S_t(j).
+    __shared__ __align__(8) uint64_t k_full[kTcStages], k_empty[kTcStages];
+    __shared__ __align__(8) uint64_t v_full[kTcStages], v_empty[kTcStages];
+    __shared__ __align__(8) uint64_t s_full[kTcTiles], p_full[kTcTiles], pv_done[kTcTiles], q_ready;
+    __shared__ __align__(8) uint64_t code_full[kF8MaxConverters][kF8MaxDepth];   // FP8: codes landed, per converter and buffer
+    __shared__ uint32_t s_tmem;
+    // partial row maxima of the two threads of a row (double-buffered by key
+    // tile), a "stop" flag beside each, and the partial row sums at the end
+    __shared__ float xmax[2][kTcTiles][2][kTcRows];
+    __shared__ uint8_t xstop[2][kTcTiles][2][kTcRows];
+    __shared__ float xsum[kTcTiles][2][kTcRows];
+    __shared__ uint8_t xstop_end[kTcTiles][2][kTcRows];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    auto set_up = [&]() {   // barriers and tensor memory (whole block)
+        if (tid == 0) {
+            for (int i = 0; i < kTcStages; ++i) {
+                // FP8: one arrival per widened chunk; 16-bit pools and the direct
+                // K codes: the TMA's
+                mbar_init(smem_u32(&k_full[i]), F8 && !kDirectK ? kTcKeys / kF8ChunkKeys : 1);
+                mbar_init(smem_u32(&k_empty[i]), 1);
+                mbar_init(smem_u32(&v_full[i]), F8 ? kTcKeys / kF8ChunkKeys : 1);
+                mbar_init(smem_u32(&v_empty[i]), 1);
+            }
+            for (int t = 0; t < kTcTiles; ++t) {
+                mbar_init(smem_u32(&s_full[t]), 1);
+                mbar_init(smem_u32(&p_full[t]), 8);
+                mbar_init(smem_u32(&pv_done[t]), 1);
+            }
+            mbar_init(smem_u32(&q_ready), kSoftmaxWarps);
+            for (int i = 0; i < kF8MaxDepth * kF8MaxConverters; ++i)
+                mbar_init(smem_u32(&code_full[i / kF8MaxDepth][i % kF8MaxDepth]), 1);
+        }
+        if (warp == kMmaWarp) {
+            tmem_alloc(smem_u32(&s_tmem), kTmemCols);
+            tmem_relinquish();
+        }
+        fence_mbar_init();
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+    };
+
     // heavier CTAs first, as the grid is scheduled in index order: the z index
     // is the request's rank by context length (longest first, ties by index;
     // up to kRankedReqs requests, else request order), and within a request
@@ -313,9 +376,13 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     __shared__ int s_member[kShared ? kUnitMembers : 1];
     if constexpr (kShared) {
         allow_dependent_launch();   // the sequences' own part may start beside this pass
+        set_up();
         plan_prefix_unit(sc, sp, n_kv, group, BS, max_blocks, reinterpret_cast<int*>(dyn_smem), s_member,
                          &s_unit, err);
-        if (!s_unit.live) return;
+        if (!s_unit.live) {
+            if (warp == kMmaWarp) tmem_dealloc(s_tmem, kTmemCols);
+            return;
+        }
         __syncthreads();   // the members are listed, and the scratch is free
     }
     auto unit = [&]() -> PrefixUnit {
@@ -405,51 +472,11 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     }
     const int n_tiles = max(n_t[0], n_t[1]);
 
-    // Every barrier below is waited on in completion order and its waiter is
-    // never two phases behind: S_t(j + 1) is issued after P_t(j) V, which
-    // waits for P_t(j), which needs S_t(j).
-    __shared__ __align__(8) uint64_t k_full[kTcStages], k_empty[kTcStages];
-    __shared__ __align__(8) uint64_t v_full[kTcStages], v_empty[kTcStages];
-    __shared__ __align__(8) uint64_t s_full[kTcTiles], p_full[kTcTiles], pv_done[kTcTiles], q_ready;
-    __shared__ __align__(8) uint64_t code_full[kF8MaxConverters][kF8MaxDepth];   // FP8: codes landed, per converter and buffer
-    __shared__ uint32_t s_tmem;
-    // partial row maxima of the two threads of a row (double-buffered by key
-    // tile), a "stop" flag beside each, and the partial row sums at the end
-    __shared__ float xmax[2][kTcTiles][2][kTcRows];
-    __shared__ uint8_t xstop[2][kTcTiles][2][kTcRows];
-    __shared__ float xsum[kTcTiles][2][kTcRows];
-    __shared__ uint8_t xstop_end[kTcTiles][2][kTcRows];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn_smem) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
     const uint32_t sbase = smem_u32(smem);
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (tid == 0) {
-        for (int i = 0; i < kTcStages; ++i) {
-            // FP8: one arrival per widened chunk; 16-bit pools and the direct
-            // K codes: the TMA's
-            mbar_init(smem_u32(&k_full[i]), F8 && !kDirectK ? kTcKeys / kF8ChunkKeys : 1);
-            mbar_init(smem_u32(&k_empty[i]), 1);
-            mbar_init(smem_u32(&v_full[i]), F8 ? kTcKeys / kF8ChunkKeys : 1);
-            mbar_init(smem_u32(&v_empty[i]), 1);
-        }
-        for (int t = 0; t < kTcTiles; ++t) {
-            mbar_init(smem_u32(&s_full[t]), 1);
-            mbar_init(smem_u32(&p_full[t]), 8);
-            mbar_init(smem_u32(&pv_done[t]), 1);
-        }
-        mbar_init(smem_u32(&q_ready), kSoftmaxWarps);
-        for (int i = 0; i < kF8MaxDepth * kF8MaxConverters; ++i)
-            mbar_init(smem_u32(&code_full[i / kF8MaxDepth][i % kF8MaxDepth]), 1);
-    }
-    if (warp == kMmaWarp) {
-        tmem_alloc(smem_u32(&s_tmem), kTmemCols);
-        tmem_relinquish();
-    }
-    fence_mbar_init();
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
+    if constexpr (!kShared) set_up();
     const uint32_t tmem = s_tmem;
 
     static_assert(!F8 || std::is_same<T, __half>::value, "FP8 codes widen to fp16 operands");
@@ -1221,10 +1248,24 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(o[i]) * inv;
                     if constexpr (kShared) {
-                        if (valid) store_row<T>(sp.acc, obase, hf * (D / 2) + c0, v, 32, PA_F32);
+                        // through shared memory (the operands are no longer read), as one
+                        // bulk store a half row: stores straight from registers, 16 bytes
+                        // a row and instruction, took 3.6 us of a block's 33
+                        const uint32_t at = sbase + (t * kTcRows + rr) * kORow + (hf * (D / 2) + c0) * 4;
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4)
+                            st_shared_v4(at + i * 4, __float_as_uint(v[i]), __float_as_uint(v[i + 1]),
+                                         __float_as_uint(v[i + 2]), __float_as_uint(v[i + 3]));
                     } else {
                         if (valid) store_row<T>(out, obase, hf * (D / 2) + c0, v, 32, out_dtype);
                     }
+                }
+                if constexpr (kShared) {
+                    fence_proxy_async_smem();
+                    if (valid)
+                        bulk_store(sp.acc + obase + hf * (D / 2),
+                                   sbase + (t * kTcRows + rr) * kORow + hf * (D / 2) * 4, D / 2 * 4);
+                    bulk_store_wait();
                 }
             }
         }

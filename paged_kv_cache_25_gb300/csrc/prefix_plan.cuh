@@ -82,8 +82,8 @@ __device__ __forceinline__ void plan_prefix_unit(const ScoreParams& sc, const Pr
                 u.row0 = left % tr * kUnitRows;        // row tiles of one K/V range are neighbours
                 u.kvh = left / tr % n_kv;
                 u.split = left / tr / n_kv;
-                u.tile0 = static_cast<int>(static_cast<int64_t>(u.split) * kt / n);
-                u.tiles = static_cast<int>(static_cast<int64_t>(u.split + 1) * kt / n) - u.tile0;
+                u.tile0 = u.split * kt / n;            // (kt <= 2^23, n <= 32)
+                u.tiles = (u.split + 1) * kt / n - u.tile0;
                 u.rows = count[g] * group;
                 u.first_seq = first[g];
                 u.prefix = prefix_tokens(sc.group_prefix, g, block_size, max_blocks);
