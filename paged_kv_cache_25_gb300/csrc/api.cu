@@ -555,6 +555,7 @@ static pa_status decode_common(void* out, pa_dtype out_dtype, const void* q, con
         pass.ml = a.ws_ml; pass.acc = a.ws_acc;
         pass.splits = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + kControlBytes);
         pass.max_splits = splits;
+        pass.ticket = a.ticket;
         score->group_splits = pass.splits;
         const cudaError_t e0 = launch_prefix_pass(a, pass, static_cast<cudaStream_t>(stream));
         if (e0 != cudaSuccess) return cuda_fail(e0, "prefix pass launch");

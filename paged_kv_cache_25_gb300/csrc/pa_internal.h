@@ -76,6 +76,7 @@ struct PrefixPass {
     float* ml;          // [B][n_q][slots][2]
     float* acc;         // [B][n_q][slots][d]
     int32_t* splits;    // [num_groups], written by the pass
+    unsigned* ticket;   // work counter of the decode kernel that follows, cleared by the pass
     int max_splits;     // ranges a prefix may be cut into (at most 32, at most slot0)
     int target;         // thread blocks that run at once
 };

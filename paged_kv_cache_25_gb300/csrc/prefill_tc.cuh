@@ -375,8 +375,18 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     __shared__ std::conditional_t<kShared, PrefixUnit, NoScore> s_unit;
     __shared__ int s_member[kShared ? kUnitMembers : 1];
     if constexpr (kShared) {
-        allow_dependent_launch();   // the sequences' own part may start beside this pass
         set_up();
+        // launched as a programmatic dependent: every input may come from the kernel before
+        grid_dependency_wait();
+        // The sequences' own part may start beside this pass.  Its work counter is
+        // cleared here, fenced before this block lets it start (a memset would cost a
+        // launch of its own); it takes tickets by atomics only.
+        if (blockIdx.x == 0 && tid == 0) {
+            atomicExch(sp.ticket, 0u);
+            __threadfence();
+        }
+        if (blockIdx.x == 0) __syncthreads();
+        allow_dependent_launch();
         plan_prefix_unit(sc, sp, n_kv, group, BS, max_blocks, reinterpret_cast<int*>(dyn_smem), s_member,
                          &s_unit, err);
         if (!s_unit.live) {

@@ -36,12 +36,21 @@ static cudaError_t run_prefix(const DecodeArgs& a, const PrefixPass& pass, cudaS
     const int64_t row_tiles = rows / kUnitRows + (a.score->num_groups < a.num_seqs ? a.score->num_groups : a.num_seqs);
     const int64_t units = row_tiles * n_kv;
     const unsigned grid = static_cast<unsigned>(units > pass.target ? units : pass.target);
-    kern<<<grid, PfWarps<F8, D, kBq>::kThreads, Ly::kDynBytes, s>>>(
-        kmap, vmap, static_cast<const uint8_t*>(a.k_cache), static_cast<const uint8_t*>(a.v_cache),
-        nullptr, PA_F32, static_cast<const QT*>(a.q), a.block_tables, a.max_blocks, nullptr,
-        a.context_lens, 0, a.n_q, n_kv, group, a.cache.num_blocks, F8 ? sl2 * a.cache.k_scale : sl2,
-        F8 ? a.cache.v_scale : 1.f, a.err, *a.score, pass);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(PfWarps<F8, D, kBq>::kThreads);
+    cfg.dynamicSmemBytes = Ly::kDynBytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(
+        &cfg, kern, kmap, vmap, static_cast<const uint8_t*>(a.k_cache), static_cast<const uint8_t*>(a.v_cache),
+        static_cast<void*>(nullptr), PA_F32, static_cast<const QT*>(a.q), a.block_tables, a.max_blocks,
+        static_cast<const int32_t*>(nullptr), a.context_lens, 0, a.n_q, n_kv, group, a.cache.num_blocks,
+        F8 ? sl2 * a.cache.k_scale : sl2, F8 ? a.cache.v_scale : 1.f, a.err, *a.score, pass);
 }
 
 template <typename T, typename QT, bool F8>
@@ -58,13 +67,9 @@ static cudaError_t run_prefix_dt(const DecodeArgs& a, const PrefixPass& p, cudaS
 cudaError_t launch_prefix_pass(const DecodeArgs& a, const PrefixPass& pass, cudaStream_t s)
 {
     const float sl2 = a.scale * kLog2e;
-    // the work counter of the decode kernel that follows: nothing may come between
-    // the two launches
-    cudaError_t e = cudaMemsetAsync(a.ticket, 0, sizeof(unsigned), s);
-    if (e != cudaSuccess) return e;
     PrefixPass p = pass;
     int dev = 0;
-    e = cudaGetDevice(&dev);
+    cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&p.target, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
     if (a.cache.dtype == PA_BF16) return run_prefix_dt<__nv_bfloat16, __nv_bfloat16, false>(a, p, s, sl2);

@@ -22,7 +22,7 @@ constexpr int kUnitRows = 256, kUnitKeys = 128;
 constexpr int kUnitMembers = kUnitRows + 1;   // members that a row tile can touch
 constexpr float kUnitOverhead = 2.f;
 
-// Every thread of the block calls it.  scratch: 2 * num_groups ints of shared memory;
+// Every thread of the block calls it.  scratch: 3 * num_groups ints of shared memory;
 // members: kUnitMembers ints, filled with the sequences of the unit's rows (member
 // m of the tile serves rows m * group - row0 .. of it, from member row0 / group on).
 __device__ __forceinline__ void plan_prefix_unit(const ScoreParams& sc, const PrefixPass& sp, int n_kv,
@@ -34,13 +34,16 @@ __device__ __forceinline__ void plan_prefix_unit(const ScoreParams& sc, const Pr
     const int G = sc.num_groups;
     int* count = scratch;
     int* first = scratch + G;
+    int* prefix = scratch + 2 * G;
+    const int mine0 = tid < sp.num_seqs ? __ldg(sc.group_of_seq + tid) : -1;   // in flight meanwhile
     for (int g = tid; g < G; g += threads) {
         count[g] = 0;
         first[g] = INT_MAX;
+        prefix[g] = prefix_tokens(sc.group_prefix, g, block_size, max_blocks);
     }
     __syncthreads();
     for (int s = tid; s < sp.num_seqs; s += threads) {
-        const int g = __ldg(sc.group_of_seq + s);
+        const int g = s == tid ? mine0 : __ldg(sc.group_of_seq + s);
         if (g >= G) set_error(err, PA_ERR_OUT_OF_RANGE);   // (such a sequence shares nothing)
         if (g < 0 || g >= G) continue;
         atomicAdd(&count[g], 1);
@@ -49,7 +52,7 @@ __device__ __forceinline__ void plan_prefix_unit(const ScoreParams& sc, const Pr
     __syncthreads();
     auto row_tiles = [&](int g) { return (count[g] * group + kUnitRows - 1) / kUnitRows; };
     auto key_tiles = [&](int g) {
-        return count[g] ? (prefix_tokens(sc.group_prefix, g, block_size, max_blocks) + kUnitKeys - 1) / kUnitKeys : 0;
+        return count[g] ? (prefix[g] + kUnitKeys - 1) / kUnitKeys : 0;
     };
     if (warp == 0) {
         int longest = 0;
@@ -86,7 +89,7 @@ __device__ __forceinline__ void plan_prefix_unit(const ScoreParams& sc, const Pr
                 u.tiles = (u.split + 1) * kt / n - u.tile0;
                 u.rows = count[g] * group;
                 u.first_seq = first[g];
-                u.prefix = prefix_tokens(sc.group_prefix, g, block_size, max_blocks);
+                u.prefix = prefix[g];
                 if (left == 0) sp.splits[g] = n;       // for the merge
                 break;
             }
@@ -99,7 +102,8 @@ __device__ __forceinline__ void plan_prefix_unit(const ScoreParams& sc, const Pr
     const int m1 = (min(unit->rows, unit->row0 + kUnitRows) - 1) / group;
     for (int base = 0, run = 0; base < sp.num_seqs && run <= m1; base += threads) {
         const int s = base + tid;
-        const bool mine = s < sp.num_seqs && __ldg(sc.group_of_seq + s) == unit->group;
+        const bool mine = s < sp.num_seqs &&
+                          (base == 0 ? mine0 : __ldg(sc.group_of_seq + s)) == unit->group;
         const unsigned mask = __ballot_sync(0xffffffffu, mine);
         if (lane == 0) s_warp[warp] = __popc(mask);
         __syncthreads();
