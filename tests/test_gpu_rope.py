@@ -182,6 +182,14 @@ def test_no_rotation_is_the_plain_cache_write(fp8):
     assert torch.equal(c.q_out, c.q)
 
 
+@pytest.mark.parametrize("scale", [0.013, 1.0, 0.25])
+def test_fp8_other_scales(scale):
+    """Scales with and without an exact reciprocal."""
+    c = Case(28, 37, 8, 4, 64, 16, BF, 32, False, 3, fp8=True, scale=scale).start()
+    c.run()
+    c.check()
+
+
 def test_fp8_saturates():
     c = Case(22, 20, 4, 2, 128, 16, BF, 128, False, 0, fp8=True, scale=1.0 / 1024).start()
     c.run()
@@ -212,6 +220,16 @@ def test_q_in_place(interleaved):
     c.q_out = c.q
     c.run()
     c.check()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_more_tokens_than_the_grid_covers_at_once(fp8):
+    c = Case(29, 3001, 8, 4, 128, 16, BF, 128, False, 9, fp8=fp8).start()
+    c.slots[[0, 1700, 3000]] = -1
+    c.run()
+    w = np.ones(3001, bool)
+    w[[0, 1700, 3000]] = False
+    c.check(w)
 
 
 def test_no_tokens():
