@@ -1011,19 +1011,33 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         if constexpr (kCap) cap = cap_form(sc.cap2, sc.cap_rate, scale_log2);
         if constexpr (kBias) slope2 = __ldg(sc.slopes + head) * kLog2e;
         const int q_pos = ctx0 + pos_local;
-        // modified scores of keys d .. d + 3 past the position, minus a reference
-        // (neg_ref = -reference); clamp: see soft_cap4
-        using Clamp = std::true_type;
-        auto modified4 = [&](auto clamp, const float (&s)[4], float d, float neg_ref, float (&z)[4]) {
-            if constexpr (kCap) {
-                soft_cap4<decltype(clamp)::value>(cap, s, neg_ref, z);
+        const int warp_min_q = kBias ? __reduce_min_sync(0xffffffffu, q_pos) : 0;
+        // modified scores of the four keys i .. i + 3 of this thread's half tile, whose
+        // first key lies d0 past the position, minus a reference (neg_ref = -reference).
+        // clamp: see soft_cap4.  ahead: some visible key may lie past its row's position
+        // (a prefix mask); else the bias is linear in the key, slope2 * (d0 + i).
+        using Yes = std::true_type;
+        auto modified4 = [&](auto clamp, auto ahead, const float (&s)[4], float d0, int i, float neg_ref,
+                             float (&z)[4]) {
+            float add[4];
+            if constexpr (kCap) neg_ref += cap.cap2;
+            if constexpr (!kBias) {
+                add[0] = add[1] = add[2] = add[3] = neg_ref;
+            } else if constexpr (decltype(ahead)::value) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) add[e] = fmaf(-slope2, fabsf(d0 + (i + e)), neg_ref);
             } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) z[i] = fmaf(s[i], scale_log2, neg_ref);
+                const float2 first = both(fmaf(slope2, d0, neg_ref));
+                const float2 a0 = fma2(both(slope2), make_float2(i, i + 1), first);
+                const float2 a1 = fma2(both(slope2), make_float2(i + 2, i + 3), first);
+                add[0] = a0.x; add[1] = a0.y; add[2] = a1.x; add[3] = a1.y;
             }
-            if constexpr (kBias) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) z[i] = fmaf(-slope2, fabsf(d + i), z[i]);
+            if constexpr (kCap) {
+                soft_cap4<decltype(clamp)::value>(cap, s, add, z);
+            } else {
+                const float2 z0 = fma2(make_float2(s[0], s[1]), both(scale_log2), make_float2(add[0], add[1]));
+                const float2 z1 = fma2(make_float2(s[2], s[3]), both(scale_log2), make_float2(add[2], add[3]));
+                z[0] = z0.x; z[1] = z0.y; z[2] = z1.x; z[3] = z1.y;
             }
         };
         const float unit_log2 = kZ ? 1.f : scale_log2;   // log2 units of the running maximum
@@ -1038,6 +1052,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             const int key0 = (tile0 + j) * kTcKeys, hkey0 = key0 + hf * 64;
             const bool full_tile = key0 + kTcKeys - 1 <= warp_min_pos && (MODE == 0 || key0 >= warp_max_lo);
             const float d0 = kBias ? static_cast<float>(hkey0 - q_pos) : 0.f;
+            const bool linear = prefix_end == 0 || key0 + kTcKeys - 1 <= warp_min_q;   // no visible key ahead
 
             // pass 1: max over this thread's 64 raw scores, swapped with the
             // partner's (scores stay unscaled until the exponent: p =
@@ -1049,21 +1064,28 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                 tmem_ld32(lane_addr + s_col + 32, sb);
                 tmem_ld_wait();
                 if constexpr (kBias) {
+                    auto pass1 = [&](auto ahead) {
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        const float s0[4] = {__uint_as_float(sa[i]), __uint_as_float(sa[i + 1]),
-                                             __uint_as_float(sa[i + 2]), __uint_as_float(sa[i + 3])};
-                        const float s1[4] = {__uint_as_float(sb[i]), __uint_as_float(sb[i + 1]),
-                                             __uint_as_float(sb[i + 2]), __uint_as_float(sb[i + 3])};
-                        float za[4], zb[4];
-                        modified4(Clamp{}, s0, d0 + i, 0.f, za);
-                        modified4(Clamp{}, s1, d0 + (32 + i), 0.f, zb);
+                        for (int i = 0; i < 32; i += 4) {
+                            const float s0[4] = {__uint_as_float(sa[i]), __uint_as_float(sa[i + 1]),
+                                                 __uint_as_float(sa[i + 2]), __uint_as_float(sa[i + 3])};
+                            const float s1[4] = {__uint_as_float(sb[i]), __uint_as_float(sb[i + 1]),
+                                                 __uint_as_float(sb[i + 2]), __uint_as_float(sb[i + 3])};
+                            float za[4], zb[4];
+                            modified4(Yes{}, ahead, s0, d0, i, 0.f, za);
+                            modified4(Yes{}, ahead, s1, d0, 32 + i, 0.f, zb);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            if (full_tile || sees(hkey0 + i + e)) m4[e] = fmaxf(m4[e], za[e]);
-                            if (full_tile || sees(hkey0 + 32 + i + e)) m4[e] = fmaxf(m4[e], zb[e]);
+                            for (int e = 0; e < 4; ++e) {
+                                if (!full_tile) {
+                                    za[e] = sees(hkey0 + i + e) ? za[e] : -INFINITY;
+                                    zb[e] = sees(hkey0 + 32 + i + e) ? zb[e] : -INFINITY;
+                                }
+                                m4[e] = max3f(m4[e], za[e], zb[e]);
+                            }
                         }
-                    }
+                    };
+                    if (linear) pass1(std::false_type{});
+                    else pass1(Yes{});
                 } else if (full_tile) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
@@ -1085,9 +1107,9 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             bool open = true;   // kCap: no score of these rows needs the clamp
             if constexpr (kCap && !kBias) {
                 open = __all_sync(0xffffffffu, mx * cap.rate <= kCapExp);
-                const float s[4] = {mx, mx, mx, mx};
+                const float s[4] = {mx, mx, mx, mx}, top[4] = {cap.cap2, cap.cap2, cap.cap2, cap.cap2};
                 float z[4];
-                soft_cap4<true>(cap, s, 0.f, z);
+                soft_cap4<true>(cap, s, top, z);
                 mx = mx == -INFINITY ? mx : z[0];
             }
             stop = stop || !ok || xstop[j & 1][t][hf ^ 1][rr] != 0;
@@ -1131,7 +1153,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                 tmem_ld_wait();
                 uint32_t ph[16], pl[16];
                 float z[4];   // modified scores of two neighbouring pairs of keys
-                auto full = [&](auto clamp) {
+                auto full = [&](auto clamp, auto ahead) {
                     // pairs of keys in paired fp32 instructions: the exponent's
                     // argument, the row sum and P's lo residual
                     const float2 c2 = make_float2(scale_log2, scale_log2), n2 = make_float2(neg_mc, neg_mc);
@@ -1142,7 +1164,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                             if (i % 2 == 0) {
                                 const float s[4] = {__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1]),
                                                     __uint_as_float(sr[2 * i + 2]), __uint_as_float(sr[2 * i + 3])};
-                                modified4(clamp, s, d0 + (h2 * 32 + 2 * i), neg_mc, z);
+                                modified4(clamp, ahead, s, d0, h2 * 32 + 2 * i, neg_mc, z);
                             }
                             x = make_float2(z[2 * (i % 2)], z[2 * (i % 2) + 1]);
                         } else {
@@ -1164,10 +1186,11 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                         }
                     }
                 };
-                if (full_tile && open) {
-                    full(std::bool_constant<kBias>{});
-                } else if (full_tile) {
-                    full(std::true_type{});
+                using No = std::false_type;
+                if (full_tile && (kBias ? linear : open)) {
+                    full(std::bool_constant<kCap && kBias>{}, No{});
+                } else if (kZ && full_tile) {
+                    full(Yes{}, std::bool_constant<kBias>{});
                 } else {   // masked keys give exactly 0 (even with scale 0, where -inf * 0 is NaN)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
@@ -1175,7 +1198,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                         if (i % 2 == 0) {
                             const float s[4] = {__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1]),
                                                 __uint_as_float(sr[2 * i + 2]), __uint_as_float(sr[2 * i + 3])};
-                            modified4(Clamp{}, s, d0 + (h2 * 32 + 2 * i), neg_mc, z);
+                            modified4(Yes{}, std::bool_constant<kBias>{}, s, d0, h2 * 32 + 2 * i, neg_mc, z);
                         }
                         const float p0 = sees(k) ? fast_exp2(z[2 * (i % 2)]) : 0.f;
                         const float p1 = sees(k + 1) ? fast_exp2(z[2 * (i % 2) + 1]) : 0.f;

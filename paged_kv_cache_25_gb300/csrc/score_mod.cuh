@@ -63,11 +63,11 @@ __device__ __forceinline__ CapForm cap_form(float cap2, float cap_rate, float sc
 
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
-// z[i] = C tanh(x_i) + add
+// z[i] = C tanh(x_i) + (top[i] - C)
 template <bool CLAMP>
-__device__ __forceinline__ void soft_cap4(const CapForm& f, const float (&s)[4], float add, float (&z)[4])
+__device__ __forceinline__ void soft_cap4(const CapForm& f, const float (&s)[4], const float (&top)[4],
+                                          float (&z)[4])
 {
-    const float top = f.cap2 + add;
     float2 t[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -82,8 +82,8 @@ __device__ __forceinline__ void soft_cap4(const CapForm& f, const float (&s)[4],
     }
     const float qa = t[0].x * t[0].y, qb = t[1].x * t[1].y;
     const float r = fast_rcp(qa * qb), ra = r * qb, rb = r * qa;   // 1 / qa, 1 / qb
-    z[0] = fmaf(ra, t[0].y, top); z[1] = fmaf(ra, t[0].x, top);
-    z[2] = fmaf(rb, t[1].y, top); z[3] = fmaf(rb, t[1].x, top);
+    z[0] = fmaf(ra, t[0].y, top[0]); z[1] = fmaf(ra, t[0].x, top[1]);
+    z[2] = fmaf(rb, t[1].y, top[2]); z[3] = fmaf(rb, t[1].x, top[3]);
 }
 
 // Tokens of group g's prefix, in whole blocks.
