@@ -872,7 +872,8 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         const int p_abs = !valid ? L - 1   // padding rows see every key
                           : kShared ? min(L, __ldg(context_lens + seq)) - 1 : last_key(pos_local);
         const int p_lo = MODE != 0 && valid ? first_key(pos_local) : 0;
-        auto sees = [&](int k) -> bool { return k <= p_abs && (MODE == 0 || k >= p_lo); };
+        // the low n bits (0 <= n clamped to 32)
+        auto bits_below = [](int n) -> uint32_t { return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u); };
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
         const uint32_t s_col = Ly::kTmemS + t * 128 + hf * 64;      // this thread's 64 keys
         const uint32_t o_col = Ly::kTmemO + t * D + hf * (D / 2);   // this thread's O columns
@@ -1054,6 +1055,20 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             const float d0 = kBias ? static_cast<float>(hkey0 - q_pos) : 0.f;
             const bool linear = prefix_end == 0 || key0 + kTcKeys - 1 <= warp_min_q;   // no visible key ahead
 
+            // (FP8 pools with a cap keep the bounds: the mask costs them 218 -> 236 us on
+            // full tiles, where it is not even read)
+            constexpr bool kBits = MODE != 0 && !kShared && !(F8 && kCap);
+            // masked tiles of a scored call: the visible ones of keys h .. h + 31 of this
+            // thread's half tile as a bit mask (one test a key instead of two bounds)
+            auto mask_of = [&](int h) -> uint32_t {
+                if constexpr (!kBits) return 0u;
+                else return full_tile ? ~0u : bits_below(p_abs + 1 - hkey0 - h) & ~bits_below(p_lo - hkey0 - h);
+            };
+            auto sees = [&](uint32_t mask, int i, int k) -> bool {   // key k, bit i of its mask
+                if constexpr (kBits) return ((mask >> i) & 1u) != 0;
+                else return k <= p_abs && (MODE == 0 || kShared || k >= p_lo);
+            };
+
             // pass 1: max over this thread's 64 raw scores, swapped with the
             // partner's (scores stay unscaled until the exponent: p =
             // 2^(s*c - m*c) is one FFMA and one EX2)
@@ -1064,6 +1079,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                 tmem_ld32(lane_addr + s_col + 32, sb);
                 tmem_ld_wait();
                 if constexpr (kBias) {
+                    const uint32_t see_a = mask_of(0), see_b = mask_of(32);
                     auto pass1 = [&](auto ahead) {
 #pragma unroll
                         for (int i = 0; i < 32; i += 4) {
@@ -1077,8 +1093,8 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 if (!full_tile) {
-                                    za[e] = sees(hkey0 + i + e) ? za[e] : -INFINITY;
-                                    zb[e] = sees(hkey0 + 32 + i + e) ? zb[e] : -INFINITY;
+                                    za[e] = sees(see_a, i + e, hkey0 + i + e) ? za[e] : -INFINITY;
+                                    zb[e] = sees(see_b, i + e, hkey0 + 32 + i + e) ? zb[e] : -INFINITY;
                                 }
                                 m4[e] = max3f(m4[e], za[e], zb[e]);
                             }
@@ -1091,10 +1107,11 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                     for (int i = 0; i < 32; ++i)
                         m4[i & 3] = max3f(m4[i & 3], __uint_as_float(sa[i]), __uint_as_float(sb[i]));
                 } else {
+                    const uint32_t see_a = mask_of(0), see_b = mask_of(32);
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
-                        if (sees(hkey0 + i)) m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(sa[i]));
-                        if (sees(hkey0 + 32 + i)) m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(sb[i]));
+                        if (sees(see_a, i, hkey0 + i)) m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(sa[i]));
+                        if (sees(see_b, i, hkey0 + 32 + i)) m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(sb[i]));
                     }
                 }
             }
@@ -1192,6 +1209,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                 } else if (kZ && full_tile) {
                     full(Yes{}, std::bool_constant<kBias>{});
                 } else {   // masked keys give exactly 0 (even with scale 0, where -inf * 0 is NaN)
+                    const uint32_t see = mask_of(h2 * 32);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const int k = hkey0 + h2 * 32 + 2 * i;
@@ -1200,8 +1218,8 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                                                 __uint_as_float(sr[2 * i + 2]), __uint_as_float(sr[2 * i + 3])};
                             modified4(Yes{}, std::bool_constant<kBias>{}, s, d0, h2 * 32 + 2 * i, neg_mc, z);
                         }
-                        const float p0 = sees(k) ? fast_exp2(z[2 * (i % 2)]) : 0.f;
-                        const float p1 = sees(k + 1) ? fast_exp2(z[2 * (i % 2) + 1]) : 0.f;
+                        const float p0 = sees(see, 2 * i, k) ? fast_exp2(z[2 * (i % 2)]) : 0.f;
+                        const float p1 = sees(see, 2 * i + 1, k + 1) ? fast_exp2(z[2 * (i % 2) + 1]) : 0.f;
                         s4[i & 3] += p0 + p1;
                         if constexpr (kOneP) ph[i] = Cvt<__half>::pack(p0, p1);
                         else split_trunc<T>(p0, p1, ph[i], pl[i]);
