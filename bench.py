@@ -42,16 +42,16 @@ FALLBACK_HBM_GBS = 6800.0
 # K/V bytes of the captured launch, what was captured); a record of another
 # batch of the same workload is scaled by its unique K/V bytes.
 NCU_TRAFFIC = {
-    ("llama3-8b-bf16", "c4ea871a6ef948da"): (2371993088 + 13370880, 2359717888,
+    ("llama3-8b-bf16", "6aa7e3d8522fdb81"): (2371980544 + 13389312, 2359717888,
                                              "full 256-sequence batch, one-pass capture"),
-    ("llama3-8b-fp8", "c4ea871a6ef948da"): (1188198656 + 12378112, 1179858944,
+    ("llama3-8b-fp8", "6aa7e3d8522fdb81"): (1188299776 + 12441856, 1179858944,
                                             "full 256-sequence batch, one-pass capture"),
 }
 # chunked prefill of the mixed step (the compact-pool capture runs the same four
 # chunks as the 60 GB pool): bytes per launch
 NCU_PREFILL_TRAFFIC = {
-    ("mixed-llama3-8b-bf16", "4262d850e1fa2e78"): (98472960 + 3946496, "compact pool, one-pass capture"),
-    ("mixed-llama3-8b-fp8", "4262d850e1fa2e78"): (57580288 + 948480, "compact pool, one-pass capture"),
+    ("mixed-llama3-8b-bf16", "7a80a00bf28eb997"): (98526464 + 4051456, "compact pool, one-pass capture"),
+    ("mixed-llama3-8b-fp8", "7a80a00bf28eb997"): (57575168 + 1105408, "compact pool, one-pass capture"),
 }
 
 

@@ -10,7 +10,9 @@ One step (the timed hot path): append the new tokens' K/V
 (pa_reshape_and_cache), decode one token for every decode sequence
 (pa_decode, split-K plus reduce; pa_decode_verify when a sequence brings
 several query rows), and run the chunked-prefill requests, if any
-(pa_prefill_chunk).  All of it runs in the library's CUDA kernels.
+(pa_prefill_chunk).  With share_prefix the decode reads leading blocks that
+sequences have in common once (pa_decode_shared, groups found in the block tables).
+All of it runs in the library's CUDA kernels.
 """
 from __future__ import annotations
 
@@ -49,7 +51,9 @@ def _ordered_window(ex, fn, items, window):
 class PagedStep:
     def __init__(self, wl: Workload, seed: int | None = None, device="cuda",
                  out_dtype: torch.dtype | None = None, upload_chunk_tokens: int = 1 << 18,
-                 prefill_out_dtype: torch.dtype | None = None):
+                 prefill_out_dtype: torch.dtype | None = None, share_prefix: bool = False):
+        if share_prefix and wl.q_per_seq != 1:
+            raise ValueError("share_prefix is for one query row per sequence")
         self.wl = wl
         self.draws = dr = Draws(wl, seed)
         self.device = torch.device(device)
@@ -127,8 +131,15 @@ class PagedStep:
         self.context_lens = torch.from_numpy(self.lens.astype(np.int32)).to(dev)
         od = out_dtype or wl.dtype
         self.out = torch.empty(tuple(self.q.shape), dtype=od, device=dev)
-        ws = pa.pa_decode_verify_workspace_size(B, nq, wl.n_q_heads, n_kv, d, bs,
-                                                self.max_blocks * bs)
+        if share_prefix:
+            group, prefix_lens = pa.pa_shared_prefix_groups(self.tables, self.lens, bs)
+            self.group_of_seq = torch.from_numpy(group).to(dev)
+            self.prefix_lens = torch.from_numpy(prefix_lens).to(dev)
+            ws = pa.pa_decode_shared_workspace_size(B, wl.n_q_heads, n_kv, d, bs,
+                                                    self.max_blocks * bs, len(prefix_lens))
+        else:
+            ws = pa.pa_decode_verify_workspace_size(B, nq, wl.n_q_heads, n_kv, d, bs,
+                                                    self.max_blocks * bs)
         self.workspace = torch.empty(max(ws, 1), dtype=torch.uint8, device=dev) if ws else None
         if self.R:
             self.p_q_dev = torch.cat(self.p_q).to(dev).contiguous()
@@ -199,6 +210,7 @@ class PagedStep:
     # ------------------------------------------------------------------
     # per-step inputs and outputs, replaceable by another set (see io_set)
     IO_NAMES = ("q", "new_k", "new_v", "new_slots", "block_tables", "context_lens", "out",
+                "group_of_seq", "prefix_lens",
                 "p_q_dev", "query_start_loc", "p_block_tables", "p_context_lens", "p_out")
 
     def io_set(self, clone: bool = False) -> dict:
@@ -233,10 +245,15 @@ class PagedStep:
                                 **self.kv_scales)
             if prefill_events is not None:
                 prefill_events[1].record(side)
-        decode = pa.pa_decode if wl.q_per_seq == 1 else pa.pa_decode_verify
-        decode(t["out"], t["q"], self.k_cache, self.v_cache, t["block_tables"],
-               t["context_lens"], wl.scale, wl.block_size, self.workspace, stream=main,
-               **self.kv_scales)
+        if "group_of_seq" in t:
+            pa.pa_decode_shared(t["out"], t["q"], self.k_cache, self.v_cache, t["block_tables"],
+                                t["context_lens"], t["group_of_seq"], t["prefix_lens"], wl.scale,
+                                wl.block_size, self.workspace, stream=main, **self.kv_scales)
+        else:
+            decode = pa.pa_decode if wl.q_per_seq == 1 else pa.pa_decode_verify
+            decode(t["out"], t["q"], self.k_cache, self.v_cache, t["block_tables"],
+                   t["context_lens"], wl.scale, wl.block_size, self.workspace, stream=main,
+                   **self.kv_scales)
         if self.R:
             main.wait_stream(side)
 
