@@ -59,7 +59,8 @@ decode_simt_kernel(void* __restrict__ out, pa_dtype out_dtype, const T* __restri
     // tokens in groups of kTok: their K/V rows are loaded before any of them is
     // used, so the loads of a group overlap (one token at a time left every
     // warp waiting on one row's latency per token)
-    constexpr int kTok = 4;
+    // (a scored call takes eight while their registers fit: a short context is all latency)
+    constexpr int kTok = SC && DPL <= 4 ? 8 : 4;
     const int32_t* table = block_tables + static_cast<int64_t>(s) * max_blocks;
     for (int p0 = tok0; p0 < tok1; p0 += kTok) {
         float kf[kTok][DPL], vf[kTok][DPL];
@@ -177,13 +178,17 @@ decode_merge_kernel(void* __restrict__ out, pa_dtype out_dtype,
     grid_dependency_wait();                              // the partials are written
     if (!mine || L < nq) return;                         // (nothing of a sequence below nq is written)
     if (!member && J <= 1) return;                       // finished by the partial kernel
+    const float* ml = ws_ml + 2 * sh * sc.slots;
+    // every lane's prefix slot (at most 32 of them), whether the pass wrote it or not: its
+    // load goes out with that of the number of slots written
+    const float pre_m = member && lane < sc.slot0 ? ml[2 * lane] : -INFINITY;
+    float M = -INFINITY;
+    for (int i = lane; i < J; i += 32) M = fmaxf(M, ml[2 * (sc.slot0 + i)]);
     const int P = member ? sc.group_splits[g] : 0;
+    if (lane < P) M = fmaxf(M, pre_m);
     // partial i of P + J: slot i of the prefix pass's, or partition i - P
     const int n = P + J;
-    const float* ml = ws_ml + 2 * sh * sc.slots;
     auto slot = [&](int i) { return i < P ? i : sc.slot0 + i - P; };
-    float M = -INFINITY;
-    for (int i = lane; i < n; i += 32) M = fmaxf(M, ml[2 * slot(i)]);
 #pragma unroll
     for (int w = 16; w > 0; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
     const float M_use = M == -INFINITY ? 0.f : M;

@@ -497,11 +497,12 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 
     // ---- the first unit: ids checked before any load is issued
     int64_t u = blockIdx.x;
-    if (beside) {                                     // the first unit and the next one
-        if (tid == 0) s_next = atomicAdd(ticket, 2u);
+    if (beside) {
+        if (tid == 0) s_next = atomicAdd(ticket, 1u);
         __syncthreads();
         u = s_next;
         __syncthreads();
+        if (tid == 0 && u < units) s_next = atomicAdd(ticket, 1u);   // the next one's, meanwhile
     }
     const int64_t dealt = beside ? 0 : static_cast<int64_t>(gridDim.x);   // units dealt without a ticket
     if (u >= units) {                                 // uniform over the CTA
@@ -514,8 +515,8 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         if (cu.live && tid < cu.nblk) s_blk[0][tid] = load_id(cu, tid, bad);
         load_q(cu);
         const int any_bad = __syncthreads_or(bad);
-        if (tid == 0)
-            s_next = beside ? u + 1 : ticket ? dealt + atomicAdd(ticket, 1u) : u + static_cast<long long>(gridDim.x);
+        if (tid == 0 && !beside)
+            s_next = ticket ? dealt + atomicAdd(ticket, 1u) : u + static_cast<long long>(gridDim.x);
         cu.live = cu.live && !any_bad;
         __syncthreads();
     }
