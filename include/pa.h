@@ -296,9 +296,10 @@ int pa_shared_prefix_groups(const int32_t* tables, int max_blocks, const int32_t
  * and row i sees the keys  max(i - window + 1, first_key of the row, 0) <= j <=
  * max(i, prefix_len - 1)  of the sequence's context_lens tokens; out = softmax(z) V over
  * them.  A row that sees no key (its first_key lies past its last) is 0.
- * Keys that no row of the sequence's call sees may hold anything, and table entries of
- * blocks in which no row sees a key are never read (blocks behind a window may have been
- * freed); a key that some row sees must be finite for the others. */
+ * Keys of a sequence before the first one that any of the call's rows sees, and past its
+ * context, may hold anything, and table entries of blocks before that first key are never
+ * read (blocks behind a window may have been freed); the keys between must be finite, also
+ * for the rows that do not see them. */
 typedef struct {
     float softcap;              /* in [0.125, 1e6]: cap; 0: none (others are refused)          */
     const float* alibi_slopes;  /* device fp32 [n_q_heads] (linear distance bias), or NULL    */

@@ -188,12 +188,18 @@ def _attention_args(out, q, k_cache, v_cache, block_tables, context_lens, seqs: 
     kv = k_cache.dtype
     if v_cache.dtype != kv or (q.dtype != kv and kv != torch.float8_e4m3fn):
         raise TypeError("q and the pools must have one dtype (FP8 pools: bf16 or fp16 q)")
-    _check_device(q)
+    if not (torch.cuda.current_device() == q.get_device() == out.get_device() ==
+            k_cache.get_device() == v_cache.get_device() == block_tables.get_device() ==
+            context_lens.get_device()):
+        raise ValueError(_WRONG_DEVICE)
+
+
+_WRONG_DEVICE = "the tensors must be on the current CUDA device"
 
 
 def _check_device(t):
     if t.get_device() != torch.cuda.current_device():
-        raise ValueError("the tensors must be on the current CUDA device")
+        raise ValueError(_WRONG_DEVICE)
 
 
 def pa_status_string(st: int) -> str:
@@ -263,18 +269,16 @@ def pa_rope_and_cache(q_out, q, k, v, positions, cos_sin, k_cache, v_cache, slot
     [T][n_kv][d] go to slot_mapping (int64 [T]) of the pools.  q, k and v may be slices of one
     projection (any token stride).  cos_sin: fp32 [max_position][rot_dim], see pa_rope_table.
     FP8 pools take their scales."""
-    shape = q.shape
-    T, n_q, hd = shape
-    kv_shape = k.shape
-    n_kv = k_cache.shape[1]
-    if q_out.shape != shape or v.shape != kv_shape or kv_shape != (T, n_kv, hd) or \
-            hd != k_cache.shape[3]:
+    T, n_q, hd = shape = q.shape
+    _, n_kv, _, pool_d = k_cache.shape
+    kv_shape = (T, n_kv, hd)
+    if q_out.shape != shape or v.shape != kv_shape or k.shape != kv_shape or hd != pool_d:
         raise ValueError("q_out, q [T][n_q][d] and k, v [T][n_kv][d] expected")
     dt = q.dtype
-    if q_out.dtype != dt or k.dtype != dt or v.dtype != dt:
+    if not (dt is q_out.dtype is k.dtype is v.dtype):
         raise TypeError("q_out, q, k and v must have one dtype")
-    if positions.dtype != torch.int32 or slot_mapping.dtype != torch.int64 or \
-            cos_sin.dtype != torch.float32:
+    if positions.dtype is not torch.int32 or slot_mapping.dtype is not torch.int64 or \
+            cos_sin.dtype is not torch.float32:
         raise TypeError("positions int32, slot_mapping int64 and cos_sin float32 expected")
     max_position, rot_dim = cos_sin.shape
     if positions.numel() != T or slot_mapping.numel() != T or \
@@ -287,7 +291,10 @@ def pa_rope_and_cache(q_out, q, k, v, positions, cos_sin, k_cache, v_cache, slot
         raise ValueError("contiguous pools of one dtype and size expected")
     strides = (_token_stride(q_out, T, n_q, hd), _token_stride(q, T, n_q, hd),
                _token_stride(k, T, n_kv, hd), _token_stride(v, T, n_kv, hd))
-    _check_device(q)
+    if not (torch.cuda.current_device() == q.get_device() == q_out.get_device() == k.get_device() ==
+            v.get_device() == positions.get_device() == cos_sin.get_device() ==
+            k_cache.get_device() == v_cache.get_device() == slot_mapping.get_device()):
+        raise ValueError(_WRONG_DEVICE)
     d = _desc(k_cache, k_scale, v_scale, dt)
     st = lib().pa_rope_and_cache(
         q_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), _DT[dt],
@@ -358,6 +365,8 @@ def pa_decode_shared(out, q, k_cache, v_cache, block_tables, context_lens, group
             not prefix_lens.is_contiguous():
         raise ValueError("group_of_seq [B] and prefix_lens [groups], contiguous, expected")
     _attention_args(out, q, k_cache, v_cache, block_tables, context_lens, B)
+    _check_device(group_of_seq)
+    _check_device(prefix_lens)
     d = _desc(k_cache, k_scale, v_scale, q.dtype)
     ws, ws_bytes = (workspace.data_ptr(), workspace.nbytes) if workspace is not None else (None, 0)
     st = lib().pa_decode_shared(
@@ -401,6 +410,7 @@ class ScoreMod:
                 raise TypeError(f"{name}: {dt} expected")
             if t.numel() != n or not t.is_contiguous():
                 raise ValueError(f"{name}: {n} contiguous values expected")
+            _check_device(t)
             return t.data_ptr()
 
         return _ScoreMod(self.softcap, array("alibi_slopes", self.alibi_slopes, torch.float32, n_q),
@@ -465,6 +475,7 @@ def pa_prefill_scored(out, q, k_cache, v_cache, block_tables, query_start_loc, c
             not query_start_loc.is_contiguous():
         raise ValueError("query_start_loc int32 [R + 1], contiguous, expected")
     _attention_args(out, q, k_cache, v_cache, block_tables, context_lens, R)
+    _check_device(query_start_loc)
     d = _desc(k_cache, k_scale, v_scale, q.dtype)
     m = mod._c(n_q, total, R)
     st = lib().pa_prefill_scored(
