@@ -91,6 +91,15 @@ def test_shared_decode(form, batch):
          *FORMS[form][:5], fp8=FORMS[form][5]).test()
 
 
+@pytest.mark.parametrize("dtype,fp8,d", [(BF, False, 128), (FH, False, 64), (BF, True, 128), (FH, True, 64)])
+@pytest.mark.parametrize("prefixes", [(384, 640, 1152, 1024), (256, 128, 2176, 16), (2048,)])
+def test_few_rows_and_many_heads(prefixes, dtype, fp8, d):
+    """Groups of a few rows whose blocks fill the GPU uncut: both row tiles hold the same rows
+    and share the key tiles, an even or an odd number of them."""
+    groups = [(p, [3, 40, 1][:2 + i % 2]) for i, p in enumerate(prefixes)]
+    Case(88, groups, [70], 40, 40, d, 16, dtype, fp8=fp8).test()
+
+
 @pytest.mark.parametrize("form", ["bf16-g4", "fp8-g4", "bf16-mha-d64-bs32"])
 def test_many_groups_and_sequences(form):
     """Row tiles of several sizes, more sequences than a block has threads and than the
