@@ -575,13 +575,20 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         }
     };
     while (u < units) {
+        // this unit's first stages go out before anything of the next unit is
+        // looked up (about 1 us of dependent loads)
+        const int my_n = cu.live ? my_stages(cu) : 0;
+        if (!issued && lane == 0 && my_n > 0) {
+            fence_proxy_async_smem();
+            for (int k = 0; k < min(NS, my_n); ++k) issue(s_blk[cb], cu.kvh, k, kt);
+        }
         const Unit nx = describe(un);
         // the next unit's block ids: in flight while this unit streams
         int nb_bad = 0, nb_id = -1;
         if (nx.live && tid < nx.nblk) nb_id = load_id(nx, tid, nb_bad);
 
         const int s = cu.s, part = cu.part, L = cu.L, tok0 = cu.tok0, kvh = cu.kvh;
-        const int h0 = cu.h0, r0 = cu.r0, nh = cu.nh, nchunk = cu.nchunk;
+        const int h0 = cu.h0, r0 = cu.r0, nh = cu.nh;
         // keys this thread's row may see: query qi of nq sits at L - nq + qi
         const int lim = g < nh ? L - nq + (r0 + g) % nq + 1 : L;
         const int lim1 = (R16 && g + 8 < nh) ? L - nq + (r0 + g + 8) % nq + 1 : L;
@@ -614,12 +621,6 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         int timed_out = 0;
         if (cu.live) {
             // ---- per-warp TMA ring over the partition's 16-row stages --------
-            const int my_n = nchunk > warp ? (nchunk - warp + kDecWarps - 1) / kDecWarps : 0;
-            if (!issued && lane == 0) {
-                fence_proxy_async_smem();
-                for (int k = 0; k < min(NS, my_n); ++k) issue(s_blk[cb], kvh, k, kt);
-            }
-
             scale_q();
             // kTr: softmax scale of this thread's two columns (heads 2*t4 and
             // 2*t4 + 1, mod 4), held by the quads g = 2*t4 and 2*t4 + 1
