@@ -42,16 +42,16 @@ FALLBACK_HBM_GBS = 6800.0
 # K/V bytes of the captured launch, what was captured); a record of another
 # batch of the same workload is scaled by its unique K/V bytes.
 NCU_TRAFFIC = {
-    ("llama3-8b-bf16", "6aa7e3d8522fdb81"): (2371980544 + 13389312, 2359717888,
+    ("llama3-8b-bf16", "57c4294ac64d3c44"): (2371996416 + 13414400, 2359717888,
                                              "full 256-sequence batch, one-pass capture"),
-    ("llama3-8b-fp8", "6aa7e3d8522fdb81"): (1188299776 + 12441856, 1179858944,
+    ("llama3-8b-fp8", "57c4294ac64d3c44"): (1188191744 + 12496640, 1179858944,
                                             "full 256-sequence batch, one-pass capture"),
 }
 # chunked prefill of the mixed step (the compact-pool capture runs the same four
 # chunks as the 60 GB pool): bytes per launch
 NCU_PREFILL_TRAFFIC = {
-    ("mixed-llama3-8b-bf16", "7a80a00bf28eb997"): (98526464 + 4051456, "compact pool, one-pass capture"),
-    ("mixed-llama3-8b-fp8", "7a80a00bf28eb997"): (57575168 + 1105408, "compact pool, one-pass capture"),
+    ("mixed-llama3-8b-bf16", "7a80a00bf28eb997"): (98477824 + 4136960, "compact pool, one-pass capture"),
+    ("mixed-llama3-8b-fp8", "7a80a00bf28eb997"): (57576192 + 972032, "compact pool, one-pass capture"),
 }
 
 
