@@ -131,9 +131,10 @@ def lib(path: str | None = None):
 
 
 def dtype_code(dt: torch.dtype) -> int:
-    if dt not in _DT:
+    code = _DT.get(dt)
+    if code is None:
         raise TypeError(f"unsupported dtype {dt}")
-    return _DT[dt]
+    return code
 
 
 def _check(st: int, what: str):
@@ -172,26 +173,38 @@ def _desc(k_cache: torch.Tensor, k_scale=None, v_scale=None, act_dtype=None) -> 
     return _Desc(nb, bs, n_kv, d, dt, 1.0, 1.0, dt)
 
 
-def _attention_args(out, q, k_cache, v_cache, block_tables, context_lens, seqs: int):
+def _attention_args(out, q, k_cache, v_cache, block_tables, context_lens, seqs: int, k_scale,
+                    v_scale):
     """Layout checks of a scored or shared-prefix call: what the library reads through bare
-    pointers has the types, the order and the device that it expects."""
+    pointers has the types, the order and the device that it expects.  Returns the cache's
+    descriptor, the code of out's dtype and the tables' width."""
     if not (out.is_contiguous() and q.is_contiguous() and k_cache.is_contiguous() and
             v_cache.is_contiguous() and block_tables.is_contiguous() and
             context_lens.is_contiguous()):
         raise ValueError("contiguous tensors expected")
-    if out.shape != q.shape or q.shape[-1] != k_cache.shape[3] or v_cache.numel() != k_cache.numel():
+    shape = q.shape
+    nb, n_kv, bs, d = k_cache.shape
+    if out.shape != shape or shape[-1] != d or v_cache.numel() != k_cache.numel():
         raise ValueError("out and q [..][n_q][d] and pools of that head_dim expected")
-    if block_tables.shape[0] < seqs or context_lens.numel() < seqs:
+    tables, width = block_tables.shape
+    if tables < seqs or context_lens.numel() < seqs:
         raise ValueError("a block table and a context length for every sequence expected")
-    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+    if not (block_tables.dtype is context_lens.dtype is torch.int32):
         raise TypeError("block_tables and context_lens: int32 expected")
-    kv = k_cache.dtype
-    if v_cache.dtype != kv or (q.dtype != kv and kv != torch.float8_e4m3fn):
+    kv, act = k_cache.dtype, q.dtype
+    fp8 = kv is torch.float8_e4m3fn
+    if v_cache.dtype is not kv or not (fp8 or act is kv):
         raise TypeError("q and the pools must have one dtype (FP8 pools: bf16 or fp16 q)")
     if not (torch.cuda.current_device() == q.get_device() == out.get_device() ==
             k_cache.get_device() == v_cache.get_device() == block_tables.get_device() ==
             context_lens.get_device()):
         raise ValueError(_WRONG_DEVICE)
+    code = dtype_code(kv)
+    if fp8:      # missing scales reach the library as 0 and are refused there
+        desc = _Desc(nb, bs, n_kv, d, code, k_scale or 0.0, v_scale or 0.0, dtype_code(act))
+    else:
+        desc = _Desc(nb, bs, n_kv, d, code, 1.0, 1.0, code)
+    return desc, dtype_code(out.dtype), width
 
 
 _WRONG_DEVICE = "the tensors must be on the current CUDA device"
@@ -364,14 +377,14 @@ def pa_decode_shared(out, q, k_cache, v_cache, block_tables, context_lens, group
     if group_of_seq.numel() != B or not group_of_seq.is_contiguous() or \
             not prefix_lens.is_contiguous():
         raise ValueError("group_of_seq [B] and prefix_lens [groups], contiguous, expected")
-    _attention_args(out, q, k_cache, v_cache, block_tables, context_lens, B)
+    d, out_code, width = _attention_args(out, q, k_cache, v_cache, block_tables, context_lens, B,
+                                         k_scale, v_scale)
     _check_device(group_of_seq)
     _check_device(prefix_lens)
-    d = _desc(k_cache, k_scale, v_scale, q.dtype)
     ws, ws_bytes = (workspace.data_ptr(), workspace.nbytes) if workspace is not None else (None, 0)
     st = lib().pa_decode_shared(
-        out.data_ptr(), dtype_code(out.dtype), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-        C.byref(d), block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), B, n_q,
+        out.data_ptr(), out_code, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        C.byref(d), block_tables.data_ptr(), width, context_lens.data_ptr(), B, n_q,
         scale, block_size, group_of_seq.data_ptr(), prefix_lens.data_ptr(), groups, ws, ws_bytes,
         _stream(stream))
     if st != PA_OK:
@@ -403,19 +416,20 @@ class ScoreMod:
     prefix_lens: torch.Tensor | None = None       # int32 [requests], prefill: keys every row sees
 
     def _c(self, n_q: int, rows: int, reqs: int) -> _ScoreMod:
-        def array(name, t, dt, n):
+        ptrs = []
+        for name, t, dt, n in (("alibi_slopes", self.alibi_slopes, torch.float32, n_q),
+                               ("first_key", self.first_key, torch.int32, rows),
+                               ("prefix_lens", self.prefix_lens, torch.int32, reqs)):
             if t is None:
-                return None
+                ptrs.append(None)
+                continue
             if t.dtype != dt:
                 raise TypeError(f"{name}: {dt} expected")
             if t.numel() != n or not t.is_contiguous():
                 raise ValueError(f"{name}: {n} contiguous values expected")
             _check_device(t)
-            return t.data_ptr()
-
-        return _ScoreMod(self.softcap, array("alibi_slopes", self.alibi_slopes, torch.float32, n_q),
-                         self.window, array("first_key", self.first_key, torch.int32, rows),
-                         array("prefix_lens", self.prefix_lens, torch.int32, reqs))
+            ptrs.append(t.data_ptr())
+        return _ScoreMod(self.softcap, ptrs[0], self.window, ptrs[1], ptrs[2])
 
 
 def pa_decode_scored_workspace_size(num_seqs, q_per_seq, n_q_heads, n_kv_heads, head_dim,
@@ -431,13 +445,13 @@ def pa_decode_scored(out, q, k_cache, v_cache, block_tables, context_lens, mod: 
     biased scores and masks (mod)."""
     B, *nq, n_q, _ = q.shape
     nq = nq[0] if nq else 1
-    _attention_args(out, q, k_cache, v_cache, block_tables, context_lens, B)
-    d = _desc(k_cache, k_scale, v_scale, q.dtype)
+    d, out_code, width = _attention_args(out, q, k_cache, v_cache, block_tables, context_lens, B,
+                                         k_scale, v_scale)
     m = mod._c(n_q, B * nq, B)
     ws, ws_bytes = (workspace.data_ptr(), workspace.nbytes) if workspace is not None else (None, 0)
     st = lib().pa_decode_scored(
-        out.data_ptr(), dtype_code(out.dtype), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-        C.byref(d), block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), B, nq, n_q,
+        out.data_ptr(), out_code, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        C.byref(d), block_tables.data_ptr(), width, context_lens.data_ptr(), B, nq, n_q,
         scale, block_size, C.byref(m), ws, ws_bytes, _stream(stream))
     if st != PA_OK:
         _check(st, "pa_decode_scored")
@@ -474,13 +488,13 @@ def pa_prefill_scored(out, q, k_cache, v_cache, block_tables, query_start_loc, c
     if query_start_loc.dtype != torch.int32 or query_start_loc.numel() != R + 1 or \
             not query_start_loc.is_contiguous():
         raise ValueError("query_start_loc int32 [R + 1], contiguous, expected")
-    _attention_args(out, q, k_cache, v_cache, block_tables, context_lens, R)
+    d, out_code, width = _attention_args(out, q, k_cache, v_cache, block_tables, context_lens, R,
+                                         k_scale, v_scale)
     _check_device(query_start_loc)
-    d = _desc(k_cache, k_scale, v_scale, q.dtype)
     m = mod._c(n_q, total, R)
     st = lib().pa_prefill_scored(
-        out.data_ptr(), dtype_code(out.dtype), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-        C.byref(d), block_tables.data_ptr(), block_tables.shape[1], query_start_loc.data_ptr(),
+        out.data_ptr(), out_code, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        C.byref(d), block_tables.data_ptr(), width, query_start_loc.data_ptr(),
         context_lens.data_ptr(), R, max_query_len, n_q, scale, block_size, C.byref(m), _stream(stream))
     if st != PA_OK:
         _check(st, "pa_prefill_scored")

@@ -387,8 +387,8 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         }
         if (blockIdx.x == 0) __syncthreads();
         allow_dependent_launch();
-        plan_prefix_unit(sc, sp, n_kv, group, BS, max_blocks, reinterpret_cast<int*>(dyn_smem), s_member,
-                         &s_unit, err);
+        plan_prefix_unit(sc, sp, n_kv, group, BS, max_blocks, context_lens, reinterpret_cast<int*>(dyn_smem),
+                         s_member, &s_unit, err);
         if (!s_unit.live) {
             if (warp == kMmaWarp) tmem_dealloc(s_tmem, kTmemCols);
             return;

@@ -22,11 +22,12 @@ constexpr int kUnitRows = 256, kUnitKeys = 128;
 constexpr int kUnitMembers = kUnitRows + 1;   // members that a row tile can touch
 constexpr float kUnitOverhead = 2.f;
 
-// Every thread of the block calls it.  scratch: 3 * num_groups ints of shared memory;
+// Every thread of the block calls it.  scratch: 4 * num_groups ints of shared memory;
 // members: kUnitMembers ints, filled with the sequences of the unit's rows (member
 // m of the tile serves rows m * group - row0 .. of it, from member row0 / group on).
 __device__ __forceinline__ void plan_prefix_unit(const ScoreParams& sc, const PrefixPass& sp, int n_kv,
-                                                 int group, int block_size, int max_blocks, int* scratch,
+                                                 int group, int block_size, int max_blocks,
+                                                 const int32_t* context_lens, int* scratch,
                                                  int* members, PrefixUnit* unit, unsigned* err)
 {
     __shared__ int s_warp[32];
@@ -35,10 +36,13 @@ __device__ __forceinline__ void plan_prefix_unit(const ScoreParams& sc, const Pr
     int* count = scratch;
     int* first = scratch + G;
     int* prefix = scratch + 2 * G;
+    int* context = scratch + 3 * G;    // longest member's: nothing of the prefix lies past it
     const int mine0 = tid < sp.num_seqs ? __ldg(sc.group_of_seq + tid) : -1;   // in flight meanwhile
+    const int len0 = tid < sp.num_seqs ? __ldg(context_lens + tid) : 0;
     for (int g = tid; g < G; g += threads) {
         count[g] = 0;
         first[g] = INT_MAX;
+        context[g] = 0;
         prefix[g] = prefix_tokens(sc.group_prefix, g, block_size, max_blocks);
     }
     __syncthreads();
@@ -48,11 +52,13 @@ __device__ __forceinline__ void plan_prefix_unit(const ScoreParams& sc, const Pr
         if (g < 0 || g >= G) continue;
         atomicAdd(&count[g], 1);
         atomicMin(&first[g], s);
+        atomicMax(&context[g], s == tid ? len0 : __ldg(context_lens + s));
     }
     __syncthreads();
+    auto prefix_of = [&](int g) { return min(prefix[g], context[g]); };
     auto row_tiles = [&](int g) { return (count[g] * group + kUnitRows - 1) / kUnitRows; };
     auto key_tiles = [&](int g) {
-        return count[g] ? (prefix[g] + kUnitKeys - 1) / kUnitKeys : 0;
+        return count[g] ? (prefix_of(g) + kUnitKeys - 1) / kUnitKeys : 0;
     };
     if (warp == 0) {
         int longest = 0;
@@ -89,7 +95,7 @@ __device__ __forceinline__ void plan_prefix_unit(const ScoreParams& sc, const Pr
                 u.tiles = (u.split + 1) * kt / n - u.tile0;
                 u.rows = count[g] * group;
                 u.first_seq = first[g];
-                u.prefix = prefix[g];
+                u.prefix = prefix_of(g);
                 if (left == 0) sp.splits[g] = n;       // for the merge
                 break;
             }

@@ -222,6 +222,15 @@ def test_q_in_place(interleaved):
     c.check()
 
 
+def test_q_out_may_be_a_slice():
+    c = Case(30, 45, 8, 2, 64, 16, BF, 64, False, 1).start()
+    wide = torch.full((45, 24, 64), float("nan"), dtype=BF, device="cuda")
+    c.q_out = wide[:, 8:16]
+    c.run()
+    c.check()
+    assert torch.isnan(wide[:, :8]).all() and torch.isnan(wide[:, 16:]).all()
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_more_tokens_than_the_grid_covers_at_once(fp8):
     c = Case(29, 3001, 8, 4, 128, 16, BF, 128, False, 9, fp8=fp8).start()

@@ -167,6 +167,19 @@ def test_more_requests_than_are_ranked_and_a_chunk_beyond_the_grid():
     assert pa.pa_get_device_error() == 0
 
 
+def test_rows_behind_the_last_request_are_left_alone():
+    c = Case(38, REQS, 8, 2, 64, 16, BF, window=50)
+    n = c.q.shape[0]
+    c.qd = torch.cat([c.qd, torch.full((9, 8, 64), float("nan"), dtype=BF, device="cuda")])
+    out = torch.full(c.qd.shape, 7.0, device="cuda")
+    c.run(out=out)
+    torch.cuda.synchronize()
+    assert pa.pa_get_device_error() == 0
+    c.qd = c.qd[:n]
+    check(out[:n], c.ref(), 2e-3)
+    assert (out[n:] == 7).all()
+
+
 def test_replayed_graph():
     c = Case(37, REQS, 8, 2, 128, 16, BF, softcap=20.0, doc=100)
     out = torch.zeros(c.q.shape, device="cuda")

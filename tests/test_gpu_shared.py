@@ -140,6 +140,33 @@ def test_members_shorter_than_the_prefix():
     c.test()
 
 
+@pytest.mark.parametrize("form", ["bf16-g4", "fp8-g4", "fp16-g3"])
+def test_a_prefix_past_every_member(form):
+    """Rows of shared blocks that no member has reached yet hold NaN and are not seen."""
+    c = Case(100, [(256, [0, 0, 0]), (96, [4, 20])], [33], *FORMS[form][:5], fp8=FORMS[form][5])
+    for s, L in zip(np.flatnonzero(c.group == 0), [200, 170, 9]):
+        c.p.lens[s] = L
+        c.p.k64[s], c.p.v64[s] = c.p.k64[s][:L], c.p.v64[s][:L]
+    s = int(np.flatnonzero(c.group == 0)[0])
+    at = np.arange(200, 256)
+    b, o = c.p.tables[s, at // c.p.bs].astype(np.int64), at % c.p.bs
+    if c.p.fp8:
+        c.p.kc.view(torch.uint8)[b, :, o] = 0x7F
+        c.p.vc.view(torch.uint8)[b, :, o // 16, :, o % 16] = 0x7F
+    else:
+        c.p.kc[b, :, o] = float("nan")
+        c.p.vc[b, :, o] = float("nan")
+    c.tables[c.gd == 0, -(-200 // c.p.bs):] = -1          # nor are blocks behind them read
+    c.lens = torch.from_numpy(c.p.lens).cuda()
+    c.test()
+
+
+def test_groups_without_members():
+    c = Case(101, [(64, [5, 20])], [300, 33], *FORMS["bf16-g4"][:5])
+    c.gd.fill_(-3)
+    c.test()
+
+
 def test_a_group_out_of_range_is_flagged_and_shares_nothing():
     c = Case(94, [(64, [5, 20]), (96, [1, 2])], [33], *FORMS["bf16-g4"][:5])
     c.gd[c.gd == 1] = 2
