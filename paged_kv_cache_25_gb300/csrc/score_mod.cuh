@@ -34,9 +34,9 @@ __device__ __forceinline__ float soft_cap(float z, float cap2, float cap_rate)
 
 // The prefill's form of the cap, for four raw scores of a row at a time: with
 // t_i = 1 + 2^(rate s_i) and h = -1 / (2C), z_i = C + 1 / (h t_i), and the four quotients
-// share one reciprocal, r = 1 / (h t_0 h t_1 h t_2 h t_3).  The prefill's softmax is bound by
-// its instructions and, with three results of the exponent unit a score (16 results a
-// cycle and SM), by that unit; sharing leaves 2.25 results.  Mixed step's four chunks
+// share one reciprocal, r = 1 / (h t_0 h t_1 h t_2 h t_3).  The prefill is bound by the
+// latency of a tile's softmax, so by the instructions of a score: sharing leaves 4.5 of
+// them and 2.25 results of the exponent unit, against 5 and 3.  Mixed step's four chunks
 // (bf16 / fp16 / FP8 pool): 284 / 256 / 267 us with a reciprocal each, 257 / 221 / 232 with
 // one for two, 251 / 210 / 217 with one for four (193 / 153 / 149 without a cap).  Also
 // measured: tanh as a rational function of degree 7/6 on the FMA pipe (330 / 286 / 301),
