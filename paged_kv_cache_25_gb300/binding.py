@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes as C
 import dataclasses
+import importlib.util
 import os
 import threading
 
@@ -103,6 +104,7 @@ EXPORTED = tuple(_SIGS)
 
 _lock = threading.Lock()
 _lib = None
+_marshal_mod = None
 
 
 class PAError(RuntimeError):
@@ -131,10 +133,9 @@ def lib(path: str | None = None):
 
 
 def dtype_code(dt: torch.dtype) -> int:
-    code = _DT.get(dt)
-    if code is None:
+    if dt not in _DT:
         raise TypeError(f"unsupported dtype {dt}")
-    return code
+    return _DT[dt]
 
 
 def _check(st: int, what: str):
@@ -162,6 +163,10 @@ def _stream(stream) -> int | None:
     return stream
 
 
+def _handle(stream) -> int:
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
 def _desc(k_cache: torch.Tensor, k_scale=None, v_scale=None, act_dtype=None) -> _Desc:
     """Cache descriptor; FP8 pools (torch.float8_e4m3fn) need the two scales and
     the activation dtype (of q and of the rows written into the pool)."""
@@ -173,46 +178,24 @@ def _desc(k_cache: torch.Tensor, k_scale=None, v_scale=None, act_dtype=None) -> 
     return _Desc(nb, bs, n_kv, d, dt, 1.0, 1.0, dt)
 
 
-def _attention_args(out, q, k_cache, v_cache, block_tables, context_lens, seqs: int, k_scale,
-                    v_scale):
-    """Layout checks of a scored or shared-prefix call: what the library reads through bare
-    pointers has the types, the order and the device that it expects.  Returns the cache's
-    descriptor, the code of out's dtype and the tables' width."""
-    if not (out.is_contiguous() and q.is_contiguous() and k_cache.is_contiguous() and
-            v_cache.is_contiguous() and block_tables.is_contiguous() and
-            context_lens.is_contiguous()):
-        raise ValueError("contiguous tensors expected")
-    shape = q.shape
-    nb, n_kv, bs, d = k_cache.shape
-    if out.shape != shape or shape[-1] != d or v_cache.numel() != k_cache.numel():
-        raise ValueError("out and q [..][n_q][d] and pools of that head_dim expected")
-    tables, width = block_tables.shape
-    if tables < seqs or context_lens.numel() < seqs:
-        raise ValueError("a block table and a context length for every sequence expected")
-    if not (block_tables.dtype is context_lens.dtype is torch.int32):
-        raise TypeError("block_tables and context_lens: int32 expected")
-    kv, act = k_cache.dtype, q.dtype
-    fp8 = kv is torch.float8_e4m3fn
-    if v_cache.dtype is not kv or not (fp8 or act is kv):
-        raise TypeError("q and the pools must have one dtype (FP8 pools: bf16 or fp16 q)")
-    if not (torch.cuda.current_device() == q.get_device() == out.get_device() ==
-            k_cache.get_device() == v_cache.get_device() == block_tables.get_device() ==
-            context_lens.get_device()):
-        raise ValueError(_WRONG_DEVICE)
-    code = dtype_code(kv)
-    if fp8:      # missing scales reach the library as 0 and are refused there
-        desc = _Desc(nb, bs, n_kv, d, code, k_scale or 0.0, v_scale or 0.0, dtype_code(act))
-    else:
-        desc = _Desc(nb, bs, n_kv, d, code, 1.0, 1.0, code)
-    return desc, dtype_code(out.dtype), width
-
-
-_WRONG_DEVICE = "the tensors must be on the current CUDA device"
-
-
-def _check_device(t):
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(_WRONG_DEVICE)
+def _marshal():
+    """The compiled argument marshalling of the serving calls (built beside libpa.so)."""
+    global _marshal_mod
+    if _marshal_mod is None:
+        h = lib()
+        with _lock:
+            if _marshal_mod is None:
+                if not os.path.exists(_build.MARSHAL):
+                    raise RuntimeError(f"{_build.MARSHAL} not found: build it first "
+                                       "(python -c 'import __graft_entry__ as g; g.build()')")
+                spec = importlib.util.spec_from_file_location("_pa_marshal", _build.MARSHAL)
+                mod = importlib.util.module_from_spec(spec)
+                spec.loader.exec_module(mod)
+                mod.bind(*(C.cast(getattr(h, n), C.c_void_p).value for n in (
+                    "pa_rope_and_cache", "pa_decode_shared", "pa_decode_scored",
+                    "pa_prefill_scored")))
+                _marshal_mod = mod
+    return _marshal_mod
 
 
 def pa_status_string(st: int) -> str:
@@ -268,52 +251,14 @@ def pa_reshape_and_cache_quant(k, v, k_cache, v_cache, slot_mapping, k_scale=Non
            "pa_reshape_and_cache_quant")
 
 
-def _token_stride(t, T: int, heads: int, d: int) -> int:
-    """Elements from token to token of t [T][heads][d]; a token's heads are contiguous."""
-    tok, head, elem = t.stride()
-    if elem != 1 or (head != d and heads > 1):
-        raise ValueError("[tokens][heads][head_dim] with contiguous heads expected")
-    return tok if T > 1 else heads * d
-
-
 def pa_rope_and_cache(q_out, q, k, v, positions, cos_sin, k_cache, v_cache, slot_mapping,
                       interleaved: bool = False, stream=None, k_scale=None, v_scale=None):
     """q_out [T][n_q][d] = q rotated by its tokens' positions (int32 [T]); k, rotated, and v
     [T][n_kv][d] go to slot_mapping (int64 [T]) of the pools.  q, k and v may be slices of one
     projection (any token stride).  cos_sin: fp32 [max_position][rot_dim], see pa_rope_table.
     FP8 pools take their scales."""
-    T, n_q, hd = shape = q.shape
-    _, n_kv, _, pool_d = k_cache.shape
-    kv_shape = (T, n_kv, hd)
-    if q_out.shape != shape or v.shape != kv_shape or k.shape != kv_shape or hd != pool_d:
-        raise ValueError("q_out, q [T][n_q][d] and k, v [T][n_kv][d] expected")
-    dt = q.dtype
-    if not (dt is q_out.dtype is k.dtype is v.dtype):
-        raise TypeError("q_out, q, k and v must have one dtype")
-    if positions.dtype is not torch.int32 or slot_mapping.dtype is not torch.int64 or \
-            cos_sin.dtype is not torch.float32:
-        raise TypeError("positions int32, slot_mapping int64 and cos_sin float32 expected")
-    max_position, rot_dim = cos_sin.shape
-    if positions.numel() != T or slot_mapping.numel() != T or \
-            not (positions.is_contiguous() and slot_mapping.is_contiguous() and
-                 cos_sin.is_contiguous()):
-        raise ValueError("positions [T], slot_mapping [T] and cos_sin [max_position][rot_dim], "
-                         "contiguous, expected")
-    if not (k_cache.is_contiguous() and v_cache.is_contiguous()) or v_cache.dtype != k_cache.dtype \
-            or v_cache.numel() != k_cache.numel():
-        raise ValueError("contiguous pools of one dtype and size expected")
-    strides = (_token_stride(q_out, T, n_q, hd), _token_stride(q, T, n_q, hd),
-               _token_stride(k, T, n_kv, hd), _token_stride(v, T, n_kv, hd))
-    if not (torch.cuda.current_device() == q.get_device() == q_out.get_device() == k.get_device() ==
-            v.get_device() == positions.get_device() == cos_sin.get_device() ==
-            k_cache.get_device() == v_cache.get_device() == slot_mapping.get_device()):
-        raise ValueError(_WRONG_DEVICE)
-    d = _desc(k_cache, k_scale, v_scale, dt)
-    st = lib().pa_rope_and_cache(
-        q_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), _DT[dt],
-        *strides, positions.data_ptr(), cos_sin.data_ptr(), max_position, rot_dim,
-        interleaved, k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), T, n_q,
-        C.byref(d), _stream(stream))
+    st = _marshal().rope(q_out, q, k, v, positions, cos_sin, k_cache, v_cache, slot_mapping,
+                         interleaved, None if stream is None else _handle(stream), k_scale, v_scale)
     if st != PA_OK:
         _check(st, "pa_rope_and_cache")
 
@@ -370,23 +315,9 @@ def pa_decode_shared(out, q, k_cache, v_cache, block_tables, context_lens, group
                      k_scale=None, v_scale=None):
     """pa_decode with the common prefix of each group of sequences read once: group_of_seq int32
     [B] (negative: none), prefix_lens int32 [groups], see pa_shared_prefix_groups."""
-    B, n_q, _ = q.shape
-    groups = prefix_lens.numel()
-    if group_of_seq.dtype != torch.int32 or prefix_lens.dtype != torch.int32:
-        raise TypeError("group_of_seq and prefix_lens: int32 expected")
-    if group_of_seq.numel() != B or not group_of_seq.is_contiguous() or \
-            not prefix_lens.is_contiguous():
-        raise ValueError("group_of_seq [B] and prefix_lens [groups], contiguous, expected")
-    d, out_code, width = _attention_args(out, q, k_cache, v_cache, block_tables, context_lens, B,
-                                         k_scale, v_scale)
-    _check_device(group_of_seq)
-    _check_device(prefix_lens)
-    ws, ws_bytes = (workspace.data_ptr(), workspace.nbytes) if workspace is not None else (None, 0)
-    st = lib().pa_decode_shared(
-        out.data_ptr(), out_code, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-        C.byref(d), block_tables.data_ptr(), width, context_lens.data_ptr(), B, n_q,
-        scale, block_size, group_of_seq.data_ptr(), prefix_lens.data_ptr(), groups, ws, ws_bytes,
-        _stream(stream))
+    st = _marshal().decode_shared(out, q, k_cache, v_cache, block_tables, context_lens, group_of_seq,
+                                  prefix_lens, scale, block_size, workspace,
+                                  None if stream is None else _handle(stream), k_scale, v_scale)
     if st != PA_OK:
         _check(st, "pa_decode_shared")
 
@@ -415,22 +346,6 @@ class ScoreMod:
     first_key: torch.Tensor | None = None         # int32, one per query row: its first visible key
     prefix_lens: torch.Tensor | None = None       # int32 [requests], prefill: keys every row sees
 
-    def _c(self, n_q: int, rows: int, reqs: int) -> _ScoreMod:
-        ptrs = []
-        for name, t, dt, n in (("alibi_slopes", self.alibi_slopes, torch.float32, n_q),
-                               ("first_key", self.first_key, torch.int32, rows),
-                               ("prefix_lens", self.prefix_lens, torch.int32, reqs)):
-            if t is None:
-                ptrs.append(None)
-                continue
-            if t.dtype != dt:
-                raise TypeError(f"{name}: {dt} expected")
-            if t.numel() != n or not t.is_contiguous():
-                raise ValueError(f"{name}: {n} contiguous values expected")
-            _check_device(t)
-            ptrs.append(t.data_ptr())
-        return _ScoreMod(self.softcap, ptrs[0], self.window, ptrs[1], ptrs[2])
-
 
 def pa_decode_scored_workspace_size(num_seqs, q_per_seq, n_q_heads, n_kv_heads, head_dim,
                                     block_size, max_context_len, window: int = 0) -> int:
@@ -443,16 +358,9 @@ def pa_decode_scored(out, q, k_cache, v_cache, block_tables, context_lens, mod: 
                      v_scale=None):
     """out, q [B][n_q][d] or [B][q_per_seq][n_q][d]: pa_decode / pa_decode_verify with capped or
     biased scores and masks (mod)."""
-    B, *nq, n_q, _ = q.shape
-    nq = nq[0] if nq else 1
-    d, out_code, width = _attention_args(out, q, k_cache, v_cache, block_tables, context_lens, B,
-                                         k_scale, v_scale)
-    m = mod._c(n_q, B * nq, B)
-    ws, ws_bytes = (workspace.data_ptr(), workspace.nbytes) if workspace is not None else (None, 0)
-    st = lib().pa_decode_scored(
-        out.data_ptr(), out_code, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-        C.byref(d), block_tables.data_ptr(), width, context_lens.data_ptr(), B, nq, n_q,
-        scale, block_size, C.byref(m), ws, ws_bytes, _stream(stream))
+    st = _marshal().decode_scored(out, q, k_cache, v_cache, block_tables, context_lens, mod, scale,
+                                  block_size, workspace,
+                                  None if stream is None else _handle(stream), k_scale, v_scale)
     if st != PA_OK:
         _check(st, "pa_decode_scored")
 
@@ -483,19 +391,9 @@ def pa_prefill_scored(out, q, k_cache, v_cache, block_tables, query_start_loc, c
                       stream=None, k_scale=None, v_scale=None):
     """pa_prefill_chunk with capped or biased scores and masks (mod); first_key is [total_q],
     prefix_lens [R]."""
-    R = context_lens.numel()
-    total, n_q, _ = q.shape
-    if query_start_loc.dtype != torch.int32 or query_start_loc.numel() != R + 1 or \
-            not query_start_loc.is_contiguous():
-        raise ValueError("query_start_loc int32 [R + 1], contiguous, expected")
-    d, out_code, width = _attention_args(out, q, k_cache, v_cache, block_tables, context_lens, R,
-                                         k_scale, v_scale)
-    _check_device(query_start_loc)
-    m = mod._c(n_q, total, R)
-    st = lib().pa_prefill_scored(
-        out.data_ptr(), out_code, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-        C.byref(d), block_tables.data_ptr(), width, query_start_loc.data_ptr(),
-        context_lens.data_ptr(), R, max_query_len, n_q, scale, block_size, C.byref(m), _stream(stream))
+    st = _marshal().prefill_scored(out, q, k_cache, v_cache, block_tables, context_lens,
+                                   query_start_loc, max_query_len, mod, scale, block_size,
+                                   None if stream is None else _handle(stream), k_scale, v_scale)
     if st != PA_OK:
         _check(st, "pa_prefill_scored")
 

@@ -2,7 +2,9 @@
 
 Each translation unit compiles in parallel; the shared library links the CUDA
 runtime statically and reaches the driver's tensor-map encoder through the
-runtime's entry-point query, so it needs no -lcuda at link time.
+runtime's entry-point query, so it needs no -lcuda at link time.  Beside it
+_pa_marshal.so, the argument marshalling of the serving calls for Python (C++
+against the installed torch's headers).
 """
 from __future__ import annotations
 
@@ -10,12 +12,15 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 SRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT, "libpa.so")
+MARSHAL = os.path.join(OUT, "_pa_marshal.so")
+MARSHAL_SOURCE = "marshal.cpp"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CUDA_SOURCES = ["api.cu", "cache_write.cu", "cache_rope.cu", "copy_blocks.cu", "decode.cu", "decode_verify.cu", "decode_scored.cu", "decode_no_alloc.cu", "prefill_tc.cu",
                 "prefill_scored.cu", "prefix_pass.cu", "prefill_scored_bias.cu"]
@@ -37,10 +42,22 @@ def _deps():
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(MARSHAL)):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(MARSHAL))
     return any(os.path.getmtime(f) > t for f in _deps())
+
+
+def _torch_flags(nvcc: str):
+    """(compile, link) flags for a Python extension against the installed torch."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    inc = [sysconfig.get_paths()["include"], os.path.join(root, "include"),
+           os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")]
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    return ([x for i in inc for x in ("-isystem", i)] + [f"-D_GLIBCXX_USE_CXX11_ABI={abi}"],
+            ["-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"])
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
@@ -59,6 +76,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     for f in CXX_SOURCES:
         obj = os.path.join(OUT, f + ".o")
         jobs.append((obj, ["g++", "-O2", "-std=c++17", "-fPIC", "-c", os.path.join(SRC, f), "-o", obj]))
+    marshal_obj = os.path.join(OUT, MARSHAL_SOURCE + ".o")
+    cflags, ldflags = _torch_flags(nvcc)
+    jobs.append((marshal_obj, ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", *cflags, "-c",
+                               os.path.join(SRC, MARSHAL_SOURCE), "-o", marshal_obj]))
 
     def run(job):
         obj, cmd = job
@@ -75,13 +96,19 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             raise RuntimeError(f"compile failed: {' '.join(cmd)}")
         if (verbose or ptxas_info) and (p.stdout or p.stderr):
             sys.stderr.write(p.stdout + p.stderr)
-    tmp = LIB + f".{os.getpid()}.tmp"
-    link = [nvcc, *ARCH, "-shared", "-o", tmp, *[o for o, _, _ in results]]
-    p = subprocess.run(link, capture_output=True, text=True)
-    if p.returncode != 0:
-        sys.stderr.write(p.stdout + p.stderr)
-        raise RuntimeError("link failed: " + " ".join(link))
-    os.replace(tmp, LIB)
+
+    def link_to(path, cmd):
+        tmp = path + f".{os.getpid()}.tmp"
+        cmd = [*cmd, "-o", tmp]
+        p = subprocess.run(cmd, capture_output=True, text=True)
+        if p.returncode != 0:
+            sys.stderr.write(p.stdout + p.stderr)
+            raise RuntimeError("link failed: " + " ".join(cmd))
+        os.replace(tmp, path)
+
+    link_to(LIB, [nvcc, *ARCH, "-shared", *[o for o, _, _ in results if o != marshal_obj]])
+    # (takes the library's functions by address; torch's libraries are loaded before it)
+    link_to(MARSHAL, ["g++", "-shared", marshal_obj, *ldflags])
     return LIB
 
 

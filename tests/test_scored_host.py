@@ -123,3 +123,27 @@ def test_bindings_check_layouts_and_types():
         pa.pa_decode_shared(group_of_seq=cl.long(), prefix_lens=cl, **base)
     with pytest.raises(ValueError):
         pa.pa_decode_shared(group_of_seq=cl[:1], prefix_lens=cl, **base)
+
+
+def test_bindings_refuse_what_is_not_on_the_current_device():
+    """Well-formed CPU tensors, and objects that are no tensors, never reach the library."""
+    q = torch.zeros(2, 4, 64, dtype=torch.bfloat16)
+    kv = torch.zeros(2, 2, 64, dtype=torch.bfloat16)
+    kc = torch.zeros(8, 2, 16, 64, dtype=torch.bfloat16)
+    bt, cl = torch.zeros(2, 3, dtype=torch.int32), torch.ones(2, dtype=torch.int32)
+    slots, cs = torch.zeros(2, dtype=torch.int64), torch.zeros(8, 64)
+    qs = torch.zeros(3, dtype=torch.int32)
+    base = dict(out=q, q=q, k_cache=kc, v_cache=kc, block_tables=bt, context_lens=cl, scale=0.1,
+                block_size=16)
+    calls = [lambda **k: pa.pa_decode_scored(mod=pa.ScoreMod(), **{**base, **k}),
+             lambda **k: pa.pa_decode_shared(group_of_seq=cl, prefix_lens=cl, **{**base, **k}),
+             lambda **k: pa.pa_prefill_scored(mod=pa.ScoreMod(), query_start_loc=qs, max_query_len=1,
+                                              **{**base, **k}),
+             lambda **k: pa.pa_rope_and_cache(**{**dict(
+                 q_out=q, q=q, k=kv, v=kv, positions=cl, cos_sin=cs, k_cache=kc, v_cache=kc,
+                 slot_mapping=slots), **k})]
+    for call in calls:
+        with pytest.raises(ValueError, match="current CUDA device"):
+            call(stream=0)
+        with pytest.raises(TypeError):
+            call(stream=0, q=[0.0])
