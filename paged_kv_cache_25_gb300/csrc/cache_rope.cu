@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) rope_f8_kernel
     constexpr int kItems = kVTok * kPieces * kHeads;   // = threads
     static_assert(kItems == kRopeThreads, "one 16-element piece a thread");
     __shared__ __align__(16) uint8_t vt[kHeads][D][kVTok];
-    __shared__ int64_t s_slot[kVTok];
+    __shared__ int64_t s_slot[kVTok], s_byte[kVTok];   // token's slot; its byte of head 0, row 0
     const int tid = threadIdx.x;
     const int head_tiles = (p.n_kv + kHeads - 1) / kHeads;
     const unsigned tile = blockIdx.x - qk_blocks;
@@ -254,7 +254,11 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) rope_f8_kernel
         s_slot[tid] = -1;
         if (t0 + tid < p.num_tokens) {
             const Place w = rope_place(p, t0 + tid);
-            if (rope_written(p, w)) s_slot[tid] = w.slot;
+            if (rope_written(p, w)) {
+                const int64_t b = w.slot / p.block_size, o = w.slot - b * p.block_size;
+                s_slot[tid] = w.slot;
+                s_byte[tid] = (b * p.n_kv * (p.block_size / 16) + o / 16) * (D * 16) + (o & 15);
+            }
         }
     }
     {
@@ -282,17 +286,14 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) rope_f8_kernel
     const int hh = tid / D, d = tid % D, h = h0 + hh;
     if (h >= p.n_kv) return;
     const uint8_t* row = vt[hh][d];
-    auto dst = [&](int64_t sl) {   // byte address of slot sl's code in row d
-        const int64_t b = sl / p.block_size, o = sl - b * p.block_size;
-        return static_cast<uint8_t*>(p.v_cache) +
-               (((b * p.n_kv + h) * (p.block_size / 16) + o / 16) * D + d) * 16 + (o & 15);
-    };
+    uint8_t* const out = static_cast<uint8_t*>(p.v_cache) +
+                         (static_cast<int64_t>(h) * (p.block_size / 16) * D + d) * 16;
     const int64_t s0 = s_slot[0];
     bool whole = s0 >= 0 && s0 % kVTok == 0;
 #pragma unroll
     for (int i = 1; i < kVTok; ++i) whole = whole && s_slot[i] == s0 + i;
     if (whole) {
-        *reinterpret_cast<uint4*>(dst(s0)) = *reinterpret_cast<const uint4*>(row);
+        *reinterpret_cast<uint4*>(out + s_byte[0]) = *reinterpret_cast<const uint4*>(row);
         return;
     }
 #pragma unroll
@@ -300,11 +301,11 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) rope_f8_kernel
         const int64_t a = s_slot[q4];
         if (a >= 0 && a % 4 == 0 && s_slot[q4 + 1] == a + 1 && s_slot[q4 + 2] == a + 2 &&
             s_slot[q4 + 3] == a + 3) {
-            *reinterpret_cast<uint32_t*>(dst(a)) = *reinterpret_cast<const uint32_t*>(row + q4);
+            *reinterpret_cast<uint32_t*>(out + s_byte[q4]) = *reinterpret_cast<const uint32_t*>(row + q4);
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (s_slot[q4 + i] >= 0) *dst(s_slot[q4 + i]) = row[q4 + i];
+                if (s_slot[q4 + i] >= 0) out[s_byte[q4 + i]] = row[q4 + i];
         }
     }
 }
