@@ -254,8 +254,8 @@ pa_status pa_decode_no_alloc(void* out, pa_dtype out_dtype, const void* q,
  * common blocks are read once for all its members instead of once per member.  The
  * result is pa_decode's up to rounding.
  *   group_of_seq  : int32 [num_seqs] on the device, the group of each sequence, or a negative
- *                   value for one that shares nothing.  A value >= num_groups sets
- *                   PA_ERR_OUT_OF_RANGE on the device and counts as negative.
+ *                   value for one that shares nothing.  A value >= num_groups counts as
+ *                   negative and, where groups are read, sets PA_ERR_OUT_OF_RANGE on the device.
  *   prefix_lens   : int32 [num_groups] on the device: tokens that the group's members have in
  *                   common, rounded down to whole blocks (and to the table's width).  The
  *                   members' first prefix_lens / block_size table entries must be the same
@@ -265,7 +265,9 @@ pa_status pa_decode_no_alloc(void* out, pa_dtype out_dtype, const void* q,
  *   workspace     : pa_decode_shared_workspace_size(...) bytes for the same shapes and
  *                   num_groups; other rules as pa_decode's.
  * Both arrays are read on the device only: a captured call follows new groups, lengths and
- * tables.  bf16/fp16/FP8 pools with head_dim 64 or 128 (else PA_ERR_UNSUPPORTED); other
+ * tables.  They are not read where the tables can hold so little (num_seqs *
+ * max_blocks_per_seq blocks of at most 64 MiB together) that reading the prefixes apart
+ * would cost more than it saves: such a call is pa_decode.  bf16/fp16/FP8 pools with head_dim 64 or 128 (else PA_ERR_UNSUPPORTED); other
  * rules as pa_decode.  From fp16 and FP8 pools the prefix's probabilities enter P V as one
  * fp16 part, as in pa_prefill_chunk. */
 pa_status pa_decode_shared(void* out, pa_dtype out_dtype, const void* q,

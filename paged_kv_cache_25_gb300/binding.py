@@ -313,8 +313,9 @@ def pa_decode_shared_workspace_size(num_seqs, n_q_heads, n_kv_heads, head_dim, b
 def pa_decode_shared(out, q, k_cache, v_cache, block_tables, context_lens, group_of_seq,
                      prefix_lens, scale: float, block_size: int, workspace=None, stream=None,
                      k_scale=None, v_scale=None):
-    """pa_decode with the common prefix of each group of sequences read once: group_of_seq int32
-    [B] (negative: none), prefix_lens int32 [groups], see pa_shared_prefix_groups."""
+    """pa_decode with the common prefix of each group of sequences read once (where the tables hold
+    enough for that to pay): group_of_seq int32 [B] (negative: none), prefix_lens int32 [groups],
+    see pa_shared_prefix_groups."""
     st = _marshal().decode_shared(out, q, k_cache, v_cache, block_tables, context_lens, group_of_seq,
                                   prefix_lens, scale, block_size, workspace,
                                   None if stream is None else _handle(stream), k_scale, v_scale)

@@ -112,7 +112,9 @@ def test_prompt_cache_prefill_and_decode_steps():
     group, prefix = pa.pa_shared_prefix_groups(tables, lens, BS)
     assert list(prefix) == [64] and list(group) == [0, 0, 0, 0, -1]
     # decode steps: one captured graph, replayed over the step's tensors
-    bt, gd, pd = dev(tables), dev(group), dev(prefix)
+    # (tables as wide as the longest sequence that the server takes)
+    wide = 2048
+    bt, gd, pd = dev(np.pad(tables, ((0, 0), (0, wide - max_blocks)), constant_values=-1)), dev(group), dev(prefix)
     cl, posd = dev(lens), dev(lens)
     slot = torch.zeros(B, dtype=torch.int64, device="cuda")
     qkv_d = torch.zeros(B, (N_Q + 2 * N_KV) * D, dtype=BF, device="cuda")
@@ -120,9 +122,9 @@ def test_prompt_cache_prefill_and_decode_steps():
     q_out = torch.empty(B, N_Q, D, dtype=BF, device="cuda")
     table_d = m.table.cuda()
     shared, scored = (torch.empty(B, N_Q, D, device="cuda") for _ in range(2))
-    ws = torch.empty(pa.pa_decode_shared_workspace_size(B, N_Q, N_KV, D, BS, max_blocks * BS, 1),
+    ws = torch.empty(pa.pa_decode_shared_workspace_size(B, N_Q, N_KV, D, BS, wide * BS, 1),
                      dtype=torch.uint8, device="cuda")
-    ws2 = torch.empty(pa.pa_decode_scored_workspace_size(B, 1, N_Q, N_KV, D, BS, max_blocks * BS, 60),
+    ws2 = torch.empty(pa.pa_decode_scored_workspace_size(B, 1, N_Q, N_KV, D, BS, wide * BS, 60),
                       dtype=torch.uint8, device="cuda")
 
     def step():

@@ -18,6 +18,9 @@ def _built():
     assert pa.pa_get_device_error() == 0
 
 
+WORTH = 64 << 20      # bytes of the tables' blocks above which prefixes are read apart
+
+
 class Case:
     """groups: list of (prefix tokens, [own tokens of each member]); loners: lengths."""
 
@@ -34,6 +37,12 @@ class Case:
         order = np.random.default_rng(seed).permutation(len(lens)) if shuffle else np.arange(len(lens))
         p.lens, p.tables = p.lens[order], p.tables[order]
         p.k64, p.v64 = [p.k64[i] for i in order], [p.v64[i] for i in order]
+        # Tables wide enough that the prefixes are read apart (the drawn ones, `narrow` columns,
+        # mostly hold too little for that).
+        self.narrow = p.tables.shape[1]
+        block = 2 * n_kv * bs * d * (1 if fp8 else 2)
+        wide = max(self.narrow, WORTH // (block * len(lens)) + 1)
+        p.tables = np.pad(p.tables, ((0, 0), (0, wide - self.narrow)), constant_values=-1)
         self.group = np.array(gid, np.int32)[order]
         self.prefix = np.array([g[0] for g in groups], np.int32)
         g = torch.Generator().manual_seed(seed + 1)
@@ -41,7 +50,8 @@ class Case:
         self.dtype, self.n_q = dtype, n_q
         self.tables, self.lens = p.dev()
         self.gd, self.pd = torch.from_numpy(self.group).cuda(), torch.from_numpy(self.prefix).cuda()
-        size = pa.pa_decode_shared_workspace_size(len(lens), n_q, n_kv, d, bs, p.max_ctx, len(groups))
+        size = max(pa.pa_decode_shared_workspace_size(len(lens), n_q, n_kv, d, bs, n * bs, len(groups))
+                   for n in (wide, self.narrow))
         self.ws = torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda")   # NaN partials
 
     def run(self, out_dtype=FF, out=None):
@@ -59,7 +69,13 @@ class Case:
         out = self.run()
         torch.cuda.synchronize()
         assert pa.pa_get_device_error() == error
-        check(out, self.ref(), 2e-3)
+        ref = self.ref()
+        check(out, ref, 2e-3)
+        if not error:                                  # and with the drawn tables
+            wide, self.tables = self.tables, self.tables[:, :self.narrow].contiguous()
+            check(self.run(), ref, 2e-3)
+            assert pa.pa_get_device_error() == 0
+            self.tables = wide
         return out
 
 
@@ -180,6 +196,26 @@ def test_a_bad_prefix_block_is_flagged():
     c.run()
     torch.cuda.synchronize()
     assert pa.pa_get_device_error() == pa.PA_ERR_OUT_OF_RANGE
+
+
+@pytest.mark.parametrize("form", ["bf16-g4", "fp8-g4"])
+def test_a_call_with_small_tables_is_pa_decode(form):
+    """Up to and including the limit bit for bit; one block more reads the prefixes apart."""
+    n_q, n_kv, d, bs, _, fp8 = FORMS[form]
+    c = Case(102, [(64, [5, 20, 33])], [40], *FORMS[form][:5], fp8=fp8)
+    at_most = WORTH // (2 * n_kv * bs * d * (1 if fp8 else 2) * 4)
+    assert c.tables.shape[1] == at_most + 1
+    c.gd[c.gd == 0] = 7                                # flagged only where groups are read
+    c.run()
+    torch.cuda.synchronize()
+    assert pa.pa_get_device_error() == pa.PA_ERR_OUT_OF_RANGE
+    c.tables = c.tables[:, :at_most].contiguous()
+    plain = torch.empty(c.q.shape, device="cuda")
+    ws = torch.empty(pa.pa_decode_workspace_size(4, n_q, n_kv, d, bs, at_most * bs), dtype=torch.uint8,
+                     device="cuda")
+    pa.pa_decode(plain, c.q, c.p.kc, c.p.vc, c.tables, c.lens, c.p.scale, bs, ws, **c.p.scales)
+    assert torch.equal(c.run(), plain)
+    assert pa.pa_get_device_error() == 0
 
 
 @pytest.mark.parametrize("out_dtype", [BF, FH])
