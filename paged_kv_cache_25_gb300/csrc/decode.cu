@@ -8,24 +8,15 @@
 
 namespace pa {
 
-__device__ __forceinline__ int simt_first(const NoScore&, int, int, int) { return 0; }
-// first visible key of a sequence's only row (past its position: it sees none)
-__device__ __forceinline__ int simt_first(const ScoreParams& sc, int s, int L, int lo)
-{
-    return max(lo, row_first(sc, s, 1, 0, L - 1));
-}
-
-// CUDA-core path: one warp per (partition, query head, sequence).  SC: scored decode
-// (score_mod.cuh); the sequence's keys start at its first visible block.
-template <typename T, int DPL, bool SC>
+// CUDA-core path: one warp per (partition, query head, sequence).
+template <typename T, int DPL>
 __global__ void __launch_bounds__(128)
 decode_simt_kernel(void* __restrict__ out, pa_dtype out_dtype, const T* __restrict__ q,
                    const T* __restrict__ kc, const T* __restrict__ vc,
                    const int32_t* __restrict__ block_tables, int max_blocks,
                    const int32_t* __restrict__ context_lens, int n_q, int n_kv, int group,
                    int num_blocks, int block_size, float scale_log2, float* __restrict__ ws_ml,
-                   float* __restrict__ ws_acc, int part_tokens, int max_parts, unsigned* err,
-                   const std::conditional_t<SC, ScoreParams, NoScore> sc)
+                   float* __restrict__ ws_acc, int part_tokens, int max_parts, unsigned* err)
 {
     constexpr int D = DPL * 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -35,18 +26,10 @@ decode_simt_kernel(void* __restrict__ out, pa_dtype out_dtype, const T* __restri
     if (h >= n_q) return;
     const int kvh = h / group;
     const int L = __ldg(context_lens + s);
-    int lo = 0;              // SC: first visible key
-    float slope = 0.f;
-    if constexpr (SC) {
-        lo = first_visible(sc, s, L, 1, block_size, max_blocks, err);
-        if (sc.slopes) slope = __ldg(sc.slopes + h) * kLog2e;
-    }
-    const int base = lo / block_size * block_size;
-    const int tok0 = base + j * part_tokens;
+    const int tok0 = j * part_tokens;
     if (tok0 >= L) return;
     const int tok1 = min(L, tok0 + part_tokens);
-    const int nparts = min((L - base + part_tokens - 1) / part_tokens, max_parts);
-    const int first = simt_first(sc, s, L, lo);
+    const int nparts = min((L + part_tokens - 1) / part_tokens, max_parts);
 
     float qv[DPL], acc[DPL];
     const T* qp = q + (static_cast<int64_t>(s) * n_q + h) * D;
@@ -59,8 +42,7 @@ decode_simt_kernel(void* __restrict__ out, pa_dtype out_dtype, const T* __restri
     // tokens in groups of kTok: their K/V rows are loaded before any of them is
     // used, so the loads of a group overlap (one token at a time left every
     // warp waiting on one row's latency per token)
-    // (a scored call takes eight while their registers fit: a short context is all latency)
-    constexpr int kTok = SC && DPL <= 4 ? 8 : 4;
+    constexpr int kTok = 4;
     const int32_t* table = block_tables + static_cast<int64_t>(s) * max_blocks;
     for (int p0 = tok0; p0 < tok1; p0 += kTok) {
         float kf[kTok][DPL], vf[kTok][DPL];
@@ -68,7 +50,7 @@ decode_simt_kernel(void* __restrict__ out, pa_dtype out_dtype, const T* __restri
 #pragma unroll
         for (int u = 0; u < kTok; ++u) {
             const int p = p0 + u;
-            if (p < tok1 && p >= first) {
+            if (p < tok1) {
                 const int lb = p / block_size;
                 const int b = lb < max_blocks ? __ldg(table + lb) : -1;
                 bad = bad || b < 0 || b >= num_blocks;
@@ -105,20 +87,14 @@ decode_simt_kernel(void* __restrict__ out, pa_dtype out_dtype, const T* __restri
         float m_new = m_run;
 #pragma unroll
         for (int u = 0; u < kTok; ++u) {
-            z[u] *= scale_log2;
-            if constexpr (SC) {
-                if (sc.cap2 > 0.f) z[u] = sc.cap2 * tanhf(z[u] / sc.cap2);
-                z[u] = fmaf(slope, static_cast<float>(p0 + u + 1 - L), z[u]);
-            }
-            z[u] = p0 + u < tok1 && p0 + u >= first ? z[u] : -INFINITY;
+            z[u] = p0 + u < tok1 ? z[u] * scale_log2 : -INFINITY;
             m_new = fmaxf(m_new, z[u]);
         }
-        if (SC && m_new == -INFINITY) continue;     // no visible key so far
         const float alpha = exp2f(m_run - m_new);   // 0 on the first group (m_run = -inf)
         float pz[kTok], psum = 0.f;
 #pragma unroll
         for (int u = 0; u < kTok; ++u) {
-            pz[u] = p0 + u < tok1 ? exp2f(z[u] - m_new) : 0.f;   // (0 for a masked key: z = -inf)
+            pz[u] = p0 + u < tok1 ? exp2f(z[u] - m_new) : 0.f;
             psum += pz[u];
         }
         l_run = l_run * alpha + psum;
@@ -134,11 +110,9 @@ decode_simt_kernel(void* __restrict__ out, pa_dtype out_dtype, const T* __restri
     const int64_t sh = static_cast<int64_t>(s) * n_q + h;
     if (nparts == 1) {
 #pragma unroll
-        for (int i = 0; i < DPL; ++i)
-            store_any(out, sh * D + lane + 32 * i, SC && l_run == 0.f ? 0.f : acc[i] / l_run, out_dtype);
+        for (int i = 0; i < DPL; ++i) store_any(out, sh * D + lane + 32 * i, acc[i] / l_run, out_dtype);
     } else {
-        int64_t u = sh * max_parts + j;
-        if constexpr (SC) u = sh * sc.slots + sc.slot0 + j;
+        const int64_t u = sh * max_parts + j;
 #pragma unroll
         for (int i = 0; i < DPL; ++i) ws_acc[u * D + lane + 32 * i] = acc[i];
         if (lane == 0) {
@@ -268,39 +242,28 @@ decode_reduce_kernel(void* __restrict__ out, pa_dtype out_dtype,
 
 // ------------------------------------------------------------------ launch
 
-template <typename T, int DPL, bool SC>
+template <typename T, int DPL>
 static cudaError_t run_simt(const DecodeArgs& a, cudaStream_t s, float scale_log2)
 {
     dim3 grid(a.max_parts, (a.n_q + 3) / 4, a.num_seqs);
-    decode_simt_kernel<T, DPL, SC><<<grid, 128, 0, s>>>(
+    decode_simt_kernel<T, DPL><<<grid, 128, 0, s>>>(
         a.out, a.out_dtype, static_cast<const T*>(a.q), static_cast<const T*>(a.k_cache),
         static_cast<const T*>(a.v_cache), a.block_tables, a.max_blocks, a.context_lens, a.n_q,
         a.cache.n_kv_heads, a.n_q / a.cache.n_kv_heads, a.cache.num_blocks, a.cache.block_size,
-        scale_log2, a.ws_ml, a.ws_acc, a.part_tokens, a.max_parts, a.err,
-        score_params<SC>(a));
+        scale_log2, a.ws_ml, a.ws_acc, a.part_tokens, a.max_parts, a.err);
     return cudaGetLastError();
 }
 
-template <typename T, bool SC>
+template <typename T>
 static cudaError_t run_simt_dt(const DecodeArgs& a, cudaStream_t s, float sl2)
 {
     switch (a.cache.head_dim) {
-        case 32: return run_simt<T, 1, SC>(a, s, sl2);
-        case 64: return run_simt<T, 2, SC>(a, s, sl2);
-        case 96: return run_simt<T, 3, SC>(a, s, sl2);
-        case 128: return run_simt<T, 4, SC>(a, s, sl2);
-        case 256: return run_simt<T, 8, SC>(a, s, sl2);
+        case 32: return run_simt<T, 1>(a, s, sl2);
+        case 64: return run_simt<T, 2>(a, s, sl2);
+        case 96: return run_simt<T, 3>(a, s, sl2);
+        case 128: return run_simt<T, 4>(a, s, sl2);
+        case 256: return run_simt<T, 8>(a, s, sl2);
         default: return cudaErrorInvalidValue;
-    }
-}
-
-template <bool SC>
-static cudaError_t run_simt_any(const DecodeArgs& a, cudaStream_t s, float sl2)
-{
-    switch (a.cache.dtype) {
-        case PA_BF16: return run_simt_dt<__nv_bfloat16, SC>(a, s, sl2);
-        case PA_F16: return run_simt_dt<__half, SC>(a, s, sl2);
-        default: return run_simt_dt<float, SC>(a, s, sl2);
     }
 }
 
@@ -359,12 +322,18 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t s)
     cudaError_t e;
     if (a.score) {
         e = launch_decode_scored(a, s, sl2);
-        if (e == cudaErrorNotSupported && a.q_per_seq == 1) e = run_simt_any<true>(a, s, sl2);
+        if (e == cudaErrorNotSupported && a.q_per_seq == 1) e = launch_decode_scored_simt(a, s, sl2);
     } else if (a.q_per_seq > 1) {
         e = launch_decode_mq(a, s, sl2);
     } else {
         e = run_mma_any<false>(a, s, sl2);
-        if (e == cudaErrorNotSupported) e = run_simt_any<false>(a, s, sl2);   // fp32 pools, other head dims
+        if (e == cudaErrorNotSupported) {        // fp32 pools, other head dims
+            switch (a.cache.dtype) {
+                case PA_BF16: e = run_simt_dt<__nv_bfloat16>(a, s, sl2); break;
+                case PA_F16: e = run_simt_dt<__half>(a, s, sl2); break;
+                default: e = run_simt_dt<float>(a, s, sl2); break;
+            }
+        }
     }
     if (ev1) cudaEventRecord(ev1, s);
     if (e != cudaSuccess) return e;

@@ -99,6 +99,7 @@ struct DecodeArgs {
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t s);
 // attention kernel of a scored or shared-prefix call (decode_scored.cu)
 cudaError_t launch_decode_scored(const DecodeArgs& a, cudaStream_t s, float scale_log2);
+cudaError_t launch_decode_scored_simt(const DecodeArgs& a, cudaStream_t s, float scale_log2);
 // prefix pass of a shared-prefix call (prefix_pass.cu)
 cudaError_t launch_prefix_pass(const DecodeArgs& a, const PrefixPass& pass, cudaStream_t s);
 // attention kernel of a call with q_per_seq > 1 (decode_verify.cu)
