@@ -212,3 +212,40 @@ def test_two_streams_with_workspaces_of_their_own_and_a_replayed_graph():
     a.pos = a.p.lens[:, None].astype(np.int64) - 1
     check(out, a.ref(), 2e-3)
     assert pa.pa_get_device_error() == 0
+
+
+CUDA_CORE = {   # (n_q, n_kv, d, bs, dtype): one, two and four heads a block, chunks with spare heads
+    "fp32-d128-g4": (8, 2, 128, 16, FF),
+    "fp32-d128-g2": (4, 2, 128, 32, FF),
+    "fp32-d128-mha": (3, 3, 128, 16, FF),
+    "fp32-d32-g5": (10, 2, 32, 16, FF),
+    "fp32-d64-g7": (7, 1, 64, 32, FF),
+    "fp32-d256-g3": (6, 2, 256, 16, FF),
+    "fp16-d32-g3": (6, 2, 32, 32, FH),
+    "bf16-d96-mha": (3, 3, 96, 16, BF),
+    "fp16-d96-g6": (6, 1, 96, 16, FH),
+    "fp16-d256-mha": (2, 2, 256, 32, FH),
+}
+
+
+@pytest.mark.parametrize("mod", ["none", "cap-bias", "window1", "window37-cap", "window700-bias"])
+@pytest.mark.parametrize("form", CUDA_CORE)
+def test_cuda_core_decode(form, mod):
+    n_q, n_kv, d, bs, dtype = CUDA_CORE[form]
+    Case(2000 + 10 * sorted(CUDA_CORE).index(form) + sorted(MODS).index(mod), LENS, n_q, n_kv, d, bs,
+         dtype, **MODS[mod]).test()
+
+
+@pytest.mark.parametrize("form", ["fp32-d128-g4", "bf16-d96-mha"])
+def test_cuda_core_rows_without_a_key_and_bad_blocks(form):
+    n_q, n_kv, d, bs, dtype = CUDA_CORE[form]
+    first = np.zeros((3, 1), np.int64)
+    first[1] = 2 ** 30                              # sees nothing
+    c = Case(2200, [300, 40, 77], n_q, n_kv, d, bs, dtype, first=first, spoil=False)
+    c.test()
+    assert not c.run()[1].any()
+    c.tables[2, 1] = c.p.nb                         # the other sequences are not touched by it
+    out = c.run()
+    torch.cuda.synchronize()
+    assert pa.pa_get_device_error() == pa.PA_ERR_OUT_OF_RANGE
+    check(out[:2], c.ref()[:2], tolerance(dtype))
