@@ -163,8 +163,8 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     using Cfg = DecodeCfg<T, D, NS, FP8, RU>;
     static_assert(!FP8 || std::is_same<T, __half>::value, "FP8 pools compute in fp16");
     constexpr bool R16 = RU == 16;
-    static_assert(RU == 8 || (RU == 16 && MQ && !FP8) || (RU == 4 && FP8 && !MQ),
-                  "16-row units: multi-query, 16-bit pools; 4-row units: FP8 decode");
+    static_assert(RU == 8 || (RU == 16 && MQ && (SC || !FP8)) || (RU == 4 && FP8 && !MQ),
+                  "16-row units: multi-query, 16-bit pools or scored; 4-row units: FP8 decode");
     // Transposed FP8 decode (RU 4): S^T = K q^T with the stage's 16 tokens as
     // the M rows and 8 columns: the unit's <= 4 heads, then the same heads
     // again (same q).  Columns 0-3 carry P's hi part and columns 4-7 its lo
@@ -337,6 +337,7 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     uint32_t qa[D / 16][2];
     uint32_t qb[R16 ? D / 16 : 1][2];
     float row_l2 = scale_log2;   // softmax scale (log2 domain) of row g's scores
+    float row_l2b = scale_log2;  // RU 16: of row g + 8's
     // the unit row this thread's q fragments hold: row g, or (kTr) column g,
     // whose head is g mod 4
     const int gq = kTr ? (g & 3) : g;
@@ -347,6 +348,16 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             // overlaps the combine)
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
+                if constexpr (R16) {
+                    qb[kk][0] = qb[kk][1] = 0u;
+                    if (g + 8 < x.nh) {
+                        const int hh = (x.r0 + g + 8) / nq, qi = x.r0 + g + 8 - hh * nq;
+                        const QT* row =
+                            q + ((static_cast<int64_t>(x.s) * nq + qi) * n_q + x.h0 + hh) * D + kk * 16;
+                        qb[kk][0] = __ldg(reinterpret_cast<const unsigned int*>(row + 4 * t4));
+                        qb[kk][1] = __ldg(reinterpret_cast<const unsigned int*>(row + 4 * t4 + 2));
+                    }
+                }
                 if (gq < x.nh) {
                     const int hh = (x.r0 + gq) / nq, qi = x.r0 + gq - hh * nq;
                     const QT* row =
@@ -365,8 +376,8 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                         const int hh = (x.r0 + g + 8) / nq, qi = x.r0 + g + 8 - hh * nq;
                         const QT* row =
                             q + ((static_cast<int64_t>(x.s) * nq + qi) * n_q + x.h0 + hh) * D + kk * 16;
-                        qb[kk][0] = q_pair<QT, T>(row + 2 * t4);
-                        qb[kk][1] = q_pair<QT, T>(row + 2 * t4 + 8);
+                        qb[kk][0] = q_pair<QT, T>(row + (FP8 ? 4 : 2) * t4);
+                        qb[kk][1] = q_pair<QT, T>(row + (FP8 ? 4 * t4 + 2 : 2 * t4 + 8));
                     } else {
                         qb[kk][0] = 0u;
                         qb[kk][1] = 0u;
@@ -397,27 +408,31 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     // that this lands in [2^14, 2^15), exact for every element down to 2^-29 of
     // the largest, and 2^e goes into the row's softmax scale: no bf16 query
     // overflows fp16 or sinks into its subnormals.
+    auto scale_row = [&](auto& qx, float& l2) {
+        uint32_t amax = 0;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                amax = max(amax, max(qx[kk][h] & 0x7FFFu, (qx[kk][h] >> 16) & 0x7FFFu));
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        // e from the exponent field (bf16 subnormals take the floor, -100)
+        const int e = amax == 0u ? 0 : max(static_cast<int>((amax >> 7) & 0xFFu) - 141, -100);
+        l2 = scale_log2 * __int_as_float((127 + e) << 23);        // exact: powers of two
+        const float down = __int_as_float((127 - e) << 23);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float2 f = Cvt<__nv_bfloat16>::unpack(qx[kk][h]);
+                qx[kk][h] = Cvt<__half>::pack(f.x * down, f.y * down);
+            }
+    };
     auto scale_q = [&]() {
         if constexpr (FP8 && std::is_same<QT, __nv_bfloat16>::value) {
-            uint32_t amax = 0;
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    amax = max(amax, max(qa[kk][h] & 0x7FFFu, (qa[kk][h] >> 16) & 0x7FFFu));
-            amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-            amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            // e from the exponent field (bf16 subnormals take the floor, -100)
-            const int e = amax == 0u ? 0 : max(static_cast<int>((amax >> 7) & 0xFFu) - 141, -100);
-            row_l2 = scale_log2 * __int_as_float((127 + e) << 23);    // exact: powers of two
-            const float down = __int_as_float((127 - e) << 23);
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float2 f = Cvt<__nv_bfloat16>::unpack(qa[kk][h]);
-                    qa[kk][h] = Cvt<__half>::pack(f.x * down, f.y * down);
-                }
+            scale_row(qa, row_l2);
+            if constexpr (R16) scale_row(qb, row_l2b);
         }
     };
     // stage k of a unit (blk = its block ids, kvh_ its KV head) into this
@@ -753,7 +768,8 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 #pragma unroll
                                 for (int jj = 0; jj < 4; ++jj) {
                                     const int kk = kq * 4 + jj;
-                                    const uint32_t a[4] = {qa[kk][0], 0u, qa[kk][1], 0u};
+                                    const uint32_t a[4] = {qa[kk][0], R16 ? qb[R16 ? kk : 0][0] : 0u, qa[kk][1],
+                                                           R16 ? qb[R16 ? kk : 0][1] : 0u};
                                     uint32_t b0, b1;
                                     e4m3x4_to_h2x2(w[jj], b0, b1);
                                     // two accumulator chains (even / odd 16 columns) halve the
@@ -824,9 +840,9 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                         for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
                             for (int e = 2; e < 4; ++e) {
-                                const int p = pos0 + nt * 8 + 2 * t4 + e - 2;
+                                const int p = pos0 + (FP8 ? 4 * t4 + 2 * nt : nt * 8 + 2 * t4) + e - 2;
                                 const bool in = p < lim1 && (!SC || p >= first1);
-                                const float z = in ? modify(sv[nt][e] * scale_log2, slope1, p + 1 - lim1) : -INFINITY;
+                                const float z = in ? modify(sv[nt][e] * row_l2b, slope1, p + 1 - lim1) : -INFINITY;
                                 sv[nt][e] = z;
                                 mx1 = fmaxf(mx1, z);
                             }
@@ -888,6 +904,7 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                                 uint32_t b0, b1;
                                 e4m3x4_to_h2x2(w[jj], b0, b1);
                                 MmaOp<T>::run(o[nd + jj], pa, b0, b1);
+                                if constexpr (R16) MmaOp<T>::run(o[nd + jj], pb, b0, b1);
                             }
                         }
                     } else {
@@ -1142,6 +1159,21 @@ cudaError_t run_fp8_qt(const DecodeArgs& a, cudaStream_t s, float sl2)
             if (D == 64 && BS == 32) return run_mma<__half, QT, 64, 32, true, false, 4, SC>(a, s, sl2);
             if (D == 128 && BS == 16) return run_mma<__half, QT, 128, 16, true, false, 4, SC>(a, s, sl2);
             if (D == 128 && BS == 32) return run_mma<__half, QT, 128, 32, true, false, 4, SC>(a, s, sl2);
+            return cudaErrorNotSupported;
+        }
+    }
+    if constexpr (MQ && SC) {
+        // more than 8 rows: 16-row units as for 16-bit pools (256 sequences, 4 rows, Llama-3-8B's
+        // heads: 472 -> 351 us; two CTAs an SM without the few spills: 382), unless two 8-row
+        // units for each still leave SMs short of work (12 sequences of 770: 11.4 against 12.7)
+        const int rows = a.q_per_seq * (a.n_q / a.cache.n_kv_heads);
+        const int64_t units16 = static_cast<int64_t>(a.num_seqs) * a.max_parts * a.cache.n_kv_heads *
+                                ((rows + 15) / 16);
+        if (rows > 8 && units16 >= 2 * decode_sm_count()) {
+            if (D == 64 && BS == 16) return run_mma<__half, QT, 64, 16, true, MQ, 16, SC>(a, s, sl2);
+            if (D == 64 && BS == 32) return run_mma<__half, QT, 64, 32, true, MQ, 16, SC>(a, s, sl2);
+            if (D == 128 && BS == 16) return run_mma<__half, QT, 128, 16, true, MQ, 16, SC>(a, s, sl2);
+            if (D == 128 && BS == 32) return run_mma<__half, QT, 128, 32, true, MQ, 16, SC>(a, s, sl2);
             return cudaErrorNotSupported;
         }
     }

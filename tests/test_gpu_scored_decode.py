@@ -249,3 +249,19 @@ def test_cuda_core_rows_without_a_key_and_bad_blocks(form):
     torch.cuda.synchronize()
     assert pa.pa_get_device_error() == pa.PA_ERR_OUT_OF_RANGE
     check(out[:2], c.ref()[:2], tolerance(dtype))
+
+
+@pytest.mark.parametrize("mod", ["none", "cap-bias", "window1", "window37-cap", "window700-bias"])
+@pytest.mark.parametrize("form", [(8, 2, 128, 16, BF, 4), (8, 2, 128, 32, FH, 4), (16, 1, 128, 16, BF, 2),
+                                  (10, 2, 64, 16, BF, 2), (6, 2, 64, 32, FH, 7)],
+                         ids=lambda f: "-".join(map(str, f)))
+def test_sixteen_rows_over_an_fp8_pool(form, mod):
+    n_q, n_kv, d, bs, dtype, nq = form
+    c = Case(2300 + sorted(MODS).index(mod), [max(L, nq) for L in LENS], n_q, n_kv, d, bs, dtype, nq,
+             fp8=True, max_blocks=2 ** 15 // bs, **MODS[mod])     # (a table that wide counts as much work)
+    if mod == "none" and dtype == BF:      # rows of very different size: each has its own scale
+        grow = 2.0 ** torch.arange(-12, 12, 24 / (nq * n_q)).view(1, nq, n_q, 1)[:, :nq]
+        small = c.q.float() * grow.clamp(max=1.0)
+        c.q = small.to(BF)
+        c.qd = c.q.cuda()
+    c.test()
