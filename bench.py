@@ -42,9 +42,9 @@ FALLBACK_HBM_GBS = 6800.0
 # K/V bytes of the captured launch, what was captured); a record of another
 # batch of the same workload is scaled by its unique K/V bytes.
 NCU_TRAFFIC = {
-    ("llama3-8b-bf16", "ccc70de059a9bc00"): (2372029184 + 13405952, 2359717888,
+    ("llama3-8b-bf16", "034c34a0e73d16f3"): (2371994880 + 13447168, 2359717888,
                                              "full 256-sequence batch, one-pass capture"),
-    ("llama3-8b-fp8", "ccc70de059a9bc00"): (1188178432 + 12422400, 1179858944,
+    ("llama3-8b-fp8", "034c34a0e73d16f3"): (1188182272 + 12398592, 1179858944,
                                             "full 256-sequence batch, one-pass capture"),
 }
 # chunked prefill of the mixed step (the compact-pool capture runs the same four

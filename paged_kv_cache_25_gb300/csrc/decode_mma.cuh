@@ -625,13 +625,26 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                 }
             }
         }
-        // a visible score (log2 domain) with the cap and the bias; `ahead` = key - query position
-        auto modify = [&](float z, float slope, int ahead) -> float {
+        // the cap and the bias of four scores (log2 domain) of rows with slopes sa, sb, sa, sb; keys
+        // `ahead` and `ahead` + far of the row's position.  Branches that the whole grid takes
+        // alike, once for the four.
+        auto modify = [&](float& za, float& zb, float& zc, float& zd, float sa, float sb, int ahead, float far,
+                          int ahead_b) {
             if constexpr (SC) {
-                if (sc.cap2 > 0.f) z = soft_cap(z, sc.cap2, sc.cap_rate);
-                return fmaf(slope, static_cast<float>(ahead), z);
+                if (sc.cap2 > 0.f) {
+                    za = soft_cap(za, sc.cap2, sc.cap_rate);
+                    zb = soft_cap(zb, sc.cap2, sc.cap_rate);
+                    zc = soft_cap(zc, sc.cap2, sc.cap_rate);
+                    zd = soft_cap(zd, sc.cap2, sc.cap_rate);
+                }
+                if (sc.slopes) {
+                    const float fa = static_cast<float>(ahead), fb = static_cast<float>(ahead_b);
+                    za = fmaf(sa, fa, za);
+                    zb = fmaf(sb, fb, zb);
+                    zc = fmaf(sa, fa + far, zc);
+                    zd = fmaf(sb, fb + far, zd);
+                }
             }
-            return z;
         };
         int timed_out = 0;
         if (cu.live) {
@@ -694,10 +707,13 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                     const int tA = pos0 + 4 * (g >> 1) + (g & 1);
                     const bool inA = tA < L && (!SC || tA >= first0);
                     const bool inB = tA + 2 < L && (!SC || tA + 2 >= first0);
-                    const float z0 = inA ? modify((st[0] + st2[0]) * cl2_0, slope0, tA + 1 - L) : -INFINITY;
-                    const float z1 = inA ? modify((st[1] + st2[1]) * cl2_1, slope1, tA + 1 - L) : -INFINITY;
-                    const float z2 = inB ? modify((st[2] + st2[2]) * cl2_0, slope0, tA + 3 - L) : -INFINITY;
-                    const float z3 = inB ? modify((st[3] + st2[3]) * cl2_1, slope1, tA + 3 - L) : -INFINITY;
+                    float z0 = (st[0] + st2[0]) * cl2_0, z1 = (st[1] + st2[1]) * cl2_1;
+                    float z2 = (st[2] + st2[2]) * cl2_0, z3 = (st[3] + st2[3]) * cl2_1;
+                    modify(z0, z1, z2, z3, slope0, slope1, tA + 1 - L, 2.f, tA + 1 - L);
+                    z0 = inA ? z0 : -INFINITY;
+                    z1 = inA ? z1 : -INFINITY;
+                    z2 = inB ? z2 : -INFINITY;
+                    z3 = inB ? z3 : -INFINITY;
                     float mx0 = fmaxf(z0, z2), mx1 = fmaxf(z1, z3);
 #pragma unroll
                     for (int w = 4; w < 32; w <<= 1) {
@@ -816,14 +832,22 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                     }
 
                     // online softmax on row g (log2 domain)
+                    // (this thread's keys: k0, k0 + 1 and the same kFar on)
+                    constexpr int kFar = FP8 ? 2 : 8;
+                    const int k0 = pos0 + (FP8 ? 4 : 2) * t4;
                     float mx = -INFINITY;
 #pragma unroll
                     for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
+                        for (int e = 0; e < 2; ++e) sv[nt][e] *= row_l2;
+                    modify(sv[0][0], sv[0][1], sv[1][0], sv[1][1], slope0, slope0, k0 + 1 - lim, kFar,
+                           k0 + 2 - lim);
+#pragma unroll
+                    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const int p = pos0 + (FP8 ? 4 * t4 + 2 * nt + e : nt * 8 + 2 * t4 + e);
-                            const bool in = p < lim && (!SC || p >= first0);
-                            const float z = in ? modify(sv[nt][e] * row_l2, slope0, p + 1 - lim) : -INFINITY;
+                            const int p = k0 + nt * kFar + e;
+                            const float z = p < lim && (!SC || p >= first0) ? sv[nt][e] : -INFINITY;
                             sv[nt][e] = z;
                             mx = fmaxf(mx, z);
                         }
@@ -839,10 +863,15 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 #pragma unroll
                         for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
+                            for (int e = 2; e < 4; ++e) sv[nt][e] *= row_l2b;
+                        modify(sv[0][2], sv[0][3], sv[1][2], sv[1][3], slope1, slope1, k0 + 1 - lim1, kFar,
+                               k0 + 2 - lim1);
+#pragma unroll
+                        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
                             for (int e = 2; e < 4; ++e) {
-                                const int p = pos0 + (FP8 ? 4 * t4 + 2 * nt : nt * 8 + 2 * t4) + e - 2;
-                                const bool in = p < lim1 && (!SC || p >= first1);
-                                const float z = in ? modify(sv[nt][e] * row_l2b, slope1, p + 1 - lim1) : -INFINITY;
+                                const int p = k0 + nt * kFar + e - 2;
+                                const float z = p < lim1 && (!SC || p >= first1) ? sv[nt][e] : -INFINITY;
                                 sv[nt][e] = z;
                                 mx1 = fmaxf(mx1, z);
                             }
