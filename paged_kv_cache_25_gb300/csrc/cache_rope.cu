@@ -220,23 +220,25 @@ __device__ __forceinline__ void rope_rows(const RopeParams& p, unsigned index, u
 template <typename T>
 __global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) rope_kernel(const RopeParams p)
 {
+    grid_dependency_wait();     // a programmatic dependent: scheduled while the kernel before drains
     allow_dependent_launch();   // a decode launched next waits for this grid before it reads
     rope_rows<T, false>(p, blockIdx.x * kRopeThreads + threadIdx.x, gridDim.x * kRopeThreads,
                         p.n_q + 2 * p.n_kv);
 }
 
-// FP8 pools: the first qk_blocks blocks take the q and k heads; each of the
-// others a V tile of 16 tokens and 256 / D heads, whose codes are transposed
-// through shared memory and written in the pool's V layout ([d][16 tokens] per
-// piece): 16-byte rows when the 16 tokens fill one piece (a prompt's chunk),
-// 4-byte words for aligned runs of 4, single bytes else (a decode step's
-// tokens lie in 16 blocks).
+// FP8 pools: blocks v0 .. v0 + v_blocks - 1 take a V tile each, the others the q and k
+// heads.  A tile is 16 tokens of 256 / D heads, whose codes are transposed through shared
+// memory and written in the pool's V layout ([d][16 tokens] per piece): 16-byte rows when
+// the 16 tokens fill one piece (a prompt's chunk), 4-byte words for aligned runs of 4, single
+// bytes else (a decode step's tokens lie in 16 blocks).
 template <typename T, int D>
-__global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) rope_f8_kernel(const RopeParams p, unsigned qk_blocks)
+__global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) rope_f8_kernel(const RopeParams p, unsigned v0, unsigned v_blocks)
 {
+    grid_dependency_wait();
     allow_dependent_launch();
-    if (blockIdx.x < qk_blocks) {
-        rope_rows<T, true>(p, blockIdx.x * kRopeThreads + threadIdx.x, qk_blocks * kRopeThreads,
+    if (blockIdx.x < v0 || blockIdx.x >= v0 + v_blocks) {
+        const unsigned blk = blockIdx.x < v0 ? blockIdx.x : blockIdx.x - v_blocks;
+        rope_rows<T, true>(p, blk * kRopeThreads + threadIdx.x, (gridDim.x - v_blocks) * kRopeThreads,
                            p.n_q + p.n_kv);
         return;
     }
@@ -248,7 +250,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) rope_f8_kernel
     __shared__ int64_t s_slot[kVTok], s_byte[kVTok];   // token's slot; its byte of head 0, row 0
     const int tid = threadIdx.x;
     const int head_tiles = (p.n_kv + kHeads - 1) / kHeads;
-    const unsigned tile = blockIdx.x - qk_blocks;
+    const unsigned tile = blockIdx.x - v0;
     const int t0 = static_cast<int>(tile / head_tiles) * kVTok;
     const int h0 = static_cast<int>(tile % head_tiles) * kHeads;
     if (tid < kVTok) {
@@ -320,20 +322,26 @@ static cudaError_t run_rope(const RopeParams& p, bool f8, cudaStream_t s)
     // as many blocks as the GPU holds, but at least one token's threads
     const int64_t most = std::max<int64_t>(152 * kRopeBlocksPerSm, (per_token + kRopeThreads - 1) / kRopeThreads);
     const unsigned blocks = static_cast<unsigned>(std::min(most, (items + kRopeThreads - 1) / kRopeThreads));
-    if (!f8) {
-        rope_kernel<T><<<blocks, kRopeThreads, 0, s>>>(p);
-        return cudaGetLastError();
-    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(kRopeThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (!f8) return cudaLaunchKernelEx(&cfg, rope_kernel<T>, p);
     const int tile_heads = kRopeThreads / p.head_dim;
     const unsigned v_blocks = static_cast<unsigned>((p.num_tokens + kVTok - 1) / kVTok) *
                               static_cast<unsigned>((p.n_kv + tile_heads - 1) / tile_heads);
-    if (p.head_dim == 128)
-        rope_f8_kernel<T, 128><<<blocks + v_blocks, kRopeThreads, 0, s>>>(p, blocks);
-    else if (p.head_dim == 64)
-        rope_f8_kernel<T, 64><<<blocks + v_blocks, kRopeThreads, 0, s>>>(p, blocks);
-    else
-        return cudaErrorInvalidValue;
-    return cudaGetLastError();
+    // V tiles, whose chain of steps is the longer one, go first while they leave room for the
+    // others beside them (512 scattered tokens 7.3 -> 5.5 us), else last (8192 tokens: 37 against 39)
+    const unsigned v0 = v_blocks <= 152 * kRopeBlocksPerSm / 2 ? 0 : blocks;
+    cfg.gridDim = dim3(blocks + v_blocks);
+    if (p.head_dim == 128) return cudaLaunchKernelEx(&cfg, rope_f8_kernel<T, 128>, p, v0, v_blocks);
+    if (p.head_dim == 64) return cudaLaunchKernelEx(&cfg, rope_f8_kernel<T, 64>, p, v0, v_blocks);
+    return cudaErrorInvalidValue;
 }
 
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s)

@@ -395,31 +395,44 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         }
         __syncthreads();   // the members are listed, and the scratch is free
     }
+    if constexpr (MODE != 0 && !kShared) grid_dependency_wait();   // (launched as a programmatic dependent)
     auto unit = [&]() -> PrefixUnit {
         if constexpr (kShared) return s_unit;
         else return PrefixUnit{};
     };
     if constexpr (kShared) r = unit().first_seq;
+    int qs = 0, C = 0, L = 0;   // the request's first row, rows and context
     if (!kShared && gridDim.z > 1 && gridDim.z <= kRankedReqs) {
-        __shared__ int s_req;
+        __shared__ int s_req[4];
         const int R = gridDim.z, i = threadIdx.x;
         if (i < R) {
-            const int Li = __ldg(context_lens + i);
+            // (the request's other numbers are loaded beside the lengths, not after the rank)
+            const int Li = __ldg(context_lens + i), qi = __ldg(q_start + i), qe = __ldg(q_start + i + 1);
             int rank = 0;
             for (int k = 0; k < R; ++k) {
                 const int Lk = __ldg(context_lens + k);
                 rank += (Lk > Li || (Lk == Li && k < i)) ? 1 : 0;
             }
-            if (rank == static_cast<int>(blockIdx.z)) s_req = i;
+            if (rank == static_cast<int>(blockIdx.z)) {
+                s_req[0] = i;
+                s_req[1] = qi;
+                s_req[2] = qe - qi;
+                s_req[3] = Li;
+            }
         }
         __syncthreads();
-        r = s_req;
+        r = s_req[0];
+        qs = s_req[1];
+        C = s_req[2];
+        L = s_req[3];
+    } else if constexpr (!kShared) {
+        qs = __ldg(q_start + r);
+        C = __ldg(q_start + r + 1) - qs;
+        L = __ldg(context_lens + r);
     }
+    if constexpr (kShared) L = unit().prefix;
     const int blk = gridDim.x - 1 - blockIdx.x;
     const int kvh = kShared ? unit().kvh : blockIdx.y;
-    const int qs = kShared ? 0 : __ldg(q_start + r);
-    const int C = kShared ? 0 : __ldg(q_start + r + 1) - qs;
-    const int L = kShared ? unit().prefix : __ldg(context_lens + r);
     const int rows_total = kShared ? unit().rows : C * group;
     const int row0 = kShared ? unit().row0 : blk * (kTcTiles * kTcRows);
     // the grid covers max_q rows per request: a longer chunk would leave its
@@ -454,11 +467,12 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         if (sc.window > 0 || sc.first_key) {
             __shared__ int s_lo;
             if (threadIdx.x == 0) s_lo = INT_MAX;
-            __syncthreads();
             const int grow = row0 + static_cast<int>(threadIdx.x);
+            const int i = grow / group;
+            const bool mine = threadIdx.x < kTcTiles * kTcRows && grow < rows_total;
+            const int f = mine ? first_key(i) : INT_MAX;   // its load in flight over the set-up
+            set_up();
             if (threadIdx.x < kTcTiles * kTcRows) {
-                const int i = grow / group;
-                const int f = grow < rows_total ? first_key(i) : INT_MAX;
                 const int m = __reduce_min_sync(0xffffffffu, grow < rows_total && f <= last_key(i) ? f : INT_MAX);
                 if ((threadIdx.x & 31) == 0 && m != INT_MAX) atomicMin(&s_lo, m);
             }
@@ -466,6 +480,8 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             // (no row sees any key: one tile is computed, wholly masked)
             lo_cta = min(s_lo, last_key((min(rows_total, row0 + kTcTiles * kTcRows) - 1) / group));
             tile0 = lo_cta / kTcKeys;
+        } else {
+            set_up();
         }
     }
 #pragma unroll
@@ -486,7 +502,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                                                ~static_cast<uintptr_t>(1023));
     const uint32_t sbase = smem_u32(smem);
 
-    if constexpr (!kShared) set_up();
+    if constexpr (MODE == 0) set_up();
     const uint32_t tmem = s_tmem;
 
     static_assert(!F8 || std::is_same<T, __half>::value, "FP8 codes widen to fp16 operands");
@@ -1374,12 +1390,23 @@ cudaError_t run_prefill_tc(const PrefillArgs& a, cudaStream_t s, float sl2)
     const int64_t tiles = (static_cast<int64_t>(a.max_q) * group + kTcTiles * kTcRows - 1) /
                           (kTcTiles * kTcRows);
     dim3 grid(static_cast<unsigned>(tiles), a.cache.n_kv_heads, a.num_reqs);
-    kern<<<grid, PfWarps<F8, D, kBq>::kThreads, Ly::kDynBytes, s>>>(
-        kmap, vmap, static_cast<const uint8_t*>(a.k_cache), static_cast<const uint8_t*>(a.v_cache),
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(PfWarps<F8, D, kBq>::kThreads);
+    cfg.dynamicSmemBytes = Ly::kDynBytes;
+    cfg.stream = s;
+    // (a scored call is a programmatic dependent: its blocks are scheduled while the kernel
+    // before drains, and wait for it before they read anything)
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = MODE != 0 ? 1 : 0;
+    return cudaLaunchKernelEx(
+        &cfg, kern, kmap, vmap, static_cast<const uint8_t*>(a.k_cache), static_cast<const uint8_t*>(a.v_cache),
         a.out, a.out_dtype, static_cast<const QT*>(a.q), a.block_tables, a.max_blocks,
         a.q_start, a.context_lens, a.max_q, a.n_q, a.cache.n_kv_heads, group, a.cache.num_blocks,
         F8 ? sl2 * a.cache.k_scale : sl2, F8 ? a.cache.v_scale : 1.f, a.err, prefill_score<MODE>(a), NoScore{});
-    return cudaGetLastError();
 }
 
 template <typename T, typename QT, bool F8, int MODE>
