@@ -50,8 +50,8 @@ NCU_TRAFFIC = {
 # chunked prefill of the mixed step (the compact-pool capture runs the same four
 # chunks as the 60 GB pool): bytes per launch
 NCU_PREFILL_TRAFFIC = {
-    ("mixed-llama3-8b-bf16", "f55db9c7a3f8271b"): (98493696 + 3928320, "compact pool, one-pass capture"),
-    ("mixed-llama3-8b-fp8", "f55db9c7a3f8271b"): (57586176 + 1029120, "compact pool, one-pass capture"),
+    ("mixed-llama3-8b-bf16", "91dc5edd21891bf9"): (98495488 + 4095488, "compact pool, one-pass capture"),
+    ("mixed-llama3-8b-fp8", "91dc5edd21891bf9"): (57574656 + 1099008, "compact pool, one-pass capture"),
 }
 
 

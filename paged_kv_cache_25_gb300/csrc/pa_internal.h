@@ -117,5 +117,7 @@ struct PrefillArgs {
 cudaError_t launch_prefill_tc(const PrefillArgs& a, cudaStream_t s);
 cudaError_t launch_prefill_scored(const PrefillArgs& a, cudaStream_t s);
 cudaError_t launch_prefill_bias(const PrefillArgs& a, cudaStream_t s);   // (its forms with a bias)
+cudaError_t launch_prefill_split(const PrefillArgs& a, cudaStream_t s);
+cudaError_t launch_prefill_split_bias(const PrefillArgs& a, cudaStream_t s);
 
 }  // namespace pa

@@ -1,0 +1,15 @@
+// Scored chunked prefill of few rows over a long context, its key tiles split over a
+// cluster (prefill_splits in prefill_tc.cuh), in a translation unit of its own to compile
+// in parallel.
+#include "prefill_tc.cuh"
+
+namespace pa {
+
+cudaError_t launch_prefill_split(const PrefillArgs& a, cudaStream_t s)
+{
+    if (a.score->slopes) return launch_prefill_split_bias(a, s);
+    return a.score->cap2 > 0.f ? run_prefill_any<kPfScored | kPfCap | kPfSplit>(a, s)
+                               : run_prefill_any<kPfScored | kPfSplit>(a, s);
+}
+
+}  // namespace pa

@@ -57,6 +57,7 @@
 #include "prefix_plan.cuh"
 #include "score_mod.cuh"
 
+#include <algorithm>
 #include <limits.h>
 #include <math.h>
 
@@ -128,6 +129,7 @@ constexpr int kPfScored = 1;      // masks: every row has a first and a last vis
 constexpr int kPfCap = 2;         // capped scores
 constexpr int kPfBias = 4;        // distance bias
 constexpr int kPfShared = 8;      // prefix pass of the shared decode
+constexpr int kPfSplit = 16;      // scored: the key tiles of a row block split over a cluster
 
 constexpr int kTcRows = 128;      // M rows per tile
 constexpr int kTcTiles = 2;       // tiles per CTA (A, B)
@@ -218,6 +220,33 @@ __device__ __forceinline__ void bulk_store_wait()
     asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
+// Thread-block clusters (a launch without them is a cluster of one block).
+__device__ __forceinline__ int cluster_blocks()
+{
+    int n;
+    asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
+    return n;
+}
+// Every thread of the cluster arrives; what each wrote to shared memory before is visible to all.
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+// This block's shared address `addr` in block `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_address(uint32_t addr, int rank)
+{
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ float2 cluster_load2(uint32_t addr)
+{
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+
 template <typename T>
 __device__ __forceinline__ void store_row(void* out, int64_t base, int col, const float* v, int n,
                                           pa_dtype dt)
@@ -296,15 +325,16 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                   const __grid_constant__ std::conditional_t<(MODE & kPfShared) != 0, PrefixPass, NoScore> sp)
 {
     constexpr bool kShared = (MODE & kPfShared) != 0;
+    constexpr bool kSplit = (MODE & kPfSplit) != 0;
     constexpr bool kCap = (MODE & kPfCap) != 0, kBias = (MODE & kPfBias) != 0;
     constexpr bool kZ = kCap || kBias;   // maxima in the log2 domain of modified scores
     constexpr bool kBq = std::is_same<QT, __nv_bfloat16>::value;
     using Ly = PfLayout<T, D, F8, kBq>;
     using Wp = PfWarps<F8, D, kBq>;
-    // kShared: bytes of an O row staged in shared memory (16 more, so that the rows of
+    // kShared, and a block of a cluster: bytes of an O row staged in shared memory (16 more, so that the rows of
     // eight threads storing together lie in different banks)
     constexpr uint32_t kORow = D * 4 + 16;
-    static_assert(!kShared || kTcTiles * kTcRows * kORow <= Ly::kDynBytes - 1024, "O rows fit");
+    static_assert(kTcTiles * kTcRows * kORow <= Ly::kDynBytes - 1024, "O rows fit");
     constexpr bool kDirectK = Ly::kDirectK;
     constexpr int kMmaWarp = Wp::kMma;
     constexpr int kFirstConv = Wp::kFirstConverter;
@@ -335,6 +365,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     __shared__ uint8_t xstop[2][kTcTiles][2][kTcRows];
     __shared__ float xsum[kTcTiles][2][kTcRows];
     __shared__ uint8_t xstop_end[kTcTiles][2][kTcRows];
+    __shared__ float2 s_part[(MODE & kPfSplit) != 0 ? kTcTiles * kTcRows : 1];   // rows' (max, sum)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     auto set_up = [&]() {   // barriers and tensor memory (whole block)
         if (tid == 0) {
@@ -431,7 +462,11 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         L = __ldg(context_lens + r);
     }
     if constexpr (kShared) L = unit().prefix;
-    const int blk = gridDim.x - 1 - blockIdx.x;
+    // kSplit: the blocks of a cluster take a range of the key tiles each and merge their (max,
+    // sum, O) through distributed shared memory (few rows over a long context: see
+    // prefill_splits)
+    const int splits = kSplit ? cluster_blocks() : 1;
+    const int blk = static_cast<int>(gridDim.x - 1 - blockIdx.x) / splits;
     const int kvh = kShared ? unit().kvh : blockIdx.y;
     const int rows_total = kShared ? unit().rows : C * group;
     const int row0 = kShared ? unit().row0 : blk * (kTcTiles * kTcRows);
@@ -496,7 +531,15 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         // (a tile whose rows see nothing that the other's do: masked throughout)
         if (MODE != 0 && first < rows_total) n_t[t] = max(n_t[t], 1);
     }
-    const int n_tiles = max(n_t[0], n_t[1]);
+    if constexpr (kSplit) {
+        const int rank = static_cast<int>(blockIdx.x) % splits, all = max(n_t[0], n_t[1]);
+        const int a = static_cast<int>(static_cast<int64_t>(rank) * all / splits);
+        const int b = static_cast<int>(static_cast<int64_t>(rank + 1) * all / splits);
+        tile0 += a;
+#pragma unroll
+        for (int t = 0; t < kTcTiles; ++t) n_t[t] = max(0, min(n_t[t], b) - a);
+    }
+    const int n_tiles = max(n_t[0], n_t[1]);   // (0: a range with no tile, every role has nothing to do)
 
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn_smem) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
@@ -823,7 +866,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             auto wait_all = [&](uint64_t* bar, uint32_t parity) {
                 return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, err));
             };
-            bool ok = wait_all(&q_ready, 0) && wait_all(&k_full[0], 0);
+            bool ok = (!kSplit || n_tiles > 0) && wait_all(&q_ready, 0) && wait_all(&k_full[0], 0);
             tc_fence_after();
             if (ok) {
                 for (int t = 0; t < kTcTiles; ++t)
@@ -1282,6 +1325,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         }
 
         // ------------------------------------------------ epilogue: O / l
+        [[maybe_unused]] float2 part = make_float2(-INFINITY, 0.f);   // kSplit: this row's (max, sum)
         // the pair meets once more, to add its partial sums, unless it left
         // the loop together; a late failure of either warp skips the output
         if (!quit && nt > 0) {
@@ -1290,12 +1334,13 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             named_bar_sync(bar_id, 64);
             const float lsum = l + xsum[t][hf ^ 1][rr];
             stop = stop || xstop_end[t][hf ^ 1][rr] != 0;
-            const bool ok = !__any_sync(0xffffffffu, stop) &&
-                            mbar_wait(smem_u32(&pv_done[t]), 0, err);
+            bool ok = !__any_sync(0xffffffffu, stop) && mbar_wait(smem_u32(&pv_done[t]), 0, err);
+            // (the staged rows lie over operands that the other tile's MMAs may still read)
+            if (kSplit && n_t[t ^ 1] > 0) ok = ok && mbar_wait(smem_u32(&pv_done[t ^ 1]), 0, err);
             if (__all_sync(0xffffffffu, ok)) {
                 tc_fence_after();
                 // (MODE: a row that sees no key is 0)
-                const float inv = kShared ? (F8 ? v_scale : 1.f)
+                const float inv = kShared || kSplit ? (F8 ? v_scale : 1.f)
                                           : (MODE != 0 && lsum == 0.f ? 0.f : (F8 ? v_scale : 1.f) / lsum);
                 int64_t obase = (static_cast<int64_t>(q_row) * n_q + head) * D;
                 if constexpr (kShared) {
@@ -1314,7 +1359,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                     float v[32];
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(o[i]) * inv;
-                    if constexpr (kShared) {
+                    if constexpr (kShared || kSplit) {
                         // through shared memory (the operands are no longer read), as one
                         // bulk store a half row: stores straight from registers, 16 bytes
                         // a row and instruction, took 3.6 us of a block's 33
@@ -1327,6 +1372,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                         if (valid) store_row<T>(out, obase, hf * (D / 2) + c0, v, 32, out_dtype);
                     }
                 }
+                if (kSplit && lsum > 0.f) part = make_float2(m_raw * unit_log2, lsum);
                 if constexpr (kShared) {
                     fence_proxy_async_smem();
                     if (valid)
@@ -1336,12 +1382,75 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                 }
             }
         }
+        if constexpr (kSplit)
+            if (hf == 0) s_part[t * kTcRows + rr] = part;
     }
 
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+    if constexpr (kSplit) {
+        // every thread of the cluster comes here: nothing above returns once roles are taken
+        cluster_sync();
+        const int rank = static_cast<int>(blockIdx.x) % splits;
+        constexpr int kWarps = Wp::kThreads / 32, V = D / 32;
+        for (int row = rank * kWarps + warp; row < min(kTcTiles * kTcRows, rows_total - row0);
+             row += splits * kWarps) {
+            float2 p = make_float2(-INFINITY, 0.f);
+            if (lane < splits) p = cluster_load2(cluster_address(smem_u32(&s_part[row]), lane));
+            float m = p.x;
+#pragma unroll
+            for (int w = 16; w > 0; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
+            const float weight = p.x == -INFINITY ? 0.f : fast_exp2(p.x - m);
+            float sum = weight * p.y;
+#pragma unroll
+            for (int w = 16; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+            float o[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) o[i] = 0.f;
+            for (int c = 0; c < splits; ++c) {
+                const float wc = __shfl_sync(0xffffffffu, weight, c);
+                if (wc == 0.f) continue;      // (a range in which the row sees nothing has no O)
+                const uint32_t at = cluster_address(sbase + row * kORow + lane * V * 4, c);
+#pragma unroll
+                for (int i = 0; i < V; i += 2) {
+                    const float2 x = cluster_load2(at + i * 4);
+                    o[i] = fmaf(wc, x.x, o[i]);
+                    o[i + 1] = fmaf(wc, x.y, o[i + 1]);
+                }
+            }
+            const float inv = sum > 0.f ? 1.f / sum : 0.f;      // a row that sees no key is 0
+            const int grow = row0 + row;
+            const int64_t at = (static_cast<int64_t>(qs + grow / group) * n_q + kvh * group + grow % group) * D +
+                               lane * V;
+#pragma unroll
+            for (int i = 0; i < V; i += 2) {
+                const float x = o[i] * inv, y = o[i + 1] * inv;
+                if (out_dtype == PA_F32)
+                    *reinterpret_cast<float2*>(static_cast<float*>(out) + at + i) = make_float2(x, y);
+                else
+                    *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(out) + at + i) =
+                        out_dtype == PA_BF16 ? Cvt<__nv_bfloat16>::pack(x, y) : Cvt<__half>::pack(x, y);
+            }
+        }
+        cluster_sync();   // no block leaves while another reads its rows
+    }
+}
+
+// Blocks of a cluster for a scored call.  One block walks a row block's key tiles at 2 - 5 us
+// a tile; where the call has too few row blocks to fill the GPU, 2, 4 or 8 blocks share them,
+// while each has at least four tiles of the longest context that the tables can hold.
+inline int prefill_splits(const PrefillArgs& a)
+{
+    const int64_t group = a.n_q / a.cache.n_kv_heads, rows = kTcTiles * kTcRows;
+    const int64_t blocks = (a.max_q * group + rows - 1) / rows * a.cache.n_kv_heads * a.num_reqs;
+    int64_t keys = static_cast<int64_t>(a.max_blocks) * a.cache.block_size;
+    if (a.score->window > 0) keys = std::min(keys, a.score->window + rows);
+    const int64_t tiles = (keys + kTcKeys - 1) / kTcKeys;
+    int n = 1;
+    while (n < 8 && blocks * n * 2 <= 152 && tiles >= n * 2 * 4) n *= 2;
+    return n;
 }
 
 // The tensor maps of a call's pools (FP8: of the K codes, where the score MMA reads
@@ -1389,19 +1498,24 @@ cudaError_t run_prefill_tc(const PrefillArgs& a, cudaStream_t s, float sl2)
     const int group = a.n_q / a.cache.n_kv_heads;
     const int64_t tiles = (static_cast<int64_t>(a.max_q) * group + kTcTiles * kTcRows - 1) /
                           (kTcTiles * kTcRows);
-    dim3 grid(static_cast<unsigned>(tiles), a.cache.n_kv_heads, a.num_reqs);
+    int splits = 1;
+    if constexpr ((MODE & kPfSplit) != 0) splits = prefill_splits(a);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * splits), a.cache.n_kv_heads, a.num_reqs);
     cfg.blockDim = dim3(PfWarps<F8, D, kBq>::kThreads);
     cfg.dynamicSmemBytes = Ly::kDynBytes;
     cfg.stream = s;
     // (a scored call is a programmatic dependent: its blocks are scheduled while the kernel
     // before drains, and wait for it before they read anything)
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = splits;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = MODE != 0 ? 1 : 0;
+    cfg.numAttrs = MODE == 0 ? 0 : ((MODE & kPfSplit) != 0 ? 2 : 1);
     return cudaLaunchKernelEx(
         &cfg, kern, kmap, vmap, static_cast<const uint8_t*>(a.k_cache), static_cast<const uint8_t*>(a.v_cache),
         a.out, a.out_dtype, static_cast<const QT*>(a.q), a.block_tables, a.max_blocks,

@@ -193,3 +193,28 @@ def test_replayed_graph():
     torch.cuda.synchronize()
     check(out, c.ref(), 2e-3)
     assert pa.pa_get_device_error() == 0
+
+
+@pytest.mark.parametrize("mod", ["none", "cap-bias", "window300-bias", "doc", "prefix-window-doc-cap"])
+@pytest.mark.parametrize("form", FORMS)
+def test_few_rows_over_long_contexts(form, mod):
+    """Key tiles split over a cluster of eight blocks, with requests too short for all of them."""
+    n_q, n_kv, d, bs, dtype, fp8 = FORMS[form]
+    Case(41, [(40, 4200), (3, 90), (1, 1)], n_q, n_kv, d, bs, dtype, fp8=fp8, **MODS[mod]).test()
+
+
+@pytest.mark.parametrize("out_dtype", [BF, FH])
+@pytest.mark.parametrize("form", ["bf16-g4", "fp16-g2-d64", "fp8-g4"])
+def test_split_prefill_output_types_and_replay(form, out_dtype):
+    n_q, n_kv, d, bs, dtype, fp8 = FORMS[form]
+    c = Case(42, [(140, 3000), (9, 700)], n_q, n_kv, d, bs, dtype, fp8=fp8, softcap=20.0)
+    check(c.run(out_dtype), c.ref(), tolerance(dtype, 20.0), out_dtype)
+    out = torch.zeros(c.q.shape, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.run(out=out)
+        c.run(out=out)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, c.run())
+    assert pa.pa_get_device_error() == 0
