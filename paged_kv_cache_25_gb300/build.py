@@ -22,8 +22,8 @@ LIB = os.path.join(OUT, "libpa.so")
 MARSHAL = os.path.join(OUT, "_pa_marshal.so")
 MARSHAL_SOURCE = "marshal.cpp"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-CUDA_SOURCES = ["api.cu", "cache_write.cu", "cache_rope.cu", "copy_blocks.cu", "decode.cu", "decode_verify.cu", "decode_scored.cu", "decode_scored_simt.cu",
-                "decode_no_alloc.cu", "prefill_tc.cu", "prefill_scored.cu", "prefix_pass.cu", "prefill_scored_bias.cu", "prefill_split.cu", "prefill_split_bias.cu"]
+CUDA_SOURCES = ["api.cu", "cache_write.cu", "cache_rope.cu", "copy_blocks.cu", "decode.cu", "decode_verify.cu", "decode_scored.cu", "decode_scored_simt.cu", "decode_wide.cu",
+                "decode_no_alloc.cu", "prefill_tc.cu", "prefill_scored.cu", "prefix_pass.cu", "prefill_scored_bias.cu", "prefill_split.cu", "prefill_split_bias.cu", "prefill_wide.cu"]
 CXX_SOURCES = ["host_alloc.cpp", "prefix_cache.cpp", "rope_table.cpp", "prefix_groups.cpp"]
 
 

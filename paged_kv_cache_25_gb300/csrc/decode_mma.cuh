@@ -41,6 +41,7 @@
 // the shared-prefix decode: a sequence's keys start at its first visible block
 // instead of 0, scores may be capped or biased (score_mod.cuh), keys before a row's
 // first are masked as keys past its last are, and a row that sees no key is 0.
+// WIDE: with a cap of the wide form (decode_wide.cu).
 #include <cuda_fp8.h>
 
 #include "pa_device.cuh"
@@ -148,7 +149,7 @@ __device__ __forceinline__ uint32_t q_pair(const QT* p)
     return __ldg(reinterpret_cast<const unsigned int*>(p));   // q already in the MMA type
 }
 
-template <typename T, typename QT, int D, int BS, int NS, bool FP8, bool MQ, int RU = 8, bool SC = false>
+template <typename T, typename QT, int D, int BS, int NS, bool FP8, bool MQ, int RU = 8, bool SC = false, bool WIDE = false>
 __global__ void __launch_bounds__(kDecWarps * 32, decode_ctas_per_sm(FP8, D, RU))
 decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                   const uint8_t* __restrict__ v_codes, void* __restrict__ out, pa_dtype out_dtype,
@@ -631,7 +632,12 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         auto modify = [&](float& za, float& zb, float& zc, float& zd, float sa, float sb, int ahead, float far,
                           int ahead_b) {
             if constexpr (SC) {
-                if (sc.cap2 > 0.f) {
+                if constexpr (WIDE) {
+                    za = soft_cap_wide(za, za * sc.cap_rate, sc.cap2);
+                    zb = soft_cap_wide(zb, zb * sc.cap_rate, sc.cap2);
+                    zc = soft_cap_wide(zc, zc * sc.cap_rate, sc.cap2);
+                    zd = soft_cap_wide(zd, zd * sc.cap_rate, sc.cap2);
+                } else if (sc.cap2 > 0.f) {
                     za = soft_cap(za, sc.cap2, sc.cap_rate);
                     zb = soft_cap(zb, sc.cap2, sc.cap_rate);
                     zc = soft_cap(zc, sc.cap2, sc.cap_rate);
@@ -1084,14 +1090,14 @@ inline int decode_sm_count()
     return cache[dev];
 }
 
-template <typename T, typename QT, int D, int BS, bool FP8, bool MQ, int RU = 8, bool SC = false>
+template <typename T, typename QT, int D, int BS, bool FP8, bool MQ, int RU = 8, bool SC = false, bool WIDE = false>
 cudaError_t run_mma(const DecodeArgs& a, cudaStream_t s, float scale_log2)
 {
     // FP8 runs 3 CTAs per SM (registers capped at 168 by the launch bounds):
     // Llama-3-8B batch 0.273 -> 0.231 ms against 2 CTAs with 24 KB rings.
     constexpr int NS = decode_stages<T, D, FP8, RU>();
     using Cfg = DecodeCfg<T, D, NS, FP8, RU>;
-    auto kern = decode_mma_kernel<T, QT, D, BS, NS, FP8, MQ, RU, SC>;
+    auto kern = decode_mma_kernel<T, QT, D, BS, NS, FP8, MQ, RU, SC, WIDE>;
     static std::once_flag once;
     static cudaError_t attr_err = cudaSuccess;
     static int per_sm = 1;

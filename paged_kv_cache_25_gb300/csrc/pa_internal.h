@@ -99,6 +99,7 @@ struct DecodeArgs {
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t s);
 // attention kernel of a scored or shared-prefix call (decode_scored.cu)
 cudaError_t launch_decode_scored(const DecodeArgs& a, cudaStream_t s, float scale_log2);
+cudaError_t launch_decode_wide(const DecodeArgs& a, cudaStream_t s, float scale_log2);   // (caps above kNearCap)
 cudaError_t launch_decode_scored_simt(const DecodeArgs& a, cudaStream_t s, float scale_log2);
 // prefix pass of a shared-prefix call (prefix_pass.cu)
 cudaError_t launch_prefix_pass(const DecodeArgs& a, const PrefixPass& pass, cudaStream_t s);
@@ -117,6 +118,7 @@ struct PrefillArgs {
 cudaError_t launch_prefill_tc(const PrefillArgs& a, cudaStream_t s);
 cudaError_t launch_prefill_scored(const PrefillArgs& a, cudaStream_t s);
 cudaError_t launch_prefill_bias(const PrefillArgs& a, cudaStream_t s);   // (its forms with a bias)
+cudaError_t launch_prefill_wide(const PrefillArgs& a, cudaStream_t s);   // (its caps above kNearCap)
 cudaError_t launch_prefill_split(const PrefillArgs& a, cudaStream_t s);
 cudaError_t launch_prefill_split_bias(const PrefillArgs& a, cudaStream_t s);
 

@@ -129,6 +129,7 @@ constexpr int kPfScored = 1;      // masks: every row has a first and a last vis
 constexpr int kPfCap = 2;         // capped scores
 constexpr int kPfBias = 4;        // distance bias
 constexpr int kPfShared = 8;      // prefix pass of the shared decode
+constexpr int kPfWide = 32;       // with kPfCap and kPfBias: a cap of the wide form, slopes or none
 constexpr int kPfSplit = 16;      // scored: the key tiles of a row block split over a cluster
 
 constexpr int kTcRows = 128;      // M rows per tile
@@ -327,6 +328,8 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     constexpr bool kShared = (MODE & kPfShared) != 0;
     constexpr bool kSplit = (MODE & kPfSplit) != 0;
     constexpr bool kCap = (MODE & kPfCap) != 0, kBias = (MODE & kPfBias) != 0;
+    constexpr bool kWide = (MODE & kPfWide) != 0;
+    static_assert(!kWide || (kCap && kBias), "the wide form comes with cap and bias");
     constexpr bool kZ = kCap || kBias;   // maxima in the log2 domain of modified scores
     constexpr bool kBq = std::is_same<QT, __nv_bfloat16>::value;
     using Ly = PfLayout<T, D, F8, kBq>;
@@ -1069,7 +1072,8 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         [[maybe_unused]] CapForm cap;
         float slope2 = 0.f;
         if constexpr (kCap) cap = cap_form(sc.cap2, sc.cap_rate, scale_log2);
-        if constexpr (kBias) slope2 = __ldg(sc.slopes + head) * kLog2e;
+        if constexpr (kBias)
+            if (!kWide || sc.slopes) slope2 = __ldg(sc.slopes + head) * kLog2e;
         const int q_pos = ctx0 + pos_local;
         const int warp_min_q = kBias ? __reduce_min_sync(0xffffffffu, q_pos) : 0;
         // modified scores of the four keys i .. i + 3 of this thread's half tile, whose
@@ -1080,7 +1084,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         auto modified4 = [&](auto clamp, auto ahead, const float (&s)[4], float d0, int i, float neg_ref,
                              float (&z)[4]) {
             float add[4];
-            if constexpr (kCap) neg_ref += cap.cap2;
+            if constexpr (kCap && !kWide) neg_ref += cap.cap2;   // (kWide: it would be rounded away)
             if constexpr (!kBias) {
                 add[0] = add[1] = add[2] = add[3] = neg_ref;
             } else if constexpr (decltype(ahead)::value) {
@@ -1092,7 +1096,11 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                 const float2 a1 = fma2(both(slope2), make_float2(i + 2, i + 3), first);
                 add[0] = a0.x; add[1] = a0.y; add[2] = a1.x; add[3] = a1.y;
             }
-            if constexpr (kCap) {
+            if constexpr (kWide) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    z[e] = soft_cap_wide(s[e] * scale_log2, s[e] * cap.rate, cap.cap2) + add[e];
+            } else if constexpr (kCap) {
                 soft_cap4<decltype(clamp)::value>(cap, s, add, z);
             } else {
                 const float2 z0 = fma2(make_float2(s[0], s[1]), both(scale_log2), make_float2(add[0], add[1]));

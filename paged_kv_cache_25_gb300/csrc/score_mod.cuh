@@ -5,8 +5,11 @@
 // cap c > 0 the score s becomes c tanh(s / c); since tanh x = 1 - 2 / (1 + e^(2x)),
 // in the log2 domain  z' = C - 2C / (1 + 2^(z * 2/c)),  C = c log2(e):  one exp2,
 // one reciprocal and one fused multiply-add.  Both SFU results are good to about
-// 2^-22 relative, so z' is off by at most ~C * 2^-22 (2e-5 for c = 50), which moves a
-// probability by 1.2e-5 relative, far below the 2^-9 of a 16-bit output.
+// 2^-22 relative and the difference is taken of numbers of size C, so z' is off by up to
+// 4.4e-7 C whatever its size (5e-7 C in the prefill's form, whose quotients are products):
+// 3.6e-5 for c = 50, 9e-5 for c = 128, which moves a probability by 6.4e-5 relative, far
+// below the 2^-9 of a 16-bit output, but 0.7 for c = 1e6.  Caps above 128 therefore take
+// kernels with the wide form (soft_cap_wide), good to 2^-20 of z' itself.
 // A distance bias then adds -slope * |i - j|.
 #pragma once
 #include "pa_device.cuh"
@@ -30,6 +33,24 @@ __device__ __forceinline__ float fast_rcp(float x)
 __device__ __forceinline__ float soft_cap(float z, float cap2, float cap_rate)
 {
     return fmaf(-2.f * cap2, fast_rcp(1.f + fast_exp2(z * cap_rate)), cap2);
+}
+
+// The largest cap (log2 domain) whose scores are off by little enough without the series.
+constexpr float kNearCap = 128.f * kLog2e;
+
+// C tanh(z / C) for any C.  With x = z / C, for |x| < 3/8 the odd series
+//   tanh x = x - x^3/3 + 2 x^5/15 - 17 x^7/315 + 62 x^9/2835 - ...,
+// whose next term is at most 5e-7 of the sum there; else the form above, whose cancellation
+// is then bounded by C / z' < 2.8.  e: z * cap_rate = 2 x log2(e).
+__device__ __forceinline__ float soft_cap_wide(float z, float e, float cap2)
+{
+    const float x = e * (0.5f / kLog2e), x2 = x * x;
+    float w = fmaf(62.f / 2835.f, x2, -17.f / 315.f);
+    w = fmaf(w, x2, 2.f / 15.f);
+    w = fmaf(w, x2, -1.f / 3.f);
+    const float near = fmaf(z, w * x2, z);      // (not selected where x2 overflows)
+    const float far = fmaf(-2.f * cap2, fast_rcp(1.f + fast_exp2(e)), cap2);
+    return fabsf(x) < 0.375f ? near : far;
 }
 
 // The prefill's form of the cap, for four raw scores of a row at a time: with
