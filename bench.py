@@ -42,16 +42,16 @@ FALLBACK_HBM_GBS = 6800.0
 # K/V bytes of the captured launch, what was captured); a record of another
 # batch of the same workload is scaled by its unique K/V bytes.
 NCU_TRAFFIC = {
-    ("llama3-8b-bf16", "034c34a0e73d16f3"): (2371994880 + 13447168, 2359717888,
+    ("llama3-8b-bf16", "8152101b3e0080f9"): (2371987456 + 13348864, 2359717888,
                                              "full 256-sequence batch, one-pass capture"),
-    ("llama3-8b-fp8", "034c34a0e73d16f3"): (1188182272 + 12398592, 1179858944,
+    ("llama3-8b-fp8", "8152101b3e0080f9"): (1188179712 + 12502272, 1179858944,
                                             "full 256-sequence batch, one-pass capture"),
 }
 # chunked prefill of the mixed step (the compact-pool capture runs the same four
 # chunks as the 60 GB pool): bytes per launch
 NCU_PREFILL_TRAFFIC = {
-    ("mixed-llama3-8b-bf16", "91dc5edd21891bf9"): (98495488 + 4095488, "compact pool, one-pass capture"),
-    ("mixed-llama3-8b-fp8", "91dc5edd21891bf9"): (57574656 + 1099008, "compact pool, one-pass capture"),
+    ("mixed-llama3-8b-bf16", "34a991c8780e1178"): (98521088 + 4571392, "compact pool, one-pass capture"),
+    ("mixed-llama3-8b-fp8", "34a991c8780e1178"): (57575424 + 1127168, "compact pool, one-pass capture"),
 }
 
 
