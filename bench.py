@@ -42,16 +42,16 @@ FALLBACK_HBM_GBS = 6800.0
 # K/V bytes of the captured launch, what was captured); a record of another
 # batch of the same workload is scaled by its unique K/V bytes.
 NCU_TRAFFIC = {
-    ("llama3-8b-bf16", "8152101b3e0080f9"): (2371987456 + 13348864, 2359717888,
+    ("llama3-8b-bf16", "39ca30ff7ff64395"): (2371993600 + 13440256, 2359717888,
                                              "full 256-sequence batch, one-pass capture"),
-    ("llama3-8b-fp8", "8152101b3e0080f9"): (1188179712 + 12502272, 1179858944,
+    ("llama3-8b-fp8", "39ca30ff7ff64395"): (1188187136 + 12206080, 1179858944,
                                             "full 256-sequence batch, one-pass capture"),
 }
 # chunked prefill of the mixed step (the compact-pool capture runs the same four
 # chunks as the 60 GB pool): bytes per launch
 NCU_PREFILL_TRAFFIC = {
-    ("mixed-llama3-8b-bf16", "34a991c8780e1178"): (98521088 + 4571392, "compact pool, one-pass capture"),
-    ("mixed-llama3-8b-fp8", "34a991c8780e1178"): (57575424 + 1127168, "compact pool, one-pass capture"),
+    ("mixed-llama3-8b-bf16", "29f0e612d6277a6b"): (98513664 + 4397312, "compact pool, one-pass capture"),
+    ("mixed-llama3-8b-fp8", "29f0e612d6277a6b"): (57574656 + 1148672, "compact pool, one-pass capture"),
 }
 
 

@@ -139,18 +139,15 @@ decode_merge_kernel(void* __restrict__ out, pa_dtype out_dtype,
     using Vec = std::conditional_t<V == 4, float4, std::conditional_t<V == 2, float2, float>>;
     const int lane = threadIdx.x & 31;
     const int64_t sh = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    const bool mine = sh < static_cast<int64_t>(num_seqs) * nq * n_q;
-    // the call's inputs, read before the wait: this kernel is a programmatic dependent of
-    // the partial kernel, whose blocks let it start only after their own wait, so
-    // whatever wrote the inputs has completed
-    const int s = mine ? static_cast<int>(sh / (static_cast<int64_t>(nq) * n_q)) : 0;
+    grid_dependency_wait();   // launched as a programmatic dependent of the partial kernel
+    if (sh >= static_cast<int64_t>(num_seqs) * nq * n_q) return;
+    const int s = static_cast<int>(sh / (static_cast<int64_t>(nq) * n_q));
     const int L = __ldg(context_lens + s);
     const int lo = first_visible(sc, s, L, nq, block_size, max_blocks, err);
     const int J = min((L - lo / block_size * block_size + part_tokens - 1) / part_tokens, max_parts);
     const bool member = sc.group_of_seq != nullptr && lo > 0;
     const int g = member ? __ldg(sc.group_of_seq + s) : 0;
-    grid_dependency_wait();                              // the partials are written
-    if (!mine || L < nq) return;                         // (nothing of a sequence below nq is written)
+    if (L < nq) return;                         // (nothing of a sequence below nq is written)
     if (!member && J <= 1) return;                       // finished by the partial kernel
     const float* ml = ws_ml + 2 * sh * sc.slots;
     // every lane's prefix slot (at most 32 of them), whether the pass wrote it or not: its

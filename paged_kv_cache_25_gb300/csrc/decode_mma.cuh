@@ -143,12 +143,6 @@ __device__ __forceinline__ void e4m3x4_to_h2x2(uint32_t w, uint32_t& lo, uint32_
         : "=r"(lo), "=r"(hi) : "r"(w));
 }
 
-template <typename QT, typename T>
-__device__ __forceinline__ uint32_t q_pair(const QT* p)
-{
-    return __ldg(reinterpret_cast<const unsigned int*>(p));   // q already in the MMA type
-}
-
 template <typename T, typename QT, int D, int BS, int NS, bool FP8, bool MQ, int RU = 8, bool SC = false, bool WIDE = false>
 __global__ void __launch_bounds__(kDecWarps * 32, decode_ctas_per_sm(FP8, D, RU))
 decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
@@ -192,12 +186,26 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // launched as a programmatic dependent: every input may come from the
     // kernel before this one in the stream.  The sequences' own part of a shared
-    // decode follows the prefix pass, of which it needs nothing (and what it reads was
-    // written before that pass began): it runs beside it, on SMs that the pass leaves
-    // free, and waits at its end, so that the merge after it finds both done.
+    // decode follows the prefix pass, of which it needs nothing: it runs beside it, on
+    // SMs that the pass leaves free, and waits at its end, so that the merge after it
+    // finds both done.  What it reads was complete before the pass began, and the pass's
+    // first block, having waited for that, releases it with the work counter: here the
+    // first ticket acquires it (fence and barrier, then loads through the coherent path;
+    // its copies, behind a proxy fence).
     bool beside = false;
     if constexpr (SC) beside = sc.group_of_seq != nullptr;
-    if (!beside) grid_dependency_wait();
+    if (!beside) {
+        grid_dependency_wait();
+    } else {
+        if (tid == 0) {
+            s_next = atomicAdd(ticket, 1u);
+            __threadfence();
+        }
+        __syncthreads();
+        fence_proxy_async_global();
+    }
+    // inputs of the scored kernels: see load_input
+    auto input = [](const auto* p) { return load_input<!SC>(p); };
     // a KV head serves group x nq rows (head-major: row = head * nq + query),
     // taken RU at a time; plain decode (MQ false) has nq = 1 at compile time
     const int nq = MQ ? nq_arg : 1;
@@ -221,7 +229,7 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         const int b0 = tid * per, b1 = min(num_seqs, b0 + per);
         int local = 0;
         for (int i = b0; i < b1; ++i) {
-            const int Lt = __ldg(context_lens + i), L = Lt - seq_base(i, Lt);
+            const int Lt = input(context_lens + i), L = Lt - seq_base(i, Lt);
             const int p = L > 0 ? min((L + part_tokens - 1) / part_tokens, max_parts) - 1 : 0;
             s_prefix[i] = p;
             local += p;
@@ -282,7 +290,7 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         const int grp = static_cast<int>(uu - static_cast<int64_t>(gp) * n_groups);
         if (gp >= n_full) {                           // a sequence's last partition
             x.s = gp - n_full;
-            const int Lt = __ldg(context_lens + x.s), Ls = Lt - seq_base(x.s, Lt);
+            const int Lt = input(context_lens + x.s), Ls = Lt - seq_base(x.s, Lt);
             x.part = Ls > 0 ? min((Ls + part_tokens - 1) / part_tokens, max_parts) - 1 : 0;
         } else if (use_prefix) {
             int lo = 0, hi = num_seqs - 1;            // first s with prefix[s] > gp
@@ -296,7 +304,7 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             x.s = gp / (max_parts - 1);
             x.part = gp - x.s * (max_parts - 1);
         }
-        x.L = __ldg(context_lens + x.s);
+        x.L = input(context_lens + x.s);
         x.lo = seq_lo(x.s, x.L);
         const int base = SC ? x.lo / BS * BS : 0;
         x.tok0 = base + x.part * part_tokens;
@@ -326,7 +334,7 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     auto load_id = [&](const Unit& x, int i, int& bad) {
         const int lb = x.blk0 + i;
         int b = -1;
-        if (lb < max_blocks) b = __ldg(block_tables + static_cast<int64_t>(x.s) * max_blocks + lb);
+        if (lb < max_blocks) b = input(block_tables + static_cast<int64_t>(x.s) * max_blocks + lb);
         if (b < 0 || b >= num_blocks) {
             bad = 1;
             set_error(err, PA_ERR_OUT_OF_RANGE);
@@ -342,6 +350,7 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     // the unit row this thread's q fragments hold: row g, or (kTr) column g,
     // whose head is g mod 4
     const int gq = kTr ? (g & 3) : g;
+    auto q_pair = [&](const QT* p) { return input(reinterpret_cast<const unsigned int*>(p)); };   // two elements
     auto load_q = [&](const Unit& x) {
         if constexpr (FP8 && std::is_same<QT, __nv_bfloat16>::value) {
             // bf16 q over an FP8 pool: the raw bf16 pairs of row g, made fp16
@@ -355,16 +364,16 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                         const int hh = (x.r0 + g + 8) / nq, qi = x.r0 + g + 8 - hh * nq;
                         const QT* row =
                             q + ((static_cast<int64_t>(x.s) * nq + qi) * n_q + x.h0 + hh) * D + kk * 16;
-                        qb[kk][0] = __ldg(reinterpret_cast<const unsigned int*>(row + 4 * t4));
-                        qb[kk][1] = __ldg(reinterpret_cast<const unsigned int*>(row + 4 * t4 + 2));
+                        qb[kk][0] = input(reinterpret_cast<const unsigned int*>(row + 4 * t4));
+                        qb[kk][1] = input(reinterpret_cast<const unsigned int*>(row + 4 * t4 + 2));
                     }
                 }
                 if (gq < x.nh) {
                     const int hh = (x.r0 + gq) / nq, qi = x.r0 + gq - hh * nq;
                     const QT* row =
                         q + ((static_cast<int64_t>(x.s) * nq + qi) * n_q + x.h0 + hh) * D + kk * 16;
-                    qa[kk][0] = __ldg(reinterpret_cast<const unsigned int*>(row + 4 * t4));
-                    qa[kk][1] = __ldg(reinterpret_cast<const unsigned int*>(row + 4 * t4 + 2));
+                    qa[kk][0] = input(reinterpret_cast<const unsigned int*>(row + 4 * t4));
+                    qa[kk][1] = input(reinterpret_cast<const unsigned int*>(row + 4 * t4 + 2));
                 } else {
                     qa[kk][0] = qa[kk][1] = 0u;
                 }
@@ -377,8 +386,8 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                         const int hh = (x.r0 + g + 8) / nq, qi = x.r0 + g + 8 - hh * nq;
                         const QT* row =
                             q + ((static_cast<int64_t>(x.s) * nq + qi) * n_q + x.h0 + hh) * D + kk * 16;
-                        qb[kk][0] = q_pair<QT, T>(row + (FP8 ? 4 : 2) * t4);
-                        qb[kk][1] = q_pair<QT, T>(row + (FP8 ? 4 * t4 + 2 : 2 * t4 + 8));
+                        qb[kk][0] = q_pair(row + (FP8 ? 4 : 2) * t4);
+                        qb[kk][1] = q_pair(row + (FP8 ? 4 * t4 + 2 : 2 * t4 + 8));
                     } else {
                         qb[kk][0] = 0u;
                         qb[kk][1] = 0u;
@@ -390,11 +399,11 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                         q + ((static_cast<int64_t>(x.s) * nq + qi) * n_q + x.h0 + hh) * D + kk * 16;
                     if constexpr (FP8) {
                         // k order of the FP8 fragments: columns 4*t4 .. 4*t4+3 of the chunk
-                        qa[kk][0] = q_pair<QT, T>(row + 4 * t4);
-                        qa[kk][1] = q_pair<QT, T>(row + 4 * t4 + 2);
+                        qa[kk][0] = q_pair(row + 4 * t4);
+                        qa[kk][1] = q_pair(row + 4 * t4 + 2);
                     } else {
-                        qa[kk][0] = q_pair<QT, T>(row + 2 * t4);
-                        qa[kk][1] = q_pair<QT, T>(row + 2 * t4 + 8);
+                        qa[kk][0] = q_pair(row + 2 * t4);
+                        qa[kk][1] = q_pair(row + 2 * t4 + 8);
                     }
                 } else {
                     qa[kk][0] = 0u;
@@ -514,9 +523,7 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     // ---- the first unit: ids checked before any load is issued
     int64_t u = blockIdx.x;
     if (beside) {
-        if (tid == 0) s_next = atomicAdd(ticket, 1u);
-        __syncthreads();
-        u = s_next;
+        u = s_next;       // (drawn above)
         __syncthreads();
         if (tid == 0 && u < units) s_next = atomicAdd(ticket, 1u);   // the next one's, meanwhile
     }
@@ -621,8 +628,8 @@ decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                 }
                 if (sc.slopes) {
                     const int a = kTr ? (2 * t4) & 3 : g, b = kTr ? a + 1 : g + 8;
-                    slope0 = a < nh ? __ldg(sc.slopes + h0 + (r0 + a) / nq) * kLog2e : 0.f;
-                    slope1 = (kTr || R16) && b < nh ? __ldg(sc.slopes + h0 + (r0 + b) / nq) * kLog2e : 0.f;
+                    slope0 = a < nh ? input(sc.slopes + h0 + (r0 + a) / nq) * kLog2e : 0.f;
+                    slope1 = (kTr || R16) && b < nh ? input(sc.slopes + h0 + (r0 + b) / nq) * kLog2e : 0.f;
                 }
             }
         }

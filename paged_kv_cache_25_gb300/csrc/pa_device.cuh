@@ -34,6 +34,28 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p)
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
+// What this thread has seen of global memory is seen by its asynchronous copies too.
+__device__ __forceinline__ void fence_proxy_async_global()
+{
+    asm volatile("fence.proxy.async.global;" ::: "memory");
+}
+
+// A load of an input that no grid_dependency_wait of this kernel has made visible, but an
+// acquire (see decode_mma_kernel): through the coherent path, not before that acquire.
+// PLAIN: an input like any other.
+template <bool PLAIN = false, typename T>
+__device__ __forceinline__ T load_input(const T* p)
+{
+    static_assert(sizeof(T) == 4, "32-bit words");
+    if constexpr (PLAIN) {
+        return __ldg(p);
+    } else {
+        uint32_t w;
+        asm volatile("ld.global.b32 %0, [%1];" : "=r"(w) : "l"(p) : "memory");
+        return *reinterpret_cast<T*>(&w);
+    }
+}
+
 // ----------------------------------------------------------------- mbarrier
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)
 {
@@ -116,7 +138,8 @@ __device__ __forceinline__ void grid_dependency_wait()
 
 // Lets the next kernel of the stream, if it was launched with programmatic
 // stream serialization, be scheduled now (it still waits for this grid's
-// completion before its reads; see grid_dependency_wait).
+// completion before its reads; see grid_dependency_wait).  Nothing is handed over: what the
+// next kernel reads without that wait needs a release and an acquire of its own.
 __device__ __forceinline__ void allow_dependent_launch()
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

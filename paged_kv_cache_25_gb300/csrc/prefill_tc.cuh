@@ -413,9 +413,11 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         // launched as a programmatic dependent: every input may come from the kernel before
         grid_dependency_wait();
         // The sequences' own part may start beside this pass.  Its work counter is
-        // cleared here, fenced before this block lets it start (a memset would cost a
-        // launch of its own); it takes tickets by atomics only.
+        // cleared here (a memset would cost a launch of its own), performed before this
+        // block lets it start; it takes tickets by atomics only.  The fence before makes
+        // the exchange a release of all inputs, which its first ticket acquires.
         if (blockIdx.x == 0 && tid == 0) {
+            __threadfence();
             atomicExch(sp.ticket, 0u);
             __threadfence();
         }

@@ -110,7 +110,7 @@ __device__ __forceinline__ void soft_cap4(const CapForm& f, const float (&s)[4],
 // Tokens of group g's prefix, in whole blocks.
 __device__ __forceinline__ int prefix_tokens(const int32_t* group_prefix, int g, int block_size, int max_blocks)
 {
-    const int p = max(__ldg(group_prefix + g), 0) / block_size;
+    const int p = max(load_input(group_prefix + g), 0) / block_size;
     return min(p, max_blocks) * block_size;
 }
 
@@ -121,15 +121,15 @@ __device__ __forceinline__ int first_visible(const ScoreParams& sc, int s, int L
 {
     if (L <= 0) return 0;
     if (sc.group_of_seq) {
-        const int g = __ldg(sc.group_of_seq + s);
+        const int g = load_input(sc.group_of_seq + s);
         if (g >= sc.num_groups) set_error(err, PA_ERR_OUT_OF_RANGE);
         if (g < 0 || g >= sc.num_groups) return 0;
         return min(prefix_tokens(sc.group_prefix, g, block_size, max_blocks), L);
     }
     int lo = sc.window > 0 ? L - nq - sc.window + 1 : 0;
     if (sc.first_key) {
-        int f = __ldg(sc.first_key + static_cast<int64_t>(s) * nq);
-        for (int i = 1; i < nq; ++i) f = min(f, __ldg(sc.first_key + static_cast<int64_t>(s) * nq + i));
+        int f = load_input(sc.first_key + static_cast<int64_t>(s) * nq);
+        for (int i = 1; i < nq; ++i) f = min(f, load_input(sc.first_key + static_cast<int64_t>(s) * nq + i));
         lo = max(lo, f);
     }
     return min(max(lo, 0), L - 1);
@@ -139,7 +139,7 @@ __device__ __forceinline__ int first_visible(const ScoreParams& sc, int s, int L
 __device__ __forceinline__ int row_first(const ScoreParams& sc, int s, int nq, int i, int pos)
 {
     int lo = sc.window > 0 ? pos - sc.window + 1 : 0;
-    if (sc.first_key) lo = max(lo, __ldg(sc.first_key + static_cast<int64_t>(s) * nq + i));
+    if (sc.first_key) lo = max(lo, load_input(sc.first_key + static_cast<int64_t>(s) * nq + i));
     return lo;
 }
 
