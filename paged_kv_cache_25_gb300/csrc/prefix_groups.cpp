@@ -19,7 +19,7 @@ extern "C" int pa_shared_prefix_groups(const int32_t* tables, int max_blocks, co
     if (num_seqs < 0 || max_blocks <= 0 || block_size <= 0) return -1;
     if (num_seqs == 0) return 0;
     if (!tables || !lens || !group_of_seq || !prefix_lens) return -1;
-    const int64_t need = min_prefix_tokens > block_size ? (min_prefix_tokens + block_size - 1) / block_size : 1;
+    const int64_t need = min_prefix_tokens > block_size ? (static_cast<int64_t>(min_prefix_tokens) + block_size - 1) / block_size : 1;
     try {
         // full blocks of each sequence, up to the first unused entry
         std::vector<int> full(num_seqs), order(num_seqs);
