@@ -261,7 +261,7 @@ pa_status pa_decode_no_alloc(void* out, pa_dtype out_dtype, const void* q,
  *                   members' first prefix_lens / block_size table entries must be the same
  *                   (those of the lowest-numbered member are read).  A member may be as short
  *                   as its prefix, or shorter: it sees its own context_lens tokens.
- *   num_groups    : 0 .. 1024; 0 is pa_decode.  Groups may be empty or have one member.
+ *   num_groups    : 0 .. PA_MAX_PREFIX_GROUPS; 0 is pa_decode.  Groups may be empty or have one member.
  *   workspace     : pa_decode_shared_workspace_size(...) bytes for the same shapes and
  *                   num_groups; other rules as pa_decode's.
  * Both arrays are read on the device only: a captured call follows new groups, lengths and
@@ -270,6 +270,7 @@ pa_status pa_decode_no_alloc(void* out, pa_dtype out_dtype, const void* q,
  * would cost more than it saves: such a call is pa_decode.  bf16/fp16/FP8 pools with head_dim 64 or 128 (else PA_ERR_UNSUPPORTED); other
  * rules as pa_decode.  From fp16 and FP8 pools the prefix's probabilities enter P V as one
  * fp16 part, as in pa_prefill_chunk. */
+#define PA_MAX_PREFIX_GROUPS 1024
 pa_status pa_decode_shared(void* out, pa_dtype out_dtype, const void* q,
                            const void* k_cache, const void* v_cache, const pa_cache_desc* cache,
                            const int32_t* block_tables, int max_blocks_per_seq,
@@ -284,7 +285,9 @@ size_t pa_decode_shared_workspace_size(int num_seqs, int n_q_heads, int n_kv_hea
  * negative).  Sequences are grouped by common leading full blocks so that the block reads saved
  * (members - 1 times the prefix's blocks, summed over the groups) are the most that nested
  * choices allow; prefixes of fewer than min_prefix_tokens (or of no full block) are left out.
- * Fills group_of_seq [num_seqs] (-1: none) and prefix_lens (room for num_seqs / 2 groups);
+ * Of more than PA_MAX_PREFIX_GROUPS groups those that save the most are kept.
+ * Fills group_of_seq [num_seqs] (-1: none) and prefix_lens (room for num_seqs / 2 groups, at
+ * most PA_MAX_PREFIX_GROUPS);
  * returns the number of groups, or -1 on bad arguments. */
 int pa_shared_prefix_groups(const int32_t* tables, int max_blocks, const int32_t* lens,
                             int num_seqs, int block_size, int min_prefix_tokens,

@@ -478,8 +478,6 @@ static int shared_max_splits(int n_kv, int max_ctx)
     return s < 1 ? 1 : (s > 32 ? 32 : s);
 }
 
-static constexpr int kMaxGroups = 1024;   // prefix groups of a call
-
 // Whether the prefixes of a shared decode are worth a pass of their own.  All that the
 // batch's tables can hold bounds what the pass can save; it costs two more launches and
 // the tensor-core kernel's start.  Batches that share nearly all of what they hold, the
@@ -617,7 +615,7 @@ size_t pa_decode_shared_workspace_size(int num_seqs, int n_q_heads, int n_kv_hea
                                        int block_size, int max_context_len, int num_groups)
 {
     if (num_seqs <= 0 || n_q_heads <= 0 || n_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 ||
-        max_context_len <= 0 || n_q_heads % n_kv_heads != 0 || num_groups < 0 || num_groups > kMaxGroups)
+        max_context_len <= 0 || n_q_heads % n_kv_heads != 0 || num_groups < 0 || num_groups > PA_MAX_PREFIX_GROUPS)
         return 0;
     if (num_groups == 0)
         return pa_decode_workspace_size(num_seqs, n_q_heads, n_kv_heads, head_dim, block_size,
@@ -640,8 +638,8 @@ pa_status pa_decode_shared(void* out, pa_dtype out_dtype, const void* q, const v
         return fail(PA_ERR_UNSUPPORTED,
                     "shared-prefix decode runs on bf16/fp16/FP8 pools with head_dim 64 or 128");
     if (num_groups < 0) return fail(PA_ERR_INVALID_ARG, "num_groups < 0");
-    if (num_groups > kMaxGroups)
-        return fail(PA_ERR_UNSUPPORTED, "more than %d prefix groups per call", kMaxGroups);
+    if (num_groups > PA_MAX_PREFIX_GROUPS)
+        return fail(PA_ERR_UNSUPPORTED, "more than %d prefix groups per call", PA_MAX_PREFIX_GROUPS);
     if (num_groups > 0 && num_seqs > 0) {
         if (!group_of_seq || !prefix_lens) return fail(PA_ERR_INVALID_ARG, "NULL pointer argument");
         if ((reinterpret_cast<uintptr_t>(group_of_seq) & 3u) || (reinterpret_cast<uintptr_t>(prefix_lens) & 3u))

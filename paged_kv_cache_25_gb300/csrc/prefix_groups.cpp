@@ -5,7 +5,8 @@
 // then give the tree of shared prefixes (an interval of sorted sequences for every
 // branching point, built with one stack).  A group at an interval of n sequences with a
 // common run of r blocks saves (n - 1) * r block reads; bottom up, an interval becomes a
-// group when that is at least what the groups inside it would save.
+// group when that is at least what the groups inside it would save.  A call takes
+// PA_MAX_PREFIX_GROUPS of them: beyond that, those that save the least are let go.
 #include <algorithm>
 #include <cstdint>
 #include <vector>
@@ -84,17 +85,25 @@ extern "C" int pa_shared_prefix_groups(const int32_t* tables, int max_blocks, co
             }
         }
         // the chosen intervals, from the outermost in
-        int groups = 0;
+        std::vector<int> chosen;
         std::vector<int> todo(done.rbegin(), done.rend());
         while (!todo.empty()) {
-            const Node& n = nodes[todo.back()];
+            const int id = todo.back();
+            const Node& n = nodes[id];
             todo.pop_back();
-            if (n.group) {
-                for (int i = n.lo; i <= n.hi; ++i) group_of_seq[order[i]] = groups;
-                prefix_lens[groups++] = n.run * block_size;
-            } else {
-                todo.insert(todo.end(), n.inside.rbegin(), n.inside.rend());
-            }
+            if (n.group) chosen.push_back(id);
+            else todo.insert(todo.end(), n.inside.rbegin(), n.inside.rend());
+        }
+        if (chosen.size() > PA_MAX_PREFIX_GROUPS) {
+            std::stable_sort(chosen.begin(), chosen.end(),
+                             [&](int a, int b) { return nodes[a].saved > nodes[b].saved; });
+            chosen.resize(PA_MAX_PREFIX_GROUPS);
+        }
+        int groups = 0;
+        for (const int id : chosen) {
+            const Node& n = nodes[id];
+            for (int i = n.lo; i <= n.hi; ++i) group_of_seq[order[i]] = groups;
+            prefix_lens[groups++] = n.run * block_size;
         }
         return groups;
     } catch (...) {
