@@ -1,13 +1,15 @@
-"""Builds libpa.so in-tree for sm_103a with nvcc (no cmake, no torch extension).
+"""Builds libpa.so in-tree for sm_103a with nvcc (no cmake, no torch).
 
 Each translation unit compiles in parallel; the shared library links the CUDA
 runtime statically and reaches the driver's tensor-map encoder through the
-runtime's entry-point query, so it needs no -lcuda at link time.  Beside it
-_pa_marshal.so, the argument marshalling of the serving calls for Python (C++
-against the installed torch's headers).
+runtime's entry-point query, so it needs no -lcuda at link time.
+
+Where torch is installed, _pa_marshal.so is built beside it: the argument
+marshalling of the serving calls for Python, C++ against torch's headers.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -34,18 +36,15 @@ def _nvcc() -> str:
     raise RuntimeError("nvcc not found: the CUDA library cannot be built")
 
 
-def _deps():
-    files = [os.path.join(SRC, f) for f in os.listdir(SRC)]
-    files.append(os.path.join(os.path.dirname(HERE), "include", "pa.h"))
-    files.append(os.path.abspath(__file__))
-    return files
+def _stale(target: str, sources) -> bool:
+    """Whether target is older than its sources, the C header or this file."""
+    files = [os.path.join(SRC, f) for f in sources]
+    files += [os.path.join(os.path.dirname(HERE), "include", "pa.h"), os.path.abspath(__file__)]
+    return not os.path.exists(target) or any(os.path.getmtime(f) > os.path.getmtime(target) for f in files)
 
 
-def _stale() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(MARSHAL)):
-        return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(MARSHAL))
-    return any(os.path.getmtime(f) > t for f in _deps())
+def _has_torch() -> bool:
+    return importlib.util.find_spec("torch") is not None
 
 
 def _torch_flags(nvcc: str):
@@ -61,54 +60,57 @@ def _torch_flags(nvcc: str):
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    if not force and not _stale():
+    lib = force or _stale(LIB, [f for f in os.listdir(SRC) if f != MARSHAL_SOURCE])
+    marshal = _has_torch() and (force or _stale(MARSHAL, [MARSHAL_SOURCE]))
+    if not (lib or marshal):
         return LIB
     os.makedirs(OUT, exist_ok=True)
     nvcc = _nvcc()
     common = ["-O3", "-std=c++17", "-Xcompiler", "-fPIC", "-I", os.path.join(os.path.dirname(HERE), "include")]
-    jobs = []
-    for f in CUDA_SOURCES:
-        obj = os.path.join(OUT, f + ".o")
-        cmd = [nvcc, *ARCH, "-lineinfo", *common, "-c", os.path.join(SRC, f), "-o", obj]
-        if ptxas_info:
-            cmd += ["-Xptxas", "-v"]
-        jobs.append((obj, cmd))
-    for f in CXX_SOURCES:
-        obj = os.path.join(OUT, f + ".o")
-        jobs.append((obj, ["g++", "-O2", "-std=c++17", "-fPIC", "-c", os.path.join(SRC, f), "-o", obj]))
-    marshal_obj = os.path.join(OUT, MARSHAL_SOURCE + ".o")
-    cflags, ldflags = _torch_flags(nvcc)
-    jobs.append((marshal_obj, ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", *cflags, "-c",
-                               os.path.join(SRC, MARSHAL_SOURCE), "-o", marshal_obj]))
+    source = lambda f: os.path.join(SRC, f)            # noqa: E731
+    obj = lambda f: os.path.join(OUT, f + ".o")        # noqa: E731
+    cmds = {}
+    if lib:
+        for f in CUDA_SOURCES:
+            cmds[f] = [nvcc, *ARCH, "-lineinfo", *common, "-c", source(f), "-o", obj(f)]
+            if ptxas_info:
+                cmds[f] += ["-Xptxas", "-v"]
+        for f in CXX_SOURCES:
+            cmds[f] = ["g++", "-O2", "-std=c++17", "-fPIC", "-c", source(f), "-o", obj(f)]
+    if marshal:
+        cflags, ldflags = _torch_flags(nvcc)
+        cmds[MARSHAL_SOURCE] = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", *cflags, "-c",
+                                source(MARSHAL_SOURCE), "-o", obj(MARSHAL_SOURCE)]
 
-    def run(job):
-        obj, cmd = job
+    def run(cmd):
         if verbose:
             print(" ".join(cmd), flush=True)
-        p = subprocess.run(cmd, capture_output=True, text=True)
-        return obj, cmd, p
+        return subprocess.run(cmd, capture_output=True, text=True)
 
-    with ThreadPoolExecutor(max(1, min(len(jobs), os.cpu_count() or 1))) as ex:
-        results = list(ex.map(run, jobs))
-    for obj, cmd, p in results:
-        if p.returncode != 0:
-            sys.stderr.write(p.stdout + p.stderr)
-            raise RuntimeError(f"compile failed: {' '.join(cmd)}")
-        if (verbose or ptxas_info) and (p.stdout or p.stderr):
-            sys.stderr.write(p.stdout + p.stderr)
+    with ThreadPoolExecutor(max(1, min(len(cmds), os.cpu_count() or 1))) as ex:
+        results = dict(zip(cmds, ex.map(run, cmds.values())))
 
-    def link_to(path, cmd):
-        tmp = path + f".{os.getpid()}.tmp"
+    def link(target, cmd, sources):
+        for f in sources:
+            p = results[f]
+            if p.returncode != 0:
+                sys.stderr.write(p.stdout + p.stderr)
+                raise RuntimeError(f"compile failed: {' '.join(cmds[f])}")
+            if (verbose or ptxas_info) and (p.stdout or p.stderr):
+                sys.stderr.write(p.stdout + p.stderr)
+        tmp = target + f".{os.getpid()}.tmp"
         cmd = [*cmd, "-o", tmp]
         p = subprocess.run(cmd, capture_output=True, text=True)
         if p.returncode != 0:
             sys.stderr.write(p.stdout + p.stderr)
             raise RuntimeError("link failed: " + " ".join(cmd))
-        os.replace(tmp, path)
+        os.replace(tmp, target)
 
-    link_to(LIB, [nvcc, *ARCH, "-shared", *[o for o, _, _ in results if o != marshal_obj]])
-    # (takes the library's functions by address; torch's libraries are loaded before it)
-    link_to(MARSHAL, ["g++", "-shared", marshal_obj, *ldflags])
+    if lib:
+        sources = CUDA_SOURCES + CXX_SOURCES
+        link(LIB, [nvcc, *ARCH, "-shared", *map(obj, sources)], sources)
+    if marshal:    # (takes the library's functions by address; torch's libraries are loaded before it)
+        link(MARSHAL, ["g++", "-shared", obj(MARSHAL_SOURCE), *ldflags], [MARSHAL_SOURCE])
     return LIB
 
 
