@@ -420,9 +420,11 @@ const char* pa_last_error_message(void);
  * outcome with pa_get_device_error. */
 pa_status pa_selftest_bounded_wait(unsigned limit_us, void* scratch, void* stream);
 
-/* Measurement hook: when both are non-NULL, pa_decode records `start` right
- * before its main attention kernel and `stop` right after it on the call's
- * stream (cudaEvent_t passed as void*).  Pass NULL, NULL to turn it off. */
+/* Measurement hook: when both are non-NULL, pa_decode (and pa_decode_verify,
+ * pa_decode_scored) records `start` right before its main attention kernel and
+ * `stop` right after it on the call's stream (cudaEvent_t passed as void*);
+ * pa_decode_shared records `start` before its prefix pass, where it has one.
+ * Pass NULL, NULL to turn it off. */
 void pa_set_profile_events(void* start, void* stop);
 
 /* ---------------------------------------------------------------- host allocator

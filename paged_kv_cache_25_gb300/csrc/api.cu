@@ -573,6 +573,9 @@ static pa_status decode_common(void* out, pa_dtype out_dtype, const void* q, con
         pass.max_splits = splits;
         pass.ticket = a.ticket;
         score->group_splits = pass.splits;
+        cudaEvent_t ev0 = nullptr, ev1 = nullptr;
+        profile_events(&ev0, &ev1);
+        if (ev0) cudaEventRecord(ev0, static_cast<cudaStream_t>(stream));   // (launch_decode: the stop)
         const cudaError_t e0 = launch_prefix_pass(a, pass, static_cast<cudaStream_t>(stream));
         if (e0 != cudaSuccess) return cuda_fail(e0, "prefix pass launch");
     }

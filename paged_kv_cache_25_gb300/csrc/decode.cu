@@ -315,7 +315,8 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t s)
     const float sl2 = a.scale * 1.4426950408889634f;   // softmax in base 2
     cudaEvent_t ev0 = nullptr, ev1 = nullptr;
     profile_events(&ev0, &ev1);
-    if (ev0) cudaEventRecord(ev0, s);
+    // (a shared decode's attention began with its prefix pass)
+    if (ev0 && !(a.score && a.score->group_of_seq)) cudaEventRecord(ev0, s);
     cudaError_t e;
     if (a.score) {
         e = launch_decode_scored(a, s, sl2);

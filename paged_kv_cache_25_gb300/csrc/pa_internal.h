@@ -26,7 +26,7 @@ unsigned* device_error_word();
 pa_status encode_pool_map(CUtensorMap* map, const void* base, pa_dtype dt, int row_elems,
                           uint64_t rows, int box_x, int box_y, int swizzle = 128);
 
-// Profiling events for the main decode kernel (may be null).
+// Profiling events around the decode's attention kernels (may be null).
 void profile_events(cudaEvent_t* start, cudaEvent_t* stop);
 
 inline int elem_bytes(pa_dtype d) { return d == PA_F32 ? 4 : (d == PA_FP8_E4M3 ? 1 : 2); }
