@@ -321,7 +321,7 @@ typedef struct {
  * prefix), first_key is [num_seqs][q_per_seq].  Pools and head dims as pa_decode for one
  * row, as pa_decode_verify for more; other rules theirs too.  Only the blocks from the first
  * visible key on are read.  workspace: pa_decode_scored_workspace_size bytes for the same
- * shapes and window (0 for none): a window bounds the partitions, so it needs less. */
+ * shapes and window, or for none (window 0), which is enough for any window. */
 pa_status pa_decode_scored(void* out, pa_dtype out_dtype, const void* q,
                            const void* k_cache, const void* v_cache, const pa_cache_desc* cache,
                            const int32_t* block_tables, int max_blocks_per_seq,

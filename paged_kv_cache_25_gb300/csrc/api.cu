@@ -163,23 +163,29 @@ static constexpr int kMaxPartBlocks = 128;   // blocks of a partition (the decod
 
 // `extra` more partial slots a row (the prefix pass of a shared decode) come
 // before the partitions' slots, and `head` bytes (256-aligned) after the control area.
+// full_ctx > 0: max_ctx is the span that a window leaves of contexts of full_ctx.
 static size_t decode_ws_bytes(int B, int nq, int n_q, int n_kv, int D, int BS, int max_ctx,
                               int* part, int* parts, int extra = 0, size_t head = 0,
-                              bool window = false)
+                              int full_ctx = 0)
 {
     // work units per partition index: (sequence, KV head, 8-row sub-group)
     const int64_t groups = static_cast<int64_t>(B) * n_kv * ((n_q / n_kv * nq + 7) / 8);
-    int p = decode_partition_tokens(groups, BS, max_ctx);
-    // several query rows a sequence (16-row units): each unit's combine and
-    // partials cost more, so large batches take 2048-token partitions
-    // (Llama-3-8B batch verifying 3 drafts: 0.837 -> 0.906 of the copy peak)
-    if (nq > 1 && p == 1024 && groups * ((max_ctx + 2047) / 2048) >= 300) p = 2048;
+    auto partition = [&](int ctx) {
+        const int p = decode_partition_tokens(groups, BS, ctx);
+        // several query rows a sequence (16-row units): each unit's combine and
+        // partials cost more, so large batches take 2048-token partitions
+        // (Llama-3-8B batch verifying 3 drafts: 0.837 -> 0.906 of the copy peak)
+        return nq > 1 && p == 1024 && groups * ((ctx + 2047) / 2048) >= 300 ? 2048 : p;
+    };
+    int p = partition(max_ctx);
     // a window makes most sequences span the same length, max_ctx: partitions of equal
     // length, at most half over the rule's (a window of 1024 keys and the rest of its first
     // block would else be one partition of 1024 tokens and one of up to 15, a second unit
-    // and a merge for nothing: 202 us against 165 for 256 sequences of Llama-3-8B's heads)
-    if (window && max_ctx > p) {
-        int n = (2 * max_ctx + p) / (2 * p);
+    // and a merge for nothing: 202 us against 165 for 256 sequences of Llama-3-8B's heads),
+    // no more of them than without the window, whose workspace is then enough for any
+    if (full_ctx > 0 && max_ctx > p) {
+        const int full = partition(full_ctx);
+        int n = std::min((2 * max_ctx + p) / (2 * p), (full_ctx + full - 1) / full);
         n = std::max(n, (max_ctx + kMaxPartBlocks * BS - 1) / (kMaxPartBlocks * BS));
         p = ((max_ctx + n - 1) / n + BS - 1) / BS * BS;
     }
@@ -531,7 +537,7 @@ static pa_status decode_common(void* out, pa_dtype out_dtype, const void* q, con
     const size_t head = shared ? align256(score->num_groups * sizeof(int32_t)) : 0;
     const size_t need = decode_ws_bytes(num_seqs, q_per_seq, n_q_heads, cache->n_kv_heads,
                                         cache->head_dim, block_size, max_ctx, &part, &parts, splits, head,
-                                        score && score->window > 0);
+                                        score && score->window > 0 ? max_blocks_per_seq * block_size : 0);
     if (parts > 65535) return fail(PA_ERR_UNSUPPORTED, "too many partitions per sequence");
     if (!workspace || workspace_bytes < need)
         return fail(PA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need,
@@ -665,7 +671,7 @@ size_t pa_decode_scored_workspace_size(int num_seqs, int q_per_seq, int n_q_head
         return 0;
     return decode_ws_bytes(num_seqs, q_per_seq, n_q_heads, n_kv_heads, head_dim, block_size,
                            scored_span(max_context_len, window, q_per_seq, block_size), nullptr, nullptr,
-                           0, 0, window > 0);
+                           0, 0, window > 0 ? max_context_len : 0);
 }
 
 pa_status pa_decode_scored(void* out, pa_dtype out_dtype, const void* q, const void* k_cache,
