@@ -42,9 +42,9 @@ FALLBACK_HBM_GBS = 6800.0
 # K/V bytes of the captured launch, what was captured); a record of another
 # batch of the same workload is scaled by its unique K/V bytes.
 NCU_TRAFFIC = {
-    ("llama3-8b-bf16", "f7fafdb75513a446"): (2372002304 + 13393152, 2359717888,
+    ("llama3-8b-bf16", "e6cb8234b000969c"): (2371998976 + 13430272, 2359717888,
                                              "full 256-sequence batch, one-pass capture"),
-    ("llama3-8b-fp8", "f7fafdb75513a446"): (1188192256 + 12467200, 1179858944,
+    ("llama3-8b-fp8", "e6cb8234b000969c"): (1188263424 + 12730112, 1179858944,
                                             "full 256-sequence batch, one-pass capture"),
 }
 # chunked prefill of the mixed step (the compact-pool capture runs the same four

@@ -136,6 +136,7 @@ pa_status pa_reshape_and_cache_quant(const void* k, const void* v, pa_dtype in_d
  *   k_cache, v_cache, slot_mapping: as for pa_reshape_and_cache; the pool has dtype in_dtype, or
  *                   is an FP8 pool (codes as pa_reshape_and_cache_quant makes them, of the rotated
  *                   k before any rounding; head_dim 64 or 128).
+ * Two tokens with one slot: which of them each element of the row comes from is unspecified.
  * Of a token with slot < 0 (padding) nothing is written, its q_out row included; neither of
  * one whose slot or position is out of range, which sets PA_ERR_OUT_OF_RANGE on the device.
  * Pointers 16-byte aligned (positions 4, slot_mapping 8); strides multiples of 16 bytes and at
@@ -252,7 +253,7 @@ pa_status pa_decode_no_alloc(void* out, pa_dtype out_dtype, const void* q,
  * pa_decode for a batch in which groups of sequences start with the same blocks (one
  * system prompt, several samples of one prompt; see the prefix cache below): a group's
  * common blocks are read once for all its members instead of once per member.  The
- * result is pa_decode's up to rounding.
+ * result is pa_decode's up to the roundings named below.
  *   group_of_seq  : int32 [num_seqs] on the device, the group of each sequence, or a negative
  *                   value for one that shares nothing.  A value >= num_groups counts as
  *                   negative and, where groups are read, sets PA_ERR_OUT_OF_RANGE on the device.
@@ -267,9 +268,9 @@ pa_status pa_decode_no_alloc(void* out, pa_dtype out_dtype, const void* q,
  * Both arrays are read on the device only: a captured call follows new groups, lengths and
  * tables.  They are not read where the tables can hold so little (num_seqs *
  * max_blocks_per_seq blocks of at most 64 MiB together) that reading the prefixes apart
- * would cost more than it saves: such a call is pa_decode.  bf16/fp16/FP8 pools with head_dim 64 or 128 (else PA_ERR_UNSUPPORTED); other
- * rules as pa_decode.  From fp16 and FP8 pools the prefix's probabilities enter P V as one
- * fp16 part, as in pa_prefill_chunk. */
+ * would cost more than it saves: such a call is pa_decode.  bf16/fp16/FP8 pools with
+ * head_dim 64 or 128 (else PA_ERR_UNSUPPORTED); other rules as pa_decode.  The prefix's
+ * probabilities and queries are rounded as in pa_prefill_chunk, the others as in pa_decode. */
 #define PA_MAX_PREFIX_GROUPS 1024
 pa_status pa_decode_shared(void* out, pa_dtype out_dtype, const void* q,
                            const void* k_cache, const void* v_cache, const pa_cache_desc* cache,
@@ -354,7 +355,13 @@ size_t pa_decode_scored_workspace_size(int num_seqs, int q_per_seq, int n_q_head
  * bf16, fp16 and FP8 E4M3 pools (f32 pools return PA_ERR_UNSUPPORTED).  FP8
  * pools keep V transposed per 16-token piece as for decode; their codes are
  * widened exactly to fp16 on chip (every E4M3 value is an fp16 value) and the
- * scales are folded into the softmax scale (k_scale) and the output (v_scale). */
+ * scales are folded into the softmax scale (k_scale) and the output (v_scale).
+ * Roundings: probabilities enter P V as two bf16 parts (about 16 bits) over bf16
+ * pools, as one fp16 part over fp16 and FP8 pools (11 bits: an output moves by at
+ * most 2^-12 of the largest |v| that it averages).  bf16 queries over an FP8 pool
+ * with head_dim 128 enter the scores as the sum of two E4M3 parts: exact for
+ * elements down to 2^-10 of the row's largest, off by at most 2^-17 of that
+ * largest below. */
 pa_status pa_prefill_chunk(void* out, pa_dtype out_dtype, const void* q,
                            const void* k_cache, const void* v_cache, const pa_cache_desc* cache,
                            const int32_t* block_tables, int max_blocks_per_seq,
@@ -370,7 +377,7 @@ size_t pa_prefill_workspace_size(int num_reqs, int n_q_heads, int head_dim, int 
  * keys below prefix_len visible to every row of the chunk, also those behind a row of the
  * prefix itself; a window and first_key then still bound a row's keys from below.  Only the
  * 128-key tiles that some row of a 256-row tile sees are computed.  Other rules as
- * pa_prefill_chunk (no workspace). */
+ * pa_prefill_chunk (no workspace), and its roundings. */
 pa_status pa_prefill_scored(void* out, pa_dtype out_dtype, const void* q,
                             const void* k_cache, const void* v_cache, const pa_cache_desc* cache,
                             const int32_t* block_tables, int max_blocks_per_seq,

@@ -109,7 +109,7 @@ __device__ __forceinline__ bool rope_written(const RopeParams& p, const Place& w
 
 constexpr int kRopeThreads = 256;
 // Blocks of a grid that covers more: four an SM (64 registers a thread).  8192 tokens
-// of Llama-3-8B heads, bf16: 34.8 us (5.8 TB/s), against 50.2 with a block for every 256
+// of Llama-3-8B heads, bf16: 34.6 us (5.9 TB/s), against 50.2 with a block for every 256
 // items and no next token in flight, 43.6 and 39.5 with grids of five and six an SM.
 constexpr int kRopeBlocksPerSm = 4;
 constexpr int kVTok = 16;             // FP8: tokens of one transposed V tile

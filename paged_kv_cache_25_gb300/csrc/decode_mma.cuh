@@ -1205,8 +1205,9 @@ cudaError_t run_fp8_qt(const DecodeArgs& a, cudaStream_t s, float sl2)
         }
     }
     if constexpr (MQ && SC) {
-        // more than 8 rows: 16-row units as for 16-bit pools (256 sequences, 4 rows, Llama-3-8B's
-        // heads: 472 -> 351 us; two CTAs an SM without the few spills: 382), unless two 8-row
+        // more than 8 rows: 16-row units as for 16-bit pools (256 sequences of 512 - 4096 tokens, 4
+        // rows, Llama-3-8B's heads: 472 -> 342 us, floor 181; two CTAs an SM without the few
+        // spills: 9 % more), unless two 8-row
         // units for each still leave SMs short of work (12 sequences of 770: 11.4 against 12.7)
         const int rows = a.q_per_seq * (a.n_q / a.cache.n_kv_heads);
         const int64_t units16 = static_cast<int64_t>(a.num_seqs) * a.max_parts * a.cache.n_kv_heads *
