@@ -27,6 +27,7 @@ def test_a_shared_decode_is_timed_with_its_prefix():
     pa.pa_set_profile_events(*inner)
     try:
         for _ in range(9):
+            torch.cuda._sleep(2_000_000)        # the launches below are enqueued meanwhile
             outer[0].record()
             c.run(out=out)
             outer[1].record()
