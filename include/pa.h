@@ -58,7 +58,10 @@ typedef enum {
     PA_ERR_CUDA = 6           /* a CUDA runtime call failed                      */
 } pa_status;
 
-typedef enum { PA_F32 = 0, PA_F16 = 1, PA_BF16 = 2, PA_FP8_E4M3 = 3 } pa_dtype;
+typedef enum {
+    PA_F32 = 0, PA_F16 = 1, PA_BF16 = 2, PA_FP8_E4M3 = 3,
+    PA_FP4_E2M1 = 4           /* pools only: 4-bit codes with a scale for every 16 of them */
+} pa_dtype;
 
 /* Shape of one layer's paged K/V pool.  head_dim in {64, 128} and block_size
  * in {16, 32} run on the tensor-core paths; fp32 pools run on a CUDA-core
@@ -75,7 +78,16 @@ typedef enum { PA_F32 = 0, PA_F16 = 1, PA_BF16 = 2, PA_FP8_E4M3 = 3 } pa_dtype;
  * [b][h][o / 16][i][o % 16].  A piece (head_dim x 16 codes) is contiguous, so
  * the kernels fetch it with one bulk copy, and a 16-byte row holds the 16
  * tokens of one head-dim element, the order the P.V fragments use; K keeps
- * the layout above. */
+ * the layout above.
+ * FP4 pools (4.5 bits an element; head_dim 64 or 128): dtype PA_FP4_E2M1, pools of bytes
+ * [num_blocks][n_kv_heads][block_size][9 * head_dim / 16], K and V alike.  A row holds head_dim / 2
+ * bytes of E2M1 codes, element 2i in the low half of byte i, then head_dim / 16 bytes of E4M3
+ * scales, one for each 16 elements; an element is e2m1(code) * e4m3(scale) * k_scale (v_scale
+ * for V), with k_scale and v_scale in [1e-30, 1e30] and act_dtype as for FP8 pools.  Of two
+ * tokens written to one slot in one call, codes and scales may come from either.  Calls that take
+ * FP4 pools: pa_reshape_and_cache_quant, the rotary writes, pa_gather_cache, pa_decode,
+ * pa_decode_verify, pa_prefill_chunk, pa_copy_blocks and pa_swap_blocks; the others return
+ * PA_ERR_UNSUPPORTED. */
 typedef struct {
     int num_blocks;
     int block_size;
@@ -108,12 +120,27 @@ pa_status pa_reshape_and_cache(const void* k, const void* v, void* k_cache, void
  * in_dtype (PA_F32, PA_F16 or PA_BF16).  Into an FP8 pool each element is
  * stored as the E4M3 code of fp32(x) / k_scale (v_scale for V), the division
  * IEEE-rounded in fp32, the code rounded to nearest even and saturated to
- * +-448.  Into a pool of in_dtype it is pa_reshape_and_cache.  Other pairs
+ * +-448.  Into an FP4 pool, for each 16 elements x of a row and S = k_scale (v_scale):
+ * scale s = E4M3 of max|x| / (6 S) kept in [2^-9, 448], codes E2M1 of x / (s S), saturated at
+ * 6, the quotients and products IEEE-rounded in fp32, the codes to nearest even (a NaN makes
+ * its 16 elements read as NaN, infinities saturate).  Into a pool of in_dtype it is
+ * pa_reshape_and_cache.  Other pairs
  * return PA_ERR_UNSUPPORTED.  Slot rules as for pa_reshape_and_cache. */
 pa_status pa_reshape_and_cache_quant(const void* k, const void* v, pa_dtype in_dtype,
                                      void* k_cache, void* v_cache,
                                      const int64_t* slot_mapping, int num_tokens,
                                      const pa_cache_desc* cache, void* stream);
+
+/* Rows read back, the inverse of the cache write: token t's K and V rows of slot slot_mapping[t]
+ * become k_out[t], v_out[t] ([num_tokens][n_kv_heads][head_dim], contiguous, out_dtype PA_F32,
+ * PA_F16 or PA_BF16), as the values that the pool's codes stand for: their exact product with the
+ * scales is rounded to fp32 (FP8 and FP4 pools), then to out_dtype.  Every pool type.  Slots may
+ * repeat.  slot < 0: the token's output rows are left as they are; so are those of a slot beyond
+ * the pool, which sets PA_ERR_OUT_OF_RANGE on the device.  k_out and v_out must not overlap the pools.
+ * Pointers 16-byte aligned (slot_mapping 8).  num_tokens == 0 is a no-op. */
+pa_status pa_gather_cache(void* k_out, void* v_out, pa_dtype out_dtype, const void* k_cache,
+                          const void* v_cache, const int64_t* slot_mapping, int num_tokens,
+                          const pa_cache_desc* cache, void* stream);
 
 /* ---------------------------------------------------------------- rotary embedding + cache write
  * Rotates q and k by the angles of their tokens' positions and appends the
@@ -134,8 +161,9 @@ pa_status pa_reshape_and_cache_quant(const void* k, const void* v, pa_dtype in_d
  *                   rot_dim / 2 angles, then their sines (pa_rope_table fills one).
  *   rot_dim       : a multiple of 16 in [16, head_dim].
  *   k_cache, v_cache, slot_mapping: as for pa_reshape_and_cache; the pool has dtype in_dtype, or
- *                   is an FP8 pool (codes as pa_reshape_and_cache_quant makes them, of the rotated
- *                   k before any rounding; head_dim 64 or 128).
+ *                   is an FP8 or FP4 pool (codes as pa_reshape_and_cache_quant makes them, of the
+ *                   rotated k in fp32; head_dim 64 or 128; for FP4 pools the rotation's
+ *                   products are rounded to fp32 before they are added).
  * Two tokens with one slot: which of them each element of the row comes from is unspecified.
  * Of a token with slot < 0 (padding) nothing is written, its q_out row included; neither of
  * one whose slot or position is out of range, which sets PA_ERR_OUT_OF_RANGE on the device.
@@ -149,6 +177,24 @@ pa_status pa_rope_and_cache(void* q_out, const void* q, const void* k, const voi
                             void* k_cache, void* v_cache, const int64_t* slot_mapping,
                             int num_tokens, int n_q_heads, const pa_cache_desc* cache,
                             void* stream);
+/* The same with several position axes (an image's or a video's tokens have a time, a height and a
+ * width): pair i turns by a_i = position(axis of pair i) * base^(-2i / rot_dim).
+ *   positions     : int32 [num_axes][axis_stride], of which each row's first num_tokens count; all
+ *                   axes' positions of a token must be in [0, max_position), used or not.
+ *   num_axes      : 1 .. PA_MAX_ROPE_AXES.
+ *   axis_of_pair  : host memory, uint8 [rot_dim / 2], each below num_axes; read before the call returns.
+ * All axes share cos_sin, whose columns may hold any angles (a table of other frequencies serves
+ * too).  Other rules as pa_rope_and_cache. */
+#define PA_MAX_ROPE_AXES 4
+#define PA_MAX_ROPE_PAIRS 128
+pa_status pa_rope_axes_and_cache(void* q_out, const void* q, const void* k, const void* v,
+                                 pa_dtype in_dtype, int64_t q_out_stride, int64_t q_stride,
+                                 int64_t k_stride, int64_t v_stride, const int32_t* positions,
+                                 int64_t axis_stride, int num_axes, const uint8_t* axis_of_pair,
+                                 const float* cos_sin, int max_position, int rot_dim, int interleaved,
+                                 void* k_cache, void* v_cache, const int64_t* slot_mapping,
+                                 int num_tokens, int n_q_heads, const pa_cache_desc* cache,
+                                 void* stream);
 /* Host: fills table (host memory, fp32 [max_position][rot_dim]) with the cosines and sines
  * above, computed in fp64.  Returns 0, or -1 on bad arguments (rot_dim odd, base <= 0, ...). */
 int pa_rope_table(float* table, int max_position, int rot_dim, double base);

@@ -20,7 +20,7 @@ from . import build as _build
 
 __all__ = [
     "PAError", "lib", "pa_reshape_and_cache", "pa_reshape_and_cache_quant",
-    "pa_rope_and_cache", "pa_rope_table", "pa_decode_shared",
+    "pa_rope_and_cache", "pa_rope_axes_and_cache", "pa_rope_axes", "pa_gather_cache", "pa_rope_table", "pa_decode_shared",
     "pa_decode_shared_workspace_size", "pa_shared_prefix_groups", "ScoreMod", "pa_decode_scored",
     "pa_decode_scored_workspace_size", "pa_prefill_scored", "pa_decode",
     "pa_decode_workspace_size", "pa_decode_verify", "pa_decode_verify_workspace_size",
@@ -32,8 +32,10 @@ __all__ = [
 
 PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_OUT_OF_RANGE = 0, 1, 2, 3
 PA_ERR_WORKSPACE, PA_ERR_TIMEOUT, PA_ERR_CUDA = 4, 5, 6
-_DT = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2, torch.float8_e4m3fn: 3}
-PA_F32, PA_F16, PA_BF16, PA_FP8_E4M3 = 0, 1, 2, 3
+_DT = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2, torch.float8_e4m3fn: 3,
+       torch.uint8: 4}     # (pools of bytes: 4-bit rows)
+PA_F32, PA_F16, PA_BF16, PA_FP8_E4M3, PA_FP4_E2M1 = 0, 1, 2, 3, 4
+PA_MAX_ROPE_AXES = 4
 
 
 class _Desc(C.Structure):
@@ -58,6 +60,9 @@ _SIGS = {
     "pa_reshape_and_cache_quant": (I, [P, P, I, P, P, P, I, C.POINTER(_Desc), P]),
     "pa_rope_and_cache": (I, [P, P, P, P, I, L, L, L, L, P, P, I, I, I, P, P, P, I, I,
                               C.POINTER(_Desc), P]),
+    "pa_rope_axes_and_cache": (I, [P, P, P, P, I, L, L, L, L, P, L, I, P, P, I, I, I, P, P, P, I, I,
+                                   C.POINTER(_Desc), P]),
+    "pa_gather_cache": (I, [P, P, I, P, P, P, I, C.POINTER(_Desc), P]),
     "pa_decode_shared": (I, [P, I, P, P, P, C.POINTER(_Desc), P, I, P, I, I, F, I, P, P, I, P, SZ, P]),
     "pa_decode_shared_workspace_size": (SZ, [I, I, I, I, I, I, I]),
     "pa_shared_prefix_groups": (I, [P, I, P, I, I, I, P, P]),
@@ -168,11 +173,16 @@ def _handle(stream) -> int:
 
 
 def _desc(k_cache: torch.Tensor, k_scale=None, v_scale=None, act_dtype=None) -> _Desc:
-    """Cache descriptor; FP8 pools (torch.float8_e4m3fn) need the two scales and
-    the activation dtype (of q and of the rows written into the pool)."""
+    """Cache descriptor; FP8 pools (torch.float8_e4m3fn) and FP4 pools (torch.uint8, rows of
+    9 * head_dim / 16 bytes) need the two scales and the activation dtype (of q and of the rows
+    written into the pool)."""
     nb, n_kv, bs, d = k_cache.shape
     dt = dtype_code(k_cache.dtype)
-    if dt == PA_FP8_E4M3:   # missing scales reach the library as 0 and are refused there
+    if dt == PA_FP4_E2M1:
+        if d % 9:
+            raise ValueError("FP4 pools [blocks][n_kv][block_size][9 * head_dim / 16] expected")
+        d = d // 9 * 16
+    if dt in (PA_FP8_E4M3, PA_FP4_E2M1):   # missing scales reach the library as 0 and are refused there
         return _Desc(nb, bs, n_kv, d, dt, float(k_scale or 0.0), float(v_scale or 0.0),
                      dtype_code(act_dtype) if act_dtype is not None else -1)
     return _Desc(nb, bs, n_kv, d, dt, 1.0, 1.0, dt)
@@ -192,8 +202,9 @@ def _marshal():
                 mod = importlib.util.module_from_spec(spec)
                 spec.loader.exec_module(mod)
                 mod.bind(*(C.cast(getattr(h, n), C.c_void_p).value for n in (
-                    "pa_rope_and_cache", "pa_decode_shared", "pa_decode_scored",
-                    "pa_prefill_scored")))
+                    "pa_rope_axes_and_cache", "pa_decode_shared", "pa_decode_scored",
+                    "pa_prefill_scored", "pa_decode_verify", "pa_prefill_chunk",
+                    "pa_gather_cache")))
                 _marshal_mod = mod
     return _marshal_mod
 
@@ -229,6 +240,9 @@ def pa_decode_verify(out, q, k_cache, v_cache, block_tables, context_lens, scale
                      block_size: int, workspace=None, stream=None, k_scale=None, v_scale=None):
     """out, q [B][q_per_seq][n_q][d]: query i of sequence s sits at position
     context_lens[s] - q_per_seq + i and sees keys up to it."""
+    if k_cache.dtype == torch.uint8 and q.dim() == 4:
+        return _decode4("pa_decode_verify", out, q, k_cache, v_cache, block_tables, context_lens, scale,
+                        block_size, workspace, stream, k_scale, v_scale)
     B, nq, n_q, _ = q.shape
     d = _desc(k_cache, k_scale, v_scale, q.dtype)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
@@ -242,7 +256,7 @@ def pa_decode_verify(out, q, k_cache, v_cache, block_tables, context_lens, scale
 def pa_reshape_and_cache_quant(k, v, k_cache, v_cache, slot_mapping, k_scale=None, v_scale=None,
                                stream=None):
     """k, v [T][n_kv][d] (fp32/fp16/bf16) -> pools, quantized to E4M3 codes of
-    x / scale when the pools are torch.float8_e4m3fn."""
+    x / scale when the pools are torch.float8_e4m3fn, to 4-bit rows when they are torch.uint8."""
     assert k.is_contiguous() and v.is_contiguous() and slot_mapping.dtype == torch.int64
     d = _desc(k_cache, k_scale, v_scale, k.dtype)
     _check(lib().pa_reshape_and_cache_quant(_ptr(k), _ptr(v), dtype_code(k.dtype), _ptr(k_cache),
@@ -256,11 +270,50 @@ def pa_rope_and_cache(q_out, q, k, v, positions, cos_sin, k_cache, v_cache, slot
     """q_out [T][n_q][d] = q rotated by its tokens' positions (int32 [T]); k, rotated, and v
     [T][n_kv][d] go to slot_mapping (int64 [T]) of the pools.  q, k and v may be slices of one
     projection (any token stride).  cos_sin: fp32 [max_position][rot_dim], see pa_rope_table.
-    FP8 pools take their scales."""
+    FP8 and FP4 pools take their scales."""
     st = _marshal().rope(q_out, q, k, v, positions, cos_sin, k_cache, v_cache, slot_mapping,
-                         interleaved, None if stream is None else _handle(stream), k_scale, v_scale)
+                         interleaved, None if stream is None else _handle(stream), k_scale, v_scale,
+                         None)
     if st != PA_OK:
         _check(st, "pa_rope_and_cache")
+
+
+def pa_rope_axes_and_cache(q_out, q, k, v, positions, axis_of_pair, cos_sin, k_cache, v_cache,
+                           slot_mapping, interleaved: bool = False, stream=None, k_scale=None,
+                           v_scale=None):
+    """pa_rope_and_cache with several position axes: positions int32 [axes][T] (rows of any stride),
+    axis_of_pair uint8 [rot_dim / 2] in host memory (bytes or a NumPy array, see pa_rope_axes): the
+    axis whose position turns each pair."""
+    if not isinstance(axis_of_pair, (bytes, np.ndarray)):
+        axis_of_pair = bytes(axis_of_pair)
+    elif isinstance(axis_of_pair, np.ndarray) and axis_of_pair.dtype != np.uint8:
+        raise TypeError("axis_of_pair: uint8 expected")
+    st = _marshal().rope(q_out, q, k, v, positions, cos_sin, k_cache, v_cache, slot_mapping,
+                         interleaved, None if stream is None else _handle(stream), k_scale, v_scale,
+                         axis_of_pair)
+    if st != PA_OK:
+        _check(st, "pa_rope_axes_and_cache")
+
+
+def pa_rope_axes(sections, in_turn: bool = False) -> np.ndarray:
+    """Axis of every rotated pair (uint8) from the number of pairs of each axis: one axis's pairs
+    after another's, or in turn as long as an axis has pairs left."""
+    sections = [int(n) for n in sections]
+    if not 1 <= len(sections) <= PA_MAX_ROPE_AXES or min(sections) < 0:
+        raise PAError(PA_ERR_INVALID_ARG, "pa_rope_axes: bad sections")
+    if not in_turn:
+        return np.repeat(np.arange(len(sections), dtype=np.uint8), sections)
+    return np.array([a for i in range(max(sections)) for a, n in enumerate(sections) if i < n], np.uint8)
+
+
+def pa_gather_cache(k_out, v_out, k_cache, v_cache, slot_mapping, stream=None, k_scale=None,
+                    v_scale=None):
+    """k_out, v_out [T][n_kv][d] (fp32/fp16/bf16) = the values of the pools' rows at slot_mapping
+    (int64 [T]; negative: the row is left as it is).  FP8 and FP4 pools take their scales."""
+    st = _marshal().gather(k_out, v_out, k_cache, v_cache, slot_mapping,
+                           None if stream is None else _handle(stream), k_scale, v_scale)
+    if st != PA_OK:
+        _check(st, "pa_gather_cache")
 
 
 def pa_rope_table(max_position: int, rot_dim: int, base: float = 10000.0) -> torch.Tensor:
@@ -273,10 +326,21 @@ def pa_rope_table(max_position: int, rot_dim: int, base: float = 10000.0) -> tor
     return table
 
 
+def _decode4(name, out, q, k_cache, v_cache, block_tables, context_lens, scale, block_size, workspace,
+             stream, k_scale, v_scale):
+    st = _marshal().decode(out, q, k_cache, v_cache, block_tables, context_lens, scale, block_size,
+                           workspace, None if stream is None else _handle(stream), k_scale, v_scale)
+    if st != PA_OK:
+        _check(st, name)
+
+
 def pa_decode(out, q, k_cache, v_cache, block_tables, context_lens, scale: float,
               block_size: int, workspace=None, stream=None, k_scale=None, v_scale=None):
     """out [B][n_q][d] (fp32/fp16/bf16) = paged decode attention of q [B][n_q][d].
-    FP8 pools also take k_scale and v_scale."""
+    FP8 and FP4 pools also take k_scale and v_scale."""
+    if k_cache.dtype == torch.uint8 and q.dim() == 3:
+        return _decode4("pa_decode", out, q, k_cache, v_cache, block_tables, context_lens, scale,
+                        block_size, workspace, stream, k_scale, v_scale)
     B, n_q, _ = q.shape
     d = _desc(k_cache, k_scale, v_scale, q.dtype)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
@@ -374,7 +438,14 @@ def pa_prefill_chunk(out, q, k_cache, v_cache, block_tables, query_start_loc, co
                      max_query_len: int, scale: float, block_size: int, workspace=None,
                      stream=None, k_scale=None, v_scale=None):
     """Chunked prefill: out/q [sum C][n_q][d]; query_start_loc int32 [R+1].
-    FP8 pools also take k_scale and v_scale."""
+    FP8 and FP4 pools also take k_scale and v_scale."""
+    if k_cache.dtype == torch.uint8:
+        st = _marshal().prefill(out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc,
+                                max_query_len, scale, block_size,
+                                None if stream is None else _handle(stream), k_scale, v_scale)
+        if st != PA_OK:
+            _check(st, "pa_prefill_chunk")
+        return
     R = int(context_lens.shape[0])
     n_q = int(q.shape[1])
     d = _desc(k_cache, k_scale, v_scale, q.dtype)

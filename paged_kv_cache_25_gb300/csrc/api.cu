@@ -127,18 +127,24 @@ int decode_partition_tokens(int64_t seq_groups, int block_size, int max_context_
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // need_act: the call reads q in act_dtype (decode); a cache write names its
-// input dtype itself and ignores act_dtype.
-static pa_status check_cache(const pa_cache_desc* c, bool need_act = true)
+// input dtype itself and ignores act_dtype.  need_scale: the call converts values (block copies do not).
+static pa_status check_cache(const pa_cache_desc* c, bool need_act = true, bool need_scale = true)
 {
     if (!c) return fail(PA_ERR_INVALID_ARG, "cache descriptor is NULL");
-    if (c->dtype != PA_F32 && c->dtype != PA_F16 && c->dtype != PA_BF16 && c->dtype != PA_FP8_E4M3)
+    if (c->dtype != PA_F32 && c->dtype != PA_F16 && c->dtype != PA_BF16 && c->dtype != PA_FP8_E4M3 &&
+        c->dtype != PA_FP4_E2M1)
         return fail(PA_ERR_INVALID_ARG, "unknown cache dtype %d", (int)c->dtype);
-    if (c->dtype == PA_FP8_E4M3) {
-        if (!(c->k_scale > 0.f) || !(c->v_scale > 0.f) || !std::isfinite(c->k_scale) ||
-            !std::isfinite(c->v_scale))
-            return fail(PA_ERR_INVALID_ARG, "FP8 pools need finite positive k_scale and v_scale");
+    const bool f4 = c->dtype == PA_FP4_E2M1;
+    if (c->dtype == PA_FP8_E4M3 || f4) {
+        const char* name = f4 ? "FP4" : "FP8";
+        if (need_scale && (!(c->k_scale > 0.f) || !(c->v_scale > 0.f) || !std::isfinite(c->k_scale) ||
+                           !std::isfinite(c->v_scale)))
+            return fail(PA_ERR_INVALID_ARG, "%s pools need finite positive k_scale and v_scale", name);
+        // (a group's scale times the pool's stays a normal fp32 number)
+        if (need_scale && f4 && (c->k_scale < 1e-30f || c->k_scale > 1e30f || c->v_scale < 1e-30f || c->v_scale > 1e30f))
+            return fail(PA_ERR_UNSUPPORTED, "FP4 pools take k_scale and v_scale in [1e-30, 1e30]");
         if (need_act && c->act_dtype != PA_BF16 && c->act_dtype != PA_F16)
-            return fail(PA_ERR_INVALID_ARG, "FP8 pools need act_dtype PA_BF16 or PA_F16");
+            return fail(PA_ERR_INVALID_ARG, "%s pools need act_dtype PA_BF16 or PA_F16", name);
     }
     if (c->num_blocks <= 0 || c->n_kv_heads <= 0)
         return fail(PA_ERR_INVALID_ARG, "num_blocks and n_kv_heads must be positive");
@@ -149,6 +155,8 @@ static pa_status check_cache(const pa_cache_desc* c, bool need_act = true)
         return fail(PA_ERR_UNSUPPORTED, "head_dim %d not supported (32/64/96/128/256)", c->head_dim);
     if (static_cast<int64_t>(c->num_blocks) * c->n_kv_heads * c->block_size >= (1ll << 31))
         return fail(PA_ERR_UNSUPPORTED, "pool has 2^31 or more rows");
+    if (f4 && c->head_dim != 64 && c->head_dim != 128)
+        return fail(PA_ERR_UNSUPPORTED, "FP4 pools take head_dim 64 or 128");
     return PA_OK;
 }
 
@@ -195,6 +203,13 @@ static size_t decode_ws_bytes(int B, int nq, int n_q, int n_kv, int D, int BS, i
     if (J <= 1 && extra == 0) return kControlBytes;
     const size_t units = static_cast<size_t>(B) * nq * n_q * ((J < 1 ? 1 : J) + extra);
     return kControlBytes + head + align256(units * 2 * sizeof(float)) + units * D * sizeof(float);
+}
+
+// What pa_decode and pa_decode_verify need whatever the pool's type (FP4 pools split their work another way).
+static size_t any_pool_ws_bytes(int B, int nq, int n_q, int n_kv, int D, int BS, int max_ctx)
+{
+    const size_t n = decode_ws_bytes(B, nq, n_q, n_kv, D, BS, max_ctx, nullptr, nullptr);
+    return D == 64 || D == 128 ? std::max(n, f4_workspace_bytes(B, nq, n_q / n_kv, n_kv, D, max_ctx)) : n;
 }
 
 // Tokens that the partitions of a sequence can span: with a window, its rows' keys
@@ -311,7 +326,8 @@ pa_status pa_reshape_and_cache_quant(const void* k, const void* v, pa_dtype in_d
     if (st != PA_OK) return st;
     if (in_dtype == cache->dtype)
         return pa_reshape_and_cache(k, v, k_cache, v_cache, slot_mapping, num_tokens, cache, stream);
-    if (cache->dtype != PA_FP8_E4M3 ||
+    const bool f4 = cache->dtype == PA_FP4_E2M1;
+    if ((cache->dtype != PA_FP8_E4M3 && !f4) ||
         (in_dtype != PA_F32 && in_dtype != PA_F16 && in_dtype != PA_BF16))
         return fail(PA_ERR_UNSUPPORTED, "cache write from dtype %d into dtype %d", (int)in_dtype,
                     (int)cache->dtype);
@@ -327,8 +343,9 @@ pa_status pa_reshape_and_cache_quant(const void* k, const void* v, pa_dtype in_d
         return fail(PA_ERR_INVALID_ARG, "slot_mapping must be 8-byte aligned");
     unsigned* err = device_error_word();
     if (!err) return fail(PA_ERR_CUDA, "cannot locate the device error word");
-    cudaError_t e = launch_cache_write_fp8(k, v, in_dtype, k_cache, v_cache, slot_mapping,
-                                           num_tokens, *cache, err, static_cast<cudaStream_t>(stream));
+    if (f4 && cache->n_kv_heads > 65535) return fail(PA_ERR_UNSUPPORTED, "more than 65535 KV heads");
+    cudaError_t e = (f4 ? launch_cache_write_fp4 : launch_cache_write_fp8)(
+        k, v, in_dtype, k_cache, v_cache, slot_mapping, num_tokens, *cache, err, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "cache write launch");
     return ok();
 }
@@ -339,6 +356,9 @@ pa_status pa_reshape_and_cache(const void* k, const void* v, void* k_cache, void
 {
     pa_status st = check_cache(cache, false);
     if (st != PA_OK) return st;
+    if (cache->dtype == PA_FP4_E2M1)
+        return fail(PA_ERR_UNSUPPORTED, "rows for an FP4 pool are quantised as they are written: "
+                                        "pa_reshape_and_cache_quant");
     if (cache->dtype == PA_FP8_E4M3 && cache->head_dim != 64 && cache->head_dim != 128)
         return fail(PA_ERR_UNSUPPORTED, "FP8 pools take head_dim 64 or 128");
     if (num_tokens < 0) return fail(PA_ERR_INVALID_ARG, "num_tokens < 0");
@@ -364,18 +384,19 @@ pa_status pa_reshape_and_cache(const void* k, const void* v, void* k_cache, void
     return ok();
 }
 
-pa_status pa_rope_and_cache(void* q_out, const void* q, const void* k, const void* v,
-                            pa_dtype in_dtype, int64_t q_out_stride, int64_t q_stride,
-                            int64_t k_stride, int64_t v_stride, const int32_t* positions,
-                            const float* cos_sin, int max_position, int rot_dim, int interleaved,
-                            void* k_cache, void* v_cache, const int64_t* slot_mapping,
-                            int num_tokens, int n_q_heads, const pa_cache_desc* cache, void* stream)
+static pa_status rope_common(void* q_out, const void* q, const void* k, const void* v,
+                             pa_dtype in_dtype, int64_t q_out_stride, int64_t q_stride,
+                             int64_t k_stride, int64_t v_stride, const int32_t* positions,
+                             int64_t axis_stride, int num_axes, const uint8_t* axis_of_pair,
+                             const float* cos_sin, int max_position, int rot_dim, int interleaved,
+                             void* k_cache, void* v_cache, const int64_t* slot_mapping,
+                             int num_tokens, int n_q_heads, const pa_cache_desc* cache, void* stream)
 {
     pa_status st = check_cache(cache, false);
     if (st != PA_OK) return st;
     if (in_dtype != PA_F32 && in_dtype != PA_F16 && in_dtype != PA_BF16)
         return fail(PA_ERR_INVALID_ARG, "unknown in_dtype %d", (int)in_dtype);
-    if (cache->dtype != in_dtype && cache->dtype != PA_FP8_E4M3)
+    if (cache->dtype != in_dtype && cache->dtype != PA_FP8_E4M3 && cache->dtype != PA_FP4_E2M1)
         return fail(PA_ERR_UNSUPPORTED, "cache write from dtype %d into dtype %d", (int)in_dtype,
                     (int)cache->dtype);
     if (cache->dtype == PA_FP8_E4M3 && cache->head_dim != 64 && cache->head_dim != 128)
@@ -383,9 +404,25 @@ pa_status pa_rope_and_cache(void* q_out, const void* q, const void* k, const voi
     if (n_q_heads <= 0) return fail(PA_ERR_INVALID_ARG, "n_q_heads must be positive");
     if (rot_dim < 16 || rot_dim > cache->head_dim || rot_dim % 16 != 0)
         return fail(PA_ERR_INVALID_ARG, "rot_dim %d is not a multiple of 16 in [16, head_dim]", rot_dim);
+    RopeArgs a{};
+    a.axes = num_axes;
+    a.axis_stride = axis_stride;
+    if (num_axes < 1 || num_axes > PA_MAX_ROPE_AXES)
+        return fail(PA_ERR_INVALID_ARG, "num_axes %d outside [1, %d]", num_axes, PA_MAX_ROPE_AXES);
+    if (axis_of_pair) {
+        for (int i = 0; i < rot_dim / 2; ++i) {
+            if (axis_of_pair[i] >= num_axes)
+                return fail(PA_ERR_INVALID_ARG, "axis_of_pair[%d] = %d, of %d axes", i, (int)axis_of_pair[i], num_axes);
+            a.axis[i / 16] |= static_cast<uint32_t>(axis_of_pair[i]) << (2 * (i % 16));
+        }
+    } else if (num_axes > 1) {
+        return fail(PA_ERR_INVALID_ARG, "axis_of_pair is NULL");
+    }
     if (max_position <= 0) return fail(PA_ERR_INVALID_ARG, "max_position must be positive");
     if (num_tokens < 0) return fail(PA_ERR_INVALID_ARG, "num_tokens < 0");
     if (num_tokens == 0) return ok();
+    if (num_axes > 1 && axis_stride < num_tokens)
+        return fail(PA_ERR_INVALID_ARG, "the axes' rows of positions are shorter than num_tokens");
     if (!q_out || !q || !k || !v || !positions || !cos_sin || !k_cache || !v_cache || !slot_mapping)
         return fail(PA_ERR_INVALID_ARG, "NULL pointer argument");
     if (!aligned16(q_out) || !aligned16(q) || !aligned16(k) || !aligned16(v) ||
@@ -407,7 +444,6 @@ pa_status pa_rope_and_cache(void* q_out, const void* q, const void* k, const voi
         return fail(PA_ERR_UNSUPPORTED, "too many elements for one call");
     unsigned* err = device_error_word();
     if (!err) return fail(PA_ERR_CUDA, "cannot locate the device error word");
-    RopeArgs a{};
     a.q_out = q_out; a.q = q; a.k = k; a.v = v; a.in_dtype = in_dtype;
     a.q_out_stride = q_out_stride; a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;
     a.positions = positions; a.cos_sin = cos_sin; a.max_position = max_position;
@@ -419,6 +455,59 @@ pa_status pa_rope_and_cache(void* q_out, const void* q, const void* k, const voi
     return ok();
 }
 
+pa_status pa_rope_and_cache(void* q_out, const void* q, const void* k, const void* v,
+                            pa_dtype in_dtype, int64_t q_out_stride, int64_t q_stride,
+                            int64_t k_stride, int64_t v_stride, const int32_t* positions,
+                            const float* cos_sin, int max_position, int rot_dim, int interleaved,
+                            void* k_cache, void* v_cache, const int64_t* slot_mapping,
+                            int num_tokens, int n_q_heads, const pa_cache_desc* cache, void* stream)
+{
+    return rope_common(q_out, q, k, v, in_dtype, q_out_stride, q_stride, k_stride, v_stride, positions, 0, 1,
+                       nullptr, cos_sin, max_position, rot_dim, interleaved, k_cache, v_cache, slot_mapping,
+                       num_tokens, n_q_heads, cache, stream);
+}
+
+pa_status pa_rope_axes_and_cache(void* q_out, const void* q, const void* k, const void* v,
+                                 pa_dtype in_dtype, int64_t q_out_stride, int64_t q_stride,
+                                 int64_t k_stride, int64_t v_stride, const int32_t* positions,
+                                 int64_t axis_stride, int num_axes, const uint8_t* axis_of_pair,
+                                 const float* cos_sin, int max_position, int rot_dim, int interleaved,
+                                 void* k_cache, void* v_cache, const int64_t* slot_mapping,
+                                 int num_tokens, int n_q_heads, const pa_cache_desc* cache, void* stream)
+{
+    if (!axis_of_pair) return fail(PA_ERR_INVALID_ARG, "axis_of_pair is NULL");
+    return rope_common(q_out, q, k, v, in_dtype, q_out_stride, q_stride, k_stride, v_stride, positions,
+                       axis_stride, num_axes, axis_of_pair, cos_sin, max_position, rot_dim, interleaved, k_cache,
+                       v_cache, slot_mapping, num_tokens, n_q_heads, cache, stream);
+}
+
+pa_status pa_gather_cache(void* k_out, void* v_out, pa_dtype out_dtype, const void* k_cache,
+                          const void* v_cache, const int64_t* slot_mapping, int num_tokens,
+                          const pa_cache_desc* cache, void* stream)
+{
+    pa_status st = check_cache(cache, false);
+    if (st != PA_OK) return st;
+    if (out_dtype != PA_F32 && out_dtype != PA_F16 && out_dtype != PA_BF16)
+        return fail(PA_ERR_INVALID_ARG, "unknown out_dtype %d", (int)out_dtype);
+    if (cache->dtype == PA_FP8_E4M3 && cache->head_dim != 64 && cache->head_dim != 128)
+        return fail(PA_ERR_UNSUPPORTED, "FP8 pools take head_dim 64 or 128");
+    if (cache->n_kv_heads > 65535) return fail(PA_ERR_UNSUPPORTED, "more than 65535 KV heads");
+    if (num_tokens < 0) return fail(PA_ERR_INVALID_ARG, "num_tokens < 0");
+    if (num_tokens == 0) return ok();
+    if (!k_out || !v_out || !k_cache || !v_cache || !slot_mapping)
+        return fail(PA_ERR_INVALID_ARG, "NULL pointer argument");
+    if (!aligned16(k_out) || !aligned16(v_out) || !aligned16(k_cache) || !aligned16(v_cache))
+        return fail(PA_ERR_INVALID_ARG, "k_out, v_out and the pools must be 16-byte aligned");
+    if ((reinterpret_cast<uintptr_t>(slot_mapping) & 7u) != 0)
+        return fail(PA_ERR_INVALID_ARG, "slot_mapping must be 8-byte aligned");
+    unsigned* err = device_error_word();
+    if (!err) return fail(PA_ERR_CUDA, "cannot locate the device error word");
+    const cudaError_t e = launch_gather(k_out, v_out, out_dtype, k_cache, v_cache, slot_mapping, num_tokens,
+                                        *cache, err, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "cache gather launch");
+    return ok();
+}
+
 pa_status pa_swap_blocks(const void* src_k, const void* src_v, int src_num_blocks, void* dst_k,
                          void* dst_v, int dst_num_blocks, const pa_cache_desc* layout,
                          const int32_t* block_mapping, int num_pairs, void* stream)
@@ -426,7 +515,7 @@ pa_status pa_swap_blocks(const void* src_k, const void* src_v, int src_num_block
     if (!layout) return fail(PA_ERR_INVALID_ARG, "layout descriptor is NULL");
     pa_cache_desc c = *layout;
     c.num_blocks = src_num_blocks > 0 ? src_num_blocks : 1;
-    pa_status st = check_cache(&c);
+    pa_status st = check_cache(&c, false, false);
     if (st != PA_OK) return st;
     if (num_pairs < 0 || src_num_blocks < 0 || dst_num_blocks < 0)
         return fail(PA_ERR_INVALID_ARG, "negative size");
@@ -461,8 +550,7 @@ size_t pa_decode_workspace_size(int num_seqs, int n_q_heads, int n_kv_heads, int
         max_context_len <= 0)
         return 0;
     if (n_q_heads % n_kv_heads != 0) return 0;
-    return decode_ws_bytes(num_seqs, 1, n_q_heads, n_kv_heads, head_dim, block_size,
-                           max_context_len, nullptr, nullptr);
+    return any_pool_ws_bytes(num_seqs, 1, n_q_heads, n_kv_heads, head_dim, block_size, max_context_len);
 }
 
 size_t pa_decode_verify_workspace_size(int num_seqs, int q_per_seq, int n_q_heads, int n_kv_heads,
@@ -471,8 +559,7 @@ size_t pa_decode_verify_workspace_size(int num_seqs, int q_per_seq, int n_q_head
     if (num_seqs <= 0 || q_per_seq <= 0 || n_q_heads <= 0 || n_kv_heads <= 0 || head_dim <= 0 ||
         block_size <= 0 || max_context_len <= 0 || n_q_heads % n_kv_heads != 0)
         return 0;
-    return decode_ws_bytes(num_seqs, q_per_seq, n_q_heads, n_kv_heads, head_dim, block_size,
-                           max_context_len, nullptr, nullptr);
+    return any_pool_ws_bytes(num_seqs, q_per_seq, n_q_heads, n_kv_heads, head_dim, block_size, max_context_len);
 }
 
 // Shared decode: ranges a prefix may be cut into (a thread block each for every KV
@@ -535,9 +622,17 @@ static pa_status decode_common(void* out, pa_dtype out_dtype, const void* q, con
     bool shared = score && score->group_of_seq;
     int splits = shared ? shared_max_splits(cache->n_kv_heads, max_ctx) : 0;
     const size_t head = shared ? align256(score->num_groups * sizeof(int32_t)) : 0;
-    const size_t need = decode_ws_bytes(num_seqs, q_per_seq, n_q_heads, cache->n_kv_heads,
-                                        cache->head_dim, block_size, max_ctx, &part, &parts, splits, head,
-                                        score && score->window > 0 ? max_blocks_per_seq * block_size : 0);
+    size_t need = decode_ws_bytes(num_seqs, q_per_seq, n_q_heads, cache->n_kv_heads,
+                                  cache->head_dim, block_size, max_ctx, &part, &parts, splits, head,
+                                  score && score->window > 0 ? max_blocks_per_seq * block_size : 0);
+    const bool f4 = cache->dtype == PA_FP4_E2M1;
+    if (f4) {
+        const int group = n_q_heads / cache->n_kv_heads;
+        if (f4_granules(num_seqs, q_per_seq, group, cache->n_kv_heads, max_ctx) >= (1ll << 31))
+            return fail(PA_ERR_UNSUPPORTED, "too many tokens in the tables for one call");
+        need = f4_workspace_bytes(num_seqs, q_per_seq, group, cache->n_kv_heads, cache->head_dim, max_ctx);
+        need = std::max(need, kControlBytes);
+    }
     if (parts > 65535) return fail(PA_ERR_UNSUPPORTED, "too many partitions per sequence");
     if (!workspace || workspace_bytes < need)
         return fail(PA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need,
@@ -585,7 +680,8 @@ static pa_status decode_common(void* out, pa_dtype out_dtype, const void* q, con
         const cudaError_t e0 = launch_prefix_pass(a, pass, static_cast<cudaStream_t>(stream));
         if (e0 != cudaSuccess) return cuda_fail(e0, "prefix pass launch");
     }
-    cudaError_t e = launch_decode(a, static_cast<cudaStream_t>(stream));
+    cudaError_t e = f4 ? launch_decode_fp4(a, workspace, static_cast<cudaStream_t>(stream))
+                       : launch_decode(a, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "decode launch");
     return ok();
 }
@@ -614,7 +710,7 @@ pa_status pa_decode_verify(void* out, pa_dtype out_dtype, const void* q, const v
         return fail(PA_ERR_INVALID_ARG, "q_per_seq %d outside [1, 16]", q_per_seq);
     if (cache->dtype == PA_F32 || (cache->head_dim != 64 && cache->head_dim != 128))
         return fail(PA_ERR_UNSUPPORTED,
-                    "multi-query decode runs on bf16/fp16/FP8 pools with head_dim 64 or 128");
+                    "multi-query decode runs on bf16/fp16/FP8/FP4 pools with head_dim 64 or 128");
     return decode_common(out, out_dtype, q, k_cache, v_cache, cache, block_tables,
                          max_blocks_per_seq, context_lens, num_seqs, q_per_seq, n_q_heads, scale,
                          block_size, workspace, workspace_bytes, stream);
@@ -643,7 +739,7 @@ pa_status pa_decode_shared(void* out, pa_dtype out_dtype, const void* q, const v
 {
     pa_status st = check_cache(cache);
     if (st != PA_OK) return st;
-    if (cache->dtype == PA_F32 || (cache->head_dim != 64 && cache->head_dim != 128))
+    if (cache->dtype == PA_F32 || cache->dtype == PA_FP4_E2M1 || (cache->head_dim != 64 && cache->head_dim != 128))
         return fail(PA_ERR_UNSUPPORTED,
                     "shared-prefix decode runs on bf16/fp16/FP8 pools with head_dim 64 or 128");
     if (num_groups < 0) return fail(PA_ERR_INVALID_ARG, "num_groups < 0");
@@ -688,6 +784,7 @@ pa_status pa_decode_scored(void* out, pa_dtype out_dtype, const void* q, const v
     if (q_per_seq > 1 && (cache->dtype == PA_F32 || (cache->head_dim != 64 && cache->head_dim != 128)))
         return fail(PA_ERR_UNSUPPORTED,
                     "multi-query decode runs on bf16/fp16/FP8 pools with head_dim 64 or 128");
+    if (cache->dtype == PA_FP4_E2M1) return fail(PA_ERR_UNSUPPORTED, "scored decode does not run on FP4 pools");
     ScoreParams sc{};
     st = check_mod(mod, &sc);
     if (st != PA_OK) return st;
@@ -716,7 +813,9 @@ static pa_status prefill_common(void* out, pa_dtype out_dtype, const void* q, co
     if (num_reqs < 0 || max_query_len < 0) return fail(PA_ERR_INVALID_ARG, "negative size");
     if (num_reqs == 0 || max_query_len == 0) return ok();
     if (cache->dtype == PA_F32)
-        return fail(PA_ERR_UNSUPPORTED, "chunked prefill runs on bf16/fp16/FP8 pools only");
+        return fail(PA_ERR_UNSUPPORTED, "chunked prefill runs on bf16/fp16/FP8/FP4 pools only");
+    if (score && cache->dtype == PA_FP4_E2M1)
+        return fail(PA_ERR_UNSUPPORTED, "scored prefill does not run on FP4 pools");
     if (cache->head_dim != 64 && cache->head_dim != 128)
         return fail(PA_ERR_UNSUPPORTED, "chunked prefill supports head_dim 64 and 128");
     if (out_dtype != PA_F32 && out_dtype != PA_F16 && out_dtype != PA_BF16)
@@ -745,6 +844,7 @@ static pa_status prefill_common(void* out, pa_dtype out_dtype, const void* q, co
     a.num_reqs = num_reqs; a.max_q = max_query_len; a.n_q = n_q_heads; a.scale = scale;
     a.err = err; a.score = score;
     cudaError_t e = score ? launch_prefill_scored(a, static_cast<cudaStream_t>(stream))
+                  : cache->dtype == PA_FP4_E2M1 ? launch_prefill_fp4(a, static_cast<cudaStream_t>(stream))
                           : launch_prefill_tc(a, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "prefill launch");
     return ok();

@@ -7,7 +7,10 @@
 // elements (i, i + rot/2) of the head, or (2i, 2i + 1) in the interleaved form;
 // elements at and past `rot` pass unchanged.  cos and sin come from the caller's
 // fp32 table, the products are fp32 and each result is rounded once, to the
-// dtype it is stored in (an E4M3 code of the value over the scale for FP8 pools).
+// dtype it is stored in (an E4M3 code of the value over the scale for FP8 pools, 4-bit rows for
+// FP4 pools: fp4.cuh).
+// With several position axes (time, height, width of a video's tokens) every pair has an axis of
+// its own, whose position of the token is the one that turns it; all axes share one table.
 //
 // Bound: HBM for long chunks (every element is read once and written once,
 // 3 flops each), launch latency for a decode step.
@@ -15,6 +18,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "fp4.cuh"
 #include "pa_device.cuh"
 #include "pa_internal.h"
 
@@ -84,27 +88,75 @@ struct RopeParams {
     int n_q, n_kv, head_dim, block_size;
     float k_scale, v_scale, k_inv, v_inv;
     unsigned* err;
+    // several axes: positions of axis a at positions + a * axis_stride; the axis of pair i is
+    // bits 2 (i % 16) and up of axis[i / 16]
+    int64_t axis_stride;
+    int axes;
+    uint32_t axis[PA_MAX_ROPE_PAIRS / 16];
 };
 
-// A token's slot and position.
+// A token's slot and position (AX: one for each axis).
+template <bool AX = false>
 struct Place {
     int64_t slot;
-    int pos;
+    int pos[AX ? PA_MAX_ROPE_AXES : 1];
 };
-__device__ __forceinline__ Place rope_place(const RopeParams& p, int t)
+template <bool AX = false>
+__device__ __forceinline__ Place<AX> rope_place(const RopeParams& p, int t)
 {
-    return {__ldg(p.slots + t), __ldg(p.positions + t)};
+    Place<AX> w;
+    w.slot = __ldg(p.slots + t);
+    if constexpr (AX) {
+#pragma unroll
+        for (int a = 0; a < PA_MAX_ROPE_AXES; ++a)
+            w.pos[a] = a < p.axes ? __ldg(p.positions + a * p.axis_stride + t) : 0;
+    } else {
+        w.pos[0] = __ldg(p.positions + t);
+    }
+    return w;
 }
 // Whether the token is written at all: not if it is padding or (flagged) its slot
 // or its position is out of range.
-__device__ __forceinline__ bool rope_written(const RopeParams& p, const Place& w)
+template <bool AX>
+__device__ __forceinline__ bool rope_written(const RopeParams& p, const Place<AX>& w)
 {
     if (w.slot < 0) return false;
-    if (w.slot >= p.num_slots || w.pos < 0 || w.pos >= p.max_position) {
-        set_error(p.err, PA_ERR_OUT_OF_RANGE);
-        return false;
+    bool ok = w.slot < p.num_slots;
+#pragma unroll
+    for (int pos : w.pos) ok = ok && pos >= 0 && pos < p.max_position;
+    if (!ok) set_error(p.err, PA_ERR_OUT_OF_RANGE);
+    return ok;
+}
+
+// Cosines and sines of pairs i0 .. i0 + N - 1 (i0 a multiple of 4).
+template <int N, bool AX>
+__device__ __forceinline__ void rope_angles(const RopeParams& p, const Place<AX>& at, int i0, float (&co)[N],
+                                            float (&si)[N])
+{
+    int pos = at.pos[0];
+    if constexpr (AX) {
+        static_assert(N <= 16, "the pairs' axes lie in one word");
+        const uint32_t bits = (p.axis[i0 / 16] >> (2 * (i0 % 16))) & ((1ull << (2 * N)) - 1u);
+        auto pick = [&](uint32_t a) { return a < 2 ? (a ? at.pos[1] : at.pos[0]) : (a == 2 ? at.pos[2] : at.pos[3]); };
+        if (bits != (bits & 3u) * (0x55555555u & ((1ull << (2 * N)) - 1u))) {   // pairs of several axes
+#pragma unroll
+            for (int x = 0; x < N; ++x) {
+                const float* row = p.cos_sin + static_cast<int64_t>(pick((bits >> (2 * x)) & 3u)) * p.rot + i0 + x;
+                co[x] = __ldg(row);
+                si[x] = __ldg(row + p.rot / 2);
+            }
+            return;
+        }
+        pos = pick(bits & 3u);
     }
-    return true;
+    const float4* cs = reinterpret_cast<const float4*>(p.cos_sin + static_cast<int64_t>(pos) * p.rot + i0);
+    const float4* sn = cs + p.rot / 8;
+#pragma unroll
+    for (int x = 0; x < N / 4; ++x) {
+        const float4 f = __ldg(cs + x), g = __ldg(sn + x);
+        co[4 * x] = f.x; co[4 * x + 1] = f.y; co[4 * x + 2] = f.z; co[4 * x + 3] = f.w;
+        si[4 * x] = g.x; si[4 * x + 1] = g.y; si[4 * x + 2] = g.z; si[4 * x + 3] = g.w;
+    }
 }
 
 constexpr int kRopeThreads = 256;
@@ -120,7 +172,7 @@ constexpr int kVTok = 16;             // FP8: tokens of one transposed V tile
 // pieces, then heads, then tokens; a thread keeps its head and pieces and goes from
 // token to token in steps of what the grid covers at once, the next token's pieces,
 // slot and position in flight while it works on one.
-template <typename T, bool F8>
+template <typename T, bool F8, bool AX>
 __device__ __forceinline__ void rope_rows(const RopeParams& p, unsigned index, unsigned threads, int heads)
 {
     using Pc = Piece<T>;
@@ -139,34 +191,26 @@ __device__ __forceinline__ void rope_rows(const RopeParams& p, unsigned index, u
     const int h = is_q ? head : (is_v ? head - p.n_q - p.n_kv : head - p.n_q);
     const T* src = static_cast<const T*>(is_q ? p.q : (is_v ? p.v : p.k)) + static_cast<int64_t>(h) * p.head_dim;
     const int64_t stride = is_q ? p.q_stride : (is_v ? p.v_stride : p.k_stride);
-    const float* table = p.cos_sin + c * N;
 
     uint4 ra = Pc::fetch(src + t * stride + e0), rb = Pc::fetch(src + t * stride + e1);
-    Place at = rope_place(p, t);
+    Place<AX> at = rope_place<AX>(p, t);
     while (true) {
         const int next = t + step;                               // (below 2^31: tokens and grid are)
         const bool more = next < p.num_tokens;
         uint4 na = ra, nb = rb;
-        Place next_at = at;
+        Place<AX> next_at = at;
         if (more) {
             na = Pc::fetch(src + next * stride + e0);
             nb = Pc::fetch(src + next * stride + e1);
-            next_at = rope_place(p, next);
+            next_at = rope_place<AX>(p, next);
         }
         if (rope_written(p, at)) {
             float a[N], b[N];
             Pc::widen(ra, a);
             Pc::widen(rb, b);
             if (turn) {
-                const float4* cs = reinterpret_cast<const float4*>(table + static_cast<int64_t>(at.pos) * p.rot);
-                const float4* sn = cs + p.rot / 8;
                 float co[N], si[N];
-#pragma unroll
-                for (int x = 0; x < N / 4; ++x) {
-                    const float4 f = __ldg(cs + x), g = __ldg(sn + x);
-                    co[4 * x] = f.x; co[4 * x + 1] = f.y; co[4 * x + 2] = f.z; co[4 * x + 3] = f.w;
-                    si[4 * x] = g.x; si[4 * x + 1] = g.y; si[4 * x + 2] = g.z; si[4 * x + 3] = g.w;
-                }
+                rope_angles<N, AX>(p, at, c * N, co, si);
                 if (p.interleaved) {
 #pragma unroll
                     for (int x = 0; x < N / 2; ++x) {
@@ -217,12 +261,12 @@ __device__ __forceinline__ void rope_rows(const RopeParams& p, unsigned index, u
 }
 
 // 16-bit and fp32 pools: q, k and v heads alike.
-template <typename T>
+template <typename T, bool AX>
 __global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) rope_kernel(const RopeParams p)
 {
     grid_dependency_wait();     // a programmatic dependent: scheduled while the kernel before drains
     allow_dependent_launch();   // a decode launched next waits for this grid before it reads
-    rope_rows<T, false>(p, blockIdx.x * kRopeThreads + threadIdx.x, gridDim.x * kRopeThreads,
+    rope_rows<T, false, AX>(p, blockIdx.x * kRopeThreads + threadIdx.x, gridDim.x * kRopeThreads,
                         p.n_q + 2 * p.n_kv);
 }
 
@@ -231,14 +275,14 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) rope_kernel(co
 // memory and written in the pool's V layout ([d][16 tokens] per piece): 16-byte rows when
 // the 16 tokens fill one piece (a prompt's chunk), 4-byte words for aligned runs of 4, single
 // bytes else (a decode step's tokens lie in 16 blocks).
-template <typename T, int D>
+template <typename T, int D, bool AX>
 __global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) rope_f8_kernel(const RopeParams p, unsigned v0, unsigned v_blocks)
 {
     grid_dependency_wait();
     allow_dependent_launch();
     if (blockIdx.x < v0 || blockIdx.x >= v0 + v_blocks) {
         const unsigned blk = blockIdx.x < v0 ? blockIdx.x : blockIdx.x - v_blocks;
-        rope_rows<T, true>(p, blk * kRopeThreads + threadIdx.x, (gridDim.x - v_blocks) * kRopeThreads,
+        rope_rows<T, true, AX>(p, blk * kRopeThreads + threadIdx.x, (gridDim.x - v_blocks) * kRopeThreads,
                            p.n_q + p.n_kv);
         return;
     }
@@ -256,7 +300,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) rope_f8_kernel
     if (tid < kVTok) {
         s_slot[tid] = -1;
         if (t0 + tid < p.num_tokens) {
-            const Place w = rope_place(p, t0 + tid);
+            const Place<AX> w = rope_place<AX>(p, t0 + tid);
             if (rope_written(p, w)) {
                 const int64_t b = w.slot / p.block_size, o = w.slot - b * p.block_size;
                 s_slot[tid] = w.slot;
@@ -313,11 +357,90 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) rope_f8_kernel
     }
 }
 
-template <typename T>
-static cudaError_t run_rope(const RopeParams& p, bool f8, cudaStream_t s)
+// FP4 pools: blocks v0 .. v0 + v_blocks - 1 take a tile of K and V groups each (16 elements that
+// share a scale), the others the q heads.  A thread quantises one group; a K group is rotated
+// first, with its pairs' other elements read beside it (they come from the first-level cache:
+// the neighbouring threads read the same rows).  The products of the rotation are rounded to
+// fp32 before they are added, here alone: a sum contracted one way or another could move a
+// value over the border between two codes.
+template <typename T, int D, bool AX>
+__global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) rope_f4_kernel(const RopeParams p, unsigned v0, unsigned v_blocks)
 {
+    grid_dependency_wait();
+    allow_dependent_launch();
+    if (blockIdx.x < v0 || blockIdx.x >= v0 + v_blocks) {
+        const unsigned blk = blockIdx.x < v0 ? blockIdx.x : blockIdx.x - v_blocks;
+        rope_rows<T, false, AX>(p, blk * kRopeThreads + threadIdx.x, (gridDim.x - v_blocks) * kRopeThreads, p.n_q);
+        return;
+    }
+    constexpr int kGroups = D / kFp4Group, kTok = kRopeThreads / (2 * kGroups);
+    constexpr int N = 8;
+    const int tid = threadIdx.x, c = tid % kGroups, tt = tid / kGroups % kTok;
+    const bool is_v = tid / (kGroups * kTok) != 0;
+    const unsigned tile = blockIdx.x - v0;
+    const int t = static_cast<int>(tile / p.n_kv) * kTok + tt, h = static_cast<int>(tile % p.n_kv);
+    if (t >= p.num_tokens) return;
+    const Place<AX> at = rope_place<AX>(p, t);
+    if (!rope_written(p, at)) return;
+    const T* src = static_cast<const T*>(is_v ? p.v : p.k) + t * (is_v ? p.v_stride : p.k_stride) +
+                   static_cast<int64_t>(h) * D;
+    auto load8 = [&](int e, float (&x)[N]) {
+        constexpr int n = Piece<T>::kN;
+#pragma unroll
+        for (int i = 0; i < N; i += n) {
+            float f[n];
+            Piece<T>::widen(__ldg(reinterpret_cast<const uint4*>(src + e + i)), f);
+#pragma unroll
+            for (int j = 0; j < n; ++j) x[i + j] = f[j];
+        }
+    };
+    float x[kFp4Group];
+#pragma unroll
+    for (int hf = 0; hf < kFp4Group / N; ++hf) {
+        const int e = c * kFp4Group + hf * N;
+        float a[N];
+        load8(e, a);
+        if (!is_v && e < p.rot) {
+            if (p.interleaved) {
+                float co[N / 2], si[N / 2];
+                rope_angles<N / 2, AX>(p, at, e / 2, co, si);
+#pragma unroll
+                for (int i = 0; i < N / 2; ++i) {
+                    const float u = a[2 * i], w = a[2 * i + 1];
+                    a[2 * i] = __fsub_rn(__fmul_rn(u, co[i]), __fmul_rn(w, si[i]));
+                    a[2 * i + 1] = __fadd_rn(__fmul_rn(w, co[i]), __fmul_rn(u, si[i]));
+                }
+            } else {
+                const bool second = e >= p.rot / 2;
+                const int i0 = second ? e - p.rot / 2 : e;
+                float b[N], co[N], si[N];
+                load8(second ? i0 : e + p.rot / 2, b);
+                rope_angles<N, AX>(p, at, i0, co, si);
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const float m = __fmul_rn(a[i], co[i]), o = __fmul_rn(b[i], si[i]);
+                    a[i] = second ? __fadd_rn(m, o) : __fsub_rn(m, o);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[hf * N + i] = a[i];
+    }
+    const float scale = is_v ? p.v_scale : p.k_scale;
+    uint32_t s;
+    const uint2 codes = fp4_quantise(x, scale, __fmul_rn(6.f, scale), s);
+    const unsigned sl = static_cast<unsigned>(at.slot), bs = p.block_size, blk = sl / bs;
+    fp4_store<D>(static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) +
+                     (static_cast<int64_t>(blk) * p.n_kv * bs + h * bs + sl % bs) * fp4_row_bytes(D),
+                 c, codes, s);
+}
+
+template <typename T, bool AX>
+static cudaError_t run_rope(const RopeParams& p, pa_dtype pool, cudaStream_t s)
+{
+    const bool f8 = pool == PA_FP8_E4M3, f4 = pool == PA_FP4_E2M1;
     const int per_head = p.head_dim / (2 * Piece<T>::kN);
-    const int64_t per_token = static_cast<int64_t>(p.n_q + (f8 ? 1 : 2) * p.n_kv) * per_head;
+    const int64_t per_token = static_cast<int64_t>(p.n_q + (f8 ? 1 : (f4 ? 0 : 2)) * p.n_kv) * per_head;
     const int64_t items = p.num_tokens * per_token;
     // as many blocks as the GPU holds, but at least one token's threads
     const int64_t most = std::max<int64_t>(152 * kRopeBlocksPerSm, (per_token + kRopeThreads - 1) / kRopeThreads);
@@ -331,7 +454,16 @@ static cudaError_t run_rope(const RopeParams& p, bool f8, cudaStream_t s)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (!f8) return cudaLaunchKernelEx(&cfg, rope_kernel<T>, p);
+    if (f4) {
+        const int tok = kRopeThreads / (2 * (p.head_dim / kFp4Group));
+        const unsigned kv_blocks = static_cast<unsigned>((p.num_tokens + tok - 1) / tok) * static_cast<unsigned>(p.n_kv);
+        const unsigned first = kv_blocks <= 152 * kRopeBlocksPerSm / 2 ? 0 : blocks;   // (as the V tiles below)
+        cfg.gridDim = dim3(blocks + kv_blocks);
+        if (p.head_dim == 128) return cudaLaunchKernelEx(&cfg, rope_f4_kernel<T, 128, AX>, p, first, kv_blocks);
+        if (p.head_dim == 64) return cudaLaunchKernelEx(&cfg, rope_f4_kernel<T, 64, AX>, p, first, kv_blocks);
+        return cudaErrorInvalidValue;
+    }
+    if (!f8) return cudaLaunchKernelEx(&cfg, rope_kernel<T, AX>, p);
     const int tile_heads = kRopeThreads / p.head_dim;
     const unsigned v_blocks = static_cast<unsigned>((p.num_tokens + kVTok - 1) / kVTok) *
                               static_cast<unsigned>((p.n_kv + tile_heads - 1) / tile_heads);
@@ -339,8 +471,8 @@ static cudaError_t run_rope(const RopeParams& p, bool f8, cudaStream_t s)
     // others beside them (512 scattered tokens 7.3 -> 5.5 us), else last (8192 tokens: 37 against 39)
     const unsigned v0 = v_blocks <= 152 * kRopeBlocksPerSm / 2 ? 0 : blocks;
     cfg.gridDim = dim3(blocks + v_blocks);
-    if (p.head_dim == 128) return cudaLaunchKernelEx(&cfg, rope_f8_kernel<T, 128>, p, v0, v_blocks);
-    if (p.head_dim == 64) return cudaLaunchKernelEx(&cfg, rope_f8_kernel<T, 64>, p, v0, v_blocks);
+    if (p.head_dim == 128) return cudaLaunchKernelEx(&cfg, rope_f8_kernel<T, 128, AX>, p, v0, v_blocks);
+    if (p.head_dim == 64) return cudaLaunchKernelEx(&cfg, rope_f8_kernel<T, 64, AX>, p, v0, v_blocks);
     return cudaErrorInvalidValue;
 }
 
@@ -365,11 +497,17 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s)
     };
     p.k_inv = inverse(a.cache.k_scale);
     p.v_inv = inverse(a.cache.v_scale);
-    const bool f8 = a.cache.dtype == PA_FP8_E4M3;
+    p.axes = a.axes;
+    p.axis_stride = a.axis_stride;
+    std::copy(a.axis, a.axis + PA_MAX_ROPE_PAIRS / 16, p.axis);
+    auto run = [&](auto zero) {
+        using T = decltype(zero);
+        return a.axes > 1 ? run_rope<T, true>(p, a.cache.dtype, s) : run_rope<T, false>(p, a.cache.dtype, s);
+    };
     switch (a.in_dtype) {
-        case PA_BF16: return run_rope<__nv_bfloat16>(p, f8, s);
-        case PA_F16: return run_rope<__half>(p, f8, s);
-        case PA_F32: return run_rope<float>(p, f8, s);
+        case PA_BF16: return run(__nv_bfloat16{});
+        case PA_F16: return run(__half{});
+        case PA_F32: return run(0.f);
         default: return cudaErrorInvalidValue;
     }
 }

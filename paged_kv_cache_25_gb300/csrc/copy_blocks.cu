@@ -41,8 +41,7 @@ cudaError_t launch_copy_blocks(const void* src_k, const void* src_v, int src_blo
                                void* dst_v, int dst_blocks, const pa_cache_desc& layout,
                                const int32_t* mapping, int pairs, unsigned* err, cudaStream_t s)
 {
-    const int64_t bytes = static_cast<int64_t>(layout.n_kv_heads) * layout.block_size *
-                          layout.head_dim * elem_bytes(layout.dtype);
+    const int64_t bytes = static_cast<int64_t>(layout.n_kv_heads) * layout.block_size * row_bytes(layout);
     const int64_t vecs = bytes / 16;
     const int threads = 256;
     const int64_t slices = (vecs + threads * 4 - 1) / (threads * 4);   // ~64 KB per thread block

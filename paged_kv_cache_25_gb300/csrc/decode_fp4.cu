@@ -1,0 +1,773 @@
+// Decode attention over FP4 pools, one query row a sequence or several (pa_decode,
+// pa_decode_verify).
+//
+// Mathematics: out = softmax(scale q K^T) V over each sequence's keys, in one pass with a
+// running maximum m and sum l per row; the partials (m, l, O) of key ranges merge exactly,
+//   out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
+//
+// Work: the rows of all (sequence, KV head, up to RU of its (head, query) rows), one after another,
+// are a line of 128-token granules, of which every block of a persistent grid takes an equal
+// run.  A block's run holds whole rows, which it finishes, and at most two pieces of rows that it shares with
+// its neighbours, whose partials meet in f4_merge_kernel.  (Partitions of 1024 tokens dealt by tickets, as
+// the other decode kernels have them, cost a unit's set-up and combine two to three times as often, a third of
+// all instructions of a Llama-3-8B batch: see the figures below.)  A piece's four warps take its 32-token
+// stages in turn and combine through shared memory.
+//
+// A warp streams its stages through a ring of its own by bulk copies of 16-token pieces (contiguous in
+// the pool; four lanes issue the four copies of a stage) and works on them transposed, on
+// m16n8k16 fp16 MMAs: S^T = K q^T with tokens as the MMA rows, O^T = V^T P^T with elements of d
+// as the rows, the unit's rows as the columns (NT tiles of 8).
+//   - Row r of a score tile is token 4 ((r & 7) >> 1) + 2 (r >> 3) + (r & 1) of its piece; the transpose
+//     of P (movmatrix) then leaves lane (g, t4) = (lane / 4, lane % 4) with tokens 4 t4 .. 4 t4 + 3, whose V
+//     codes it reads in 8-byte (d 64: 4-byte) pieces without bank conflicts (rows lie 72 bytes apart).
+//   - Neither K nor V is stored transposed.  K's codes lie along d, as its fragments pair them.
+//     V's fragments pair tokens: the codes of two tokens are put together half byte by half
+//     byte before they are widened (two shifts and two three-input logic operations for 16 codes).
+//   - The k order of S is free: lane t4 holds elements 64 h + 16 t4 + (0 .. 15) of its tokens, one scale
+//     each, and q is loaded to match.  Lane g holds elements (d / 8) g and on of V: one scale a token.
+//   - Codes times scales are exact in fp16 (fp4.cuh).  bf16 queries are scaled by a power of two into
+//     fp16 (exact down to 2^-29 of the row's largest element).
+//   - P enters P V as one fp16 part: 11 bits, so an output moves by at most 2^-12 of the largest |v| that it
+//     averages, far below what 4 bits do to v.  (A second part: one more MMA a tile and 14 of the
+//     ~250 instructions of a piece.)
+//
+// Bound: HBM at 4.5 bits a value; beside it the instructions that widen: a conversion and a
+// multiply for two values, 128 of the ~240 warp instructions of a 16-token piece (d 128), of which an SM issues
+// about 400 in the time that HBM takes to bring it the piece.
+#include "fp4.cuh"
+#include "pa_device.cuh"
+#include "pa_internal.h"
+
+#include <math.h>
+
+#include <algorithm>
+#include <mutex>
+#include <type_traits>
+
+namespace pa {
+
+constexpr int kF4Warps = 4;
+constexpr int kF4Threads = kF4Warps * 32;
+constexpr int kPieceTok = 16;             // tokens of a tile of scores, and of one copy
+constexpr int kStageTok = 32;             // tokens of a stage: two tiles
+constexpr int kGranule = kF4Warps * kStageTok;   // tokens of a granule
+constexpr int kF4PrefixCap = 768;         // entries of the table of granules before a sequence
+static_assert(kGranule == kF4GranuleTokens, "as the workspace counts them");
+
+struct F4Params {
+    const uint8_t *k, *v;
+    void* out;
+    const void* q;
+    const int32_t *block_tables, *context_lens;
+    int4* info;                           // [blocks]: a row begun and not finished here, or -1; whether the head piece goes on.  May be null
+    float *ws_ml, *ws_acc;                // [blocks + tails][RU] (m, l) and O
+    int row_tails;                        // whether a tail's slot goes by its row (else by its block)
+    unsigned* err;
+    pa_dtype out_dtype;
+    int max_blocks, num_seqs, n_q, nq, n_kv, group, num_blocks, bs_log;
+    float scale_log2, v_scale;            // softmax scale times k_scale, in the log2 domain
+};
+
+// Resident blocks an SM and ring stages a warp.
+template <int D, int RU>
+struct F4Cfg {
+    static constexpr int kRow = fp4_row_bytes(D);
+    static constexpr int kTile = kPieceTok * kRow;                          // bytes of a 16-token tile of K or V
+    static constexpr int kStage = 2 * (kStageTok / kPieceTok) * kTile;      // K tiles, then V tiles
+    static constexpr int kCtas = RU == 16 ? 2 : (D == 64 ? 4 : 3);
+    static constexpr int kNS = D == 64 ? 4 : 3;
+    static constexpr int kRing = kNS * kStage;                              // of a warp
+    static constexpr int kReduce = kF4Warps * RU * (D + 2) * 4;
+    static constexpr int kReds = RU == 4 ? 2 : 1;      // combine buffers: two save a barrier a piece
+    static constexpr int kDynBytes = kF4Warps * kRing + kReds * kReduce;
+    static_assert(kCtas * (kDynBytes + 1024 + 4096) <= 233472, "shared memory of an SM");
+    static_assert(kCtas <= kF4MaxCtas, "as the workspace counts them");
+};
+
+__device__ __forceinline__ void f4_store(void* out, int64_t i, float v, pa_dtype dt)
+{
+    if (dt == PA_F32) static_cast<float*>(out)[i] = v;
+    else if (dt == PA_BF16) static_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(v);
+    else static_cast<__half*>(out)[i] = __float2half_rn(v);
+}
+
+__device__ __forceinline__ void f4_store4(void* out, int64_t i, float4 v, pa_dtype dt)
+{
+    if (dt == PA_F32)
+        *reinterpret_cast<float4*>(static_cast<float*>(out) + i) = v;
+    else if (dt == PA_BF16)
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + i) =
+            make_uint2(Cvt<__nv_bfloat16>::pack(v.x, v.y), Cvt<__nv_bfloat16>::pack(v.z, v.w));
+    else
+        *reinterpret_cast<uint2*>(static_cast<__half*>(out) + i) =
+            make_uint2(Cvt<__half>::pack(v.x, v.y), Cvt<__half>::pack(v.z, v.w));
+}
+
+// S^T of one tile: st[n][0, 1] row g, [2, 3] row g + 8; columns 8 n + 2 t4 and the next.
+template <int D, int NT>
+__device__ __forceinline__ void f4_scores(const uint8_t* k, int g, int t4, const uint32_t (&q)[NT][D / 16][2],
+                                          float (&st)[NT][4])
+{
+    constexpr int kRow = fp4_row_bytes(D), kHalves = D / 64;
+    uint2 w[2][kHalves];
+    uint32_t s[2][kHalves];
+    const uint8_t* row = k + (4 * (g >> 1) + (g & 1)) * kRow;
+#pragma unroll
+    for (int i = 0; i < 2; ++i, row += 2 * kRow) {
+        if constexpr (D == 128) {
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h) w[i][h] = *reinterpret_cast<const uint2*>(row + 32 * h + 8 * t4);
+            const uint2 sc = *reinterpret_cast<const uint2*>(row + D / 2);
+            const uint32_t both = e4m3x2_to_h2(__byte_perm(sc.x, sc.y, t4 | ((4 + t4) << 4)));
+            s[i][0] = __byte_perm(both, 0, 0x1010);
+            s[i][kHalves - 1] = __byte_perm(both, 0, 0x3232);
+        } else {      // (rows of 36 bytes)
+            w[i][0].x = *reinterpret_cast<const uint32_t*>(row + 8 * t4);
+            w[i][0].y = *reinterpret_cast<const uint32_t*>(row + 8 * t4 + 4);
+            s[i][0] = e4m3x2_to_h2(__byte_perm(*reinterpret_cast<const uint32_t*>(row + D / 2), 0, t4 * 0x11));
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) st[n][e] = 0.f;
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {          // 8 codes: two steps of 4
+            uint32_t u[4], x[4];
+            fp4x8_to_h2x4(y ? w[0][h].y : w[0][h].x, u[0], u[1], u[2], u[3]);
+            fp4x8_to_h2x4(y ? w[1][h].y : w[1][h].x, x[0], x[1], x[2], x[3]);
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+                const int kk = 4 * h + 2 * y + z;
+                const uint32_t a[4] = {hmul2(u[2 * z], s[0][h]), hmul2(x[2 * z], s[1][h]),
+                                       hmul2(u[2 * z + 1], s[0][h]), hmul2(x[2 * z + 1], s[1][h])};
+#pragma unroll
+                for (int n = 0; n < NT; ++n) MmaOp<__half>::run(st[n], a, q[n][kk][0], q[n][kk][1]);
+            }
+        }
+}
+
+// O^T += V^T P^T of one tile.  Byte b of a lane's codes is m-tile b, its low half row g, its high half row
+// g + 8.  valid: tokens of the tile that exist; the scales of the others may be anything, even NaN, and count as 0.
+template <int D, int NT>
+__device__ __forceinline__ void f4_values(const uint8_t* v, int g, int t4, int valid, const uint32_t (&pt)[NT][2],
+                                          float (&o)[NT][D / 16][4])
+{
+    constexpr int kRow = fp4_row_bytes(D), kWords = D / 64;       // words of 8 codes a token
+    const uint8_t* row = v + 4 * t4 * kRow;
+    uint32_t x[4][kWords], sc[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if constexpr (D == 128) {
+            const uint2 u = *reinterpret_cast<const uint2*>(row + j * kRow + 8 * g);
+            x[j][0] = u.x;
+            x[j][kWords - 1] = u.y;
+        } else {
+            x[j][0] = *reinterpret_cast<const uint32_t*>(row + j * kRow + 4 * g);
+        }
+        sc[j] = row[j * kRow + D / 2 + (D == 128 ? g : g >> 1)];
+    }
+    if (valid < kPieceTok) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sc[j] = 4 * t4 + j < valid ? sc[j] : 0u;
+    }
+    const uint32_t s01 = e4m3x2_to_h2(sc[0] | sc[1] << 8), s23 = e4m3x2_to_h2(sc[2] | sc[3] << 8);
+    constexpr uint32_t kM = 0x0F0F0F0Fu;
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) {
+        uint32_t a0[4], a1[4], a2[4], a3[4];
+        fp4x8_to_h2x4((x[0][w] & kM) | ((x[1][w] << 4) & ~kM), a0[0], a0[1], a0[2], a0[3]);
+        fp4x8_to_h2x4(((x[0][w] >> 4) & kM) | (x[1][w] & ~kM), a1[0], a1[1], a1[2], a1[3]);
+        fp4x8_to_h2x4((x[2][w] & kM) | ((x[3][w] << 4) & ~kM), a2[0], a2[1], a2[2], a2[3]);
+        fp4x8_to_h2x4(((x[2][w] >> 4) & kM) | (x[3][w] & ~kM), a3[0], a3[1], a3[2], a3[3]);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const uint32_t a[4] = {hmul2(a0[b], s01), hmul2(a1[b], s01), hmul2(a2[b], s23), hmul2(a3[b], s23)};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) MmaOp<__half>::run(o[n][4 * w + b], a, pt[n][0], pt[n][1]);
+        }
+    }
+}
+
+template <typename QT, int D, int RU, bool MQ>
+__global__ void __launch_bounds__(kF4Threads, F4Cfg<D, RU>::kCtas) f4_decode_kernel(const __grid_constant__ F4Params p)
+{
+    using Cfg = F4Cfg<D, RU>;
+    constexpr int NT = RU == 16 ? 2 : 1, NS = Cfg::kNS, kTiles = kStageTok / kPieceTok;
+    constexpr bool kBf16 = std::is_same<QT, __nv_bfloat16>::value;
+
+    __shared__ int s_table[kF4PrefixCap];        // granules up to a sequence, then the sequences' lengths
+    __shared__ int s_scan[kF4Warps];
+    __shared__ __align__(8) uint64_t s_bar[kF4Warps * NS];
+    extern __shared__ __align__(16) uint8_t smem[];
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+    const int nq = MQ ? p.nq : 1;
+    const int rows_kv = p.group * nq;                        // rows of a KV head, head-major
+    const int n_groups = p.n_kv * ((rows_kv + RU - 1) / RU);
+    const int max_ctx = p.max_blocks << p.bs_log;
+    if (tid < kF4Warps * NS) mbar_init(smem_u32(&s_bar[tid]), 1);
+    fence_mbar_init();
+    grid_dependency_wait();      // launched as a programmatic dependent: every input may come from the kernel before
+
+    // ---- this block's run of granules.  s_table[c]: granules (of one group) of the first c + 1 chunks of
+    // `per` sequences (one a chunk, unless the batch is larger than the table).
+    auto granules = [&](int L) { return L < nq || L <= 0 ? 0 : (min(L, max_ctx) + kGranule - 1) / kGranule; };
+    const int per = (p.num_seqs + kF4PrefixCap - 1) / kF4PrefixCap;
+    const int chunks = (p.num_seqs + per - 1) / per;
+    {
+        const int mine = (chunks + kF4Threads - 1) / kF4Threads;
+        const int c0 = tid * mine, c1 = min(chunks, c0 + mine);
+        int local = 0;
+        for (int c = c0; c < c1; ++c) {
+            for (int s = c * per; s < min(p.num_seqs, (c + 1) * per); ++s) {
+                const int L = __ldg(p.context_lens + s);
+                if (L > 0 && L < nq) set_error(p.err, PA_ERR_OUT_OF_RANGE);   // fewer keys than query rows
+                local += granules(L);
+            }
+            s_table[c] = local;
+        }
+        int run = local;
+#pragma unroll
+        for (int w = 1; w < 32; w <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, run, w);
+            if (lane >= w) run += up;
+        }
+        if (lane == 31) s_scan[warp] = run;
+        __syncthreads();
+        run -= local;
+        for (int i = 0; i < warp; ++i) run += s_scan[i];
+        for (int c = c0; c < c1; ++c) s_table[c] += run;
+        __syncthreads();
+    }
+    int left;                                    // granules of the run that are not in a piece yet
+    int at_s, at_gran, at_grp;                   // where the next piece begins
+    {
+        const int total = s_table[chunks - 1] * n_groups, blocks = gridDim.x;
+        const int base = total / blocks, more = total - base * blocks, b = blockIdx.x;
+        const int begin = b * base + min(b, more);
+        left = base + (b < more ? 1 : 0);
+        if (left == 0) {                         // uniform over the block
+            if (tid == 0 && p.info) p.info[blockIdx.x] = make_int4(-1, 0, 0, 0);
+            return;
+        }
+        const int x = begin / n_groups;
+        int lo = 0, hi = chunks - 1;             // the first chunk that ends past x
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (s_table[mid] > x) hi = mid; else lo = mid + 1;
+        }
+        int before = lo ? s_table[lo - 1] : 0;
+        at_s = lo * per;
+        int J = granules(__ldg(p.context_lens + at_s));
+        while (before + J <= x) {                // (larger batches: on through the chunk)
+            before += J;
+            J = granules(__ldg(p.context_lens + ++at_s));
+        }
+        const int off = begin - before * n_groups;
+        at_grp = off / J;
+        at_gran = off - at_grp * J;
+        __syncthreads();
+        if (per == 1)
+            for (int s = tid; s < p.num_seqs; s += kF4Threads) s_table[s] = __ldg(p.context_lens + s);
+        __syncthreads();
+    }
+    auto len_of = [&](int s) { return per == 1 ? s_table[s] : __ldg(p.context_lens + s); };
+
+    // A piece: tokens [t0, t1) of the rows r0 .. r0 + nh - 1 of a KV head of sequence s.
+    struct Piece {
+        int s, L, grp, kvh, r0, nh, t0, t1;
+        bool live, tail;                         // tail: the rows' keys go on past t1
+    };
+    auto next_piece = [&]() {
+        Piece x{};
+        x.live = left > 0;
+        if (!x.live) return x;
+        x.L = len_of(at_s);
+        int J = granules(x.L);
+        if (at_grp == n_groups) {                // on to the next sequence with keys
+            at_grp = 0;
+            do {
+                x.L = len_of(++at_s);
+                J = granules(x.L);
+            } while (J == 0);
+        }
+        x.s = at_s;
+        x.grp = at_grp;
+        const int n_sub = n_groups / p.n_kv;
+        x.kvh = n_sub == 1 ? at_grp : at_grp / n_sub;
+        x.r0 = (at_grp - x.kvh * n_sub) * RU;
+        x.nh = min(RU, rows_kv - x.r0);
+        x.t0 = at_gran * kGranule;
+        const int n = min(left, J - at_gran), end = min(x.L, max_ctx);
+        x.t1 = min(end, (at_gran + n) * kGranule);
+        x.tail = x.t1 < end;
+        left -= n;
+        at_gran = 0;
+        ++at_grp;
+        return x;
+    };
+    uint8_t* const ring = smem + warp * Cfg::kRing;
+    const uint32_t ring32 = smem_u32(ring), bar0 = smem_u32(&s_bar[warp * NS]);
+
+    // query fragments: columns 8 n + g; steps 4 h .. 4 h + 3 are elements 64 h + 16 t4 + (0 .. 15).  A negative
+    // softmax scale is applied as -q, so the largest raw score is the largest score.
+    const uint32_t qsign = p.scale_log2 < 0.f ? 0x80008000u : 0u;
+    uint32_t q[NT][D / 16][2];
+    float c_q[NT];            // softmax scale of column 8 n + g (log2 domain)
+    auto load_q = [&](const Piece& x) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int r = 8 * n + g;
+            if (r >= x.nh) {
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) q[n][kk][0] = q[n][kk][1] = 0u;
+                continue;
+            }
+            const int hh = (x.r0 + r) / nq, qi = x.r0 + r - hh * nq;
+            const QT* row = static_cast<const QT*>(p.q) +
+                            ((static_cast<int64_t>(x.s) * nq + qi) * p.n_q + x.kvh * p.group + hh) * D + 16 * t4;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; kk += 2) {
+                const uint4 u = __ldg(reinterpret_cast<const uint4*>(row + 64 * (kk / 4) + 4 * (kk % 4)));
+                q[n][kk][0] = u.x;
+                q[n][kk][1] = u.y;
+                q[n][kk + 1][0] = u.z;
+                q[n][kk + 1][1] = u.w;
+            }
+        }
+    };
+    // Once the piece starts (so that the loads' latency overlaps the combine): signs, and bf16 -> fp16.  A quad holds
+    // a row; the row is scaled by 2^-e so that its largest magnitude lands in [2^14, 2^15), and
+    // 2^e goes into its softmax scale.
+    auto scale_q = [&]() {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            c_q[n] = fabsf(p.scale_log2);
+            if constexpr (kBf16) {
+                uint32_t top = 0;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        top = max(top, max(q[n][kk][h] & 0x7FFFu, (q[n][kk][h] >> 16) & 0x7FFFu));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const int e = top == 0u ? 0 : max(static_cast<int>((top >> 7) & 0xFFu) - 141, -100);
+                c_q[n] *= __int_as_float((127 + e) << 23);
+                const float down = __int_as_float((127 - e) << 23);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float2 f = Cvt<__nv_bfloat16>::unpack(q[n][kk][h]);
+                        q[n][kk][h] = Cvt<__half>::pack(f.x * down, f.y * down);
+                    }
+            }
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                q[n][kk][0] ^= qsign;
+                q[n][kk][1] ^= qsign;
+            }
+        }
+    };
+
+    Piece cu = next_piece();
+    const bool head = cu.t0 > 0;                 // the run begins inside a row
+    bool first = true;
+    load_q(cu);
+    Piece nx = next_piece();
+
+    // ---- the warp's stages, copied ahead: it_* is the next one to copy, of this piece or the next; lanes 0 .. 3
+    // copy K's two tiles and V's two, and hold the block id of theirs (loaded a stage ahead)
+    int it_s, it_kvh, it_tok, it_end, it_id = 0, slot = 0, ahead = 0;
+    uint32_t phase = 0;                          // of ring slot `slot`, the next one to be consumed
+    bool it_next = false;
+    const int it_tile = (lane & 1) * kPieceTok;
+    auto it_begin = [&](const Piece& x) {
+        it_s = x.s;
+        it_kvh = x.kvh;
+        it_tok = x.t0 + warp * kStageTok;
+        it_end = x.t1;
+    };
+    auto it_settle = [&]() {                     // on to the next piece; the block id
+        if (it_tok >= it_end && !it_next && nx.live) {
+            it_begin(nx);
+            it_next = true;
+        }
+        if (lane < 2 * kTiles && it_tok + it_tile < it_end)
+            it_id = __ldg(p.block_tables + static_cast<int64_t>(it_s) * p.max_blocks + ((it_tok + it_tile) >> p.bs_log));
+    };
+    auto copy_ahead = [&]() {                    // whole warp: as many stages as the ring has room for
+        while (ahead < NS && it_tok < it_end) {
+            const int to = slot + ahead >= NS ? slot + ahead - NS : slot + ahead;
+            const uint32_t bar = bar0 + to * 8;
+            // (a tile past the end is left out: its tokens are masked)
+            if (lane == 0) mbar_arrive_expect_tx(bar, (it_tok + kPieceTok < it_end ? 4 : 2) * Cfg::kTile);
+            __syncwarp();
+            if (lane < 2 * kTiles && it_tok + it_tile < it_end) {
+                int id = it_id;
+                if (id < 0 || id >= p.num_blocks) {
+                    set_error(p.err, PA_ERR_OUT_OF_RANGE);
+                    id = 0;                      // keep the ring moving; the outputs are flagged
+                }
+                const int tok = it_tok + it_tile;
+                const int64_t row = ((static_cast<int64_t>(id) * p.n_kv + it_kvh) << p.bs_log) + (tok & ((1 << p.bs_log) - 1));
+                bulk_load(ring32 + to * Cfg::kStage + lane * Cfg::kTile, (lane >> 1 ? p.v : p.k) + row * Cfg::kRow,
+                          Cfg::kTile, bar);
+            }
+            ++ahead;
+            it_tok += kGranule;
+            it_settle();
+        }
+    };
+    static_assert(kTiles == 2, "lane & 1 is the tile, lane / 2 is K or V");
+    it_begin(cu);
+    it_settle();
+    copy_ahead();
+
+    float o[NT][D / 16][4];
+    int buf = 0, timed_out = 0;
+    while (cu.live) {
+        scale_q();
+        // this lane's columns 8 n + 2 t4 + e: softmax scales, running maxima (raw scores), sums, key limits
+        float c[NT][2], m[NT][2], l[NT][2];
+        int lim[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                c[n][e] = __shfl_sync(0xffffffffu, c_q[n], 8 * t4 + 4 * e);
+                const int col = 8 * n + 2 * t4 + e;
+                lim[n][e] = MQ && col < cu.nh ? cu.L - nq + (cu.r0 + col) % nq + 1 : cu.L;
+                m[n][e] = -INFINITY;
+                l[n][e] = 0.f;
+#pragma unroll
+                for (int mt = 0; mt < D / 16; ++mt) o[n][mt][e] = o[n][mt][2 + e] = 0.f;
+            }
+        const int open = cu.L - nq + 1;              // keys below it are visible to every row
+        const int tA = 4 * (g >> 1) + (g & 1);       // this lane's tokens of a tile: tA and tA + 2
+#pragma unroll 1
+        for (int pos0 = cu.t0 + warp * kStageTok; pos0 < cu.t1; pos0 += kGranule) {
+            const bool ok = mbar_wait(bar0 + slot * 8, phase, p.err);
+            if (!__all_sync(0xffffffffu, ok)) {      // leave together: shuffles follow
+                timed_out = 1;
+                break;
+            }
+            const uint8_t* st_k = ring + slot * Cfg::kStage;
+            const uint8_t* st_v = st_k + kTiles * Cfg::kTile;
+            float z[kTiles][NT][4];
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i) f4_scores<D, NT>(st_k + i * Cfg::kTile, g, t4, q, z[i]);
+            const bool masked = pos0 + kStageTok > min(open, cu.t1);
+            if (masked) {
+#pragma unroll
+                for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (pos0 + i * kPieceTok + tA + (e & 2) >= min(lim[n][e & 1], cu.t1)) z[i][n][e] = -INFINITY;
+            }
+            // the columns' largest raw scores, met over the eight lanes of each t4.  The reference m moves only
+            // when the first key sets it or the largest has grown by more than 2^8 (lazily: P stays below 2^8).
+            float mx[NT][2];
+            bool moved = false;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float x = fmaxf(z[0][n][e], z[0][n][2 + e]);
+#pragma unroll
+                    for (int i = 1; i < kTiles; ++i) x = max3f(x, z[i][n][e], z[i][n][2 + e]);
+#pragma unroll
+                    for (int w = 4; w < 32; w <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, w));
+                    mx[n][e] = x;
+                    // (written so that no infinity meets a scale of 0)
+                    moved = moved || (x > m[n][e] && (m[n][e] == -INFINITY || (x - m[n][e]) * c[n][e] > 8.f));
+                }
+            if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float mn = fmaxf(m[n][e], mx[n][e]);
+                        const float f = m[n][e] == -INFINITY ? 0.f : fast_exp2((m[n][e] - mn) * c[n][e]);
+                        m[n][e] = mn;
+                        l[n][e] *= f;
+#pragma unroll
+                        for (int mt = 0; mt < D / 16; ++mt) {
+                            o[n][mt][e] *= f;
+                            o[n][mt][2 + e] *= f;
+                        }
+                    }
+            }
+            uint32_t pt[kTiles][NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const float r0 = m[n][0] == -INFINITY ? 0.f : -m[n][0] * c[n][0];
+                const float r1 = m[n][1] == -INFINITY ? 0.f : -m[n][1] * c[n][1];
+#pragma unroll
+                for (int i = 0; i < kTiles; ++i) {
+                    float x[4] = {fast_exp2(fmaf(z[i][n][0], c[n][0], r0)), fast_exp2(fmaf(z[i][n][1], c[n][1], r1)),
+                                  fast_exp2(fmaf(z[i][n][2], c[n][0], r0)), fast_exp2(fmaf(z[i][n][3], c[n][1], r1))};
+                    if (masked) {      // (even with scale 0, where the exponent is NaN)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) x[e] = z[i][n][e] == -INFINITY ? 0.f : x[e];
+                    }
+                    l[n][0] += x[0] + x[2];
+                    l[n][1] += x[1] + x[3];
+                    pt[i][n][0] = movmatrix_trans(Cvt<__half>::pack(x[0], x[1]));
+                    pt[i][n][1] = movmatrix_trans(Cvt<__half>::pack(x[2], x[3]));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i)
+                f4_values<D, NT>(st_v + i * Cfg::kTile, g, t4, cu.t1 - pos0 - i * kPieceTok, pt[i], o);
+            __syncwarp();
+            --ahead;
+            slot = slot + 1 == NS ? 0 : slot + 1;
+            phase ^= slot == 0 ? 1u : 0u;
+            if (it_tok < it_end) {
+                fence_proxy_async_smem();
+                copy_ahead();
+            }
+        }
+        // ---- this warp's partials: O of lane g's D / 8 elements and its columns, then (m, l)
+        float* const red_o = reinterpret_cast<float*>(smem + kF4Warps * Cfg::kRing + buf * Cfg::kReduce);   // [warps][RU][D]
+        float* const red_m = red_o + kF4Warps * RU * D;                                 // [warps][RU], log2 domain
+        float* const red_l = red_m + kF4Warps * RU;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int w = 4; w < 32; w <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], w);
+                const int col = 8 * n + 2 * t4 + e;
+                if (col < RU) {
+                    float4* dst = reinterpret_cast<float4*>(red_o + (warp * RU + col) * D + D / 8 * g);
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i)
+                        dst[i] = make_float4(o[n][2 * i][e], o[n][2 * i][2 + e], o[n][2 * i + 1][e], o[n][2 * i + 1][2 + e]);
+                    if (g == 0) {
+                        red_m[warp * RU + col] = m[n][e] == -INFINITY ? -INFINITY : m[n][e] * c[n][e];
+                        red_l[warp * RU + col] = l[n][e];
+                    }
+                }
+            }
+        if (nx.live) load_q(nx);                     // its latency overlaps the combine
+        else if (!timed_out) allow_dependent_launch();   // this block's last piece
+        if (__syncthreads_or(timed_out)) {           // (else every warp's partials are written)
+            // the copies still in flight land first, as far as a limit allows
+            for (int i = 0; i < ahead; ++i)
+                mbar_wait(bar0 + (slot + i >= NS ? slot + i - NS : slot + i) * 8, phase ^ (slot + i >= NS ? 1u : 0u), p.err);
+            timed_out = 1;
+            break;
+        }
+        // pieces that are not whole rows go to the workspace: slot b (the run's head), or one behind those (its tail)
+        const bool shared_head = first && head, to_ws = shared_head || cu.tail;
+        for (int idx = tid; idx < cu.nh * (D / 4); idx += kF4Threads) {
+            const int r = idx / (D / 4), dd = idx % (D / 4) * 4;
+            float M = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kF4Warps; ++w) M = fmaxf(M, red_m[w * RU + r]);
+            // M = -inf: no key of this piece is visible to the row (keys of later rows only)
+            const float M_use = MQ && M == -INFINITY ? 0.f : M;
+            float lsum = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kF4Warps; ++w) {
+                const float f = exp2f(red_m[w * RU + r] - M_use);
+                lsum += f * red_l[w * RU + r];
+                const float4 x = *reinterpret_cast<const float4*>(red_o + (w * RU + r) * D + dd);
+                acc.x = fmaf(f, x.x, acc.x);
+                acc.y = fmaf(f, x.y, acc.y);
+                acc.z = fmaf(f, x.z, acc.z);
+                acc.w = fmaf(f, x.w, acc.w);
+            }
+            if (!to_ws) {
+                const int hh = MQ ? (cu.r0 + r) / nq : cu.r0 + r, qi = MQ ? cu.r0 + r - hh * nq : 0;
+                const int64_t at = (static_cast<int64_t>(cu.s) * nq + qi) * p.n_q + cu.kvh * p.group + hh;
+                const float inv = p.v_scale / lsum;
+                f4_store4(p.out, at * D + dd, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv), p.out_dtype);
+            } else {
+                const int64_t w = (shared_head ? static_cast<int64_t>(blockIdx.x)
+                                               : static_cast<int64_t>(gridDim.x) +
+                                                     (p.row_tails ? cu.s * n_groups + cu.grp : blockIdx.x)) * RU + r;
+                *reinterpret_cast<float4*>(p.ws_acc + w * D + dd) = acc;
+                if (dd == 0) *reinterpret_cast<float2*>(p.ws_ml + 2 * w) = make_float2(M, lsum);
+            }
+        }
+        if (!nx.live && tid == 0 && p.info)
+            p.info[blockIdx.x] = make_int4(cu.tail && !shared_head ? cu.s * n_groups + cu.grp : -1,
+                                           shared_head && cu.tail ? 1 : 0, 0, 0);
+        // (two buffers: the next piece's partials go to the other; the one after meets a barrier first)
+        if constexpr (Cfg::kReds == 1) __syncthreads();
+        else buf ^= 1;
+        first = false;
+        cu = nx;
+        if (cu.live) {
+            nx = next_piece();
+            it_next = false;
+            if (it_tok >= it_end) {
+                it_settle();
+                copy_ahead();
+            }
+        }
+    }
+    if (timed_out && tid == 0 && p.info) p.info[blockIdx.x] = make_int4(-1, 0, 0, 0);
+}
+
+// Merges the pieces of rows that several blocks shared: block (b, r) row r of the rows that decode block b began
+// and did not finish, whose pieces are b's tail and the heads of the blocks after it, up to the first
+// that does not go on.  Four warps take the pieces in turn.
+template <int D, int RU>
+__global__ void __launch_bounds__(128) f4_merge_kernel(const __grid_constant__ F4Params p, int blocks)
+{
+    constexpr int V = D / 32;                 // neighbouring elements of a lane
+    using Vec = std::conditional_t<V == 4, float4, float2>;
+    __shared__ float s_acc[4][D], s_m[4], s_l[4];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = blockIdx.x, r = blockIdx.y;
+    grid_dependency_wait();
+    const int row = p.info[b].x;
+    if (row < 0) return;
+    const int rows_kv = p.group * p.nq, n_sub = (rows_kv + RU - 1) / RU, n_groups = p.n_kv * n_sub;
+    const int s = row / n_groups, grp = row - s * n_groups, kvh = grp / n_sub, r0 = (grp - kvh * n_sub) * RU;
+    if (r0 + r >= rows_kv) return;
+    int n = 1;                                // pieces after b's
+    for (int i0 = b + 1;; i0 += 32) {
+        const unsigned ends = __ballot_sync(0xffffffffu, i0 + lane >= blocks || p.info[i0 + lane].y == 0);
+        if (ends) {
+            n = i0 - b + __ffs(ends) - 1;
+            break;
+        }
+    }
+    n = min(n, blocks - 1 - b);
+    auto slot = [&](int i) {                  // of piece i
+        return (i == 0 ? static_cast<int64_t>(blocks) + (p.row_tails ? row : b) : static_cast<int64_t>(b) + i) * RU + r;
+    };
+    float M = -INFINITY, lsum = 0.f, acc[V] = {};
+    for (int i = warp; i <= n; i += 4) M = fmaxf(M, p.ws_ml[2 * slot(i)]);
+    // (rows of several queries may see no key of a piece, or of all that this warp has)
+    const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll 4
+    for (int i = warp; i <= n; i += 4) {
+        const int64_t w = slot(i);
+        const float2 ml = *reinterpret_cast<const float2*>(p.ws_ml + 2 * w);
+        const Vec x = *reinterpret_cast<const Vec*>(p.ws_acc + w * D + V * lane);
+        const float f = exp2f(ml.x - ref);
+        lsum = fmaf(f, ml.y, lsum);
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] = fmaf(f, reinterpret_cast<const float*>(&x)[e], acc[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) s_acc[warp][V * lane + e] = acc[e];
+    if (lane == 0) {
+        s_m[warp] = M;
+        s_l[warp] = lsum;
+    }
+    __syncthreads();
+    if (threadIdx.x >= D) return;
+    M = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+    float sum = 0.f, x = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const float f = exp2f(s_m[w] - M);
+        sum = fmaf(f, s_l[w], sum);
+        x = fmaf(f, s_acc[w][threadIdx.x], x);
+    }
+    const int hh = (r0 + r) / p.nq, qi = r0 + r - hh * p.nq;
+    const int64_t at = (static_cast<int64_t>(s) * p.nq + qi) * p.n_q + kvh * p.group + hh;
+    f4_store(p.out, at * D + threadIdx.x, x * (p.v_scale / sum), p.out_dtype);
+}
+
+static cudaError_t f4_resident(int* sms)
+{
+    static std::mutex mu;
+    static int cache[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || dev < 0 || dev >= 64) return e != cudaSuccess ? e : cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(mu);
+    if (!cache[dev]) e = cudaDeviceGetAttribute(&cache[dev], cudaDevAttrMultiProcessorCount, dev);
+    *sms = cache[dev];
+    return e;
+}
+
+template <typename QT, int D, int RU, bool MQ>
+static cudaError_t run_f4(F4Params p, void* workspace, cudaStream_t s)
+{
+    using Cfg = F4Cfg<D, RU>;
+    auto kern = f4_decode_kernel<QT, D, RU, MQ>;
+    static std::once_flag once;
+    static cudaError_t attr_err = cudaSuccess;
+    std::call_once(once, [&] {
+        attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kDynBytes);
+    });
+    if (attr_err != cudaSuccess) return attr_err;
+    int sms = 0;
+    cudaError_t e = f4_resident(&sms);
+    if (e != cudaSuccess) return e;
+    // (no more blocks than granules that the tables can hold; the workspace counts the same)
+    const int64_t most = f4_granules(p.num_seqs, p.nq, p.group, p.n_kv, p.max_blocks << p.bs_log);
+    const int blocks = static_cast<int>(std::min<int64_t>(most, std::min(sms, kF4Sms) * Cfg::kCtas));
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const bool split = (p.max_blocks << p.bs_log) > kGranule;    // (rows of one granule are never shared)
+    if (split) {
+        p.info = reinterpret_cast<int4*>(ws);
+        p.ws_ml = reinterpret_cast<float*>(ws + 16ll * blocks);
+        const int64_t rows = static_cast<int64_t>(p.num_seqs) * p.n_kv * ((p.group * p.nq + RU - 1) / RU);
+        p.row_tails = rows <= blocks;
+        p.ws_acc = p.ws_ml + (blocks + std::min<int64_t>(rows, blocks)) * RU * 2;
+    }
+    cudaEvent_t ev0 = nullptr, ev1 = nullptr;
+    profile_events(&ev0, &ev1);
+    if (ev0) cudaEventRecord(ev0, s);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(kF4Threads);
+    cfg.dynamicSmemBytes = Cfg::kDynBytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kern, p);
+    if (ev1) cudaEventRecord(ev1, s);
+    if (e != cudaSuccess || !split) return e;
+    cfg.gridDim = dim3(blocks, std::min(RU, p.group * p.nq));
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, f4_merge_kernel<D, RU>, p, blocks);
+}
+
+template <typename QT, int D>
+static cudaError_t run_f4_rows(const F4Params& p, void* ws, cudaStream_t s)
+{
+    switch (f4_unit_rows(p.nq * p.group)) {
+        case 4: return p.nq == 1 ? run_f4<QT, D, 4, false>(p, ws, s) : run_f4<QT, D, 4, true>(p, ws, s);
+        case 8: return p.nq == 1 ? run_f4<QT, D, 8, false>(p, ws, s) : run_f4<QT, D, 8, true>(p, ws, s);
+        default: return p.nq == 1 ? run_f4<QT, D, 16, false>(p, ws, s) : run_f4<QT, D, 16, true>(p, ws, s);
+    }
+}
+
+cudaError_t launch_decode_fp4(const DecodeArgs& a, void* workspace, cudaStream_t s)
+{
+    F4Params p{};
+    p.k = static_cast<const uint8_t*>(a.k_cache); p.v = static_cast<const uint8_t*>(a.v_cache);
+    p.out = a.out; p.q = a.q; p.block_tables = a.block_tables; p.context_lens = a.context_lens;
+    p.err = a.err; p.out_dtype = a.out_dtype;
+    p.max_blocks = a.max_blocks; p.num_seqs = a.num_seqs; p.n_q = a.n_q; p.nq = a.q_per_seq;
+    p.n_kv = a.cache.n_kv_heads; p.group = a.n_q / a.cache.n_kv_heads; p.num_blocks = a.cache.num_blocks;
+    p.bs_log = a.cache.block_size == 32 ? 5 : 4;
+    p.scale_log2 = a.scale * 1.4426950408889634f * a.cache.k_scale; p.v_scale = a.cache.v_scale;
+    const int D = a.cache.head_dim;
+    if (D != 64 && D != 128) return cudaErrorInvalidValue;
+    if (a.cache.act_dtype == PA_BF16)
+        return D == 64 ? run_f4_rows<__nv_bfloat16, 64>(p, workspace, s) : run_f4_rows<__nv_bfloat16, 128>(p, workspace, s);
+    return D == 64 ? run_f4_rows<__half, 64>(p, workspace, s) : run_f4_rows<__half, 128>(p, workspace, s);
+}
+
+}  // namespace pa

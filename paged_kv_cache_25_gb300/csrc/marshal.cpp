@@ -17,10 +17,13 @@
 namespace {
 
 // The library's calls, as the loaded libpa.so has them (bind()).
-decltype(&pa_rope_and_cache) lib_rope;
+decltype(&pa_rope_axes_and_cache) lib_rope;
 decltype(&pa_decode_shared) lib_decode_shared;
 decltype(&pa_decode_scored) lib_decode_scored;
 decltype(&pa_prefill_scored) lib_prefill_scored;
+decltype(&pa_decode_verify) lib_decode;
+decltype(&pa_prefill_chunk) lib_prefill;
+decltype(&pa_gather_cache) lib_gather;
 
 struct Raised {};   // a Python exception is set
 
@@ -43,6 +46,7 @@ pa_dtype pa_type(at::ScalarType t)
         case at::kHalf: return PA_F16;
         case at::kBFloat16: return PA_BF16;
         case at::kFloat8_e4m3fn: return PA_FP8_E4M3;
+        case at::kByte: return PA_FP4_E2M1;    // (pools of bytes)
         default: raise(PyExc_TypeError, "unsupported dtype");
     }
 }
@@ -67,7 +71,7 @@ double as_double(PyObject* o)
     return x;
 }
 
-// a scale of an FP8 pool; missing ones reach the library as 0 and are refused there
+// a scale of an FP8 or FP4 pool; missing ones reach the library as 0 and are refused there
 float scale_or_zero(PyObject* o) { return o == Py_None ? 0.f : static_cast<float>(as_double(o)); }
 
 // Other Python threads run while the library works, as they do in a foreign call.
@@ -112,7 +116,11 @@ pa_cache_desc descriptor(const at::Tensor& k_cache, at::ScalarType act, PyObject
     c.block_size = to_int(k_cache.size(2));
     c.head_dim = to_int(k_cache.size(3));
     c.dtype = pa_type(k_cache.scalar_type());
-    if (c.dtype == PA_FP8_E4M3) {
+    if (c.dtype == PA_FP4_E2M1) {   // rows of 9 bytes for 16 elements
+        if (c.head_dim % 9) raise(PyExc_ValueError, "FP4 pools [blocks][n_kv][block_size][9 * head_dim / 16] expected");
+        c.head_dim = c.head_dim / 9 * 16;
+    }
+    if (c.dtype == PA_FP8_E4M3 || c.dtype == PA_FP4_E2M1) {
         c.k_scale = scale_or_zero(k_scale);
         c.v_scale = scale_or_zero(v_scale);
         c.act_dtype = pa_type(act);
@@ -121,6 +129,12 @@ pa_cache_desc descriptor(const at::Tensor& k_cache, at::ScalarType act, PyObject
         c.act_dtype = c.dtype;
     }
     return c;
+}
+
+// elements of a pool's rows
+int64_t head_dim(const at::Tensor& pool)
+{
+    return pool.scalar_type() == at::kByte ? pool.size(3) / 9 * 16 : pool.size(3);
 }
 
 template <typename T>
@@ -143,7 +157,7 @@ Attention attention(PyObject* const* a, int64_t seqs, PyObject* k_scale, PyObjec
     Attention x{tensor(a[0]), tensor(a[1]), tensor(a[2]), tensor(a[3]), tensor(a[4]), tensor(a[5]), {}, PA_F32, 0};
     if (!all_contiguous(x.out, x.q, x.kc, x.vc, x.tables, x.lens))
         raise(PyExc_ValueError, "contiguous tensors expected");
-    if (x.q.dim() < 3 || x.out.sizes() != x.q.sizes() || x.kc.dim() != 4 || x.q.size(-1) != x.kc.size(3) ||
+    if (x.q.dim() < 3 || x.out.sizes() != x.q.sizes() || x.kc.dim() != 4 || x.q.size(-1) != head_dim(x.kc) ||
         x.vc.numel() != x.kc.numel())
         raise(PyExc_ValueError, "out and q [..][n_q][d] and pools of that head_dim expected");
     if (x.tables.dim() != 2 || x.tables.size(0) < seqs || x.lens.numel() < seqs)
@@ -151,8 +165,8 @@ Attention attention(PyObject* const* a, int64_t seqs, PyObject* k_scale, PyObjec
     if (x.tables.scalar_type() != at::kInt || x.lens.scalar_type() != at::kInt)
         raise(PyExc_TypeError, "block_tables and context_lens: int32 expected");
     const auto kv = x.kc.scalar_type();
-    if (x.vc.scalar_type() != kv || (x.q.scalar_type() != kv && kv != at::kFloat8_e4m3fn))
-        raise(PyExc_TypeError, "q and the pools must have one dtype (FP8 pools: bf16 or fp16 q)");
+    if (x.vc.scalar_type() != kv || (x.q.scalar_type() != kv && kv != at::kFloat8_e4m3fn && kv != at::kByte))
+        raise(PyExc_TypeError, "q and the pools must have one dtype (FP8 and FP4 pools: bf16 or fp16 q)");
     on_current_device(x.q, x.out, x.kc, x.vc, x.tables, x.lens);
     x.cache = descriptor(x.kc, x.q.scalar_type(), k_scale, v_scale);
     x.out_dtype = pa_type(x.out.scalar_type());
@@ -219,15 +233,25 @@ int64_t token_stride(const at::Tensor& t)
 }
 
 // ---------------------------------------------------------------- the calls
+struct Bytes {   // a contiguous buffer of bytes (bytes, a NumPy array), released at the end
+    Py_buffer b;
+    explicit Bytes(PyObject* o)
+    {
+        if (PyObject_GetBuffer(o, &b, PyBUF_SIMPLE)) throw Raised{};
+    }
+    ~Bytes() { PyBuffer_Release(&b); }
+    Bytes(const Bytes&) = delete;
+};
+
 // (q_out, q, k, v, positions, cos_sin, k_cache, v_cache, slot_mapping, interleaved, stream,
-//  k_scale, v_scale)
+//  k_scale, v_scale, axis_of_pair or None)
 int rope(PyObject* const* a)
 {
     const at::Tensor &q_out = tensor(a[0]), &q = tensor(a[1]), &k = tensor(a[2]), &v = tensor(a[3]),
                      &pos = tensor(a[4]), &cs = tensor(a[5]), &kc = tensor(a[6]), &vc = tensor(a[7]),
                      &slots = tensor(a[8]);
     if (q.dim() != 3 || kc.dim() != 4 || q_out.sizes() != q.sizes() || k.sizes() != v.sizes() || k.dim() != 3 ||
-        k.size(0) != q.size(0) || k.size(1) != kc.size(1) || k.size(2) != q.size(2) || q.size(2) != kc.size(3))
+        k.size(0) != q.size(0) || k.size(1) != kc.size(1) || k.size(2) != q.size(2) || q.size(2) != head_dim(kc))
         raise(PyExc_ValueError, "q_out, q [T][n_q][d] and k, v [T][n_kv][d] expected");
     const auto t = q.scalar_type();
     if (q_out.scalar_type() != t || k.scalar_type() != t || v.scalar_type() != t)
@@ -235,7 +259,13 @@ int rope(PyObject* const* a)
     if (pos.scalar_type() != at::kInt || slots.scalar_type() != at::kLong || cs.scalar_type() != at::kFloat)
         raise(PyExc_TypeError, "positions int32, slot_mapping int64 and cos_sin float32 expected");
     const int64_t T = q.size(0);
-    if (pos.numel() != T || slots.numel() != T || cs.dim() != 2 || !all_contiguous(pos, slots, cs))
+    // several axes: positions [axes][T], rows of any stride
+    const bool many = a[13] != Py_None;
+    const int64_t axes = many ? (pos.dim() == 2 ? pos.size(0) : 0) : 1;
+    if (many && (axes < 1 || pos.size(1) != T || (T > 1 && pos.stride(1) != 1)))
+        raise(PyExc_ValueError, "positions [axes][T] expected");
+    if ((!many && (pos.numel() != T || !pos.is_contiguous())) || slots.numel() != T || cs.dim() != 2 ||
+        !all_contiguous(slots, cs))
         raise(PyExc_ValueError, "positions [T], slot_mapping [T] and cos_sin [max_position][rot_dim], "
                                 "contiguous, expected");
     if (!all_contiguous(kc, vc) || vc.scalar_type() != kc.scalar_type() || vc.numel() != kc.numel())
@@ -248,11 +278,84 @@ int rope(PyObject* const* a)
     if (interleaved < 0) throw Raised{};
     void* const stream = stream_of(a[10]);
     const int max_position = to_int(cs.size(0)), rot_dim = to_int(cs.size(1)), tokens = to_int(T);
-    const int n_q = to_int(q.size(1));
+    const int n_q = to_int(q.size(1)), n_axes = to_int(axes);
+    auto call = [&](const uint8_t* axis_of_pair, int64_t axis_stride) {
+        const Released released;
+        return lib_rope(q_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), in, so, sq, sk, sv,
+                        data<int32_t>(pos), axis_stride, n_axes, axis_of_pair, data<float>(cs), max_position, rot_dim,
+                        interleaved, kc.data_ptr(), vc.data_ptr(), data<int64_t>(slots), tokens, n_q, &c, stream);
+    };
+    if (!many) {
+        static const uint8_t one_axis[PA_MAX_ROPE_PAIRS] = {};
+        return call(one_axis, 0);
+    }
+    const Bytes map(a[13]);
+    if (map.b.itemsize != 1 || map.b.len != rot_dim / 2)
+        raise(PyExc_ValueError, "axis_of_pair: uint8 [rot_dim / 2] expected");
+    // (rows that overlap or run backwards: refused; a single axis has no stride)
+    const int64_t stride = axes > 1 ? pos.stride(0) : T;
+    if (stride < T) raise(PyExc_ValueError, "positions: rows of at least T elements expected");
+    return call(static_cast<const uint8_t*>(map.b.buf), stride);
+}
+
+// (k_out, v_out, k_cache, v_cache, slot_mapping, stream, k_scale, v_scale)
+int gather(PyObject* const* a)
+{
+    const at::Tensor &ko = tensor(a[0]), &vo = tensor(a[1]), &kc = tensor(a[2]), &vc = tensor(a[3]), &slots = tensor(a[4]);
+    if (kc.dim() != 4 || ko.dim() != 3 || ko.sizes() != vo.sizes() || ko.size(1) != kc.size(1) ||
+        ko.size(2) != head_dim(kc) || slots.numel() != ko.size(0))
+        raise(PyExc_ValueError, "k_out, v_out [T][n_kv][d] and slot_mapping [T] expected");
+    if (ko.scalar_type() != vo.scalar_type() || slots.scalar_type() != at::kLong)
+        raise(PyExc_TypeError, "k_out and v_out of one dtype and slot_mapping int64 expected");
+    if (!all_contiguous(ko, vo, kc, vc, slots) || vc.scalar_type() != kc.scalar_type() || vc.numel() != kc.numel())
+        raise(PyExc_ValueError, "contiguous tensors and pools of one dtype and size expected");
+    on_current_device(ko, vo, kc, vc, slots);
+    const pa_dtype out = pa_type(ko.scalar_type());
+    const pa_cache_desc c = descriptor(kc, at::kBFloat16, a[6], a[7]);
+    const int tokens = to_int(slots.numel());
+    void* const stream = stream_of(a[5]);
     const Released released;
-    return lib_rope(q_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), in, so, sq, sk, sv,
-                    data<int32_t>(pos), data<float>(cs), max_position, rot_dim, interleaved, kc.data_ptr(),
-                    vc.data_ptr(), data<int64_t>(slots), tokens, n_q, &c, stream);
+    return lib_gather(ko.data_ptr(), vo.data_ptr(), out, kc.data_ptr(), vc.data_ptr(), data<int64_t>(slots), tokens, &c,
+                      stream);
+}
+
+// (out, q, k_cache, v_cache, block_tables, context_lens, scale, block_size, workspace, stream,
+//  k_scale, v_scale): one row a sequence, or q_per_seq
+int decode(PyObject* const* a)
+{
+    const at::Tensor& q = tensor(a[1]);
+    if (q.dim() != 3 && q.dim() != 4) raise(PyExc_ValueError, "q [B][n_q][d] or [B][q_per_seq][n_q][d] expected");
+    const int64_t B = q.size(0), nq = q.dim() == 4 ? q.size(1) : 1;
+    const Attention x = attention(a, B, a[10], a[11]);
+    size_t bytes;
+    void* ws = workspace(a[8], &bytes);
+    const float scale = static_cast<float>(as_double(a[6]));
+    const int block_size = as_int(a[7]), seqs = to_int(B), per_seq = to_int(nq), heads = to_int(q.size(-2));
+    void* const stream = stream_of(a[9]);
+    const Released released;
+    return lib_decode(x.out.data_ptr(), x.out_dtype, x.q.data_ptr(), x.kc.data_ptr(), x.vc.data_ptr(), &x.cache,
+                      data<int32_t>(x.tables), x.width, data<int32_t>(x.lens), seqs, per_seq, heads, scale, block_size,
+                      ws, bytes, stream);
+}
+
+// (out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc, max_query_len, scale,
+//  block_size, stream, k_scale, v_scale)
+int prefill(PyObject* const* a)
+{
+    const at::Tensor &q = tensor(a[1]), &start = tensor(a[6]);
+    const int64_t R = tensor(a[5]).numel();
+    if (q.dim() != 3) raise(PyExc_ValueError, "q [total][n_q][d] expected");
+    if (start.scalar_type() != at::kInt || start.numel() != R + 1 || !start.is_contiguous())
+        raise(PyExc_ValueError, "query_start_loc int32 [R + 1], contiguous, expected");
+    const Attention x = attention(a, R, a[11], a[12]);
+    on_current_device(start);
+    const float scale = static_cast<float>(as_double(a[8]));
+    const int block_size = as_int(a[9]), max_q = as_int(a[7]), reqs = to_int(R), n_q = to_int(q.size(1));
+    void* const stream = stream_of(a[10]);
+    const Released released;
+    return lib_prefill(x.out.data_ptr(), x.out_dtype, x.q.data_ptr(), x.kc.data_ptr(), x.vc.data_ptr(), &x.cache,
+                       data<int32_t>(x.tables), x.width, data<int32_t>(start), data<int32_t>(x.lens), reqs, max_q, n_q,
+                       scale, block_size, nullptr, 0, stream);
 }
 
 // (out, q, k_cache, v_cache, block_tables, context_lens, group_of_seq, prefix_lens, scale,
@@ -322,11 +425,12 @@ int prefill_scored(PyObject* const* a)
                               data<int32_t>(x.lens), reqs, max_q, n_q, scale, block_size, &m, stream);
 }
 
-// (addresses of pa_rope_and_cache, pa_decode_shared, pa_decode_scored, pa_prefill_scored)
+// (addresses of pa_rope_axes_and_cache, pa_decode_shared, pa_decode_scored, pa_prefill_scored,
+//  pa_decode_verify, pa_prefill_chunk, pa_gather_cache)
 int bind(PyObject* const* a)
 {
-    uintptr_t p[4];
-    for (int i = 0; i < 4; i++) {
+    uintptr_t p[7];
+    for (int i = 0; i < 7; i++) {
         p[i] = static_cast<uintptr_t>(PyLong_AsUnsignedLongLong(a[i]));
         if (PyErr_Occurred()) throw Raised{};
     }
@@ -334,6 +438,9 @@ int bind(PyObject* const* a)
     lib_decode_shared = reinterpret_cast<decltype(lib_decode_shared)>(p[1]);
     lib_decode_scored = reinterpret_cast<decltype(lib_decode_scored)>(p[2]);
     lib_prefill_scored = reinterpret_cast<decltype(lib_prefill_scored)>(p[3]);
+    lib_decode = reinterpret_cast<decltype(lib_decode)>(p[4]);
+    lib_prefill = reinterpret_cast<decltype(lib_prefill)>(p[5]);
+    lib_gather = reinterpret_cast<decltype(lib_gather)>(p[6]);
     return 0;
 }
 
@@ -360,8 +467,11 @@ PyMethodDef method(const char* name)
     return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(entry<F, N>)), METH_FASTCALL, nullptr};
 }
 
-PyMethodDef methods[] = {method<bind, 4>("bind"),
-                         method<rope, 13>("rope"),
+PyMethodDef methods[] = {method<bind, 7>("bind"),
+                         method<rope, 14>("rope"),
+                         method<gather, 8>("gather"),
+                         method<decode, 12>("decode"),
+                         method<prefill, 13>("prefill"),
                          method<decode_shared, 14>("decode_shared"),
                          method<decode_scored, 13>("decode_scored"),
                          method<prefill_scored, 14>("prefill_scored"),

@@ -29,7 +29,13 @@ pa_status encode_pool_map(CUtensorMap* map, const void* base, pa_dtype dt, int r
 // Profiling events around the decode's attention kernels (may be null).
 void profile_events(cudaEvent_t* start, cudaEvent_t* stop);
 
+// (of pools other than 4-bit ones)
 inline int elem_bytes(pa_dtype d) { return d == PA_F32 ? 4 : (d == PA_FP8_E4M3 ? 1 : 2); }
+// bytes of one token's row of one KV head, K or V
+inline int row_bytes(const pa_cache_desc& c)
+{
+    return c.dtype == PA_FP4_E2M1 ? c.head_dim / 2 + c.head_dim / 16 : c.head_dim * elem_bytes(c.dtype);
+}
 
 // ---- launchers (defined next to their kernels) ----
 cudaError_t launch_cache_write(const void* k, const void* v, void* kc, void* vc,
@@ -39,12 +45,21 @@ cudaError_t launch_cache_write_fp8(const void* k, const void* v, pa_dtype in_dty
                                    void* vc, const int64_t* slots, int T, const pa_cache_desc& c,
                                    unsigned* err, cudaStream_t s);
 
+cudaError_t launch_cache_write_fp4(const void* k, const void* v, pa_dtype in_dtype, void* kc,
+                                   void* vc, const int64_t* slots, int T, const pa_cache_desc& c,
+                                   unsigned* err, cudaStream_t s);
+cudaError_t launch_gather(void* k_out, void* v_out, pa_dtype out, const void* kc, const void* vc,
+                          const int64_t* slots, int T, const pa_cache_desc& c, unsigned* err,
+                          cudaStream_t s);
+
 struct RopeArgs {
     void* q_out; const void *q, *k, *v; pa_dtype in_dtype;
     int64_t q_out_stride, q_stride, k_stride, v_stride;   // elements between tokens
     const int32_t* positions; const float* cos_sin; int max_position; int rot_dim; int interleaved;
     void* k_cache; void* v_cache; const int64_t* slots; int num_tokens; int n_q;
     pa_cache_desc cache; unsigned* err;
+    // position axes (1: positions is one row); the axis of pair i is bits 2 (i % 16) of axis[i / 16]
+    int axes; int64_t axis_stride; uint32_t axis[PA_MAX_ROPE_PAIRS / 16];
 };
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s);
 
@@ -101,6 +116,27 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t s);
 cudaError_t launch_decode_scored(const DecodeArgs& a, cudaStream_t s, float scale_log2);
 cudaError_t launch_decode_wide(const DecodeArgs& a, cudaStream_t s, float scale_log2);   // (caps above kNearCap)
 cudaError_t launch_decode_scored_simt(const DecodeArgs& a, cudaStream_t s, float scale_log2);
+// a call on an FP4 pool, its merge included (decode_fp4.cu), and what the workspace of one has to hold: the
+// grid is at most kF4MaxCtas blocks for each of at most kF4Sms SMs, each with the head of its run and, as far
+// as there are so many, the tail, of f4_unit_rows rows
+constexpr int kF4GranuleTokens = 128, kF4MaxCtas = 4, kF4Sms = 152;
+inline int f4_unit_rows(int rows_kv) { return rows_kv <= 4 ? 4 : (rows_kv <= 8 ? 8 : 16); }
+inline int64_t f4_granules(int num_seqs, int nq, int group, int n_kv, int max_ctx)
+{
+    const int ru = f4_unit_rows(group * nq);
+    return static_cast<int64_t>(num_seqs) * n_kv * ((group * nq + ru - 1) / ru) *
+           ((max_ctx + kF4GranuleTokens - 1) / kF4GranuleTokens);
+}
+inline size_t f4_workspace_bytes(int num_seqs, int nq, int group, int n_kv, int D, int max_ctx)
+{
+    if (max_ctx <= kF4GranuleTokens) return 0;    // (no shared pieces)
+    const int ru = f4_unit_rows(group * nq), per_sm = ru == 16 ? 2 : (D == 64 ? 4 : 3);
+    const int64_t most = f4_granules(num_seqs, nq, group, n_kv, max_ctx), grid = kF4Sms * per_sm;
+    const int64_t blocks = most < grid ? most : grid;
+    const int64_t rows = static_cast<int64_t>(num_seqs) * n_kv * ((group * nq + ru - 1) / ru);
+    return blocks * 16 + static_cast<size_t>(blocks + (rows < blocks ? rows : blocks)) * ru * (D + 2) * sizeof(float);
+}
+cudaError_t launch_decode_fp4(const DecodeArgs& a, void* workspace, cudaStream_t s);
 // prefix pass of a shared-prefix call (prefix_pass.cu)
 cudaError_t launch_prefix_pass(const DecodeArgs& a, const PrefixPass& pass, cudaStream_t s);
 // attention kernel of a call with q_per_seq > 1 (decode_verify.cu)
@@ -116,6 +152,7 @@ struct PrefillArgs {
     const ScoreParams* score;   // scored prefill (host memory); else null
 };
 cudaError_t launch_prefill_tc(const PrefillArgs& a, cudaStream_t s);
+cudaError_t launch_prefill_fp4(const PrefillArgs& a, cudaStream_t s);
 cudaError_t launch_prefill_scored(const PrefillArgs& a, cudaStream_t s);
 cudaError_t launch_prefill_bias(const PrefillArgs& a, cudaStream_t s);   // (its forms with a bias)
 cudaError_t launch_prefill_wide(const PrefillArgs& a, cudaStream_t s);   // (its caps above kNearCap)

@@ -40,6 +40,8 @@
 // that with head_dim 128 and bf16 queries the score MMAs read the K codes
 // themselves (a K-loader warp TMAs them; two converters widen V alone).
 // k_scale is folded into the softmax scale and v_scale into the output.
+// FP4 pools (F4): the same converters widen 4-bit rows, codes times their scales, exactly to fp16;
+// V is stored by rows as K is, so both rings hold [keys][d] as for 16-bit pools.
 // Scored instantiations (MODE, see kPf* below): a row sees the keys between bounds
 // of its own (window, document and prefix masks), the CTA's key tiles start at the
 // one of its first visible key, and scores may be capped or biased (score_mod.cuh).
@@ -54,6 +56,7 @@
 
 #include "pa_device.cuh"
 #include "pa_internal.h"
+#include "prefill_fp4.cuh"
 #include "prefix_plan.cuh"
 #include "score_mod.cuh"
 
@@ -150,18 +153,18 @@ constexpr int kKWarp = kSoftmaxWarps, kVWarp = kSoftmaxWarps + 1;
 constexpr int kF8ChunkKeys = 32;   // keys per staged chunk of codes (16 or 32)
 constexpr int kF8MaxConverters = 3;
 constexpr int kF8MaxDepth = 2;     // staging buffers per converter
-template <bool F8, int D, bool BQ>
+template <bool F8, int D, bool BQ, bool F4 = false>
 struct PfMode {
-    static constexpr bool kDirectK = F8 && D == 128 && BQ;   // K codes straight into the score MMA
+    static constexpr bool kDirectK = F8 && !F4 && D == 128 && BQ;   // K codes straight into the score MMA
     static constexpr int kConverters = F8 ? (kDirectK ? 2 : 3) : 0;
     static constexpr int kKLoaders = kDirectK ? 1 : 0;   // direct K: a warp TMAs the K codes
     static constexpr int kDepth = 2;
 };
 // Warps after the softmax ones: the K and V producers (or the FP8
 // converters, and with direct K the K-code loader), then the MMA issuer.
-template <bool F8, int D, bool BQ>
+template <bool F8, int D, bool BQ, bool F4 = false>
 struct PfWarps {
-    using Mode = PfMode<F8, D, BQ>;
+    using Mode = PfMode<F8, D, BQ, F4>;
     static constexpr int kProducers = F8 ? Mode::kConverters + Mode::kKLoaders : 2;
     static constexpr int kFirstConverter = kSoftmaxWarps;
     static constexpr int kKLoader = kFirstConverter + Mode::kConverters;   // (direct K only)
@@ -173,22 +176,23 @@ struct PfWarps {
 };
 constexpr uint32_t kTmemCols = 512;   // S/P_A [0,128) S/P_B [128,256) O_A, O_B from 256
 
-template <typename T, int D, bool F8, bool BQ>
+template <typename T, int D, bool F8, bool BQ, bool F4 = false>
 struct PfLayout {
-    static constexpr bool kDirectK = PfMode<F8, D, BQ>::kDirectK;
+    static constexpr bool kDirectK = PfMode<F8, D, BQ, F4>::kDirectK;
     static constexpr int kHalves = D / 64;
     // one Q tile: 16-bit rows, or (direct K) the E4M3 hi part then the lo part
     static constexpr uint32_t kQBytes = kTcRows * D * 2;
     static constexpr uint32_t kQLo = kTcRows * D;                 // direct K: offset of the lo part
     static constexpr uint32_t kKBytes = kTcKeys * D * (kDirectK ? 1 : 2);   // K of one key tile
     static constexpr uint32_t kVBytes = kTcKeys * D * 2;          // V of one key tile (16-bit)
-    static constexpr uint32_t kCodeBytes = kF8ChunkKeys * D;      // FP8: codes of one staged chunk
+    // FP8, FP4: one staged chunk as it is in the pool
+    static constexpr uint32_t kCodeBytes = kF8ChunkKeys * (F4 ? fp4_row_bytes(D) : D);
     static constexpr uint32_t kOffQ = 0;                          // Q_A, Q_B
     static constexpr uint32_t kOffK = kOffQ + kTcTiles * kQBytes; // K ring
     static constexpr uint32_t kOffV = kOffK + kTcStages * kKBytes;   // V ring
     static constexpr uint32_t kOffCS = kOffV + kTcStages * kVBytes;  // FP8: 2 code buffers per converter
     static constexpr uint32_t kDynBytes =
-        kOffCS + PfMode<F8, D, BQ>::kConverters * PfMode<F8, D, BQ>::kDepth * kCodeBytes + 1024;
+        kOffCS + PfMode<F8, D, BQ, F4>::kConverters * PfMode<F8, D, BQ, F4>::kDepth * kCodeBytes + 1024;
     // S_t at t * 128; P_t overwrites it, keys 32c .. 32c+31 as hi in columns
     // 32c .. 32c+15 and (bf16 operands) lo in 32c+16 .. 32c+31 (two 16-bit
     // values per column)
@@ -197,14 +201,6 @@ struct PfLayout {
     static_assert(kDynBytes <= 232448, "shared memory per CTA");
     static_assert(kTmemO + kTcTiles * D <= kTmemCols, "tensor memory columns");
 };
-
-__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
-                                             uint32_t d)
-{
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
-                 "r"(d)
-                 : "memory");
-}
 
 // Bulk copy of `bytes` contiguous bytes shared -> global (both 16-byte aligned, bytes a
 // multiple of 16) by this thread, and the wait for all of its copies.
@@ -313,8 +309,8 @@ __device__ __forceinline__ uint4 drop_codes(uint4 c, int drop)
 // operands (the codes widen to fp16 in one instruction a pair): each q row is
 // scaled by a power of two 2^-e into fp16 (exact for bf16 values down to 2^-28
 // of the row's largest) and 2^e goes into that row's softmax scale.
-template <typename T, typename QT, int D, int BS, bool F8 = false, int MODE = 0>
-__global__ void __launch_bounds__(PfWarps<F8, D, std::is_same<QT, __nv_bfloat16>::value>::kThreads, 1)
+template <typename T, typename QT, int D, int BS, bool F8 = false, int MODE = 0, bool F4 = false>
+__global__ void __launch_bounds__(PfWarps<F8, D, std::is_same<QT, __nv_bfloat16>::value, F4>::kThreads, 1)
 prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                   const uint8_t* __restrict__ k_codes, const uint8_t* __restrict__ v_codes,
                   void* __restrict__ out, pa_dtype out_dtype, const QT* __restrict__ q,
@@ -332,8 +328,10 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     static_assert(!kWide || (kCap && kBias), "the wide form comes with cap and bias");
     constexpr bool kZ = kCap || kBias;   // maxima in the log2 domain of modified scores
     constexpr bool kBq = std::is_same<QT, __nv_bfloat16>::value;
-    using Ly = PfLayout<T, D, F8, kBq>;
-    using Wp = PfWarps<F8, D, kBq>;
+    using Ly = PfLayout<T, D, F8, kBq, F4>;
+    using Wp = PfWarps<F8, D, kBq, F4>;
+    static_assert(!F4 || F8, "FP4 pools: the FP8 kernel with other converters");
+    constexpr bool kVt = F8 && !F4;      // V transposed: [d][keys]
     // kShared, and a block of a cluster: bytes of an O row staged in shared memory (16 more, so that the rows of
     // eight threads storing together lie in different banks)
     constexpr uint32_t kORow = D * 4 + 16;
@@ -350,8 +348,8 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     constexpr uint32_t kIdescQK = idesc_f16(kBf16, false, false, kTcRows, kTcKeys);
     // kind::f8f6f4 with E4M3 A and B (type code 0 in both fields), fp32 accumulate
     constexpr uint32_t kIdescQK8 = idesc_f16(false, false, false, kTcRows, kTcKeys);
-    // P V: V as [keys][d] (MN-major) from 16-bit pools, as [d][keys] (K-major) from FP8
-    constexpr uint32_t kIdescPV = idesc_f16(kBf16, false, !F8, kTcRows, D);
+    // P V: V as [keys][d] (MN-major) from 16-bit and FP4 pools, as [d][keys] (K-major) from FP8
+    constexpr uint32_t kIdescPV = idesc_f16(kBf16, false, !kVt, kTcRows, D);
     static_assert(BS % 16 == 0 && kTcKeys % BS == 0, "block size must divide the key tile");
 
     // Every barrier below is waited on in completion order and its waiter is
@@ -606,9 +604,15 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                         set_error(err, PA_ERR_OUT_OF_RANGE);
                         b = 0;
                     }
+                    const int64_t bh = static_cast<int64_t>(b) * n_kv + kvh;
+                    if constexpr (F4) {     // 16 rows
+                        constexpr int kBytes = 16 * fp4_row_bytes(D);
+                        bulk_load(buf + x * kBytes, (k_chunk ? k_codes : v_codes) + (bh * (BS / 16) + key0 % BS / 16) * kBytes,
+                                  kBytes, bar);
+                        continue;
+                    }
                     // 16 rows of D codes (K), or the D x 16 transposed piece
                     // (V): 16 * D contiguous bytes of the pool either way
-                    const int64_t bh = static_cast<int64_t>(b) * n_kv + kvh;
                     const uint8_t* src =
                         k_chunk ? k_codes + (bh * BS + key0 % BS) * D
                                 : v_codes + (bh * (BS / 16) + (key0 % BS) / 16) * (16 * D);
@@ -648,6 +652,9 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             // the staging reads and in the ring writes.
             constexpr int kPer = kCK * D / 512;
             const uint8_t* src = stage_ptr + (n % kDepth) * Ly::kCodeBytes;
+            if constexpr (F4) {
+                f4_widen_chunk<D, kCK, kTcKeys>(src, dst, lane, e * kCK, keep_tile);
+            } else {
             uint4 c[kPer];
             int row[kPer], chunk0[kPer];
 #pragma unroll
@@ -707,6 +714,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                                           rw * 128 + (((ch & 7) ^ (rw & 7)) << 4);
                     st_shared_v4(addr, w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]);
                 }
+            }
             }
             fence_proxy_async_smem();   // ring writes -> the MMAs' reads
             __syncwarp();               // and every lane has read the staging buffer
@@ -803,8 +811,8 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         {
             const uint64_t dq = sdesc_sw128(sbase + Ly::kOffQ, 16, 1024);
             const uint64_t dk = sdesc_sw128(sbase + Ly::kOffK, 16, 1024);
-            // V: MN-major [keys][d] halves (16-bit pools) or K-major [d][keys] halves (FP8)
-            const uint64_t dv = F8 ? sdesc_sw128(sbase + Ly::kOffV, 16, 1024)
+            // V: MN-major [keys][d] halves (16-bit and FP4 pools) or K-major [d][keys] halves (FP8)
+            const uint64_t dv = kVt ? sdesc_sw128(sbase + Ly::kOffV, 16, 1024)
                                    : sdesc_sw128(sbase + Ly::kOffV, kTcKeys * 128, 1024);
             constexpr uint32_t kQHalf = (kTcRows * 128) >> 4, kKHalf = (kTcKeys * 128) >> 4;
             constexpr uint32_t kKStage = Ly::kKBytes >> 4, kVStage = Ly::kVBytes >> 4;
@@ -849,7 +857,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                 // V rows of these 16 keys: 16 rows of 128 B (MN-major), or
                 // 32 B into a 64-key half of the [d][keys] tile (K-major)
                 auto vst = [&](int ks) {
-                    return static_cast<uint32_t>(F8 ? (ks >> 2) * ((D * 128) >> 4) + (ks & 3) * 2
+                    return static_cast<uint32_t>(kVt ? (ks >> 2) * ((D * 128) >> 4) + (ks & 3) * 2
                                                     : ks * (2048 >> 4));
                 };
                 if constexpr (kOneP) {
@@ -1489,12 +1497,12 @@ std::conditional_t<MODE != 0, ScoreParams, NoScore> prefill_score(const PrefillA
     else return NoScore{};
 }
 
-template <typename T, typename QT, int D, int BS, bool F8, int MODE>
+template <typename T, typename QT, int D, int BS, bool F8, int MODE, bool F4 = false>
 cudaError_t run_prefill_tc(const PrefillArgs& a, cudaStream_t s, float sl2)
 {
     constexpr bool kBq = std::is_same<QT, __nv_bfloat16>::value;
-    using Ly = PfLayout<T, D, F8, kBq>;
-    auto kern = prefill_tc_kernel<T, QT, D, BS, F8, MODE>;
+    using Ly = PfLayout<T, D, F8, kBq, F4>;
+    auto kern = prefill_tc_kernel<T, QT, D, BS, F8, MODE, F4>;
     static std::once_flag once;
     static cudaError_t attr_err = cudaSuccess;
     std::call_once(once, [&] {
@@ -1503,8 +1511,10 @@ cudaError_t run_prefill_tc(const PrefillArgs& a, cudaStream_t s, float sl2)
     });
     if (attr_err != cudaSuccess) return attr_err;
     CUtensorMap kmap{}, vmap{};
-    const cudaError_t map_err = prefill_maps<T, D, BS, F8, kBq>(a.cache, a.k_cache, a.v_cache, &kmap, &vmap);
-    if (map_err != cudaSuccess) return map_err;
+    if constexpr (!F4) {      // (FP4: bulk copies only)
+        const cudaError_t map_err = prefill_maps<T, D, BS, F8, kBq>(a.cache, a.k_cache, a.v_cache, &kmap, &vmap);
+        if (map_err != cudaSuccess) return map_err;
+    }
     const int group = a.n_q / a.cache.n_kv_heads;
     const int64_t tiles = (static_cast<int64_t>(a.max_q) * group + kTcTiles * kTcRows - 1) /
                           (kTcTiles * kTcRows);
@@ -1512,7 +1522,7 @@ cudaError_t run_prefill_tc(const PrefillArgs& a, cudaStream_t s, float sl2)
     if constexpr ((MODE & kPfSplit) != 0) splits = prefill_splits(a);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(tiles * splits), a.cache.n_kv_heads, a.num_reqs);
-    cfg.blockDim = dim3(PfWarps<F8, D, kBq>::kThreads);
+    cfg.blockDim = dim3(PfWarps<F8, D, kBq, F4>::kThreads);
     cfg.dynamicSmemBytes = Ly::kDynBytes;
     cfg.stream = s;
     // (a scored call is a programmatic dependent: its blocks are scheduled while the kernel
@@ -1533,14 +1543,14 @@ cudaError_t run_prefill_tc(const PrefillArgs& a, cudaStream_t s, float sl2)
         F8 ? sl2 * a.cache.k_scale : sl2, F8 ? a.cache.v_scale : 1.f, a.err, prefill_score<MODE>(a), NoScore{});
 }
 
-template <typename T, typename QT, bool F8, int MODE>
+template <typename T, typename QT, bool F8, int MODE, bool F4 = false>
 cudaError_t run_prefill_tc_dt(const PrefillArgs& a, cudaStream_t s, float sl2)
 {
     const int D = a.cache.head_dim, BS = a.cache.block_size;
-    if (D == 64 && BS == 16) return run_prefill_tc<T, QT, 64, 16, F8, MODE>(a, s, sl2);
-    if (D == 64 && BS == 32) return run_prefill_tc<T, QT, 64, 32, F8, MODE>(a, s, sl2);
-    if (D == 128 && BS == 16) return run_prefill_tc<T, QT, 128, 16, F8, MODE>(a, s, sl2);
-    if (D == 128 && BS == 32) return run_prefill_tc<T, QT, 128, 32, F8, MODE>(a, s, sl2);
+    if (D == 64 && BS == 16) return run_prefill_tc<T, QT, 64, 16, F8, MODE, F4>(a, s, sl2);
+    if (D == 64 && BS == 32) return run_prefill_tc<T, QT, 64, 32, F8, MODE, F4>(a, s, sl2);
+    if (D == 128 && BS == 16) return run_prefill_tc<T, QT, 128, 16, F8, MODE, F4>(a, s, sl2);
+    if (D == 128 && BS == 32) return run_prefill_tc<T, QT, 128, 32, F8, MODE, F4>(a, s, sl2);
     return cudaErrorInvalidValue;
 }
 
