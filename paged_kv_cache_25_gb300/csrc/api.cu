@@ -95,6 +95,24 @@ pa_status encode_pool_map(CUtensorMap* map, const void* base, pa_dtype dt, int h
     return PA_OK;
 }
 
+pa_status encode_byte_rows(CUtensorMap* map, const void* base, int row_bytes, uint64_t rows)
+{
+    auto fn = encode_fn();
+    if (!fn) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    // (8-byte elements: a box has at most 256 of them)
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(row_bytes) / 8, rows};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(row_bytes / 8), 1};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT64, 2, const_cast<void*>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                          // (no wider than what divides a row: rows are read apart)
+                          row_bytes % 128 == 0 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_64B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+    return PA_OK;
+}
+
 // ------------------------------------------------------------------ profiling hook
 static std::atomic<cudaEvent_t> g_prof_start{nullptr}, g_prof_stop{nullptr};
 
@@ -209,7 +227,11 @@ static size_t decode_ws_bytes(int B, int nq, int n_q, int n_kv, int D, int BS, i
 static size_t any_pool_ws_bytes(int B, int nq, int n_q, int n_kv, int D, int BS, int max_ctx)
 {
     const size_t n = decode_ws_bytes(B, nq, n_q, n_kv, D, BS, max_ctx, nullptr, nullptr);
-    return D == 64 || D == 128 ? std::max(n, f4_workspace_bytes(B, nq, n_q / n_kv, n_kv, D, max_ctx)) : n;
+    if (D != 64 && D != 128) return n;
+    // (FP4 pools: room for the whole grid, unless there is room for three quarters of it anyway)
+    auto f4 = [&](int blocks) { return f4_workspace_bytes(B, nq, n_q / n_kv, n_kv, D, max_ctx, blocks); };
+    const int grid = f4_grid(n_q / n_kv * nq);
+    return n >= f4(grid / 4 * 3) ? n : std::max(n, f4(grid));
 }
 
 // Tokens that the partitions of a sequence can span: with a window, its rows' keys
@@ -630,7 +652,8 @@ static pa_status decode_common(void* out, pa_dtype out_dtype, const void* q, con
         const int group = n_q_heads / cache->n_kv_heads;
         if (f4_granules(num_seqs, q_per_seq, group, cache->n_kv_heads, max_ctx) >= (1ll << 31))
             return fail(PA_ERR_UNSUPPORTED, "too many tokens in the tables for one call");
-        need = f4_workspace_bytes(num_seqs, q_per_seq, group, cache->n_kv_heads, cache->head_dim, max_ctx);
+        need = f4_workspace_bytes(num_seqs, q_per_seq, group, cache->n_kv_heads, cache->head_dim, max_ctx,
+                                  f4_grid(group * q_per_seq) / 2);
         need = std::max(need, kControlBytes);
     }
     if (parts > 65535) return fail(PA_ERR_UNSUPPORTED, "too many partitions per sequence");
@@ -680,7 +703,7 @@ static pa_status decode_common(void* out, pa_dtype out_dtype, const void* q, con
         const cudaError_t e0 = launch_prefix_pass(a, pass, static_cast<cudaStream_t>(stream));
         if (e0 != cudaSuccess) return cuda_fail(e0, "prefix pass launch");
     }
-    cudaError_t e = f4 ? launch_decode_fp4(a, workspace, static_cast<cudaStream_t>(stream))
+    cudaError_t e = f4 ? launch_decode_fp4(a, workspace, workspace_bytes, static_cast<cudaStream_t>(stream))
                        : launch_decode(a, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "decode launch");
     return ok();

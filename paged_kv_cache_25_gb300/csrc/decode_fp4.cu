@@ -13,9 +13,11 @@
 // all instructions of a Llama-3-8B batch: see the figures below.)  A piece's four warps take its 32-token
 // stages in turn and combine through shared memory.
 //
-// A warp streams its stages through a ring of its own by bulk copies of 16-token pieces (contiguous in
-// the pool; four lanes issue the four copies of a stage) and works on them transposed, on
-// m16n8k16 fp16 MMAs: S^T = K q^T with tokens as the MMA rows, O^T = V^T P^T with elements of d
+// Stages of 128 tokens (32 a warp) arrive in a ring that the block's warps share, each by four
+// cp.async.bulk.tensor gathers of four 16-token tiles (a tile's rows are contiguous in the pool, so the pool is a
+// matrix with a tile a row), which the warps issue in turn.  (Untiled copies, one a tile: the
+// instructions around them were a fifth of all.)  A warp works on its tokens transposed, on m16n8k16 fp16
+// MMAs: S^T = K q^T with tokens as the MMA rows, O^T = V^T P^T with elements of d
 // as the rows, the unit's rows as the columns (NT tiles of 8).
 //   - Row r of a score tile is token 4 ((r & 7) >> 1) + 2 (r >> 3) + (r & 1) of its piece; the transpose
 //     of P (movmatrix) then leaves lane (g, t4) = (lane / 4, lane % 4) with tokens 4 t4 .. 4 t4 + 3, whose V
@@ -23,8 +25,8 @@
 //   - Neither K nor V is stored transposed.  K's codes lie along d, as its fragments pair them.
 //     V's fragments pair tokens: the codes of two tokens are put together half byte by half
 //     byte before they are widened (two shifts and two three-input logic operations for 16 codes).
-//   - The k order of S is free: lane t4 holds elements 64 h + 16 t4 + (0 .. 15) of its tokens, one scale
-//     each, and q is loaded to match.  Lane g holds elements (d / 8) g and on of V: one scale a token.
+//   - The k order of S is free: lane t4 holds elements (d / 4) t4 and on of its tokens, one or two
+//     scales, and q is loaded to match.  Lane g holds elements (d / 8) g and on of V: one scale a token.
 //   - Codes times scales are exact in fp16 (fp4.cuh).  bf16 queries are scaled by a power of two into
 //     fp16 (exact down to 2^-29 of the row's largest element).
 //   - P enters P V as one fp16 part: 11 bits, so an output moves by at most 2^-12 of the largest |v| that it
@@ -49,13 +51,12 @@ namespace pa {
 constexpr int kF4Warps = 4;
 constexpr int kF4Threads = kF4Warps * 32;
 constexpr int kPieceTok = 16;             // tokens of a tile of scores, and of one copy
-constexpr int kStageTok = 32;             // tokens of a stage: two tiles
-constexpr int kGranule = kF4Warps * kStageTok;   // tokens of a granule
+constexpr int kStageTok = 32;             // tokens of a stage that a warp takes: two tiles
+constexpr int kGranule = kF4Warps * kStageTok;   // tokens of a stage, and of a granule
 constexpr int kF4PrefixCap = 768;         // entries of the table of granules before a sequence
 static_assert(kGranule == kF4GranuleTokens, "as the workspace counts them");
 
 struct F4Params {
-    const uint8_t *k, *v;
     void* out;
     const void* q;
     const int32_t *block_tables, *context_lens;
@@ -68,20 +69,21 @@ struct F4Params {
     float scale_log2, v_scale;            // softmax scale times k_scale, in the log2 domain
 };
 
-// Resident blocks an SM and ring stages a warp.
+// Resident blocks an SM and ring stages.
 template <int D, int RU>
 struct F4Cfg {
     static constexpr int kRow = fp4_row_bytes(D);
     static constexpr int kTile = kPieceTok * kRow;                          // bytes of a 16-token tile of K or V
-    static constexpr int kStage = 2 * (kStageTok / kPieceTok) * kTile;      // K tiles, then V tiles
-    static constexpr int kCtas = RU == 16 ? 2 : (D == 64 ? 4 : 3);
-    static constexpr int kNS = D == 64 ? 4 : 3;
-    static constexpr int kRing = kNS * kStage;                              // of a warp
+    static constexpr int kTiles = kGranule / kPieceTok;                     // tiles of K, and of V, a stage
+    static constexpr int kStage = 2 * kTiles * kTile;                       // K tiles, then V tiles
+    static constexpr int kCtas = RU == 16 ? 2 : 4;
+    static constexpr int kNS = RU == 16 || D == 64 ? 4 : 2;
+    static constexpr int kRing = kNS * kStage;
     static constexpr int kReduce = kF4Warps * RU * (D + 2) * 4;
     static constexpr int kReds = RU == 4 ? 2 : 1;      // combine buffers: two save a barrier a piece
-    static constexpr int kDynBytes = kF4Warps * kRing + kReds * kReduce;
-    static_assert(kCtas * (kDynBytes + 1024 + 4096) <= 233472, "shared memory of an SM");
-    static_assert(kCtas <= kF4MaxCtas, "as the workspace counts them");
+    static constexpr int kDynBytes = kRing + kReds * kReduce + 128;         // (aligned to 128 bytes)
+    static_assert(kCtas * (kDynBytes + 1024 + 3584) <= 233472, "shared memory of an SM");
+    static_assert(kNS <= kF4Warps, "a warp copies at most one of the first stages");
 };
 
 __device__ __forceinline__ void f4_store(void* out, int64_t i, float v, pa_dtype dt)
@@ -103,6 +105,16 @@ __device__ __forceinline__ void f4_store4(void* out, int64_t i, float4 v, pa_dty
             make_uint2(Cvt<__half>::pack(v.x, v.y), Cvt<__half>::pack(v.z, v.w));
 }
 
+// Four rows of a matrix (box {row, 1}) into consecutive shared memory.
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, int r0, int r1, int r2, int r3, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(bar)
+        : "memory");
+}
+
 // S^T of one tile: st[n][0, 1] row g, [2, 3] row g + 8; columns 8 n + 2 t4 and the next.
 template <int D, int NT>
 __device__ __forceinline__ void f4_scores(const uint8_t* k, int g, int t4, const uint32_t (&q)[NT][D / 16][2],
@@ -116,9 +128,8 @@ __device__ __forceinline__ void f4_scores(const uint8_t* k, int g, int t4, const
     for (int i = 0; i < 2; ++i, row += 2 * kRow) {
         if constexpr (D == 128) {
 #pragma unroll
-            for (int h = 0; h < kHalves; ++h) w[i][h] = *reinterpret_cast<const uint2*>(row + 32 * h + 8 * t4);
-            const uint2 sc = *reinterpret_cast<const uint2*>(row + D / 2);
-            const uint32_t both = e4m3x2_to_h2(__byte_perm(sc.x, sc.y, t4 | ((4 + t4) << 4)));
+            for (int h = 0; h < kHalves; ++h) w[i][h] = *reinterpret_cast<const uint2*>(row + 16 * t4 + 8 * h);
+            const uint32_t both = e4m3x2_to_h2(*reinterpret_cast<const uint16_t*>(row + D / 2 + 2 * t4));
             s[i][0] = __byte_perm(both, 0, 0x1010);
             s[i][kHalves - 1] = __byte_perm(both, 0, 0x3232);
         } else {      // (rows of 36 bytes)
@@ -150,8 +161,8 @@ __device__ __forceinline__ void f4_scores(const uint8_t* k, int g, int t4, const
 }
 
 // O^T += V^T P^T of one tile.  Byte b of a lane's codes is m-tile b, its low half row g, its high half row
-// g + 8.  valid: tokens of the tile that exist; the scales of the others may be anything, even NaN, and count as 0.
-template <int D, int NT>
+// g + 8.  valid: tokens of the tile that exist (kMasked; else all); the scales of the others may be anything, even NaN, and count as 0.
+template <int D, int NT, bool kMasked>
 __device__ __forceinline__ void f4_values(const uint8_t* v, int g, int t4, int valid, const uint32_t (&pt)[NT][2],
                                           float (&o)[NT][D / 16][4])
 {
@@ -169,19 +180,24 @@ __device__ __forceinline__ void f4_values(const uint8_t* v, int g, int t4, int v
         }
         sc[j] = row[j * kRow + D / 2 + (D == 128 ? g : g >> 1)];
     }
-    if (valid < kPieceTok) {
+    if constexpr (kMasked) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) sc[j] = 4 * t4 + j < valid ? sc[j] : 0u;
     }
-    const uint32_t s01 = e4m3x2_to_h2(sc[0] | sc[1] << 8), s23 = e4m3x2_to_h2(sc[2] | sc[3] << 8);
-    constexpr uint32_t kM = 0x0F0F0F0Fu;
+    const uint32_t s01 = e4m3x2_to_h2(__byte_perm(sc[0], sc[1], 0x0040)), s23 = e4m3x2_to_h2(__byte_perm(sc[2], sc[3], 0x0040));
+    // the low halves of a's bytes and the high halves of b's
+    auto take = [](uint32_t a, uint32_t b) {
+        uint32_t d;
+        asm("lop3.b32 %0, %1, %2, 0x0F0F0F0F, 0xE4;" : "=r"(d) : "r"(a), "r"(b));
+        return d;
+    };
 #pragma unroll
     for (int w = 0; w < kWords; ++w) {
         uint32_t a0[4], a1[4], a2[4], a3[4];
-        fp4x8_to_h2x4((x[0][w] & kM) | ((x[1][w] << 4) & ~kM), a0[0], a0[1], a0[2], a0[3]);
-        fp4x8_to_h2x4(((x[0][w] >> 4) & kM) | (x[1][w] & ~kM), a1[0], a1[1], a1[2], a1[3]);
-        fp4x8_to_h2x4((x[2][w] & kM) | ((x[3][w] << 4) & ~kM), a2[0], a2[1], a2[2], a2[3]);
-        fp4x8_to_h2x4(((x[2][w] >> 4) & kM) | (x[3][w] & ~kM), a3[0], a3[1], a3[2], a3[3]);
+        fp4x8_to_h2x4(take(x[0][w], x[1][w] << 4), a0[0], a0[1], a0[2], a0[3]);
+        fp4x8_to_h2x4(take(x[0][w] >> 4, x[1][w]), a1[0], a1[1], a1[2], a1[3]);
+        fp4x8_to_h2x4(take(x[2][w], x[3][w] << 4), a2[0], a2[1], a2[2], a2[3]);
+        fp4x8_to_h2x4(take(x[2][w] >> 4, x[3][w]), a3[0], a3[1], a3[2], a3[3]);
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
             const uint32_t a[4] = {hmul2(a0[b], s01), hmul2(a1[b], s01), hmul2(a2[b], s23), hmul2(a3[b], s23)};
@@ -192,24 +208,32 @@ __device__ __forceinline__ void f4_values(const uint8_t* v, int g, int t4, int v
 }
 
 template <typename QT, int D, int RU, bool MQ>
-__global__ void __launch_bounds__(kF4Threads, F4Cfg<D, RU>::kCtas) f4_decode_kernel(const __grid_constant__ F4Params p)
+__global__ void __launch_bounds__(kF4Threads, F4Cfg<D, RU>::kCtas) f4_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const __grid_constant__ F4Params p)
 {
     using Cfg = F4Cfg<D, RU>;
-    constexpr int NT = RU == 16 ? 2 : 1, NS = Cfg::kNS, kTiles = kStageTok / kPieceTok;
+    constexpr int NT = RU == 16 ? 2 : 1, NS = Cfg::kNS, kTiles = kStageTok / kPieceTok;   // kTiles: a warp's of a stage
     constexpr bool kBf16 = std::is_same<QT, __nv_bfloat16>::value;
 
     __shared__ int s_table[kF4PrefixCap];        // granules up to a sequence, then the sequences' lengths
     __shared__ int s_scan[kF4Warps];
-    __shared__ __align__(8) uint64_t s_bar[kF4Warps * NS];
-    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ __align__(8) uint64_t s_full[NS], s_empty[NS];
+    extern __shared__ uint8_t dyn_smem[];
+    uint8_t* const smem = dyn_smem + (-smem_u32(dyn_smem) & 127u);     // (an offset, so that it stays a shared address)
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     const int nq = MQ ? p.nq : 1;
     const int rows_kv = p.group * nq;                        // rows of a KV head, head-major
     const int n_groups = p.n_kv * ((rows_kv + RU - 1) / RU);
     const int max_ctx = p.max_blocks << p.bs_log;
-    if (tid < kF4Warps * NS) mbar_init(smem_u32(&s_bar[tid]), 1);
+    if (tid < NS) {
+        mbar_init(smem_u32(&s_full[tid]), 1);
+        mbar_init(smem_u32(&s_empty[tid]), kF4Warps);
+    }
     fence_mbar_init();
+    if (tid == 0) {
+        prefetch_tensormap(&kmap);
+        prefetch_tensormap(&vmap);
+    }
     grid_dependency_wait();      // launched as a programmatic dependent: every input may come from the kernel before
 
     // ---- this block's run of granules.  s_table[c]: granules (of one group) of the first c + 1 chunks of
@@ -276,9 +300,9 @@ __global__ void __launch_bounds__(kF4Threads, F4Cfg<D, RU>::kCtas) f4_decode_ker
     }
     auto len_of = [&](int s) { return per == 1 ? s_table[s] : __ldg(p.context_lens + s); };
 
-    // A piece: tokens [t0, t1) of the rows r0 .. r0 + nh - 1 of a KV head of sequence s.
+    // A piece: tokens [t0, t1) of the rows r0 .. r0 + nh - 1 of a KV head of sequence s, in n stages.
     struct Piece {
-        int s, L, grp, kvh, r0, nh, t0, t1;
+        int s, L, grp, kvh, r0, nh, t0, t1, n;
         bool live, tail;                         // tail: the rows' keys go on past t1
     };
     auto next_piece = [&]() {
@@ -301,18 +325,18 @@ __global__ void __launch_bounds__(kF4Threads, F4Cfg<D, RU>::kCtas) f4_decode_ker
         x.r0 = (at_grp - x.kvh * n_sub) * RU;
         x.nh = min(RU, rows_kv - x.r0);
         x.t0 = at_gran * kGranule;
-        const int n = min(left, J - at_gran), end = min(x.L, max_ctx);
-        x.t1 = min(end, (at_gran + n) * kGranule);
+        const int end = min(x.L, max_ctx);
+        x.n = min(left, J - at_gran);
+        x.t1 = min(end, (at_gran + x.n) * kGranule);
         x.tail = x.t1 < end;
-        left -= n;
+        left -= x.n;
         at_gran = 0;
         ++at_grp;
         return x;
     };
-    uint8_t* const ring = smem + warp * Cfg::kRing;
-    const uint32_t ring32 = smem_u32(ring), bar0 = smem_u32(&s_bar[warp * NS]);
+    const uint32_t ring32 = smem_u32(smem), full0 = smem_u32(s_full), empty0 = smem_u32(s_empty);
 
-    // query fragments: columns 8 n + g; steps 4 h .. 4 h + 3 are elements 64 h + 16 t4 + (0 .. 15).  A negative
+    // query fragments: columns 8 n + g; step kk is elements (d / 4) t4 + 4 kk and on.  A negative
     // softmax scale is applied as -q, so the largest raw score is the largest score.
     const uint32_t qsign = p.scale_log2 < 0.f ? 0x80008000u : 0u;
     uint32_t q[NT][D / 16][2];
@@ -328,10 +352,10 @@ __global__ void __launch_bounds__(kF4Threads, F4Cfg<D, RU>::kCtas) f4_decode_ker
             }
             const int hh = (x.r0 + r) / nq, qi = x.r0 + r - hh * nq;
             const QT* row = static_cast<const QT*>(p.q) +
-                            ((static_cast<int64_t>(x.s) * nq + qi) * p.n_q + x.kvh * p.group + hh) * D + 16 * t4;
+                            ((static_cast<int64_t>(x.s) * nq + qi) * p.n_q + x.kvh * p.group + hh) * D + D / 4 * t4;
 #pragma unroll
             for (int kk = 0; kk < D / 16; kk += 2) {
-                const uint4 u = __ldg(reinterpret_cast<const uint4*>(row + 64 * (kk / 4) + 4 * (kk % 4)));
+                const uint4 u = __ldg(reinterpret_cast<const uint4*>(row + 4 * kk));
                 q[n][kk][0] = u.x;
                 q[n][kk][1] = u.y;
                 q[n][kk + 1][0] = u.z;
@@ -380,99 +404,112 @@ __global__ void __launch_bounds__(kF4Threads, F4Cfg<D, RU>::kCtas) f4_decode_ker
     load_q(cu);
     Piece nx = next_piece();
 
-    // ---- the warp's stages, copied ahead: it_* is the next one to copy, of this piece or the next; lanes 0 .. 3
-    // copy K's two tiles and V's two, and hold the block id of theirs (loaded a stage ahead)
-    int it_s, it_kvh, it_tok, it_end, it_id = 0, slot = 0, ahead = 0;
-    uint32_t phase = 0;                          // of ring slot `slot`, the next one to be consumed
-    bool it_next = false;
-    const int it_tile = (lane & 1) * kPieceTok;
-    auto it_begin = [&](const Piece& x) {
-        it_s = x.s;
-        it_kvh = x.kvh;
-        it_tok = x.t0 + warp * kStageTok;
-        it_end = x.t1;
+    // ---- the block's stages, numbered on through its pieces.  The first NS are copied by warps 0 .. NS - 1; then,
+    // as the warps begin on stage n, warp n % 4 copies stage n - 1 + NS into the slot of the stage before, which all
+    // have left by then or are about to.  (Every warp waits for every stage's data, its own tokens among them or not:
+    // so none can leave a slot, or wait for its next stage, before the slot's present stage has come.)
+    // `duty` is the stage that this warp copies next; lanes 0 .. 7 hold the block ids of its tiles where
+    // those are loaded already (id_stage).  A stage past the next piece has to wait until its piece is known.
+    int duty = warp, id_stage = -1, id = 0;
+    int first_n = 0;                             // number of the current piece's first stage
+    bool timed_out = false;
+    const int first_duty = (warp == 0 ? kF4Warps : warp) - 1 + NS;
+    if (duty >= NS) duty = first_duty;
+    auto load_ids = [&]() {                      // false: the stage's piece is not known
+        int i = duty - first_n;
+        const bool later = i >= cu.n;
+        if (later) i -= cu.n;
+        if (later && (!nx.live || i >= nx.n)) return false;
+        const int tok = (later ? nx.t0 : cu.t0) + i * kGranule + lane * kPieceTok;
+        if (lane < Cfg::kTiles && tok < (later ? nx.t1 : cu.t1))
+            id = __ldg(p.block_tables + static_cast<int64_t>(later ? nx.s : cu.s) * p.max_blocks + (tok >> p.bs_log));
+        id_stage = duty;
+        return true;
     };
-    auto it_settle = [&]() {                     // on to the next piece; the block id
-        if (it_tok >= it_end && !it_next && nx.live) {
-            it_begin(nx);
-            it_next = true;
+    auto copy_duty = [&]() {                     // whole warp
+        if (id_stage != duty && !load_ids()) return;
+        const int slot = duty % NS, round = duty / NS;
+        // (a wait that has run out is not waited for again: the outputs are flagged)
+        if (round > 0 && !timed_out) timed_out = !mbar_wait(empty0 + slot * 8, (round - 1) & 1, p.err);
+        __syncwarp();
+        int i = duty - first_n;
+        const bool later = i >= cu.n;
+        if (later) i -= cu.n;
+        const int begin = (later ? nx.t0 : cu.t0) + i * kGranule, end = later ? nx.t1 : cu.t1;
+        const int tok = begin + lane * kPieceTok;
+        const bool there = lane < Cfg::kTiles && tok < end;
+        int b = there ? id : 0;
+        if (b < 0 || b >= p.num_blocks) {
+            set_error(p.err, PA_ERR_OUT_OF_RANGE);
+            b = 0;                               // keep the ring moving; the outputs are flagged
         }
-        if (lane < 2 * kTiles && it_tok + it_tile < it_end)
-            it_id = __ldg(p.block_tables + static_cast<int64_t>(it_s) * p.max_blocks + ((it_tok + it_tile) >> p.bs_log));
-    };
-    auto copy_ahead = [&]() {                    // whole warp: as many stages as the ring has room for
-        while (ahead < NS && it_tok < it_end) {
-            const int to = slot + ahead >= NS ? slot + ahead - NS : slot + ahead;
-            const uint32_t bar = bar0 + to * 8;
-            // (a tile past the end is left out: its tokens are masked)
-            if (lane == 0) mbar_arrive_expect_tx(bar, (it_tok + kPieceTok < it_end ? 4 : 2) * Cfg::kTile);
-            __syncwarp();
-            if (lane < 2 * kTiles && it_tok + it_tile < it_end) {
-                int id = it_id;
-                if (id < 0 || id >= p.num_blocks) {
-                    set_error(p.err, PA_ERR_OUT_OF_RANGE);
-                    id = 0;                      // keep the ring moving; the outputs are flagged
-                }
-                const int tok = it_tok + it_tile;
-                const int64_t row = ((static_cast<int64_t>(id) * p.n_kv + it_kvh) << p.bs_log) + (tok & ((1 << p.bs_log) - 1));
-                bulk_load(ring32 + to * Cfg::kStage + lane * Cfg::kTile, (lane >> 1 ? p.v : p.k) + row * Cfg::kRow,
-                          Cfg::kTile, bar);
+        // (tiles past the end: any row; their tokens are masked)
+        const int sub = (1 << (p.bs_log - 4)) - 1;
+        const int row = there ? ((b * p.n_kv + (later ? nx.kvh : cu.kvh)) << (p.bs_log - 4)) + ((tok >> 4) & sub) : 0;
+        const bool both = begin + 4 * kPieceTok < end;      // else only the first four tiles
+        int r[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) r[k] = __shfl_sync(0xffffffffu, row, k);
+        if (lane == 0) {
+            const uint32_t bar = full0 + slot * 8, dst = ring32 + slot * Cfg::kStage;
+            mbar_arrive_expect_tx(bar, (both ? 16 : 8) * Cfg::kTile);
+            tma_gather4(dst, &kmap, r[0], r[1], r[2], r[3], bar);
+            tma_gather4(dst + 8 * Cfg::kTile, &vmap, r[0], r[1], r[2], r[3], bar);
+            if (both) {
+                tma_gather4(dst + 4 * Cfg::kTile, &kmap, r[4], r[5], r[6], r[7], bar);
+                tma_gather4(dst + 12 * Cfg::kTile, &vmap, r[4], r[5], r[6], r[7], bar);
             }
-            ++ahead;
-            it_tok += kGranule;
-            it_settle();
         }
+        __syncwarp();
+        duty = duty < NS ? first_duty : duty + kF4Warps;
+        load_ids();                              // (in flight until the duty comes)
     };
-    static_assert(kTiles == 2, "lane & 1 is the tile, lane / 2 is K or V");
-    it_begin(cu);
-    it_settle();
-    copy_ahead();
+    static_assert(Cfg::kTiles == 8, "two gathers of four tiles");
+    if (duty < NS) copy_duty();
+    int n = 0, slot = 0;                         // the next stage, its slot and the slot's phase
+    uint32_t phase = 0;
 
     float o[NT][D / 16][4];
-    int buf = 0, timed_out = 0;
+    int buf = 0;
     while (cu.live) {
         scale_q();
-        // this lane's columns 8 n + 2 t4 + e: softmax scales, running maxima (raw scores), sums, key limits
-        float c[NT][2], m[NT][2], l[NT][2];
-        int lim[NT][2];
+        // this lane's columns 8 n + 2 t4 + e: softmax scales c, sums, and of the reference m of the exponents (a raw
+        // score near the largest so far) -m c and the raw score past which it moves
+        float c[NT][2], ref[NT][2], bar_z[NT][2], l[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 c[n][e] = __shfl_sync(0xffffffffu, c_q[n], 8 * t4 + 4 * e);
-                const int col = 8 * n + 2 * t4 + e;
-                lim[n][e] = MQ && col < cu.nh ? cu.L - nq + (cu.r0 + col) % nq + 1 : cu.L;
-                m[n][e] = -INFINITY;
+                ref[n][e] = 0.f;
+                bar_z[n][e] = -INFINITY;
                 l[n][e] = 0.f;
 #pragma unroll
                 for (int mt = 0; mt < D / 16; ++mt) o[n][mt][e] = o[n][mt][2 + e] = 0.f;
             }
-        const int open = cu.L - nq + 1;              // keys below it are visible to every row
-        const int tA = 4 * (g >> 1) + (g & 1);       // this lane's tokens of a tile: tA and tA + 2
-#pragma unroll 1
-        for (int pos0 = cu.t0 + warp * kStageTok; pos0 < cu.t1; pos0 += kGranule) {
-            const bool ok = mbar_wait(bar0 + slot * 8, phase, p.err);
-            if (!__all_sync(0xffffffffu, ok)) {      // leave together: shuffles follow
-                timed_out = 1;
-                break;
-            }
-            const uint8_t* st_k = ring + slot * Cfg::kStage;
-            const uint8_t* st_v = st_k + kTiles * Cfg::kTile;
+        // One stage of this warp, 32 tokens from pos0.  Masked: some of its keys are not there, or not visible to every row.
+        auto stage = [&](auto masked, const uint8_t* st_k, const uint8_t* st_v, int pos0) {
+            constexpr bool kMasked = decltype(masked)::value;
             float z[kTiles][NT][4];
 #pragma unroll
             for (int i = 0; i < kTiles; ++i) f4_scores<D, NT>(st_k + i * Cfg::kTile, g, t4, q, z[i]);
-            const bool masked = pos0 + kStageTok > min(open, cu.t1);
-            if (masked) {
+            if constexpr (kMasked) {
+                const int tA = pos0 + 4 * (g >> 1) + (g & 1);       // this lane's tokens of a tile: tA and tA + 2
 #pragma unroll
-                for (int i = 0; i < kTiles; ++i)
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
+                    for (int e = 0; e < 2; ++e) {
+                        const int col = 8 * n + 2 * t4 + e;
+                        const int lim = min(MQ && col < cu.nh ? cu.L - nq + (cu.r0 + col) % nq + 1 : cu.L, cu.t1);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (pos0 + i * kPieceTok + tA + (e & 2) >= min(lim[n][e & 1], cu.t1)) z[i][n][e] = -INFINITY;
+                        for (int i = 0; i < kTiles; ++i) {
+                            z[i][n][e] = tA + i * kPieceTok < lim ? z[i][n][e] : -INFINITY;
+                            z[i][n][2 + e] = tA + i * kPieceTok + 2 < lim ? z[i][n][2 + e] : -INFINITY;
+                        }
+                    }
             }
-            // the columns' largest raw scores, met over the eight lanes of each t4.  The reference m moves only
-            // when the first key sets it or the largest has grown by more than 2^8 (lazily: P stays below 2^8).
+            // the columns' largest raw scores, met over the eight lanes of each t4.  The reference moves only
+            // when the first key sets it or the largest is more than 2^8 past it (lazily: P stays below 2^8).
             float mx[NT][2];
             bool moved = false;
 #pragma unroll
@@ -482,61 +519,69 @@ __global__ void __launch_bounds__(kF4Threads, F4Cfg<D, RU>::kCtas) f4_decode_ker
                     float x = fmaxf(z[0][n][e], z[0][n][2 + e]);
 #pragma unroll
                     for (int i = 1; i < kTiles; ++i) x = max3f(x, z[i][n][e], z[i][n][2 + e]);
-#pragma unroll
-                    for (int w = 4; w < 32; w <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, w));
                     mx[n][e] = x;
-                    // (written so that no infinity meets a scale of 0)
-                    moved = moved || (x > m[n][e] && (m[n][e] == -INFINITY || (x - m[n][e]) * c[n][e] > 8.f));
+                    moved = moved || x > bar_z[n][e];
                 }
             if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float mn = fmaxf(m[n][e], mx[n][e]);
-                        const float f = m[n][e] == -INFINITY ? 0.f : fast_exp2((m[n][e] - mn) * c[n][e]);
-                        m[n][e] = mn;
-                        l[n][e] *= f;
+                        float x = mx[n][e];
 #pragma unroll
-                        for (int mt = 0; mt < D / 16; ++mt) {
-                            o[n][mt][e] *= f;
-                            o[n][mt][2 + e] *= f;
+                        for (int w = 4; w < 32; w <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, w));
+                        if (x > bar_z[n][e]) {
+                            const float r = -x * c[n][e];
+                            const float f = bar_z[n][e] == -INFINITY ? 0.f : fast_exp2(r - ref[n][e]);
+                            ref[n][e] = r;
+                            bar_z[n][e] = x + 8.f / c[n][e];      // (a scale of 0: never again)
+                            l[n][e] *= f;
+#pragma unroll
+                            for (int mt = 0; mt < D / 16; ++mt) {
+                                o[n][mt][e] *= f;
+                                o[n][mt][2 + e] *= f;
+                            }
                         }
                     }
             }
             uint32_t pt[kTiles][NT][2];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const float r0 = m[n][0] == -INFINITY ? 0.f : -m[n][0] * c[n][0];
-                const float r1 = m[n][1] == -INFINITY ? 0.f : -m[n][1] * c[n][1];
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int i = 0; i < kTiles; ++i) {
-                    float x[4] = {fast_exp2(fmaf(z[i][n][0], c[n][0], r0)), fast_exp2(fmaf(z[i][n][1], c[n][1], r1)),
-                                  fast_exp2(fmaf(z[i][n][2], c[n][0], r0)), fast_exp2(fmaf(z[i][n][3], c[n][1], r1))};
-                    if (masked) {      // (even with scale 0, where the exponent is NaN)
+                    float x[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) x[e] = z[i][n][e] == -INFINITY ? 0.f : x[e];
+                    for (int e = 0; e < 4; ++e) {
+                        x[e] = fast_exp2(fmaf(z[i][n][e], c[n][e & 1], ref[n][e & 1]));
+                        // (even with scale 0, where the exponent is NaN)
+                        if constexpr (kMasked) x[e] = z[i][n][e] == -INFINITY ? 0.f : x[e];
                     }
                     l[n][0] += x[0] + x[2];
                     l[n][1] += x[1] + x[3];
                     pt[i][n][0] = movmatrix_trans(Cvt<__half>::pack(x[0], x[1]));
                     pt[i][n][1] = movmatrix_trans(Cvt<__half>::pack(x[2], x[3]));
                 }
-            }
 #pragma unroll
             for (int i = 0; i < kTiles; ++i)
-                f4_values<D, NT>(st_v + i * Cfg::kTile, g, t4, cu.t1 - pos0 - i * kPieceTok, pt[i], o);
+                f4_values<D, NT, kMasked>(st_v + i * Cfg::kTile, g, t4, cu.t1 - pos0 - i * kPieceTok, pt[i], o);
+        };
+        const int open = min(cu.L - nq + 1, cu.t1);      // keys below it are there and visible to every row
+#pragma unroll 1
+        for (; n < first_n + cu.n; ++n) {
+            const int pos0 = cu.t0 + (n - first_n) * kGranule + warp * kStageTok;
+            if (!timed_out) timed_out = !mbar_wait(full0 + slot * 8, phase, p.err);
             __syncwarp();
-            --ahead;
+            if (duty <= n - 1 + NS) copy_duty();
+            const uint8_t* st_k = smem + slot * Cfg::kStage + warp * kTiles * Cfg::kTile;
+            if (pos0 + kStageTok <= open) stage(std::false_type{}, st_k, st_k + Cfg::kTiles * Cfg::kTile, pos0);
+            else if (pos0 < cu.t1) stage(std::true_type{}, st_k, st_k + Cfg::kTiles * Cfg::kTile, pos0);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty0 + slot * 8);
             slot = slot + 1 == NS ? 0 : slot + 1;
             phase ^= slot == 0 ? 1u : 0u;
-            if (it_tok < it_end) {
-                fence_proxy_async_smem();
-                copy_ahead();
-            }
         }
         // ---- this warp's partials: O of lane g's D / 8 elements and its columns, then (m, l)
-        float* const red_o = reinterpret_cast<float*>(smem + kF4Warps * Cfg::kRing + buf * Cfg::kReduce);   // [warps][RU][D]
+        float* const red_o = reinterpret_cast<float*>(smem + Cfg::kRing + buf * Cfg::kReduce);   // [warps][RU][D]
         float* const red_m = red_o + kF4Warps * RU * D;                                 // [warps][RU], log2 domain
         float* const red_l = red_m + kF4Warps * RU;
 #pragma unroll
@@ -552,7 +597,7 @@ __global__ void __launch_bounds__(kF4Threads, F4Cfg<D, RU>::kCtas) f4_decode_ker
                     for (int i = 0; i < D / 32; ++i)
                         dst[i] = make_float4(o[n][2 * i][e], o[n][2 * i][2 + e], o[n][2 * i + 1][e], o[n][2 * i + 1][2 + e]);
                     if (g == 0) {
-                        red_m[warp * RU + col] = m[n][e] == -INFINITY ? -INFINITY : m[n][e] * c[n][e];
+                        red_m[warp * RU + col] = bar_z[n][e] == -INFINITY ? -INFINITY : -ref[n][e];
                         red_l[warp * RU + col] = l[n][e];
                     }
                 }
@@ -561,9 +606,9 @@ __global__ void __launch_bounds__(kF4Threads, F4Cfg<D, RU>::kCtas) f4_decode_ker
         else if (!timed_out) allow_dependent_launch();   // this block's last piece
         if (__syncthreads_or(timed_out)) {           // (else every warp's partials are written)
             // the copies still in flight land first, as far as a limit allows
-            for (int i = 0; i < ahead; ++i)
-                mbar_wait(bar0 + (slot + i >= NS ? slot + i - NS : slot + i) * 8, phase ^ (slot + i >= NS ? 1u : 0u), p.err);
-            timed_out = 1;
+            for (int i = 0; tid == 0 && i < NS; ++i)
+                for (uint32_t ph = 0; ph < 2; ++ph) mbar_wait(full0 + i * 8, ph, p.err, 10000000ull);
+            timed_out = true;
             break;
         }
         // pieces that are not whole rows go to the workspace: slot b (the run's head), or one behind those (its tail)
@@ -607,14 +652,11 @@ __global__ void __launch_bounds__(kF4Threads, F4Cfg<D, RU>::kCtas) f4_decode_ker
         if constexpr (Cfg::kReds == 1) __syncthreads();
         else buf ^= 1;
         first = false;
+        first_n += cu.n;
         cu = nx;
         if (cu.live) {
             nx = next_piece();
-            it_next = false;
-            if (it_tok >= it_end) {
-                it_settle();
-                copy_ahead();
-            }
+            if (duty <= n - 1 + NS) copy_duty();      // (one that waited for its piece)
         }
     }
     if (timed_out && tid == 0 && p.info) p.info[blockIdx.x] = make_int4(-1, 0, 0, 0);
@@ -697,7 +739,7 @@ static cudaError_t f4_resident(int* sms)
 }
 
 template <typename QT, int D, int RU, bool MQ>
-static cudaError_t run_f4(F4Params p, void* workspace, cudaStream_t s)
+static cudaError_t run_f4(F4Params p, const DecodeArgs& a, void* workspace, size_t workspace_bytes, cudaStream_t s)
 {
     using Cfg = F4Cfg<D, RU>;
     auto kern = f4_decode_kernel<QT, D, RU, MQ>;
@@ -710,11 +752,14 @@ static cudaError_t run_f4(F4Params p, void* workspace, cudaStream_t s)
     int sms = 0;
     cudaError_t e = f4_resident(&sms);
     if (e != cudaSuccess) return e;
-    // (no more blocks than granules that the tables can hold; the workspace counts the same)
-    const int64_t most = f4_granules(p.num_seqs, p.nq, p.group, p.n_kv, p.max_blocks << p.bs_log);
-    const int blocks = static_cast<int>(std::min<int64_t>(most, std::min(sms, kF4Sms) * Cfg::kCtas));
+    // no more blocks than granules that the tables can hold, nor than the workspace has room for
+    const int max_ctx = p.max_blocks << p.bs_log;
+    const int64_t most = f4_granules(p.num_seqs, p.nq, p.group, p.n_kv, max_ctx);
+    int blocks = static_cast<int>(std::min<int64_t>(most, sms * Cfg::kCtas));
+    while (blocks > 1 && f4_workspace_bytes(p.num_seqs, p.nq, p.group, p.n_kv, D, max_ctx, blocks) > workspace_bytes)
+        blocks -= std::max(1, blocks / 64);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    const bool split = (p.max_blocks << p.bs_log) > kGranule;    // (rows of one granule are never shared)
+    const bool split = max_ctx > kGranule;    // (rows of one granule are never shared)
     if (split) {
         p.info = reinterpret_cast<int4*>(ws);
         p.ws_ml = reinterpret_cast<float*>(ws + 16ll * blocks);
@@ -722,6 +767,10 @@ static cudaError_t run_f4(F4Params p, void* workspace, cudaStream_t s)
         p.row_tails = rows <= blocks;
         p.ws_acc = p.ws_ml + (blocks + std::min<int64_t>(rows, blocks)) * RU * 2;
     }
+    CUtensorMap kmap{}, vmap{};
+    const uint64_t tiles = static_cast<uint64_t>(p.num_blocks) * p.n_kv << (p.bs_log - 4);
+    if (encode_byte_rows(&kmap, a.k_cache, Cfg::kTile, tiles) != PA_OK || encode_byte_rows(&vmap, a.v_cache, Cfg::kTile, tiles) != PA_OK)
+        return cudaErrorInvalidValue;
     cudaEvent_t ev0 = nullptr, ev1 = nullptr;
     profile_events(&ev0, &ev1);
     if (ev0) cudaEventRecord(ev0, s);
@@ -735,28 +784,28 @@ static cudaError_t run_f4(F4Params p, void* workspace, cudaStream_t s)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, kern, p);
+    e = cudaLaunchKernelEx(&cfg, kern, kmap, vmap, p);
     if (ev1) cudaEventRecord(ev1, s);
     if (e != cudaSuccess || !split) return e;
     cfg.gridDim = dim3(blocks, std::min(RU, p.group * p.nq));
+    cfg.blockDim = dim3(128);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, f4_merge_kernel<D, RU>, p, blocks);
 }
 
 template <typename QT, int D>
-static cudaError_t run_f4_rows(const F4Params& p, void* ws, cudaStream_t s)
+static cudaError_t run_f4_rows(const F4Params& p, const DecodeArgs& a, void* ws, size_t ws_bytes, cudaStream_t s)
 {
     switch (f4_unit_rows(p.nq * p.group)) {
-        case 4: return p.nq == 1 ? run_f4<QT, D, 4, false>(p, ws, s) : run_f4<QT, D, 4, true>(p, ws, s);
-        case 8: return p.nq == 1 ? run_f4<QT, D, 8, false>(p, ws, s) : run_f4<QT, D, 8, true>(p, ws, s);
-        default: return p.nq == 1 ? run_f4<QT, D, 16, false>(p, ws, s) : run_f4<QT, D, 16, true>(p, ws, s);
+        case 4: return p.nq == 1 ? run_f4<QT, D, 4, false>(p, a, ws, ws_bytes, s) : run_f4<QT, D, 4, true>(p, a, ws, ws_bytes, s);
+        case 8: return p.nq == 1 ? run_f4<QT, D, 8, false>(p, a, ws, ws_bytes, s) : run_f4<QT, D, 8, true>(p, a, ws, ws_bytes, s);
+        default: return p.nq == 1 ? run_f4<QT, D, 16, false>(p, a, ws, ws_bytes, s) : run_f4<QT, D, 16, true>(p, a, ws, ws_bytes, s);
     }
 }
 
-cudaError_t launch_decode_fp4(const DecodeArgs& a, void* workspace, cudaStream_t s)
+cudaError_t launch_decode_fp4(const DecodeArgs& a, void* workspace, size_t workspace_bytes, cudaStream_t s)
 {
     F4Params p{};
-    p.k = static_cast<const uint8_t*>(a.k_cache); p.v = static_cast<const uint8_t*>(a.v_cache);
     p.out = a.out; p.q = a.q; p.block_tables = a.block_tables; p.context_lens = a.context_lens;
     p.err = a.err; p.out_dtype = a.out_dtype;
     p.max_blocks = a.max_blocks; p.num_seqs = a.num_seqs; p.n_q = a.n_q; p.nq = a.q_per_seq;
@@ -766,8 +815,8 @@ cudaError_t launch_decode_fp4(const DecodeArgs& a, void* workspace, cudaStream_t
     const int D = a.cache.head_dim;
     if (D != 64 && D != 128) return cudaErrorInvalidValue;
     if (a.cache.act_dtype == PA_BF16)
-        return D == 64 ? run_f4_rows<__nv_bfloat16, 64>(p, workspace, s) : run_f4_rows<__nv_bfloat16, 128>(p, workspace, s);
-    return D == 64 ? run_f4_rows<__half, 64>(p, workspace, s) : run_f4_rows<__half, 128>(p, workspace, s);
+        return D == 64 ? run_f4_rows<__nv_bfloat16, 64>(p, a, workspace, workspace_bytes, s) : run_f4_rows<__nv_bfloat16, 128>(p, a, workspace, workspace_bytes, s);
+    return D == 64 ? run_f4_rows<__half, 64>(p, a, workspace, workspace_bytes, s) : run_f4_rows<__half, 128>(p, a, workspace, workspace_bytes, s);
 }
 
 }  // namespace pa

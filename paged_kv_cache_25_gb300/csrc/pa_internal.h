@@ -26,6 +26,10 @@ unsigned* device_error_word();
 pa_status encode_pool_map(CUtensorMap* map, const void* base, pa_dtype dt, int row_elems,
                           uint64_t rows, int box_x, int box_y, int swizzle = 128);
 
+// Encodes a tensor map over `rows` rows of row_bytes bytes (a multiple of 16, at most 2048), box of one
+// row, no swizzle: for gathers of rows.
+pa_status encode_byte_rows(CUtensorMap* map, const void* base, int row_bytes, uint64_t rows);
+
 // Profiling events around the decode's attention kernels (may be null).
 void profile_events(cudaEvent_t* start, cudaEvent_t* stop);
 
@@ -116,10 +120,10 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t s);
 cudaError_t launch_decode_scored(const DecodeArgs& a, cudaStream_t s, float scale_log2);
 cudaError_t launch_decode_wide(const DecodeArgs& a, cudaStream_t s, float scale_log2);   // (caps above kNearCap)
 cudaError_t launch_decode_scored_simt(const DecodeArgs& a, cudaStream_t s, float scale_log2);
-// a call on an FP4 pool, its merge included (decode_fp4.cu), and what the workspace of one has to hold: the
-// grid is at most kF4MaxCtas blocks for each of at most kF4Sms SMs, each with the head of its run and, as far
-// as there are so many, the tail, of f4_unit_rows rows
-constexpr int kF4GranuleTokens = 128, kF4MaxCtas = 4, kF4Sms = 152;
+// a call on an FP4 pool, its merge included (decode_fp4.cu), and what its workspace holds: for each of its blocks
+// (at most f4_grid and f4_granules; fewer where there is no room, but room for half of f4_grid is asked
+// for) the head of its run of f4_unit_rows rows and, as far as there are so many such rows, the tail
+constexpr int kF4GranuleTokens = 128, kF4Sms = 152;
 inline int f4_unit_rows(int rows_kv) { return rows_kv <= 4 ? 4 : (rows_kv <= 8 ? 8 : 16); }
 inline int64_t f4_granules(int num_seqs, int nq, int group, int n_kv, int max_ctx)
 {
@@ -127,16 +131,17 @@ inline int64_t f4_granules(int num_seqs, int nq, int group, int n_kv, int max_ct
     return static_cast<int64_t>(num_seqs) * n_kv * ((group * nq + ru - 1) / ru) *
            ((max_ctx + kF4GranuleTokens - 1) / kF4GranuleTokens);
 }
-inline size_t f4_workspace_bytes(int num_seqs, int nq, int group, int n_kv, int D, int max_ctx)
+inline int f4_grid(int rows_kv) { return kF4Sms * (f4_unit_rows(rows_kv) == 16 ? 2 : 4); }   // blocks of the GPU
+inline size_t f4_workspace_bytes(int num_seqs, int nq, int group, int n_kv, int D, int max_ctx, int64_t blocks)
 {
     if (max_ctx <= kF4GranuleTokens) return 0;    // (no shared pieces)
-    const int ru = f4_unit_rows(group * nq), per_sm = ru == 16 ? 2 : (D == 64 ? 4 : 3);
-    const int64_t most = f4_granules(num_seqs, nq, group, n_kv, max_ctx), grid = kF4Sms * per_sm;
-    const int64_t blocks = most < grid ? most : grid;
+    const int ru = f4_unit_rows(group * nq);
+    const int64_t most = f4_granules(num_seqs, nq, group, n_kv, max_ctx);
+    blocks = most < blocks ? most : blocks;
     const int64_t rows = static_cast<int64_t>(num_seqs) * n_kv * ((group * nq + ru - 1) / ru);
     return blocks * 16 + static_cast<size_t>(blocks + (rows < blocks ? rows : blocks)) * ru * (D + 2) * sizeof(float);
 }
-cudaError_t launch_decode_fp4(const DecodeArgs& a, void* workspace, cudaStream_t s);
+cudaError_t launch_decode_fp4(const DecodeArgs& a, void* workspace, size_t workspace_bytes, cudaStream_t s);
 // prefix pass of a shared-prefix call (prefix_pass.cu)
 cudaError_t launch_prefix_pass(const DecodeArgs& a, const PrefixPass& pass, cudaStream_t s);
 // attention kernel of a call with q_per_seq > 1 (decode_verify.cu)

@@ -72,6 +72,14 @@ def test_several_rows(rows, n_q, n_kv, d, bs, act):
     run(ref.Pools(rows + d, lens, n_kv, d, bs), rows, n_q, act, "fp32")
 
 
+@pytest.mark.parametrize("rows,n_q,n_kv,d,bs,act", [(1, 32, 8, 128, 16, "bf16"), (1, 8, 8, 128, 32, "fp16"),
+                                                    (3, 16, 8, 128, 16, "fp16"), (1, 32, 8, 64, 32, "bf16"),
+                                                    (7, 10, 10, 64, 16, "bf16"), (5, 24, 6, 128, 32, "bf16")])
+def test_batches_with_long_runs_of_whole_and_split_rows(rows, n_q, n_kv, d, bs, act):
+    """more work than thread blocks: runs of several rows, begun and ended inside rows, with ragged ends"""
+    run(ref.Pools(rows + d, [20 + (i * 613) % 2900 for i in range(48)], n_kv, d, bs), rows, n_q, act, "fp32")
+
+
 def test_many_sequences_of_all_lengths():
     lens = [1 + (i * 7919) % 260 for i in range(1100)]      # more than the kernel keeps prefix sums for
     run(ref.Pools(9, lens, 1, 64, 16), 1, 4, "bf16", "fp32")
