@@ -650,7 +650,8 @@ static pa_status decode_common(void* out, pa_dtype out_dtype, const void* q, con
     const bool f4 = cache->dtype == PA_FP4_E2M1;
     if (f4) {
         const int group = n_q_heads / cache->n_kv_heads;
-        if (f4_granules(num_seqs, q_per_seq, group, cache->n_kv_heads, max_ctx) >= (1ll << 31))
+        // (the decode's line of work has a unit more a row)
+        if (2 * f4_granules(num_seqs, q_per_seq, group, cache->n_kv_heads, max_ctx) >= (1ll << 31))
             return fail(PA_ERR_UNSUPPORTED, "too many tokens in the tables for one call");
         need = f4_workspace_bytes(num_seqs, q_per_seq, group, cache->n_kv_heads, cache->head_dim, max_ctx,
                                   f4_grid(group * q_per_seq) / 2);

@@ -6,12 +6,12 @@
 //   out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
 //
 // Work: the rows of all (sequence, KV head, up to RU of its (head, query) rows), one after another,
-// are a line of 128-token granules, of which every block of a persistent grid takes an equal
-// run.  A block's run holds whole rows, which it finishes, and at most two pieces of rows that it shares with
-// its neighbours, whose partials meet in f4_merge_kernel.  (Partitions of 1024 tokens dealt by tickets, as
-// the other decode kernels have them, cost a unit's set-up and combine two to three times as often, a third of
-// all instructions of a Llama-3-8B batch: see the figures below.)  A piece's four warps take its 32-token
-// stages in turn and combine through shared memory.
+// are a line of 128-token granules with kRowCost more units before each row for what a piece costs beside its
+// tokens (its queries and its combine take about as long as a granule); every block of a persistent grid takes an
+// equal run of it.  (Without those units, 40 sequences of 100 - 2047 tokens and 40 KV heads took 96 us for 55: blocks
+// with rows of one granule came last.)  A block's run holds whole rows, which it finishes, and at most two pieces of rows
+// that it shares with its neighbours, whose partials meet in f4_merge_kernel.  A piece's four warps take 32 tokens of
+// each stage and combine through shared memory.
 //
 // Stages of 128 tokens (32 a warp) arrive in a ring that the block's warps share, each by four
 // cp.async.bulk.tensor gathers of four 16-token tiles (a tile's rows are contiguous in the pool, so the pool is a
@@ -53,7 +53,8 @@ constexpr int kF4Threads = kF4Warps * 32;
 constexpr int kPieceTok = 16;             // tokens of a tile of scores, and of one copy
 constexpr int kStageTok = 32;             // tokens of a stage that a warp takes: two tiles
 constexpr int kGranule = kF4Warps * kStageTok;   // tokens of a stage, and of a granule
-constexpr int kF4PrefixCap = 768;         // entries of the table of granules before a sequence
+constexpr int kRowCost = 1;               // units of a row beside its granules
+constexpr int kF4PrefixCap = 768;         // entries of the table of units before a sequence
 static_assert(kGranule == kF4GranuleTokens, "as the workspace counts them");
 
 struct F4Params {
@@ -85,13 +86,6 @@ struct F4Cfg {
     static_assert(kCtas * (kDynBytes + 1024 + 3584) <= 233472, "shared memory of an SM");
     static_assert(kNS <= kF4Warps, "a warp copies at most one of the first stages");
 };
-
-__device__ __forceinline__ void f4_store(void* out, int64_t i, float v, pa_dtype dt)
-{
-    if (dt == PA_F32) static_cast<float*>(out)[i] = v;
-    else if (dt == PA_BF16) static_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(v);
-    else static_cast<__half*>(out)[i] = __float2half_rn(v);
-}
 
 __device__ __forceinline__ void f4_store4(void* out, int64_t i, float4 v, pa_dtype dt)
 {
@@ -236,9 +230,10 @@ __global__ void __launch_bounds__(kF4Threads, F4Cfg<D, RU>::kCtas) f4_decode_ker
     }
     grid_dependency_wait();      // launched as a programmatic dependent: every input may come from the kernel before
 
-    // ---- this block's run of granules.  s_table[c]: granules (of one group) of the first c + 1 chunks of
+    // ---- this block's run of units.  s_table[c]: units (of one group) of the first c + 1 chunks of
     // `per` sequences (one a chunk, unless the batch is larger than the table).
     auto granules = [&](int L) { return L < nq || L <= 0 ? 0 : (min(L, max_ctx) + kGranule - 1) / kGranule; };
+    auto units = [&](int L) { const int J = granules(L); return J ? J + kRowCost : 0; };      // of a row
     const int per = (p.num_seqs + kF4PrefixCap - 1) / kF4PrefixCap;
     const int chunks = (p.num_seqs + per - 1) / per;
     {
@@ -249,7 +244,7 @@ __global__ void __launch_bounds__(kF4Threads, F4Cfg<D, RU>::kCtas) f4_decode_ker
             for (int s = c * per; s < min(p.num_seqs, (c + 1) * per); ++s) {
                 const int L = __ldg(p.context_lens + s);
                 if (L > 0 && L < nq) set_error(p.err, PA_ERR_OUT_OF_RANGE);   // fewer keys than query rows
-                local += granules(L);
+                local += units(L);
             }
             s_table[c] = local;
         }
@@ -266,8 +261,8 @@ __global__ void __launch_bounds__(kF4Threads, F4Cfg<D, RU>::kCtas) f4_decode_ker
         for (int c = c0; c < c1; ++c) s_table[c] += run;
         __syncthreads();
     }
-    int left;                                    // granules of the run that are not in a piece yet
-    int at_s, at_gran, at_grp;                   // where the next piece begins
+    int left;                                    // units of the run that are not in a piece yet
+    int at_s, at_unit, at_grp;                   // where the next piece begins
     {
         const int total = s_table[chunks - 1] * n_groups, blocks = gridDim.x;
         const int base = total / blocks, more = total - base * blocks, b = blockIdx.x;
@@ -285,14 +280,14 @@ __global__ void __launch_bounds__(kF4Threads, F4Cfg<D, RU>::kCtas) f4_decode_ker
         }
         int before = lo ? s_table[lo - 1] : 0;
         at_s = lo * per;
-        int J = granules(__ldg(p.context_lens + at_s));
-        while (before + J <= x) {                // (larger batches: on through the chunk)
-            before += J;
-            J = granules(__ldg(p.context_lens + ++at_s));
+        int n = units(__ldg(p.context_lens + at_s));
+        while (before + n <= x) {                // (larger batches: on through the chunk)
+            before += n;
+            n = units(__ldg(p.context_lens + ++at_s));
         }
         const int off = begin - before * n_groups;
-        at_grp = off / J;
-        at_gran = off - at_grp * J;
+        at_grp = off / n;
+        at_unit = off - at_grp * n;
         __syncthreads();
         if (per == 1)
             for (int s = tid; s < p.num_seqs; s += kF4Threads) s_table[s] = __ldg(p.context_lens + s);
@@ -307,31 +302,38 @@ __global__ void __launch_bounds__(kF4Threads, F4Cfg<D, RU>::kCtas) f4_decode_ker
     };
     auto next_piece = [&]() {
         Piece x{};
-        x.live = left > 0;
-        if (!x.live) return x;
-        x.L = len_of(at_s);
-        int J = granules(x.L);
-        if (at_grp == n_groups) {                // on to the next sequence with keys
-            at_grp = 0;
-            do {
-                x.L = len_of(++at_s);
-                J = granules(x.L);
-            } while (J == 0);
+        int J = 0, g0 = 0, g1 = 0;               // the row's granules, and the piece's
+        while (true) {
+            if (left <= 0) return x;             // (not live)
+            if (at_grp == n_groups) {
+                at_grp = 0;
+                ++at_s;
+            }
+            x.L = len_of(at_s);
+            J = granules(x.L);
+            if (J == 0) {                        // a sequence without keys
+                ++at_s;
+                continue;
+            }
+            const int n = min(left, J + kRowCost - at_unit);
+            g0 = max(0, at_unit - kRowCost);
+            g1 = max(0, at_unit + n - kRowCost);
+            left -= n;
+            at_unit = 0;
+            x.grp = at_grp++;
+            if (g1 > g0) break;                  // (else the run ends before the row's first granule)
         }
+        x.live = true;
         x.s = at_s;
-        x.grp = at_grp;
         const int n_sub = n_groups / p.n_kv;
-        x.kvh = n_sub == 1 ? at_grp : at_grp / n_sub;
-        x.r0 = (at_grp - x.kvh * n_sub) * RU;
+        x.kvh = n_sub == 1 ? x.grp : x.grp / n_sub;
+        x.r0 = (x.grp - x.kvh * n_sub) * RU;
         x.nh = min(RU, rows_kv - x.r0);
-        x.t0 = at_gran * kGranule;
         const int end = min(x.L, max_ctx);
-        x.n = min(left, J - at_gran);
-        x.t1 = min(end, (at_gran + x.n) * kGranule);
+        x.n = g1 - g0;
+        x.t0 = g0 * kGranule;
+        x.t1 = min(end, g1 * kGranule);
         x.tail = x.t1 < end;
-        left -= x.n;
-        at_gran = 0;
-        ++at_grp;
         return x;
     };
     const uint32_t ring32 = smem_u32(smem), full0 = smem_u32(s_full), empty0 = smem_u32(s_empty);
@@ -399,6 +401,10 @@ __global__ void __launch_bounds__(kF4Threads, F4Cfg<D, RU>::kCtas) f4_decode_ker
     };
 
     Piece cu = next_piece();
+    if (!cu.live) {                              // uniform over the block
+        if (tid == 0 && p.info) p.info[blockIdx.x] = make_int4(-1, 0, 0, 0);
+        return;
+    }
     const bool head = cu.t0 > 0;                 // the run begins inside a row
     bool first = true;
     load_q(cu);
@@ -662,67 +668,89 @@ __global__ void __launch_bounds__(kF4Threads, F4Cfg<D, RU>::kCtas) f4_decode_ker
     if (timed_out && tid == 0 && p.info) p.info[blockIdx.x] = make_int4(-1, 0, 0, 0);
 }
 
-// Merges the pieces of rows that several blocks shared: block (b, r) row r of the rows that decode block b began
-// and did not finish, whose pieces are b's tail and the heads of the blocks after it, up to the first
-// that does not go on.  Four warps take the pieces in turn.
+// Merges the pieces of rows that several blocks shared: block b takes the rows that decode block b began and did not
+// finish, whose pieces are b's tail and the heads of the blocks after it, up to the first that does not go on.
+// A thread has four neighbouring elements of a row; four slices of threads take the pieces in turn.
+constexpr int kMergeThreads = 512, kMergeSlices = 4;
+
 template <int D, int RU>
-__global__ void __launch_bounds__(128) f4_merge_kernel(const __grid_constant__ F4Params p, int blocks)
+__global__ void __launch_bounds__(kMergeThreads) f4_merge_kernel(const __grid_constant__ F4Params p, int blocks)
 {
-    constexpr int V = D / 32;                 // neighbouring elements of a lane
-    using Vec = std::conditional_t<V == 4, float4, float2>;
-    __shared__ float s_acc[4][D], s_m[4], s_l[4];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = blockIdx.x, r = blockIdx.y;
+    constexpr int kPer = kMergeThreads / kMergeSlices, kRows = kPer / (D / 4);      // rows at a time
+    __shared__ float4 s_acc[kMergeSlices][kPer];
+    __shared__ float s_m[kMergeSlices][kPer], s_l[kMergeSlices][kPer];
+    __shared__ int s_n;
+    const int tid = threadIdx.x, lane = tid & 31, b = blockIdx.x;
     grid_dependency_wait();
     const int row = p.info[b].x;
     if (row < 0) return;
-    const int rows_kv = p.group * p.nq, n_sub = (rows_kv + RU - 1) / RU, n_groups = p.n_kv * n_sub;
-    const int s = row / n_groups, grp = row - s * n_groups, kvh = grp / n_sub, r0 = (grp - kvh * n_sub) * RU;
-    if (r0 + r >= rows_kv) return;
-    int n = 1;                                // pieces after b's
-    for (int i0 = b + 1;; i0 += 32) {
-        const unsigned ends = __ballot_sync(0xffffffffu, i0 + lane >= blocks || p.info[i0 + lane].y == 0);
-        if (ends) {
-            n = i0 - b + __ffs(ends) - 1;
-            break;
+    if (tid < 32) {                           // pieces after b's
+        int n = 0;
+        for (int i0 = b + 1;; i0 += 32) {
+            const unsigned ends = __ballot_sync(0xffffffffu, i0 + lane >= blocks || p.info[i0 + lane].y == 0);
+            if (ends) {
+                n = i0 - b + __ffs(ends) - 1;
+                break;
+            }
         }
-    }
-    n = min(n, blocks - 1 - b);
-    auto slot = [&](int i) {                  // of piece i
-        return (i == 0 ? static_cast<int64_t>(blocks) + (p.row_tails ? row : b) : static_cast<int64_t>(b) + i) * RU + r;
-    };
-    float M = -INFINITY, lsum = 0.f, acc[V] = {};
-    for (int i = warp; i <= n; i += 4) M = fmaxf(M, p.ws_ml[2 * slot(i)]);
-    // (rows of several queries may see no key of a piece, or of all that this warp has)
-    const float ref = M == -INFINITY ? 0.f : M;
-#pragma unroll 4
-    for (int i = warp; i <= n; i += 4) {
-        const int64_t w = slot(i);
-        const float2 ml = *reinterpret_cast<const float2*>(p.ws_ml + 2 * w);
-        const Vec x = *reinterpret_cast<const Vec*>(p.ws_acc + w * D + V * lane);
-        const float f = exp2f(ml.x - ref);
-        lsum = fmaf(f, ml.y, lsum);
-#pragma unroll
-        for (int e = 0; e < V; ++e) acc[e] = fmaf(f, reinterpret_cast<const float*>(&x)[e], acc[e]);
-    }
-#pragma unroll
-    for (int e = 0; e < V; ++e) s_acc[warp][V * lane + e] = acc[e];
-    if (lane == 0) {
-        s_m[warp] = M;
-        s_l[warp] = lsum;
+        if (lane == 0) s_n = min(n, blocks - 1 - b);
     }
     __syncthreads();
-    if (threadIdx.x >= D) return;
-    M = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-    float sum = 0.f, x = 0.f;
+    const int n = s_n;
+    const int rows_kv = p.group * p.nq, n_sub = (rows_kv + RU - 1) / RU, n_groups = p.n_kv * n_sub;
+    const int s = row / n_groups, grp = row - s * n_groups, kvh = grp / n_sub, r0 = (grp - kvh * n_sub) * RU;
+    const int slice = tid / kPer, j = tid % kPer, dd = j % (D / 4) * 4;
+    for (int ra = 0; ra < min(RU, rows_kv - r0); ra += kRows) {
+        const int r = ra + j / (D / 4);
+        const bool mine = r < min(RU, rows_kv - r0);
+        auto slot = [&](int i) {              // of piece i
+            return (i == 0 ? static_cast<int64_t>(blocks) + (p.row_tails ? row : b) : static_cast<int64_t>(b) + i) * RU + r;
+        };
+        float M = -INFINITY, sum = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (mine) {
+            for (int i = slice; i <= n; i += kMergeSlices) M = fmaxf(M, p.ws_ml[2 * slot(i)]);
+            // (rows of several queries may see no key of a piece, or of all that this slice has)
+            const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll 4
+            for (int i = slice; i <= n; i += kMergeSlices) {
+                const int64_t w = slot(i);
+                const float2 ml = *reinterpret_cast<const float2*>(p.ws_ml + 2 * w);
+                const float4 x = *reinterpret_cast<const float4*>(p.ws_acc + w * D + dd);
+                const float f = exp2f(ml.x - ref);
+                sum = fmaf(f, ml.y, sum);
+                acc.x = fmaf(f, x.x, acc.x);
+                acc.y = fmaf(f, x.y, acc.y);
+                acc.z = fmaf(f, x.z, acc.z);
+                acc.w = fmaf(f, x.w, acc.w);
+            }
+        }
+        s_acc[slice][j] = acc;
+        s_m[slice][j] = M;
+        s_l[slice][j] = sum;
+        __syncthreads();
+        if (slice == 0 && mine) {
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        const float f = exp2f(s_m[w] - M);
-        sum = fmaf(f, s_l[w], sum);
-        x = fmaf(f, s_acc[w][threadIdx.x], x);
+            for (int w = 1; w < kMergeSlices; ++w) M = fmaxf(M, s_m[w][j]);
+            sum = 0.f;
+            acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kMergeSlices; ++w) {
+                const float f = exp2f(s_m[w][j] - M);
+                const float4 x = s_acc[w][j];
+                sum = fmaf(f, s_l[w][j], sum);
+                acc.x = fmaf(f, x.x, acc.x);
+                acc.y = fmaf(f, x.y, acc.y);
+                acc.z = fmaf(f, x.z, acc.z);
+                acc.w = fmaf(f, x.w, acc.w);
+            }
+            const int hh = (r0 + r) / p.nq, qi = r0 + r - hh * p.nq;
+            const int64_t at = (static_cast<int64_t>(s) * p.nq + qi) * p.n_q + kvh * p.group + hh;
+            const float inv = p.v_scale / sum;
+            f4_store4(p.out, at * D + dd, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv), p.out_dtype);
+        }
+        __syncthreads();                      // (the next rows' partials)
     }
-    const int hh = (r0 + r) / p.nq, qi = r0 + r - hh * p.nq;
-    const int64_t at = (static_cast<int64_t>(s) * p.nq + qi) * p.n_q + kvh * p.group + hh;
-    f4_store(p.out, at * D + threadIdx.x, x * (p.v_scale / sum), p.out_dtype);
 }
 
 static cudaError_t f4_resident(int* sms)
@@ -787,8 +815,8 @@ static cudaError_t run_f4(F4Params p, const DecodeArgs& a, void* workspace, size
     e = cudaLaunchKernelEx(&cfg, kern, kmap, vmap, p);
     if (ev1) cudaEventRecord(ev1, s);
     if (e != cudaSuccess || !split) return e;
-    cfg.gridDim = dim3(blocks, std::min(RU, p.group * p.nq));
-    cfg.blockDim = dim3(128);
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(kMergeThreads);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, f4_merge_kernel<D, RU>, p, blocks);
 }
