@@ -50,8 +50,8 @@ NCU_TRAFFIC = {
 # chunked prefill of the mixed step (the compact-pool capture runs the same four
 # chunks as the 60 GB pool): bytes per launch
 NCU_PREFILL_TRAFFIC = {
-    ("mixed-llama3-8b-bf16", "f301f689ab0bfad0"): (98494464 + 4046080, "compact pool, one-pass capture"),
-    ("mixed-llama3-8b-fp8", "f301f689ab0bfad0"): (57575168 + 1120256, "compact pool, one-pass capture"),
+    ("mixed-llama3-8b-bf16", "af0fe96ad2d2a2e7"): (98512896 + 3857408, "compact pool, one-pass capture"),
+    ("mixed-llama3-8b-fp8", "af0fe96ad2d2a2e7"): (57574656 + 1172736, "compact pool, one-pass capture"),
 }
 
 

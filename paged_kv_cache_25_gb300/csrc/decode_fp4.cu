@@ -99,16 +99,6 @@ __device__ __forceinline__ void f4_store4(void* out, int64_t i, float4 v, pa_dty
             make_uint2(Cvt<__half>::pack(v.x, v.y), Cvt<__half>::pack(v.z, v.w));
 }
 
-// Four rows of a matrix (box {row, 1}) into consecutive shared memory.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, int r0, int r1, int r2, int r3, uint32_t bar)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(bar)
-        : "memory");
-}
-
 // S^T of one tile: st[n][0, 1] row g, [2, 3] row g + 8; columns 8 n + 2 t4 and the next.
 template <int D, int NT>
 __device__ __forceinline__ void f4_scores(const uint8_t* k, int g, int t4, const uint32_t (&q)[NT][D / 16][2],

@@ -40,8 +40,8 @@
 // that with head_dim 128 and bf16 queries the score MMAs read the K codes
 // themselves (a K-loader warp TMAs them; two converters widen V alone).
 // k_scale is folded into the softmax scale and v_scale into the output.
-// FP4 pools (F4): the same converters widen 4-bit rows, codes times their scales, exactly to fp16;
-// V is stored by rows as K is, so both rings hold [keys][d] as for 16-bit pools.
+// FP4 pools (F4): three converters of their own (prefill_fp4.cuh) widen 4-bit rows, codes times their scales, exactly to
+// fp16; V is stored by rows as K is, so both rings hold [keys][d] as for 16-bit pools.
 // Scored instantiations (MODE, see kPf* below): a row sees the keys between bounds
 // of its own (window, document and prefix masks), the CTA's key tiles start at the
 // one of its first visible key, and scores may be capped or biased (score_mod.cuh).
@@ -158,7 +158,8 @@ struct PfMode {
     static constexpr bool kDirectK = F8 && !F4 && D == 128 && BQ;   // K codes straight into the score MMA
     static constexpr int kConverters = F8 ? (kDirectK ? 2 : 3) : 0;
     static constexpr int kKLoaders = kDirectK ? 1 : 0;   // direct K: a warp TMAs the K codes
-    static constexpr int kDepth = 2;
+    static constexpr int kDepth = F4 ? 1 : 2;
+    static constexpr int kChunkKeys = F4 ? kF4ChunkKeys : kF8ChunkKeys;
 };
 // Warps after the softmax ones: the K and V producers (or the FP8
 // converters, and with direct K the K-code loader), then the MMA issuer.
@@ -186,11 +187,12 @@ struct PfLayout {
     static constexpr uint32_t kKBytes = kTcKeys * D * (kDirectK ? 1 : 2);   // K of one key tile
     static constexpr uint32_t kVBytes = kTcKeys * D * 2;          // V of one key tile (16-bit)
     // FP8, FP4: one staged chunk as it is in the pool
-    static constexpr uint32_t kCodeBytes = kF8ChunkKeys * (F4 ? fp4_row_bytes(D) : D);
+    static constexpr uint32_t kCodeBytes =
+        PfMode<F8, D, BQ, F4>::kChunkKeys * (F4 ? fp4_row_bytes(D) : D);
     static constexpr uint32_t kOffQ = 0;                          // Q_A, Q_B
     static constexpr uint32_t kOffK = kOffQ + kTcTiles * kQBytes; // K ring
     static constexpr uint32_t kOffV = kOffK + kTcStages * kKBytes;   // V ring
-    static constexpr uint32_t kOffCS = kOffV + kTcStages * kVBytes;  // FP8: 2 code buffers per converter
+    static constexpr uint32_t kOffCS = kOffV + kTcStages * kVBytes;  // code buffers of the converters
     static constexpr uint32_t kDynBytes =
         kOffCS + PfMode<F8, D, BQ, F4>::kConverters * PfMode<F8, D, BQ, F4>::kDepth * kCodeBytes + 1024;
     // S_t at t * 128; P_t overwrites it, keys 32c .. 32c+31 as hi in columns
@@ -373,9 +375,9 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             for (int i = 0; i < kTcStages; ++i) {
                 // FP8: one arrival per widened chunk; 16-bit pools and the direct
                 // K codes: the TMA's
-                mbar_init(smem_u32(&k_full[i]), F8 && !kDirectK ? kTcKeys / kF8ChunkKeys : 1);
+                mbar_init(smem_u32(&k_full[i]), F8 && !kDirectK ? kTcKeys / Wp::Mode::kChunkKeys : 1);
                 mbar_init(smem_u32(&k_empty[i]), 1);
-                mbar_init(smem_u32(&v_full[i]), F8 ? kTcKeys / kF8ChunkKeys : 1);
+                mbar_init(smem_u32(&v_full[i]), F8 ? kTcKeys / Wp::Mode::kChunkKeys : 1);
                 mbar_init(smem_u32(&v_empty[i]), 1);
             }
             for (int t = 0; t < kTcTiles; ++t) {
@@ -552,7 +554,15 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     const uint32_t tmem = s_tmem;
 
     static_assert(!F8 || std::is_same<T, __half>::value, "FP8 codes widen to fp16 operands");
-    if (F8 && warp >= kFirstConv && warp < kFirstConv + Wp::Mode::kConverters) {
+    static_assert(!F4 || MODE == 0, "FP4: the plain causal prefill");
+    if (F4 && warp >= kFirstConv && warp < kMmaWarp) {
+        const int pw = warp - kFirstConv;
+        f4_convert<D, BS, kTcKeys, kTcStages>(
+            &kmap, &vmap, block_tables + static_cast<int64_t>(r) * max_blocks, max_blocks, num_blocks, n_kv, kvh, L, n_tiles, pw,
+            lane, smem + Ly::kOffCS + pw * Ly::kCodeBytes, sbase + Ly::kOffCS + pw * Ly::kCodeBytes, sbase + Ly::kOffK,
+            sbase + Ly::kOffV, smem_u32(&code_full[pw][0]), smem_u32(k_full), smem_u32(k_empty), smem_u32(v_full),
+            smem_u32(v_empty), err);
+    } else if (F8 && warp >= kFirstConv && warp < kFirstConv + Wp::Mode::kConverters) {
         // ------------------------------------------------ FP8 converters
         // Chunk g (tile g / kPerTile; K chunks first, then V) is widened by
         // converter g % kNc into its ring stage, which then gets
@@ -605,12 +615,6 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                         b = 0;
                     }
                     const int64_t bh = static_cast<int64_t>(b) * n_kv + kvh;
-                    if constexpr (F4) {     // 16 rows
-                        constexpr int kBytes = 16 * fp4_row_bytes(D);
-                        bulk_load(buf + x * kBytes, (k_chunk ? k_codes : v_codes) + (bh * (BS / 16) + key0 % BS / 16) * kBytes,
-                                  kBytes, bar);
-                        continue;
-                    }
                     // 16 rows of D codes (K), or the D x 16 transposed piece
                     // (V): 16 * D contiguous bytes of the pool either way
                     const uint8_t* src =
@@ -652,9 +656,6 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             // the staging reads and in the ring writes.
             constexpr int kPer = kCK * D / 512;
             const uint8_t* src = stage_ptr + (n % kDepth) * Ly::kCodeBytes;
-            if constexpr (F4) {
-                f4_widen_chunk<D, kCK, kTcKeys>(src, dst, lane, e * kCK, keep_tile);
-            } else {
             uint4 c[kPer];
             int row[kPer], chunk0[kPer];
 #pragma unroll
@@ -714,7 +715,6 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                                           rw * 128 + (((ch & 7) ^ (rw & 7)) << 4);
                     st_shared_v4(addr, w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]);
                 }
-            }
             }
             fence_proxy_async_smem();   // ring writes -> the MMAs' reads
             __syncwarp();               // and every lane has read the staging buffer
@@ -1511,7 +1511,12 @@ cudaError_t run_prefill_tc(const PrefillArgs& a, cudaStream_t s, float sl2)
     });
     if (attr_err != cudaSuccess) return attr_err;
     CUtensorMap kmap{}, vmap{};
-    if constexpr (!F4) {      // (FP4: bulk copies only)
+    if constexpr (F4) {       // a row of the matrix: 16 rows of a pool
+        const uint64_t rows = static_cast<uint64_t>(a.cache.num_blocks) * a.cache.n_kv_heads * (BS / 16);
+        for (int v = 0; v < 2; ++v)
+            if (encode_byte_rows(v ? &vmap : &kmap, v ? a.v_cache : a.k_cache, 16 * fp4_row_bytes(D), rows) != PA_OK)
+                return cudaErrorInvalidValue;
+    } else {
         const cudaError_t map_err = prefill_maps<T, D, BS, F8, kBq>(a.cache, a.k_cache, a.v_cache, &kmap, &vmap);
         if (map_err != cudaSuccess) return map_err;
     }
