@@ -33,9 +33,17 @@ __device__ __forceinline__ float e4m3_to_float(uint32_t byte)
 // Sixteen elements as codes (8 bytes, first element lowest) and their scale's code.
 // scale: S; six: 6 S in fp32.  Every step is rounded to fp32 by itself (IEEE division), so the bytes
 // do not depend on how the compiler contracts: s = e4m3(max|x| / (6 S)) kept in [2^-9, 448],
-// codes e2m1(x / (s S)), to nearest even, saturated at 6.  (Division, not a product with a
-// reciprocal: 16-bit inputs often lie exactly between two codes.)  A NaN among the
+// codes e2m1(x / (s S)), to nearest even, saturated at 6.  (Quotients rounded as IEEE division rounds them, not
+// products with a reciprocal: 16-bit inputs often lie exactly between two codes.)  A NaN among the
 // sixteen becomes the scale's NaN, so that all of them read as NaN; infinities saturate.
+//
+// The sixteen quotients x / r share their divisor, so they are made by Markstein's method (Computation of elementary
+// functions on the IBM RISC System/6000 processor, 1990) from y = 1 / r rounded to nearest: with y' = y (1 - r y), the
+// rest of 1 / r, q = x y + x y' is one of the two fp32 neighbours of x / r, its remainder x - q r is
+// exact, and q + (x - q r) y rounds to the quotient.  That holds while nothing over- or underflows, which
+// r in [2^-60, 2^60] and |x| <= 8 r make sure of (a remainder too small to be exact comes with a
+// quotient that is far below the first border, 1/4); a group outside of that divides.  The sign is x's own (-0 keeps
+// its code).  The rotary write of 8192 tokens of Llama-3-8B's heads: 63.5 -> 61.4 us.
 __device__ __forceinline__ uint2 fp4_quantise(const float (&x)[kFp4Group], float scale, float six, uint32_t& code)
 {
     float a = 0.f;
@@ -48,14 +56,26 @@ __device__ __forceinline__ uint2 fp4_quantise(const float (&x)[kFp4Group], float
     const float t = fminf(fmaxf(__fdiv_rn(a, six), 0x1p-9f), 448.f);
     code = __nv_cvt_float_to_fp8(t, __NV_SATFINITE, __NV_E4M3);
     const float r = __fmul_rn(e4m3_to_float(code), scale);
+    float q[kFp4Group];
+    if (r >= 0x1p-60f && r <= 0x1p60f && a <= 8.f * r) {
+        const float y = __frcp_rn(r), rest = __fmul_rn(y, __fmaf_rn(-r, y, 1.f));
+#pragma unroll
+        for (int i = 0; i < kFp4Group; ++i) {
+            const float n = __fmaf_rn(x[i], y, __fmul_rn(x[i], rest));
+            q[i] = copysignf(__fmaf_rn(__fmaf_rn(-n, r, x[i]), y, n), x[i]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kFp4Group; ++i) q[i] = __fdiv_rn(x[i], r);
+    }
     uint32_t w[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         w[h] = 0u;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float lo = __fdiv_rn(x[8 * h + 2 * i], r), hi = __fdiv_rn(x[8 * h + 2 * i + 1], r);
-            w[h] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(make_float2(lo, hi), __NV_E2M1, cudaRoundNearest))
+            w[h] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(make_float2(q[8 * h + 2 * i], q[8 * h + 2 * i + 1]),
+                                                                   __NV_E2M1, cudaRoundNearest))
                     << (8 * i);
         }
     }

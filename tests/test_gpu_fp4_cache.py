@@ -71,6 +71,32 @@ def test_rows_are_written_bit_for_bit(T, n_kv, d, bs, dtype, kind):
         assert np.array_equal(got.cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("scale", [1.0, 0.0371, 1 / 3, 7.7e-5, 3.3e8, 2.0 ** -55, 2.0 ** 52, 2.0 ** 54 * 1.3, 1.1e-17, 1e-25])
+def test_borders_between_codes(scale):
+    """elements that are a few units in the last place beside the quotients' borders, in both forms of the division
+    (the divisors lie on both sides of 2^-60 and 2^60), and groups that saturate"""
+    rng = np.random.default_rng(int(abs(np.log2(scale)) * 8))
+    T, n_kv, d, bs = 500, 8, 128, 16
+    s = rng.choice(ref.E4M3[1:127], (T, n_kv, d // 16, 1))
+    r = (s.astype(np.float32) * np.float32(scale)).astype(np.float32)
+    border = rng.choice([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 0.5, 3.0], (T, n_kv, d // 16, 16))
+    with np.errstate(all="ignore"):
+        x = (r.astype(np.float64) * border * rng.choice([-1, 1], border.shape)).astype(np.float32)
+        ulps = rng.integers(-3, 4, x.shape).astype(np.int32)
+        x = (x.view(np.int32) + np.where(np.abs(x) > 1e-37, ulps, 0)).view(np.float32)
+        x[..., 7] = (r[..., 0].astype(np.float64) * 6).astype(np.float32)          # the group's largest, which makes its scale
+        x[::7, :, :, 3] *= np.float32(300)                                           # (and some that are far larger)
+        x[::5, :, :, 2] = -0.0
+    x = torch.from_numpy(np.ascontiguousarray(x.reshape(T, n_kv, d)))
+    slots = np.arange(T)
+    kc, vc = (torch.zeros(T // bs + 1, n_kv, bs, 9 * d // 16, dtype=torch.uint8, device="cuda") for _ in range(2))
+    pa.pa_reshape_and_cache_quant(x.cuda(), (-x).cuda(), kc, vc, torch.from_numpy(slots).cuda(), scale, scale)
+    torch.cuda.synchronize()
+    assert pa.pa_get_device_error() == 0
+    for got, y in ((kc, x), (vc, -x)):
+        assert np.array_equal(got.cpu().numpy()[slots // bs, :, slots % bs], bytes_of(y, scale))
+
+
 @pytest.mark.parametrize("scale", [1e-30, 2.0 ** -40, 1e30])
 def test_extreme_scales(scale):
     x = torch.randn(40, 2, 64, generator=torch.Generator().manual_seed(1)) * torch.tensor(
