@@ -159,7 +159,7 @@ struct PfMode {
     static constexpr int kConverters = F8 ? (kDirectK ? 2 : 3) : 0;
     static constexpr int kKLoaders = kDirectK ? 1 : 0;   // direct K: a warp TMAs the K codes
     static constexpr int kDepth = F4 ? 1 : 2;
-    static constexpr int kChunkKeys = F4 ? kF4ChunkKeys : kF8ChunkKeys;
+    static constexpr int kChunkKeys = F4 ? kF4ChunkKeys<D> : kF8ChunkKeys;
 };
 // Warps after the softmax ones: the K and V producers (or the FP8
 // converters, and with direct K the K-code loader), then the MMA issuer.
@@ -431,7 +431,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         }
         __syncthreads();   // the members are listed, and the scratch is free
     }
-    if constexpr (MODE != 0 && !kShared) grid_dependency_wait();   // (launched as a programmatic dependent)
+    if constexpr ((MODE != 0 || F4) && !kShared) grid_dependency_wait();   // (launched as a programmatic dependent)
     auto unit = [&]() -> PrefixUnit {
         if constexpr (kShared) return s_unit;
         else return PrefixUnit{};
@@ -554,11 +554,11 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     const uint32_t tmem = s_tmem;
 
     static_assert(!F8 || std::is_same<T, __half>::value, "FP8 codes widen to fp16 operands");
-    static_assert(!F4 || MODE == 0, "FP4: the plain causal prefill");
+    static_assert(!F4 || (MODE & ~(kPfScored | kPfSplit)) == 0, "FP4: the plain causal prefill, split or not");
     if (F4 && warp >= kFirstConv && warp < kMmaWarp) {
         const int pw = warp - kFirstConv;
         f4_convert<D, BS, kTcKeys, kTcStages>(
-            &kmap, &vmap, block_tables + static_cast<int64_t>(r) * max_blocks, max_blocks, num_blocks, n_kv, kvh, L, n_tiles, pw,
+            &kmap, &vmap, block_tables + static_cast<int64_t>(r) * max_blocks, max_blocks, num_blocks, n_kv, kvh, L, tile0, n_tiles, pw,
             lane, smem + Ly::kOffCS + pw * Ly::kCodeBytes, sbase + Ly::kOffCS + pw * Ly::kCodeBytes, sbase + Ly::kOffK,
             sbase + Ly::kOffV, smem_u32(&code_full[pw][0]), smem_u32(k_full), smem_u32(k_empty), smem_u32(v_full),
             smem_u32(v_empty), err);
@@ -961,7 +961,20 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             const uint4* qp = reinterpret_cast<const uint4*>(
                 q + (static_cast<int64_t>(q_row) * n_q + head) * D);
             const uint32_t qbase = sbase + Ly::kOffQ + t * Ly::kQBytes;
-            if constexpr (kDirectK) {
+            if constexpr (F4) {
+                // (the slot of key tile 1's maxima: the pair meets at tile 0 before either writes it again)
+                f4_stage_queries<QT, D, kTcRows>(
+                    [&](int i) -> const QT* {
+                        const int g = row0 + t * kTcRows + i, pos = g / group;
+                        if (g >= rows_total) return nullptr;
+                        return q + (static_cast<int64_t>(qs + pos) * n_q + kvh * group + g - pos * group) * D;
+                    },
+                    qbase, quarter * 32 + hf * 16, lane, qsign, xmax[1][t][0]);
+                if constexpr (kBq) {
+                    named_bar_sync(bar_id, 64);
+                    scale_log2 *= xmax[1][t][0][rr];
+                }
+            } else if constexpr (kDirectK) {
                 // bf16 q -> two E4M3 parts: the row is scaled by 2^-e so that its
                 // largest magnitude lands in [128, 256), hi = e4m3(x) and lo =
                 // e4m3(x - hi) (exact for every element down to 2^-10 of the
@@ -1369,8 +1382,39 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                         *reinterpret_cast<float2*>(sp.ml + 2 * slot) =
                             make_float2(lsum > 0.f ? m_raw * unit_log2 : -INFINITY, lsum);
                 }
+                if constexpr (F4 && !kSplit) {
+                    if (out_dtype != PA_F32) {
+                        // through this tile's query rows, which no MMA reads any more
+                        uint4 w[D / 16];
+#pragma unroll
+                        for (int c0 = 0; c0 < D / 2; c0 += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(lane_addr + o_col + c0, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int i = 0; i < 32; i += 8) {
+                                uint32_t h[4];
+#pragma unroll
+                                for (int x = 0; x < 4; ++x) {
+                                    const float a = __uint_as_float(o[i + 2 * x]) * inv, b = __uint_as_float(o[i + 2 * x + 1]) * inv;
+                                    h[x] = out_dtype == PA_BF16 ? Cvt<__nv_bfloat16>::pack(a, b) : Cvt<__half>::pack(a, b);
+                                }
+                                w[(c0 + i) / 8] = make_uint4(h[0], h[1], h[2], h[3]);
+                            }
+                        }
+                        f4_store_rows<D>(
+                            [&](int i) -> uint16_t* {
+                                const int g = row0 + t * kTcRows + quarter * 32 + i, pos = g / group;
+                                if (g >= rows_total) return nullptr;
+                                return static_cast<uint16_t*>(out) +
+                                       (static_cast<int64_t>(qs + pos) * n_q + kvh * group + g - pos * group) * D + hf * (D / 2);
+                            },
+                            sbase + Ly::kOffQ + t * Ly::kQBytes + (hf * 4 + quarter) * 32 * D, lane, w);
+                    }
+                }
 #pragma unroll
                 for (int c0 = 0; c0 < D / 2; c0 += 32) {
+                    if (F4 && !kSplit && out_dtype != PA_F32) break;      // (stored above)
                     uint32_t o[32];
                     tmem_ld32(lane_addr + o_col + c0, o);
                     tmem_ld_wait();
@@ -1530,7 +1574,7 @@ cudaError_t run_prefill_tc(const PrefillArgs& a, cudaStream_t s, float sl2)
     cfg.blockDim = dim3(PfWarps<F8, D, kBq, F4>::kThreads);
     cfg.dynamicSmemBytes = Ly::kDynBytes;
     cfg.stream = s;
-    // (a scored call is a programmatic dependent: its blocks are scheduled while the kernel
+    // (a scored call, and one over FP4 pools, is a programmatic dependent: its blocks are scheduled while the kernel
     // before drains, and wait for it before they read anything)
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1540,7 +1584,7 @@ cudaError_t run_prefill_tc(const PrefillArgs& a, cudaStream_t s, float sl2)
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = MODE == 0 ? 0 : ((MODE & kPfSplit) != 0 ? 2 : 1);
+    cfg.numAttrs = MODE == 0 ? (F4 ? 1 : 0) : ((MODE & kPfSplit) != 0 ? 2 : 1);
     return cudaLaunchKernelEx(
         &cfg, kern, kmap, vmap, static_cast<const uint8_t*>(a.k_cache), static_cast<const uint8_t*>(a.v_cache),
         a.out, a.out_dtype, static_cast<const QT*>(a.q), a.block_tables, a.max_blocks,
