@@ -54,7 +54,7 @@ constexpr int kPieceTok = 16;             // tokens of a tile of scores, and of 
 constexpr int kStageTok = 32;             // tokens of a stage that a warp takes: two tiles
 constexpr int kGranule = kF4Warps * kStageTok;   // tokens of a stage, and of a granule
 constexpr int kRowCost = 1;               // units of a row beside its granules
-constexpr int kF4PrefixCap = 768;         // entries of the table of units before a sequence
+constexpr int kF4PrefixCap = 768;         // sequences whose lengths are kept in shared memory
 static_assert(kGranule == kF4GranuleTokens, "as the workspace counts them");
 
 struct F4Params {
@@ -198,8 +198,8 @@ __global__ void __launch_bounds__(kF4Threads, F4Cfg<D, RU>::kCtas) f4_decode_ker
     constexpr int NT = RU == 16 ? 2 : 1, NS = Cfg::kNS, kTiles = kStageTok / kPieceTok;   // kTiles: a warp's of a stage
     constexpr bool kBf16 = std::is_same<QT, __nv_bfloat16>::value;
 
-    __shared__ int s_table[kF4PrefixCap];        // granules up to a sequence, then the sequences' lengths
-    __shared__ int s_scan[kF4Warps];
+    __shared__ int s_table[kF4PrefixCap];        // the sequences' lengths
+    __shared__ int s_scan[kF4Warps], s_begin[3];
     __shared__ __align__(8) uint64_t s_full[NS], s_empty[NS];
     extern __shared__ uint8_t dyn_smem[];
     uint8_t* const smem = dyn_smem + (-smem_u32(dyn_smem) & 127u);     // (an offset, so that it stays a shared address)
@@ -220,23 +220,21 @@ __global__ void __launch_bounds__(kF4Threads, F4Cfg<D, RU>::kCtas) f4_decode_ker
     }
     grid_dependency_wait();      // launched as a programmatic dependent: every input may come from the kernel before
 
-    // ---- this block's run of units.  s_table[c]: units (of one group) of the first c + 1 chunks of
-    // `per` sequences (one a chunk, unless the batch is larger than the table).
+    // ---- this block's run of units.  A thread takes `mine` neighbouring sequences, and the one in whose rows the run begins finds the place.
     auto granules = [&](int L) { return L < nq || L <= 0 ? 0 : (min(L, max_ctx) + kGranule - 1) / kGranule; };
     auto units = [&](int L) { const int J = granules(L); return J ? J + kRowCost : 0; };      // of a row
-    const int per = (p.num_seqs + kF4PrefixCap - 1) / kF4PrefixCap;
-    const int chunks = (p.num_seqs + per - 1) / per;
+    const bool tabled = p.num_seqs <= kF4PrefixCap;
+    int left;                                    // units of the run that are not in a piece yet
+    int at_s, at_unit, at_grp;                   // where the next piece begins
     {
-        const int mine = (chunks + kF4Threads - 1) / kF4Threads;
-        const int c0 = tid * mine, c1 = min(chunks, c0 + mine);
+        const int mine = (p.num_seqs + kF4Threads - 1) / kF4Threads;
+        const int s0 = min(p.num_seqs, tid * mine), s1 = min(p.num_seqs, s0 + mine);
         int local = 0;
-        for (int c = c0; c < c1; ++c) {
-            for (int s = c * per; s < min(p.num_seqs, (c + 1) * per); ++s) {
-                const int L = __ldg(p.context_lens + s);
-                if (L > 0 && L < nq) set_error(p.err, PA_ERR_OUT_OF_RANGE);   // fewer keys than query rows
-                local += units(L);
-            }
-            s_table[c] = local;
+        for (int s = s0; s < s1; ++s) {
+            const int L = __ldg(p.context_lens + s);
+            if (L > 0 && L < nq) set_error(p.err, PA_ERR_OUT_OF_RANGE);   // fewer keys than query rows
+            if (tabled) s_table[s] = L;
+            local += units(L);
         }
         int run = local;
 #pragma unroll
@@ -247,14 +245,13 @@ __global__ void __launch_bounds__(kF4Threads, F4Cfg<D, RU>::kCtas) f4_decode_ker
         if (lane == 31) s_scan[warp] = run;
         __syncthreads();
         run -= local;
-        for (int i = 0; i < warp; ++i) run += s_scan[i];
-        for (int c = c0; c < c1; ++c) s_table[c] += run;
-        __syncthreads();
-    }
-    int left;                                    // units of the run that are not in a piece yet
-    int at_s, at_unit, at_grp;                   // where the next piece begins
-    {
-        const int total = s_table[chunks - 1] * n_groups, blocks = gridDim.x;
+        int sum = 0;
+#pragma unroll
+        for (int i = 0; i < kF4Warps; ++i) {
+            if (i < warp) run += s_scan[i];
+            sum += s_scan[i];
+        }
+        const int total = sum * n_groups, blocks = gridDim.x;
         const int base = total / blocks, more = total - base * blocks, b = blockIdx.x;
         const int begin = b * base + min(b, more);
         left = base + (b < more ? 1 : 0);
@@ -263,27 +260,23 @@ __global__ void __launch_bounds__(kF4Threads, F4Cfg<D, RU>::kCtas) f4_decode_ker
             return;
         }
         const int x = begin / n_groups;
-        int lo = 0, hi = chunks - 1;             // the first chunk that ends past x
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (s_table[mid] > x) hi = mid; else lo = mid + 1;
+        if (run <= x && x < run + local) {       // one thread
+            int s = s0, n = units(__ldg(p.context_lens + s));
+            while (run + n <= x) {
+                run += n;
+                n = units(__ldg(p.context_lens + ++s));
+            }
+            const int off = begin - run * n_groups, grp = off / n;
+            s_begin[0] = s;
+            s_begin[1] = grp;
+            s_begin[2] = off - grp * n;
         }
-        int before = lo ? s_table[lo - 1] : 0;
-        at_s = lo * per;
-        int n = units(__ldg(p.context_lens + at_s));
-        while (before + n <= x) {                // (larger batches: on through the chunk)
-            before += n;
-            n = units(__ldg(p.context_lens + ++at_s));
-        }
-        const int off = begin - before * n_groups;
-        at_grp = off / n;
-        at_unit = off - at_grp * n;
         __syncthreads();
-        if (per == 1)
-            for (int s = tid; s < p.num_seqs; s += kF4Threads) s_table[s] = __ldg(p.context_lens + s);
-        __syncthreads();
+        at_s = s_begin[0];
+        at_grp = s_begin[1];
+        at_unit = s_begin[2];
     }
-    auto len_of = [&](int s) { return per == 1 ? s_table[s] : __ldg(p.context_lens + s); };
+    auto len_of = [&](int s) { return tabled ? s_table[s] : __ldg(p.context_lens + s); };
 
     // A piece: tokens [t0, t1) of the rows r0 .. r0 + nh - 1 of a KV head of sequence s, in n stages.
     struct Piece {
@@ -397,8 +390,7 @@ __global__ void __launch_bounds__(kF4Threads, F4Cfg<D, RU>::kCtas) f4_decode_ker
     }
     const bool head = cu.t0 > 0;                 // the run begins inside a row
     bool first = true;
-    load_q(cu);
-    Piece nx = next_piece();
+    Piece nx{};
 
     // ---- the block's stages, numbered on through its pieces.  The first NS are copied by warps 0 .. NS - 1; then,
     // as the warps begin on stage n, warp n % 4 copies stage n - 1 + NS into the slot of the stage before, which all
@@ -461,6 +453,9 @@ __global__ void __launch_bounds__(kF4Threads, F4Cfg<D, RU>::kCtas) f4_decode_ker
         load_ids();                              // (in flight until the duty comes)
     };
     static_assert(Cfg::kTiles == 8, "two gathers of four tiles");
+    if (duty < NS) load_ids();                   // (in flight over the queries' loads)
+    load_q(cu);
+    nx = next_piece();
     if (duty < NS) copy_duty();
     int n = 0, slot = 0;                         // the next stage, its slot and the slot's phase
     uint32_t phase = 0;
