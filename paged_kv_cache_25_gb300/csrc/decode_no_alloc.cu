@@ -55,6 +55,8 @@ extern "C" pa_status pa_decode_no_alloc(void* out, pa_dtype out_dtype, const voi
                                         void* stream)
 {
     if (!cache) return pa::fail(PA_ERR_INVALID_ARG, "cache descriptor is NULL");
+    if (cache->dtype == PA_FP4_E2M1)
+        return pa::fail(PA_ERR_UNSUPPORTED, "pa_decode_no_alloc takes no FP4 pools (pa_decode does)");
     if (num_seqs > 0 && max_blocks_per_seq > 0 && block_size > 0) {
         const int64_t max_ctx = static_cast<int64_t>(max_blocks_per_seq) * block_size;
         if (max_ctx <= (1 << 30)) {

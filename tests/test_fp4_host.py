@@ -115,6 +115,7 @@ def test_calls_that_do_not_take_4_bit_pools():
     lib, d = pa.lib(), C.byref(desc())
     mod = C.byref(pa._ScoreMod(0.0, None, 0, None, None))
     assert lib.pa_reshape_and_cache(0x1000, 0x2000, 0x3000, 0x4000, 0x5000, 3, d, None) == UNSUPPORTED
+    assert lib.pa_decode_no_alloc(0x1000, 2, 0x2000, 0x3000, 0x4000, d, 0x5000, 8, 0x6000, 2, 32, 0.1, 16, None) == UNSUPPORTED
     assert lib.pa_decode_scored(0x1000, 2, 0x2000, 0x3000, 0x4000, d, 0x5000, 8, 0x6000, 2, 1, 32, 0.1, 16, mod, 0x10000,
                                 1 << 30, None) == UNSUPPORTED
     assert lib.pa_decode_shared(0x1000, 2, 0x2000, 0x3000, 0x4000, d, 0x5000, 8, 0x6000, 2, 32, 0.1, 16, 0x7000, 0x8000, 1,
