@@ -230,7 +230,7 @@ static size_t any_pool_ws_bytes(int B, int nq, int n_q, int n_kv, int D, int BS,
     if (D != 64 && D != 128) return n;
     // (FP4 pools: room for the whole grid, unless there is room for three quarters of it anyway)
     auto f4 = [&](int blocks) { return f4_workspace_bytes(B, nq, n_q / n_kv, n_kv, D, max_ctx, blocks); };
-    const int grid = f4_grid(n_q / n_kv * nq);
+    const int grid = f4_grid(n_q / n_kv * nq, D);
     return n >= f4(grid / 4 * 3) ? n : std::max(n, f4(grid));
 }
 
@@ -654,7 +654,7 @@ static pa_status decode_common(void* out, pa_dtype out_dtype, const void* q, con
         if (2 * f4_granules(num_seqs, q_per_seq, group, cache->n_kv_heads, max_ctx) >= (1ll << 31))
             return fail(PA_ERR_UNSUPPORTED, "too many tokens in the tables for one call");
         need = f4_workspace_bytes(num_seqs, q_per_seq, group, cache->n_kv_heads, cache->head_dim, max_ctx,
-                                  f4_grid(group * q_per_seq) / 2);
+                                  f4_grid(group * q_per_seq, cache->head_dim) / 2);
         need = std::max(need, kControlBytes);
     }
     if (parts > 65535) return fail(PA_ERR_UNSUPPORTED, "too many partitions per sequence");

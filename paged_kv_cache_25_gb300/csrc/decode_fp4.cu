@@ -1,5 +1,5 @@
 // Decode attention over FP4 pools, one query row a sequence or several (pa_decode,
-// pa_decode_verify).
+// pa_decode_verify), up to 32 rows a KV head; calls of more go to the chunked prefill's kernel.
 //
 // Mathematics: out = softmax(scale q K^T) V over each sequence's keys, in one pass with a
 // running maximum m and sum l per row; the partials (m, l, O) of key ranges merge exactly,
@@ -77,8 +77,10 @@ struct F4Cfg {
     static constexpr int kTile = kPieceTok * kRow;                          // bytes of a 16-token tile of K or V
     static constexpr int kTiles = kGranule / kPieceTok;                     // tiles of K, and of V, a stage
     static constexpr int kStage = 2 * kTiles * kTile;                       // K tiles, then V tiles
-    static constexpr int kCtas = RU == 16 ? 2 : 4;
-    static constexpr int kNS = RU == 16 || D == 64 ? 4 : 2;
+    // (16 rows, two tiles of accumulators: with three blocks an SM 256 sequences of 16 rows of 64 elements took 145 us for
+    // 176, of 128 elements, whose accumulators spilled, 254 for 240)
+    static constexpr int kCtas = RU == 16 ? (D == 64 ? 3 : 2) : 4;
+    static constexpr int kNS = RU == 16 ? (D == 64 ? 3 : 4) : (D == 64 ? 4 : 2);
     static constexpr int kRing = kNS * kStage;
     static constexpr int kReduce = kF4Warps * RU * (D + 2) * 4;
     static constexpr int kReds = RU == 4 ? 2 : 1;      // combine buffers: two save a barrier a piece
@@ -816,8 +818,28 @@ static cudaError_t run_f4_rows(const F4Params& p, const DecodeArgs& a, void* ws,
     }
 }
 
+// Rows of a KV head past which the chunked prefill's kernel takes the call, its sequences as chunks of
+// q_per_seq rows: one pass over the keys, on tcgen05, for up to 128 rows a tile, where the kernel above reads and widens them
+// again for every 16.  64 sequences of 512 - 4096 tokens of 8 KV heads of 128 elements: 137 us for any
+// number of rows up to 128, against 145 with 32 rows, 199 with 48, 260 with 64, 485 with 128 (two of 60,000 tokens
+// on one KV head each are better off there, whose line of work fills the GPU: 94 us with 64 rows against 109).
+constexpr int kF4DecodeRows = 32;
+
 cudaError_t launch_decode_fp4(const DecodeArgs& a, void* workspace, size_t workspace_bytes, cudaStream_t s)
 {
+    if (a.n_q / a.cache.n_kv_heads * a.q_per_seq > kF4DecodeRows) {
+        PrefillArgs c{};
+        c.out = a.out; c.out_dtype = a.out_dtype; c.q = a.q;
+        c.k_cache = a.k_cache; c.v_cache = a.v_cache; c.cache = a.cache;
+        c.block_tables = a.block_tables; c.max_blocks = a.max_blocks; c.context_lens = a.context_lens;
+        c.num_reqs = a.num_seqs; c.max_q = a.q_per_seq; c.n_q = a.n_q; c.scale = a.scale; c.err = a.err;
+        cudaEvent_t ev0 = nullptr, ev1 = nullptr;
+        profile_events(&ev0, &ev1);
+        if (ev0) cudaEventRecord(ev0, s);
+        const cudaError_t e = launch_prefill_fp4(c, s);
+        if (ev1) cudaEventRecord(ev1, s);
+        return e;
+    }
     F4Params p{};
     p.out = a.out; p.q = a.q; p.block_tables = a.block_tables; p.context_lens = a.context_lens;
     p.err = a.err; p.out_dtype = a.out_dtype;

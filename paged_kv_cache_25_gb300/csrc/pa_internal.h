@@ -131,7 +131,10 @@ inline int64_t f4_granules(int num_seqs, int nq, int group, int n_kv, int max_ct
     return static_cast<int64_t>(num_seqs) * n_kv * ((group * nq + ru - 1) / ru) *
            ((max_ctx + kF4GranuleTokens - 1) / kF4GranuleTokens);
 }
-inline int f4_grid(int rows_kv) { return kF4Sms * (f4_unit_rows(rows_kv) == 16 ? 2 : 4); }   // blocks of the GPU
+inline int f4_grid(int rows_kv, int D)      // blocks of the GPU
+{
+    return kF4Sms * (f4_unit_rows(rows_kv) == 16 ? (D == 64 ? 3 : 2) : 4);
+}
 inline size_t f4_workspace_bytes(int num_seqs, int nq, int group, int n_kv, int D, int max_ctx, int64_t blocks)
 {
     if (max_ctx <= kF4GranuleTokens) return 0;    // (no shared pieces)

@@ -438,12 +438,14 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     };
     if constexpr (kShared) r = unit().first_seq;
     int qs = 0, C = 0, L = 0;   // the request's first row, rows and context
+    // (FP4: without q_start every request has max_q rows, as a decode of several)
+    auto start_of = [&](int i) -> int { return F4 && !q_start ? i * max_q : __ldg(q_start + i); };
     if (!kShared && gridDim.z > 1 && gridDim.z <= kRankedReqs) {
         __shared__ int s_req[4];
         const int R = gridDim.z, i = threadIdx.x;
         if (i < R) {
             // (the request's other numbers are loaded beside the lengths, not after the rank)
-            const int Li = __ldg(context_lens + i), qi = __ldg(q_start + i), qe = __ldg(q_start + i + 1);
+            const int Li = __ldg(context_lens + i), qi = start_of(i), qe = start_of(i + 1);
             int rank = 0;
             for (int k = 0; k < R; ++k) {
                 const int Lk = __ldg(context_lens + k);
@@ -462,10 +464,11 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         C = s_req[2];
         L = s_req[3];
     } else if constexpr (!kShared) {
-        qs = __ldg(q_start + r);
-        C = __ldg(q_start + r + 1) - qs;
+        qs = start_of(r);
+        C = start_of(r + 1) - qs;
         L = __ldg(context_lens + r);
     }
+    if (F4 && !q_start && L <= 0) return;      // (a decode's sequence without keys)
     if constexpr (kShared) L = unit().prefix;
     // kSplit: the blocks of a cluster take a range of the key tiles each and merge their (max,
     // sum, O) through distributed shared memory (few rows over a long context: see

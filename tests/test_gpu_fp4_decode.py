@@ -151,3 +151,52 @@ def test_results_do_not_change_from_call_to_call():
         call(p, q, o, ws, 0.09)
         outs.append(o)
     assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
+@pytest.mark.parametrize("rows,n_q,n_kv,d,bs,act,out,seqs", [
+    (1, 40, 1, 128, 16, "bf16", "bf16", 5), (1, 48, 1, 64, 32, "fp16", "fp32", 3), (16, 8, 2, 128, 16, "bf16", "fp32", 5),
+    (16, 32, 1, 64, 16, "fp16", "fp16", 4), (9, 8, 2, 128, 32, "fp16", "fp32", 70), (11, 3, 1, 64, 16, "bf16", "fp32", 1),
+    (16, 64, 4, 128, 16, "bf16", "bf16", 2), (16, 17, 1, 128, 16, "bf16", "fp32", 3)])
+def test_more_rows_than_the_decode_kernel_takes(rows, n_q, n_kv, d, bs, act, out, seqs):
+    lens = [rows + (i * 811) % 2600 for i in range(seqs)]
+    run(ref.Pools(rows + n_q, lens, n_kv, d, bs), rows, n_q, act, out)
+
+
+@pytest.mark.parametrize("rows,n_q", [(4, 8), (16, 8)])
+def test_padded_batches(rows, n_q):
+    """sequences of length 0 (padding) are no error, and the others are what they are without them; too short
+    ones are flagged and left alone"""
+    p = ref.Pools(81, [700, 40, 40, 40, 95], 2, 128, 16)
+    p.context[2:4] = 0
+    q = ref.draw_q(8, (5, rows, n_q, 128), torch.bfloat16)
+    out = torch.full(q.shape, 5.0, device="cuda")
+    call(p, q, out, workspace(p, rows, n_q), 0.1)
+    assert pa.pa_get_device_error() == 0
+    for s in (0, 1, 4):
+        w = ref.attend(q[s].double().cpu().numpy(), p.k[s], p.v[s], p.lens[s] - rows + np.arange(rows), 0.1)
+        ref.check(out[s], w, ref.tolerance(p.vmax), torch.float32)
+    p.context[2] = rows - 1
+    out.fill_(5.0)
+    call(p, q, out, workspace(p, rows, n_q), 0.1)
+    assert pa.pa_get_device_error() == pa.PA_ERR_OUT_OF_RANGE
+    assert (out[2] == 5).all()
+    ref.check(out[4], w, ref.tolerance(p.vmax), torch.float32)
+
+
+def test_lengths_of_a_captured_call_of_many_rows():
+    p = ref.Pools(83, [1500, 300], 1, 64, 16)
+    q = ref.draw_q(9, (2, 16, 4, 64), torch.bfloat16)
+    out, ws = torch.zeros(q.shape, device="cuda"), workspace(p, 16, 4)
+    call(p, q, out, ws, 0.125)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(p, q, out, ws, 0.125)
+    for lens in ([1500, 300], [16, 299], [1000, 17]):
+        p.context.copy_(torch.tensor(lens, dtype=torch.int32))
+        g.replay()
+        torch.cuda.synchronize()
+        for s, n in enumerate(lens):
+            w = ref.attend(q[s].double().cpu().numpy(), p.k[s][:n], p.v[s][:n], n - 16 + np.arange(16), 0.125)
+            ref.check(out[s], w, ref.tolerance(p.vmax), torch.float32)
+    assert pa.pa_get_device_error() == 0
