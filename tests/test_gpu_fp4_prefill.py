@@ -45,6 +45,15 @@ def test_prefill(chunks, ctx, n_q, n_kv, d, bs, act):
     run(p, chunks, n_q, act, "fp32")
 
 
+@pytest.mark.parametrize("chunks,ctx", [([70], [5000]), ([5, 70], [0, 4500]), ([300], [2100]), ([1, 1, 1], [2047, 2048, 3])],
+                         ids=str)
+@pytest.mark.parametrize("n_q,n_kv,d,bs,act,out", [(8, 2, 128, 16, "bf16", "fp32"), (4, 1, 64, 32, "fp16", "fp16"),
+                                                   (5, 1, 128, 32, "fp16", "fp32"), (8, 2, 64, 16, "bf16", "bf16")])
+def test_few_rows_over_long_contexts(chunks, ctx, n_q, n_kv, d, bs, act, out):
+    """calls whose key tiles are split over clusters of up to 8 blocks, some of whose ranges are empty"""
+    run(ref.Pools(sum(ctx) + d, [a + b for a, b in zip(chunks, ctx)], n_kv, d, bs), chunks, n_q, act, out)
+
+
 @pytest.mark.parametrize("act,out", [("bf16", "bf16"), ("fp16", "fp16"), ("bf16", "fp16"), ("fp16", "bf16")])
 def test_outputs_in_16_bits(act, out):
     run(ref.Pools(4, [200, 333], 2, 128, 16), [150, 40], 8, act, out)

@@ -173,3 +173,34 @@ def test_in_place_and_rows_of_positions_apart():
     torch.cuda.synchronize()
     assert pa.pa_get_device_error() == 0
     assert torch.equal(c.q, want.q_out) and torch.equal(c.kc, want.kc) and torch.equal(c.vc, want.vc)
+
+
+@pytest.mark.parametrize("T,n_q,n_kv,d,act,pool,rot,axes", [
+    (6000, 8, 2, 128, "bf16", "fp4", 128, 3), (6000, 8, 2, 64, "fp16", "fp8", 32, 4), (2600, 14, 1, 128, "bf16", "bf16", 112, 2),
+    (6100, 3, 3, 64, "bf16", "fp4", 64, 3), (2000, 14, 1, 64, "fp32", "fp32", 64, 4)])
+def test_long_chunks_with_padding_and_bad_places(T, n_q, n_kv, d, act, pool, rot, axes):
+    """more tokens than the grid covers at once; the last axis turns no pair, and its positions are checked like the others'"""
+    c = Case(T, T, n_q, n_kv, d, 16, act, pool, rot, False, axes, "random", False)
+    c.axis[c.axis == axes - 1] = 0
+    w = np.ones(T, bool)
+    rng = np.random.default_rng(T)
+    bad = rng.permutation(T)[:60]
+    w[bad] = False
+    c.given[bad[:20]] = -1
+    c.given[bad[20:30]] = c.kc.shape[0] * 16
+    for i, t in enumerate(bad[30:]):
+        c.given_pos[i % axes, t] = -1 if i % 2 else 999
+    c.given_pos[0, bad[:10]] = 12345                       # padding: its positions do not matter
+    c.run()
+    c.check(w, pa.PA_ERR_OUT_OF_RANGE)
+
+
+@pytest.mark.parametrize("n_q", [8, 3])
+def test_padding_with_any_positions_is_no_error(n_q):
+    c = Case(6, 50, n_q, 1, 128, 16, "bf16", "fp4", 128, False, 3, "in turn")
+    w = np.ones(50, bool)
+    w[10:30] = False
+    c.given[10:30] = -1
+    c.given_pos[:, 10:30] = -7
+    c.run()
+    c.check(w)
