@@ -5,6 +5,9 @@
 // One thread quantises one group of 16 elements of a row; the groups of a row, then
 // the tokens of a 16-token tile, then K and V are neighbours, so that a prompt's chunk is read in
 // whole rows and written as one run of bytes a (block, head).
+//
+// Bound: instructions (a group's quotients and conversions, fp4.cuh) and HBM: 8192 tokens of 8 heads of
+// 128 bf16 elements about 14 us, HBM floor 6.3.
 #include "fp4.cuh"
 #include "pa_device.cuh"
 #include "pa_internal.h"

@@ -13,7 +13,8 @@
 // its own, whose position of the token is the one that turns it; all axes share one table.
 //
 // Bound: HBM for long chunks (every element is read once and written once,
-// 3 flops each), launch latency for a decode step.
+// 3 flops each), launch latency for a decode step; for FP4 pools also the ~390 instructions of a group
+// of 16 (K and V of 8192 tokens of 8 heads of 128 elements: 24 us, issue 46 %, HBM floor 6).
 #include <cuda_fp8.h>
 #include <algorithm>
 #include <cmath>

@@ -6,19 +6,21 @@
 //   out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
 //
 // Work: the rows of all (sequence, KV head, up to RU of its (head, query) rows), one after another,
-// are a line of 128-token granules with kRowCost more units before each row for what a piece costs beside its
-// tokens (its queries and its combine take about as long as a granule); every block of a persistent grid takes an
-// equal run of it.  (Without those units, 40 sequences of 100 - 2047 tokens and 40 KV heads took 96 us for 55: blocks
-// with rows of one granule came last.)  A block's run holds whole rows, which it finishes, and at most two pieces of rows
-// that it shares with its neighbours, whose partials meet in f4_merge_kernel.  A piece's four warps take 32 tokens of
-// each stage and combine through shared memory.
+// are a line of 128-token granules with kRowCost more units before each row for what a piece costs
+// beside its tokens (its queries and its combine take about as long as a granule); every block of a
+// persistent grid takes an equal run of it.  (Without those units 40 sequences of 100 - 2047 tokens
+// and 40 KV heads took 98 us, now 72: blocks with rows of one granule came last.  Two units: 74.)
+// A block's run holds whole rows, which it finishes, and at most two pieces of rows that it shares
+// with its neighbours, whose partials meet in f4_merge_kernel.  A piece's four warps take 32 tokens
+// of each stage and combine through shared memory.
 //
 // Stages of 128 tokens (32 a warp) arrive in a ring that the block's warps share, each by four
-// cp.async.bulk.tensor gathers of four 16-token tiles (a tile's rows are contiguous in the pool, so the pool is a
-// matrix with a tile a row), which the warps issue in turn.  (Untiled copies, one a tile: the
-// instructions around them were a fifth of all.)  A warp works on its tokens transposed, on m16n8k16 fp16
-// MMAs: S^T = K q^T with tokens as the MMA rows, O^T = V^T P^T with elements of d
-// as the rows, the unit's rows as the columns (NT tiles of 8).
+// cp.async.bulk.tensor gathers of four 16-token tiles (a tile's rows are contiguous in the pool, so
+// the pool is a matrix with a tile a row), which the warps issue in turn.  (Rings of a warp's own,
+// one untiled copy a tile: 174 us for 151 at the sizes below, by the instructions around the copies;
+// filled by cp.async: 155 - 160.)  A warp works on its tokens transposed, on m16n8k16 fp16 MMAs:
+// S^T = K q^T with tokens as the MMA rows, O^T = V^T P^T with elements of d as the rows, the unit's
+// rows as the columns (NT tiles of 8).
 //   - Row r of a score tile is token 4 ((r & 7) >> 1) + 2 (r >> 3) + (r & 1) of its piece; the transpose
 //     of P (movmatrix) then leaves lane (g, t4) = (lane / 4, lane % 4) with tokens 4 t4 .. 4 t4 + 3, whose V
 //     codes it reads in 8-byte (d 64: 4-byte) pieces without bank conflicts (rows lie 72 bytes apart).
@@ -30,12 +32,15 @@
 //   - Codes times scales are exact in fp16 (fp4.cuh).  bf16 queries are scaled by a power of two into
 //     fp16 (exact down to 2^-29 of the row's largest element).
 //   - P enters P V as one fp16 part: 11 bits, so an output moves by at most 2^-12 of the largest |v| that it
-//     averages, far below what 4 bits do to v.  (A second part: one more MMA a tile and 14 of the
-//     ~250 instructions of a piece.)
+//     averages, far below what 4 bits do to v.
 //
-// Bound: HBM at 4.5 bits a value; beside it the instructions that widen: a conversion and a
-// multiply for two values, 128 of the ~240 warp instructions of a 16-token piece (d 128), of which an SM issues
-// about 400 in the time that HBM takes to bring it the piece.
+// Bound: HBM at 4.5 bits a value, and beside it the instructions that widen.  HBM gives an SM's
+// quarter 397 clocks for 16 tokens of a head (d 128); its 64 conversions and 64 multiplies issue
+// every other clock and its 16 MMAs hold the dispatch for 8 clocks each, 254 in all, of ~240
+// instructions.  256 sequences of 512 - 4096 tokens of Llama-3-8B's heads: 134 us, 5.1 TB/s (0.75 of
+// the copy rate), issue 60 %; 8 us pass before the first stage is there and 4 until the merge is
+// done.  Eight sequences of 20,000 - 110,000 tokens: 109 us, 5.5 TB/s.  (K's products on tcgen05 with
+// scores back from TMEM: 178 us, by the threads around the MMAs.)
 #include "fp4.cuh"
 #include "pa_device.cuh"
 #include "pa_internal.h"
@@ -61,7 +66,8 @@ struct F4Params {
     void* out;
     const void* q;
     const int32_t *block_tables, *context_lens;
-    int4* info;                           // [blocks]: a row begun and not finished here, or -1; whether the head piece goes on.  May be null
+    // [blocks]: a row begun and not finished here, or -1; whether the head piece goes on.  May be null
+    int4* info;
     float *ws_ml, *ws_acc;                // [blocks + tails][RU] (m, l) and O
     int row_tails;                        // whether a tail's slot goes by its row (else by its block)
     unsigned* err;
@@ -147,7 +153,8 @@ __device__ __forceinline__ void f4_scores(const uint8_t* k, int g, int t4, const
 }
 
 // O^T += V^T P^T of one tile.  Byte b of a lane's codes is m-tile b, its low half row g, its high half row
-// g + 8.  valid: tokens of the tile that exist (kMasked; else all); the scales of the others may be anything, even NaN, and count as 0.
+// g + 8.  valid: tokens of the tile that exist (kMasked; else all); the scales of the others may be
+// anything, even NaN, and count as 0.
 template <int D, int NT, bool kMasked>
 __device__ __forceinline__ void f4_values(const uint8_t* v, int g, int t4, int valid, const uint32_t (&pt)[NT][2],
                                           float (&o)[NT][D / 16][4])
@@ -194,7 +201,9 @@ __device__ __forceinline__ void f4_values(const uint8_t* v, int g, int t4, int v
 }
 
 template <typename QT, int D, int RU, bool MQ>
-__global__ void __launch_bounds__(kF4Threads, F4Cfg<D, RU>::kCtas) f4_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const __grid_constant__ F4Params p)
+__global__ void __launch_bounds__(kF4Threads, F4Cfg<D, RU>::kCtas)
+f4_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                 const __grid_constant__ F4Params p)
 {
     using Cfg = F4Cfg<D, RU>;
     constexpr int NT = RU == 16 ? 2 : 1, NS = Cfg::kNS, kTiles = kStageTok / kPieceTok;   // kTiles: a warp's of a stage
@@ -222,7 +231,8 @@ __global__ void __launch_bounds__(kF4Threads, F4Cfg<D, RU>::kCtas) f4_decode_ker
     }
     grid_dependency_wait();      // launched as a programmatic dependent: every input may come from the kernel before
 
-    // ---- this block's run of units.  A thread takes `mine` neighbouring sequences, and the one in whose rows the run begins finds the place.
+    // ---- this block's run of units.  A thread takes `mine` neighbouring sequences, and the one in
+    // whose rows the run begins finds the place.
     auto granules = [&](int L) { return L < nq || L <= 0 ? 0 : (min(L, max_ctx) + kGranule - 1) / kGranule; };
     auto units = [&](int L) { const int J = granules(L); return J ? J + kRowCost : 0; };      // of a row
     const bool tabled = p.num_seqs <= kF4PrefixCap;
