@@ -259,7 +259,7 @@ int rope(PyObject* const* a)
     if (pos.scalar_type() != at::kInt || slots.scalar_type() != at::kLong || cs.scalar_type() != at::kFloat)
         raise(PyExc_TypeError, "positions int32, slot_mapping int64 and cos_sin float32 expected");
     const int64_t T = q.size(0);
-    // several axes: positions [axes][T], rows of any stride
+    // several axes: positions [axes][T], rows at least T apart
     const bool many = a[13] != Py_None;
     const int64_t axes = many ? (pos.dim() == 2 ? pos.size(0) : 0) : 1;
     if (many && (axes < 1 || pos.size(1) != T || (T > 1 && pos.stride(1) != 1)))
