@@ -264,3 +264,40 @@ def _takes(call, n):
     except pa.PAError as e:
         assert e.status == pa.PA_ERR_WORKSPACE
         return False
+
+
+def test_rows_past_4_gib():
+    """pools of 4.7 GiB each, whose last blocks hold the sequences: write, prefill, decode, rows read back and a block copy"""
+    m = Layer(5, 2, 128, width=12)
+    nb = 550000
+    m.kc, m.vc = (torch.full((nb, 8, BS, 72), 0xFF, dtype=torch.uint8, device="cuda") for _ in range(2))
+    m.tables = (nb - 1 - m.rng.permutation(24)).reshape(2, 12).astype(np.int32)
+    n_kv, n_q, T = 8, 16, 180
+    assert int(m.tables.min()) * 8 * BS * 72 > 2 ** 32
+    qkv = torch.from_numpy(m.rng.standard_normal((2 * T, (n_q + 2 * n_kv) * 128))).to(BF).cuda()
+    q, k, v = (t.unflatten(1, (-1, 128)) for t in qkv.split([n_q * 128, n_kv * 128, n_kv * 128], 1))
+    pos = dev(m.rng.integers(0, 4000, (3, 2 * T)))
+    at = np.arange(T)
+    slots = dev(np.concatenate([t[at // BS].astype(np.int64) * BS + at % BS for t in m.tables]), np.int64)
+    q_out = torch.empty(2 * T, n_q, 128, dtype=BF, device="cuda")
+    pa.pa_rope_axes_and_cache(q_out, q, k, v, pos, m.axis, m.table.cuda(), m.kc, m.vc, slots, **SCALES)
+    read = [torch.empty(2 * T, n_kv, 128, device="cuda") for _ in range(2)]
+    pa.pa_gather_cache(read[0], read[1], m.kc, m.vc, slots, **SCALES)
+    want_v = ref.values(ref.quantise(v.float().cpu().numpy(), VS), VS)
+    assert np.array_equal(read[1].cpu().numpy(), want_v.astype(np.float32))
+    rows = [r.double().cpu().numpy().reshape(2, T, n_kv, 128) for r in read]
+    vmax = np.abs(rows[1]).max()
+    out = torch.empty(2 * T, n_q, 128, device="cuda")
+    pa.pa_prefill_chunk(out, q_out, m.kc, m.vc, dev(m.tables), dev([0, T, 2 * T]), dev([T, T]), T, 0.09, BS, **SCALES)
+    ws = torch.empty(pa.pa_decode_workspace_size(2, n_q, n_kv, 128, BS, 12 * BS), dtype=torch.uint8, device="cuda")
+    one = torch.empty(2, n_q, 128, device="cuda")
+    last = q_out[[T - 1, 2 * T - 1]].contiguous()
+    pa.pa_decode(one, last, m.kc, m.vc, dev(m.tables), dev([T, T]), 0.09, BS, ws, **SCALES)
+    for s in range(2):
+        x = q_out[s * T:(s + 1) * T].double().cpu().numpy()
+        ref.check(out[s * T:(s + 1) * T], ref.attend(x, rows[0][s], rows[1][s], at, 0.09), ref.tolerance(vmax), torch.float32)
+        ref.check(one[s:s + 1], ref.attend(x[-1:], rows[0][s], rows[1][s], at[-1:], 0.09), ref.tolerance(vmax), torch.float32)
+    pa.pa_copy_blocks(m.kc, m.vc, dev([[int(m.tables[0, 3]), 1]]))
+    torch.cuda.synchronize()
+    assert torch.equal(m.kc[1], m.kc[int(m.tables[0, 3])]) and torch.equal(m.vc[1], m.vc[int(m.tables[0, 3])])
+    assert (m.kc[2:1000] == 0xFF).all() and (m.kc[0] == 0xFF).all() and pa.pa_get_device_error() == 0
