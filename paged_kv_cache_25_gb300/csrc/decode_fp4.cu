@@ -469,7 +469,7 @@ f4_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     load_q(cu);
     nx = next_piece();
     if (duty < NS) copy_duty();
-    int n = 0, slot = 0;                         // the next stage, its slot and the slot's phase
+    int number = 0, slot = 0;                         // the next stage, its slot and the slot's phase
     uint32_t phase = 0;
 
     float o[NT][D / 16][4];
@@ -570,11 +570,11 @@ f4_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         };
         const int open = min(cu.L - nq + 1, cu.t1);      // keys below it are there and visible to every row
 #pragma unroll 1
-        for (; n < first_n + cu.n; ++n) {
-            const int pos0 = cu.t0 + (n - first_n) * kGranule + warp * kStageTok;
+        for (; number < first_n + cu.n; ++number) {
+            const int pos0 = cu.t0 + (number - first_n) * kGranule + warp * kStageTok;
             if (!timed_out) timed_out = !mbar_wait(full0 + slot * 8, phase, p.err);
             __syncwarp();
-            if (duty <= n - 1 + NS) copy_duty();
+            if (duty <= number - 1 + NS) copy_duty();
             const uint8_t* st_k = smem + slot * Cfg::kStage + warp * kTiles * Cfg::kTile;
             if (pos0 + kStageTok <= open) stage(std::false_type{}, st_k, st_k + Cfg::kTiles * Cfg::kTile, pos0);
             else if (pos0 < cu.t1) stage(std::true_type{}, st_k, st_k + Cfg::kTiles * Cfg::kTile, pos0);
@@ -659,7 +659,7 @@ f4_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         cu = nx;
         if (cu.live) {
             nx = next_piece();
-            if (duty <= n - 1 + NS) copy_duty();      // (one that waited for its piece)
+            if (duty <= number - 1 + NS) copy_duty();      // (one that waited for its piece)
         }
     }
     if (timed_out && tid == 0 && p.info) p.info[blockIdx.x] = make_int4(-1, 0, 0, 0);
