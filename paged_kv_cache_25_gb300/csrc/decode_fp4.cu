@@ -31,8 +31,11 @@
 //     scales, and q is loaded to match.  Lane g holds elements (d / 8) g and on of V: one scale a token.
 //   - Codes times scales are exact in fp16 (fp4.cuh).  bf16 queries are scaled by a power of two into
 //     fp16 (exact down to 2^-29 of the row's largest element).
-//   - P enters P V as one fp16 part: 11 bits, so an output moves by at most 2^-12 of the largest |v| that it
-//     averages, far below what 4 bits do to v.
+//   - P enters P V as one fp16 part, 11 bits, half a step of which is 2^-11 of P.  The exponents' reference lies 7
+//     powers of two below the largest score that set it (kPRoom), so P begins at 2^7 and what fp16 rounds off below its
+//     smallest normal number is at most 2^-32 of the largest weight: an output moves by at most 2^-11 of the largest |v|
+//     that it averages and 2^-32 of it for each key, far below what 4 bits do to v.  (With P from 1 on, a key 17.4 nats
+//     above 520,000 equal ones moved outputs by 3e-3 of |v|: each of the others is 0 in fp16, and together they are not.)
 //
 // Bound: HBM at 4.5 bits a value, and beside it the instructions that widen.  HBM gives an SM's
 // quarter 397 clocks for 16 tokens of a head (d 128); its 64 conversions and 64 multiplies issue
@@ -59,6 +62,7 @@ constexpr int kPieceTok = 16;             // tokens of a tile of scores, and of 
 constexpr int kStageTok = 32;             // tokens of a stage that a warp takes: two tiles
 constexpr int kGranule = kF4Warps * kStageTok;   // tokens of a stage, and of a granule
 constexpr int kRowCost = 1;               // units of a row beside its granules
+constexpr float kPRoom = 7.f;             // powers of two that P has left below 2^15: the reference moves only past 2^8
 constexpr int kF4PrefixCap = 768;         // sequences whose lengths are kept in shared memory
 static_assert(kGranule == kF4GranuleTokens, "as the workspace counts them");
 
@@ -477,7 +481,7 @@ f4_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     while (cu.live) {
         scale_q();
         // this lane's columns 8 n + 2 t4 + e: softmax scales c, sums, and of the reference m of the exponents (a raw
-        // score near the largest so far) -m c and the raw score past which it moves
+        // score near the largest so far) kPRoom - m c and the raw score past which it moves
         float c[NT][2], ref[NT][2], bar_z[NT][2], l[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -512,7 +516,7 @@ f4_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
                     }
             }
             // the columns' largest raw scores, met over the eight lanes of each t4.  The reference moves only
-            // when the first key sets it or the largest is more than 2^8 past it (lazily: P stays below 2^8).
+            // when the first key sets it or the largest is more than 2^8 past it (lazily: P stays below 2^(8 + kPRoom)).
             float mx[NT][2];
             bool moved = false;
 #pragma unroll
@@ -534,7 +538,8 @@ f4_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
 #pragma unroll
                         for (int w = 4; w < 32; w <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, w));
                         if (x > bar_z[n][e]) {
-                            const float r = -x * c[n][e];
+                            // (scores so large that the products' rounding would use that room up keep it free)
+                            const float far = -x * c[n][e], r = fabsf(far) < 0x1p20f ? far + kPRoom : far;
                             const float f = bar_z[n][e] == -INFINITY ? 0.f : fast_exp2(r - ref[n][e]);
                             ref[n][e] = r;
                             bar_z[n][e] = x + 8.f / c[n][e];      // (a scale of 0: never again)
