@@ -403,8 +403,8 @@ size_t pa_decode_scored_workspace_size(int num_seqs, int q_per_seq, int n_q_head
  * widened exactly to fp16 on chip (every E4M3 value is an fp16 value) and the
  * scales are folded into the softmax scale (k_scale) and the output (v_scale).
  * Roundings: probabilities enter P V as two bf16 parts (about 16 bits) over bf16
- * pools, as one fp16 part over fp16 and FP8 pools (11 bits: an output moves by at
- * most 2^-12 of the largest |v| that it averages).  bf16 queries over an FP8 pool
+ * pools, as one fp16 part over fp16, FP8 and FP4 pools (11 bits: an output moves by at
+ * most 2^-11 of the largest |v| that it averages, and 2^-32 of it for each key).  bf16 queries over an FP8 pool
  * with head_dim 128 enter the scores as the sum of two E4M3 parts: exact for
  * elements down to 2^-10 of the row's largest, off by at most 2^-17 of that
  * largest below. */

@@ -342,11 +342,16 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     constexpr int kMmaWarp = Wp::kMma;
     constexpr int kFirstConv = Wp::kFirstConverter;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
-    // P for P V: fp16 operands (fp16 and FP8 pools) take P as one fp16 part,
-    // 11 significant bits, so each output moves by at most 2^-12 of the
-    // largest |v| it averages; bf16 operands take P as hi + lo bf16 parts
-    // (8 significant bits each, ~16 together)
+    // P for P V: fp16 operands (fp16, FP8 and FP4 pools) take P as one fp16 part,
+    // 11 significant bits, half a step of which is 2^-11 of P; bf16 operands take P as
+    // hi + lo bf16 parts (8 significant bits each, ~16 together).  One part: the exponents'
+    // reference lies 7 powers of two below the largest score that set it, so P begins at
+    // 2^7 and what fp16 rounds off below its smallest normal number is at most 2^-32 of the
+    // largest weight.  Each output then moves by at most 2^-11 of the largest |v| it averages
+    // and 2^-32 of it for each key.  (With P from 1 on, a key 17.4 nats above 131,000 equal
+    // ones moved outputs by 3.6e-3 of |v|: each of those is 0 in fp16, and together they are not.)
     constexpr bool kOneP = !kBf16;
+    constexpr float kPRoom = 7.f;     // (the reference moves only past 2^8: P stays below 2^15)
     constexpr uint32_t kIdescQK = idesc_f16(kBf16, false, false, kTcRows, kTcKeys);
     // kind::f8f6f4 with E4M3 A and B (type code 0 in both fields), fp32 accumulate
     constexpr uint32_t kIdescQK8 = idesc_f16(false, false, false, kTcRows, kTcKeys);
@@ -1136,6 +1141,12 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         };
         const float unit_log2 = kZ ? 1.f : scale_log2;   // log2 units of the running maximum
         float m_raw = -INFINITY, l = 0.f;
+        // powers of two by which the exponents' reference lies below the maximum m: none for scores so
+        // large that the products' own rounding would use them up
+        auto room = [&](float m) -> float {
+            if constexpr (kOneP) return fabsf(m * unit_log2) < 0x1p20f ? kPRoom : 0.f;
+            else return 0.f;
+        };
         bool stop = false;   // a wait of this warp ran out
         bool quit = false;   // the pair left the loop together
         for (int j = 0; j < nt; ++j) {
@@ -1234,11 +1245,14 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             const bool resc = first ? (mx > -INFINITY) : ((mx - m_raw) * unit_log2 > 8.f);
             float fac = 1.f;
             if (resc) {
-                fac = first ? 0.f : fast_exp2((m_raw - mx) * unit_log2);
+                fac = (m_raw - mx) * unit_log2;
+                if constexpr (kOneP) fac += room(mx) - room(m_raw);
+                fac = first ? 0.f : fast_exp2(fac);
                 m_raw = mx;
                 l *= fac;
             }
-            const float neg_mc = -m_raw * unit_log2;
+            float neg_mc = -m_raw * unit_log2;
+            if constexpr (kOneP) neg_mc += room(m_raw);
             if (j >= 1 && __any_sync(0xffffffffu, resc)) {   // TMEM access is warp-wide
 #pragma unroll
                 for (int c0 = 0; c0 < D / 2; c0 += 32) {
@@ -1383,7 +1397,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                     obase = slot * D;
                     if (valid && hf == 0)
                         *reinterpret_cast<float2*>(sp.ml + 2 * slot) =
-                            make_float2(lsum > 0.f ? m_raw * unit_log2 : -INFINITY, lsum);
+                            make_float2(lsum > 0.f ? m_raw * unit_log2 - room(m_raw) : -INFINITY, lsum);
                 }
                 if constexpr (F4 && !kSplit) {
                     if (out_dtype != PA_F32) {
@@ -1437,7 +1451,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                         if (valid) store_row<T>(out, obase, hf * (D / 2) + c0, v, 32, out_dtype);
                     }
                 }
-                if (kSplit && lsum > 0.f) part = make_float2(m_raw * unit_log2, lsum);
+                if (kSplit && lsum > 0.f) part = make_float2(m_raw * unit_log2 - room(m_raw), lsum);
                 if constexpr (kShared) {
                     fence_proxy_async_smem();
                     if (valid)

@@ -46,9 +46,10 @@ def check_sink(out, keys, scale):
     assert np.isfinite(worst).all() and (worst <= tol).all(), (worst.max(), (worst / tol).max())
 
 
-@pytest.mark.parametrize("rows,n_q,n_kv,d,seqs,blocks", [(1, 8, 8, 64, 64, 32768), (2, 16, 4, 128, 64, 16384), (1, 32, 2, 64, 128, 32768)])
+@pytest.mark.parametrize("rows,n_q,n_kv,d,seqs,blocks", [(1, 8, 8, 64, 64, 32768), (2, 16, 4, 128, 64, 16384), (1, 32, 2, 64, 128, 32768),
+                                                         (5, 8, 1, 64, 160, 8192)])
 def test_a_long_flat_rest_below_one_key(rows, n_q, n_kv, d, seqs, blocks):
-    """long runs of a block"""
+    """long runs of a block (the last: through the prefill's kernel)"""
     bs = 16
     n, scale = blocks * bs - 3, NATS / 96
     kc, vc = sink_pool(blocks, n_kv, d, bs, 5)
@@ -87,6 +88,34 @@ def test_scores_far_from_zero(seqs):
     out = torch.empty(q.shape, device="cuda")
     ws = torch.empty(pa.pa_decode_workspace_size(seqs, 4, 1, 64, 16, 256), dtype=torch.uint8, device="cuda")
     pa.pa_decode(out, q, kc, vc, tables, lens, scale, 16, ws, k_scale=1.0, v_scale=1.0)
+    torch.cuda.synchronize()
+    assert pa.pa_get_device_error() == 0
+    assert ((out - 1).abs() <= 2.0 ** -11 + 256 * 2.0 ** -23).all()
+
+
+@pytest.mark.parametrize("reqs,n_kv,d,act", [(20, 8, 128, "bfloat16"), (20, 8, 64, "float16"), (2, 1, 64, "bfloat16")])
+def test_prefill_of_a_long_flat_rest_below_one_key(reqs, n_kv, d, act):
+    """(the last: key tiles split over clusters)"""
+    bs, blocks, chunk = 32, 4096, 3
+    n, scale = blocks * bs, NATS / 96
+    kc, vc = sink_pool(blocks, n_kv, d, bs, 700)
+    tables = torch.arange(blocks, dtype=torch.int32, device="cuda").repeat(reqs, 1)
+    lens = torch.full((reqs,), n, dtype=torch.int32, device="cuda")
+    start = torch.arange(reqs + 1, dtype=torch.int32, device="cuda") * chunk
+    q = torch.ones(reqs * chunk, 2 * n_kv, d, dtype=getattr(torch, act), device="cuda")
+    out = torch.empty(q.shape, device="cuda")
+    pa.pa_prefill_chunk(out, q, kc, vc, tables, start, lens, chunk, scale, bs, k_scale=1.0, v_scale=1.0)
+    torch.cuda.synchronize()
+    assert pa.pa_get_device_error() == 0
+    check_sink(out, np.tile(n - chunk + 1 + np.arange(chunk), reqs), scale)
+
+
+def test_prefill_of_scores_far_from_zero():
+    kc, vc, q, tables, scale = far_pool(160, 32)
+    lens = torch.full((160,), 256, dtype=torch.int32, device="cuda")
+    start = torch.arange(161, dtype=torch.int32, device="cuda")
+    out = torch.empty(q.shape, device="cuda")
+    pa.pa_prefill_chunk(out, q, kc, vc, tables, start, lens, 1, scale, 32, k_scale=1.0, v_scale=1.0)
     torch.cuda.synchronize()
     assert pa.pa_get_device_error() == 0
     assert ((out - 1).abs() <= 2.0 ** -11 + 256 * 2.0 ** -23).all()
