@@ -1451,7 +1451,9 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                         if (valid) store_row<T>(out, obase, hf * (D / 2) + c0, v, 32, out_dtype);
                     }
                 }
-                if (kSplit && lsum > 0.f) part = make_float2(m_raw * unit_log2 - room(m_raw), lsum);
+                // (a sum that is NaN counts, though its scores may have no maximum)
+                if (kSplit && lsum != 0.f)
+                    part = make_float2(m_raw == -INFINITY ? 0.f : m_raw * unit_log2 - room(m_raw), lsum);
                 if constexpr (kShared) {
                     fence_proxy_async_smem();
                     if (valid)
@@ -1488,9 +1490,10 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             float o[V];
 #pragma unroll
             for (int i = 0; i < V; ++i) o[i] = 0.f;
+            const uint32_t there = __ballot_sync(0xffffffffu, p.x != -INFINITY);
             for (int c = 0; c < splits; ++c) {
                 const float wc = __shfl_sync(0xffffffffu, weight, c);
-                if (wc == 0.f) continue;      // (a range in which the row sees nothing has no O)
+                if (!((there >> c) & 1u)) continue;      // (a range in which the row sees nothing has no O)
                 const uint32_t at = cluster_address(sbase + row * kORow + lane * V * 4, c);
 #pragma unroll
                 for (int i = 0; i < V; i += 2) {
@@ -1499,7 +1502,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                     o[i + 1] = fmaf(wc, x.y, o[i + 1]);
                 }
             }
-            const float inv = sum > 0.f ? 1.f / sum : 0.f;      // a row that sees no key is 0
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;     // a row that sees no key is 0, a NaN stays one
             const int grow = row0 + row;
             const int64_t at = (static_cast<int64_t>(qs + grow / group) * n_q + kvh * group + grow % group) * D +
                                lane * V;
