@@ -50,8 +50,8 @@ NCU_TRAFFIC = {
 # chunked prefill of the mixed step (the compact-pool capture runs the same four
 # chunks as the 60 GB pool): bytes per launch
 NCU_PREFILL_TRAFFIC = {
-    ("mixed-llama3-8b-bf16", "febbb0c36b72ee29"): (98479872 + 4337152, "compact pool, one-pass capture"),
-    ("mixed-llama3-8b-fp8", "febbb0c36b72ee29"): (57575936 + 959488, "compact pool, one-pass capture"),
+    ("mixed-llama3-8b-bf16", "aa7e5c255e155cc6"): (98555648 + 4024832, "compact pool, one-pass capture"),
+    ("mixed-llama3-8b-fp8", "aa7e5c255e155cc6"): (57575936 + 1071360, "compact pool, one-pass capture"),
 }
 
 

@@ -492,6 +492,8 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         return;
     }
     const int ctx0 = kShared ? 0 : L - C;
+    // (a decode's rows past the table are clamped away; the query rows keep their positions)
+    if (F4 && !q_start) L = min(L, max_blocks * BS);
     // key tiles each tile's rows need (0: the tile has no rows); when both
     // tiles have rows, n_t[0] <= n_t[1]
     int n_t[kTcTiles];
@@ -510,7 +512,10 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         }
         return f;
     };
-    auto last_key = [&](int i) -> int { return MODE != 0 ? max(ctx0 + i, prefix_end - 1) : ctx0 + i; };
+    auto last_key = [&](int i) -> int {
+        const int k = MODE != 0 ? max(ctx0 + i, prefix_end - 1) : ctx0 + i;
+        return F4 ? min(k, L - 1) : k;
+    };
     if constexpr (MODE != 0 && !kShared) {
         if (sc.window > 0 || sc.first_key) {
             __shared__ int s_lo;
@@ -1096,7 +1101,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         // smallest query position of this warp's rows (rows are position-major)
         const int wrow = row0 + t * kTcRows + quarter * 32;
         const int warp_min_pos = MODE != 0 ? __reduce_min_sync(0xffffffffu, p_abs)
-                                           : (wrow < rows_total ? ctx0 + wrow / group : L - 1);
+                                           : (wrow < rows_total ? last_key(wrow / group) : L - 1);
         const int warp_max_lo = MODE != 0 ? __reduce_max_sync(0xffffffffu, p_lo) : 0;
         // modified scores (log2 domain): the cap, the row's slope, and d = key -
         // position for the bias -slope * |d|
