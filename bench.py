@@ -42,16 +42,16 @@ FALLBACK_HBM_GBS = 6800.0
 # K/V bytes of the captured launch, what was captured); a record of another
 # batch of the same workload is scaled by its unique K/V bytes.
 NCU_TRAFFIC = {
-    ("llama3-8b-bf16", "e6cb8234b000969c"): (2371998976 + 13430272, 2359717888,
+    ("llama3-8b-bf16", "2dd35a15cd38c3cd"): (2371981568 + 13404928, 2359717888,
                                              "full 256-sequence batch, one-pass capture"),
-    ("llama3-8b-fp8", "e6cb8234b000969c"): (1188263424 + 12730112, 1179858944,
+    ("llama3-8b-fp8", "2dd35a15cd38c3cd"): (1188189696 + 12449280, 1179858944,
                                             "full 256-sequence batch, one-pass capture"),
 }
 # chunked prefill of the mixed step (the compact-pool capture runs the same four
 # chunks as the 60 GB pool): bytes per launch
 NCU_PREFILL_TRAFFIC = {
-    ("mixed-llama3-8b-bf16", "aa7e5c255e155cc6"): (98555648 + 4024832, "compact pool, one-pass capture"),
-    ("mixed-llama3-8b-fp8", "aa7e5c255e155cc6"): (57575936 + 1071360, "compact pool, one-pass capture"),
+    ("mixed-llama3-8b-bf16", "2c27b8205dda9f87"): (98481664 + 3973376, "compact pool, one-pass capture"),
+    ("mixed-llama3-8b-fp8", "2c27b8205dda9f87"): (57575168 + 955648, "compact pool, one-pass capture"),
 }
 
 

@@ -773,11 +773,8 @@ static cudaError_t run_f4(F4Params p, const DecodeArgs& a, void* workspace, size
 {
     using Cfg = F4Cfg<D, RU>;
     auto kern = f4_decode_kernel<QT, D, RU, MQ>;
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [&] {
-        attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kDynBytes);
-    });
+    static SmemOptIn opt_in;
+    const cudaError_t attr_err = opt_in(reinterpret_cast<const void*>(kern), Cfg::kDynBytes);
     if (attr_err != cudaSuccess) return attr_err;
     int sms = 0;
     cudaError_t e = f4_resident(&sms);

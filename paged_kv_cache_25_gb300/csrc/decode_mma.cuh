@@ -1105,19 +1105,17 @@ cudaError_t run_mma(const DecodeArgs& a, cudaStream_t s, float scale_log2)
     constexpr int NS = decode_stages<T, D, FP8, RU>();
     using Cfg = DecodeCfg<T, D, NS, FP8, RU>;
     auto kern = decode_mma_kernel<T, QT, D, BS, NS, FP8, MQ, RU, SC, WIDE>;
+    static SmemOptIn opt_in;
+    const cudaError_t attr_err = opt_in(reinterpret_cast<const void*>(kern), Cfg::kDynBytes);
+    if (attr_err != cudaSuccess) return attr_err;
     static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    static int per_sm = 1;
+    static int per_sm = 1;        // (the same on every device of this kind)
     std::call_once(once, [&] {
-        attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        Cfg::kDynBytes);
-        if (attr_err == cudaSuccess &&
-            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kDecWarps * 32,
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kDecWarps * 32,
                                                           Cfg::kDynBytes) != cudaSuccess)
             per_sm = 1;
         if (per_sm < 1) per_sm = 1;
     });
-    if (attr_err != cudaSuccess) return attr_err;
     CUtensorMap kmap{}, vmap{};
     const uint64_t rows = static_cast<uint64_t>(a.cache.num_blocks) * a.cache.n_kv_heads * BS;
     if constexpr (FP8) {

@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "../../include/pa.h"
+#include "smem_opt_in.h"
 
 namespace pa {
 

@@ -64,7 +64,6 @@
 #include <limits.h>
 #include <math.h>
 
-#include <mutex>
 #include <type_traits>
 
 namespace pa {
@@ -1572,12 +1571,8 @@ cudaError_t run_prefill_tc(const PrefillArgs& a, cudaStream_t s, float sl2)
     constexpr bool kBq = std::is_same<QT, __nv_bfloat16>::value;
     using Ly = PfLayout<T, D, F8, kBq, F4>;
     auto kern = prefill_tc_kernel<T, QT, D, BS, F8, MODE, F4>;
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [&] {
-        attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        static_cast<int>(Ly::kDynBytes));
-    });
+    static SmemOptIn opt_in;
+    const cudaError_t attr_err = opt_in(reinterpret_cast<const void*>(kern), static_cast<int>(Ly::kDynBytes));
     if (attr_err != cudaSuccess) return attr_err;
     CUtensorMap kmap{}, vmap{};
     if constexpr (F4) {       // a row of the matrix: 16 rows of a pool

@@ -20,12 +20,8 @@ static cudaError_t run_prefix(const DecodeArgs& a, const PrefixPass& pass, cudaS
     constexpr bool kBq = std::is_same<QT, __nv_bfloat16>::value;
     using Ly = PfLayout<T, D, F8, kBq>;
     auto kern = prefill_tc_kernel<T, QT, D, BS, F8, kPfShared>;
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [&] {
-        attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        static_cast<int>(Ly::kDynBytes));
-    });
+    static SmemOptIn opt_in;
+    const cudaError_t attr_err = opt_in(reinterpret_cast<const void*>(kern), static_cast<int>(Ly::kDynBytes));
     if (attr_err != cudaSuccess) return attr_err;
     CUtensorMap kmap{}, vmap{};
     const cudaError_t map_err = prefill_maps<T, D, BS, F8, kBq>(a.cache, a.k_cache, a.v_cache, &kmap, &vmap);
