@@ -282,10 +282,10 @@ def pa_rope_axes_and_cache(q_out, q, k, v, positions, axis_of_pair, cos_sin, k_c
                            slot_mapping, interleaved: bool = False, stream=None, k_scale=None,
                            v_scale=None):
     """pa_rope_and_cache with several position axes: positions int32 [axes][T] (rows at least T apart),
-    axis_of_pair uint8 [rot_dim / 2] in host memory (bytes or a NumPy array, see pa_rope_axes): the
-    axis whose position turns each pair."""
+    axis_of_pair uint8 [rot_dim / 2] in host memory (bytes, a NumPy array or a sequence of numbers,
+    see pa_rope_axes): the axis whose position turns each pair."""
     if not isinstance(axis_of_pair, (bytes, np.ndarray)):
-        axis_of_pair = bytes(axis_of_pair)
+        axis_of_pair = bytes(list(axis_of_pair))     # (of a number, bytes would be as many zeros)
     elif isinstance(axis_of_pair, np.ndarray) and axis_of_pair.dtype != np.uint8:
         raise TypeError("axis_of_pair: uint8 expected")
     st = _marshal().rope(q_out, q, k, v, positions, cos_sin, k_cache, v_cache, slot_mapping,
