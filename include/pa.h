@@ -71,7 +71,8 @@ typedef enum {
  * dtype PA_FP8_E4M3,
  * each stored code c means decode_e4m3(c) * k_scale for K (v_scale for V);
  * act_dtype (PA_BF16 or PA_F16) is the dtype of q and of the K/V rows given
- * to pa_reshape_and_cache_quant.  The three fields are ignored otherwise.
+ * to pa_reshape_and_cache_quant.  The three fields are ignored otherwise (and by
+ * the block copies).
  * In FP8 pools the V codes of each 16-token piece of a (block, KV head) are
  * stored transposed, v_cache [num_blocks][n_kv_heads][block_size / 16]
  * [head_dim][16]: the code of slot offset o, element i sits at
@@ -441,7 +442,8 @@ pa_status pa_prefill_scored(void* out, pa_dtype out_dtype, const void* q,
  * Every source block is read as it was before the call; a destination must not
  * also be a source in the same call (the copies run in parallel).  An id
  * outside [0, num_blocks) sets PA_ERR_OUT_OF_RANGE on the device and that pair
- * is skipped. */
+ * is skipped.  Every pool type: the bytes are moved as they are, so an FP8 or FP4
+ * descriptor's k_scale, v_scale and act_dtype are ignored here. */
 pa_status pa_copy_blocks(void* k_cache, void* v_cache, const pa_cache_desc* cache,
                          const int32_t* block_mapping, int num_pairs, void* stream);
 
