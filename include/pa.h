@@ -207,7 +207,8 @@ int pa_rope_table(float* table, int max_position, int rot_dim, double base);
  * table ("How the attention kernel actually reads paged blocks").  Query head
  * h reads KV head h / (n_q_heads / n_kv_heads) (grouped-query attention).
  *   out          : [num_seqs][n_q_heads][head_dim] in out_dtype.
- *   q            : [num_seqs][n_q_heads][head_dim], cache dtype.
+ *   q            : [num_seqs][n_q_heads][head_dim], cache dtype (FP8 and FP4 pools:
+ *                  cache->act_dtype).
  *   block_tables : int32 [num_seqs][max_blocks_per_seq]; entries past
  *                  ceil(len / block_size) are never read.
  *   context_lens : int32 [num_seqs]; the count includes the newest token
@@ -224,12 +225,21 @@ int pa_rope_table(float* table, int max_position, int rot_dim, double base);
  *                  that uses one; batches of a few units per resident thread
  *                  block are dealt round robin and use none) and, for long
  *                  contexts split over several thread blocks,
- *                  the partial results the second kernel combines.  Calls that
- *                  overlap on the GPU must not share one workspace.
+ *                  the partial results the second kernel combines.  (FP4 pools:
+ *                  no counter; for tables of more than 128 tokens a record and
+ *                  the partial results of each thread block.  The size covers
+ *                  every pool type.)  Calls that overlap on the GPU must not
+ *                  share one workspace.
  * n_q_heads must be a multiple of n_kv_heads.  Accumulation is fp32.
  * FP8 pools: q is in cache->act_dtype; K/V codes are widened exactly to fp16
  * and q is rounded to fp16 for the tensor-core products (exact for bf16 q of
- * magnitude in [2^-14, 65504]); the scales multiply the scores and the output. */
+ * magnitude in [2^-14, 65504]); the scales multiply the scores and the output.
+ * FP4 pools: q is in cache->act_dtype; codes times their scales are exact in fp16, bf16 q
+ * is scaled into fp16 by a power of two a row (exact for elements down to 2^-28 of the
+ * row's largest), and k_scale and v_scale multiply the scores and the output.
+ * Probabilities enter P V as one fp16 part (11 bits: an output moves by at most 2^-11 of the
+ * largest |v| that it averages, and 2^-32 of it for each key); over 16-bit and FP8 pools of
+ * head_dim 64 or 128 they do as two parts (about 16 bits). */
 pa_status pa_decode(void* out, pa_dtype out_dtype, const void* q,
                     const void* k_cache, const void* v_cache, const pa_cache_desc* cache,
                     const int32_t* block_tables, int max_blocks_per_seq,
@@ -254,12 +264,12 @@ size_t pa_decode_workspace_size(int num_seqs, int n_q_heads, int n_kv_heads, int
  * rows of one tensor-core tile, so each K/V slab is still read once for all
  * of them.
  *   out, q       : [num_seqs][q_per_seq][n_q_heads][head_dim] (out in out_dtype,
- *                  q in the cache dtype, or cache->act_dtype for FP8 pools).
+ *                  q in the cache dtype, or cache->act_dtype for FP8 and FP4 pools).
  *   context_lens : include the q_per_seq new rows; a length below q_per_seq
  *                  flags PA_ERR_OUT_OF_RANGE in the device error word and the
  *                  sequence's rows are not written.
  *   workspace    : pa_decode_verify_workspace_size(...) bytes, as for pa_decode.
- * q_per_seq in [1, 16]; q_per_seq = 1 is pa_decode.  bf16/fp16/FP8 pools with
+ * q_per_seq in [1, 16]; q_per_seq = 1 is pa_decode.  bf16/fp16/FP8/FP4 pools with
  * head_dim 64 or 128 (else PA_ERR_UNSUPPORTED); other rules as pa_decode. */
 pa_status pa_decode_verify(void* out, pa_dtype out_dtype, const void* q,
                            const void* k_cache, const void* v_cache, const pa_cache_desc* cache,
@@ -389,7 +399,7 @@ size_t pa_decode_scored_workspace_size(int num_seqs, int q_per_seq, int n_q_head
  * prefill of the whole prompt.
  *   out, q          : [total_q][n_q_heads][head_dim], request r's rows start at
  *                     query_start_loc[r]; out in out_dtype, q in the cache
- *                     dtype (FP8 pools: in cache->act_dtype).
+ *                     dtype (FP8 and FP4 pools: in cache->act_dtype).
  *   query_start_loc : int32 [num_reqs + 1] on the device, non-decreasing,
  *                     query_start_loc[0] = 0; C_r = difference of neighbours.
  *   context_lens    : int32 [num_reqs] on the device: total tokens L_r of
@@ -399,16 +409,17 @@ size_t pa_decode_scored_workspace_size(int num_seqs, int q_per_seq, int n_q_head
  *                     device error word (its rows past max_query_len are not
  *                     written).
  *   workspace       : reserved; pass NULL / 0 (pa_prefill_workspace_size is 0).
- * bf16, fp16 and FP8 E4M3 pools (f32 pools return PA_ERR_UNSUPPORTED).  FP8
+ * bf16, fp16, FP8 and FP4 pools (f32 pools return PA_ERR_UNSUPPORTED).  FP8
  * pools keep V transposed per 16-token piece as for decode; their codes are
  * widened exactly to fp16 on chip (every E4M3 value is an fp16 value) and the
  * scales are folded into the softmax scale (k_scale) and the output (v_scale).
  * Roundings: probabilities enter P V as two bf16 parts (about 16 bits) over bf16
  * pools, as one fp16 part over fp16, FP8 and FP4 pools (11 bits: an output moves by at
- * most 2^-11 of the largest |v| that it averages, and 2^-32 of it for each key).  bf16 queries over an FP8 pool
- * with head_dim 128 enter the scores as the sum of two E4M3 parts: exact for
- * elements down to 2^-10 of the row's largest, off by at most 2^-17 of that
- * largest below. */
+ * most 2^-11 of the largest |v| that it averages, and 2^-32 of it for each key).  bf16
+ * queries over an FP8 pool with head_dim 128 enter the scores as the sum of two E4M3
+ * parts: exact for elements down to 2^-10 of the row's largest, off by at most 2^-17 of
+ * that largest below.  Other bf16 queries over FP8 and FP4 pools are scaled into fp16 by a power
+ * of two a row: exact for elements down to 2^-28 of the row's largest. */
 pa_status pa_prefill_chunk(void* out, pa_dtype out_dtype, const void* q,
                            const void* k_cache, const void* v_cache, const pa_cache_desc* cache,
                            const int32_t* block_tables, int max_blocks_per_seq,

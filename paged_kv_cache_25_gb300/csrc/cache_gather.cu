@@ -6,8 +6,8 @@
 // 16 elements of a row.  V of an FP8 pool lies transposed in 16-token pieces, so a token's
 // 16 codes are 16 single bytes, 16 apart; neighbouring threads take neighbouring tokens there, whose
 // bytes share the same sectors.
-// 32,768 tokens of 8 heads of 128 elements out of an FP4 pool into bf16: 32.4 us, 5.3 TB/s (0.78 of the copy
-// rate), issue 61 %; out of an FP8 pool 51, by V's single bytes, of a bf16 pool 47 (floors 25, 30, 40).
+// 32,768 tokens of 8 heads of 128 elements out of an FP4 pool into bf16: 32.6 us, 5.3 TB/s (0.78 of the copy
+// rate), issue 60 %; out of an FP8 pool 47.7, by V's single bytes, of a bf16 pool 42.5 (floors 25, 30, 40).
 #include <algorithm>
 
 #include "fp4.cuh"

@@ -14,7 +14,8 @@
 //
 // Bound: HBM for long chunks (every element is read once and written once,
 // 3 flops each), launch latency for a decode step; for FP4 pools also the ~390 instructions of a group
-// of 16 (K and V of 8192 tokens of 8 heads of 128 elements: 24 us, issue 46 %, HBM floor 6).
+// of 16 (K and V of 8192 tokens of 8 heads of 128 elements: 24 us, issue 46 %, HBM floor 6).  The forms with several
+// axes of 16-bit types spill 48 - 56 bytes a thread at 64 registers, as they hold two loops over the tokens; the others none.
 #include <cuda_fp8.h>
 #include <algorithm>
 #include <cmath>
@@ -248,7 +249,7 @@ struct RopeItem {
 // Several axes, where a warp's items are of one token and the table's row has at most 128 values: the lanes load
 // the angles of two pairs each and share them through shared memory, the next token's in flight with its pieces, the
 // positions (one axis a lane) two tokens ahead.  (With every thread picking its own pairs' positions and angles, 8192
-// tokens of Llama-3-8B's heads and three axes took 55 us into an FP8 pool, now 45, 61 into an FP4 pool, now 59.)
+// tokens of Llama-3-8B's heads and three axes took 48 us into an FP8 pool, now 41, 48.6 into an FP4 pool, now 46.5.)
 template <typename T, bool F8>
 __device__ __forceinline__ void rope_warp(const RopeParams& p, const RopeItem<T, F8>& w, int t, int step, uint4 ra, uint4 rb)
 {

@@ -8,8 +8,8 @@
 // Work: the rows of all (sequence, KV head, up to RU of its (head, query) rows), one after another,
 // are a line of 128-token granules with kRowCost more units before each row for what a piece costs
 // beside its tokens (its queries and its combine take about as long as a granule); every block of a
-// persistent grid takes an equal run of it.  (Without those units 40 sequences of 100 - 2047 tokens
-// and 40 KV heads took 98 us, now 72: blocks with rows of one granule came last.  Two units: 74.)
+// persistent grid takes an equal run of it.  (40 sequences of 100 - 2047 tokens and 40 KV heads, kernels
+// alone: 98 us without those units, when blocks with rows of one granule came last, 72 with one, 74 with two.)
 // A block's run holds whole rows, which it finishes, and at most two pieces of rows that it shares
 // with its neighbours, whose partials meet in f4_merge_kernel.  A piece's four warps take 32 tokens
 // of each stage and combine through shared memory.
@@ -88,7 +88,7 @@ struct F4Cfg {
     static constexpr int kTiles = kGranule / kPieceTok;                     // tiles of K, and of V, a stage
     static constexpr int kStage = 2 * kTiles * kTile;                       // K tiles, then V tiles
     // (16 rows, two tiles of accumulators: with three blocks an SM 256 sequences of 16 rows of 64 elements took 145 us for
-    // 176, of 128 elements, whose accumulators spilled, 254 for 240)
+    // 176, of 128 elements, whose accumulators spilled, 254 for 240; kernels alone)
     static constexpr int kCtas = RU == 16 ? (D == 64 ? 3 : 2) : 4;
     static constexpr int kNS = RU == 16 ? (D == 64 ? 3 : 4) : (D == 64 ? 4 : 2);
     static constexpr int kRing = kNS * kStage;
@@ -832,9 +832,11 @@ static cudaError_t run_f4_rows(const F4Params& p, const DecodeArgs& a, void* ws,
 
 // Rows of a KV head past which the chunked prefill's kernel takes the call, its sequences as chunks of
 // q_per_seq rows: one pass over the keys, on tcgen05, for up to 128 rows a tile, where the kernel above reads and widens them
-// again for every 16.  64 sequences of 512 - 4096 tokens of 8 KV heads of 128 elements: 137 us for any
-// number of rows up to 128, against 145 with 32 rows, 199 with 48, 260 with 64, 485 with 128 (two of 60,000 tokens
-// on one KV head each are better off there, whose line of work fills the GPU: 94 us with 64 rows against 109).
+// again for every 16.  64 sequences of 512 - 4096 tokens of 8 KV heads of 128 elements: 132 us for any
+// number of rows up to 128, against 133 with 32 rows here, 177 - 188 with 40, 236 - 254 with 64, 458 with 128.
+// The rule looks at rows alone, and a few long sequences lose by it: their row blocks, each cut over a cluster of at most
+// eight, leave most of the GPU idle, where the line of work above fills it.  One of 60,000 tokens on one KV head 104 us
+// with 40 rows against 34, on eight KV heads 107 against 69; eight of 20,000 - 110,000 on eight 701 against 475.
 constexpr int kF4DecodeRows = 32;
 
 cudaError_t launch_decode_fp4(const DecodeArgs& a, void* workspace, size_t workspace_bytes, cudaStream_t s)

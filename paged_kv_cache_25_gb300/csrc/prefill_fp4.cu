@@ -1,7 +1,8 @@
 // Chunked prefill over FP4 pools (pa_prefill_chunk): the tcgen05 prefill kernel, whose
 // converter warps widen 4-bit rows into its rings (prefill_fp4.cuh).  Calls of few row blocks over long contexts split
 // their key tiles over clusters as scored calls do, by the same rule (prefill_splits): one chunk of 512 rows after
-// 3584 tokens of Llama-3-8B's heads, 64 blocks: 55 us against 78; four such chunks, 256 blocks: 198 against 150, not split.
+// 3584 tokens of Llama-3-8B's heads, 64 blocks: 45 us in clusters of two, 67 not split, 132 in clusters of eight; four such
+// chunks, 256 blocks: 130 not split, as they run, 470 in clusters of eight.
 #include "prefill_tc.cuh"
 
 namespace pa {

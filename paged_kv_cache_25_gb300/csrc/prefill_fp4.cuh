@@ -34,7 +34,7 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t
 // What bounds it: a lone warp beside four softmax warps, so the latency of its instructions, of which a chunk
 // has ~24 for 16 elements and ~100 more around them (chunks of 32 rows by two untiled copies, their loads between
 // the stores and the block ids loaded when they were needed: the converters took 7000 clocks a tile, now 3500).
-// Four chunks of 512 rows after 1024 - 8192 tokens of Llama-3-8B's heads: 154 us, 1060 TFLOP/s (247 at first).
+// Four chunks of 512 rows after 1024 - 8192 tokens of Llama-3-8B's heads: 155 us, 1060 TFLOP/s (247 at first).
 template <int D, int BS, int kKeys, int kStages>
 __device__ __forceinline__ void f4_convert(const CUtensorMap* kmap, const CUtensorMap* vmap, const int32_t* table,
                                            int max_blocks, int num_blocks, int n_kv, int kvh, int L, int tile0, int n_tiles,
